@@ -26,6 +26,8 @@
  *   - same page, section 3.2: 32 consecutive head_dim values packed together.
  *   - TurboQuant 3-bit article, section 3.1: eight 3-bit codes in 24 bits; section
  *     6.1: a paged cache of 32-token blocks.
+ * The calls on runs of several tokens (kvq_append_chunk, kvq_chunk_attention,
+ * kvq_cross_attention, kvq_read_tokens) are this library's additions.
  *
  * ---------------------------------------------------------------------------
  * Notation
@@ -137,6 +139,7 @@ typedef enum {
 #define KVQ_ERRBIT_BADLEN 0x8u   /* seq_lens[b] < 0 or > Lmax; that sequence was skipped */
 #define KVQ_ERRBIT_BADPAGE 0x10u /* a block-table page outside [0, NP): pack/append wrote nothing
                                    there; decode output of that sequence is undefined */
+#define KVQ_ERRBIT_BADPOS 0x20u  /* a position outside the rotation table; the nearest row was used */
 
 /* Static description of one layer's cache.  group must be 32.  Every field is
  * significant: zero-initialise the struct (sink = 0 keeps no sink window). */
@@ -366,6 +369,113 @@ kvq_status kvq_decode_step_host(const kvq_cache_desc* desc, const kvq_cache_view
 kvq_status kvq_decode_attention_noalloc(const kvq_cache_desc* desc, const kvq_cache_view* view,
                                         const void* q, int32_t num_q_heads, void* out,
                                         uint32_t flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Runs of several tokens.  The calls below take, for each sequence, a run of
+ * consecutive tokens: the drafts of a speculative step, a piece of a prompt, a
+ * decoder's prompt over encoder states.  Runs are ragged and concatenated:
+ *   cu_seqlens  int32 device [B + 1], nondecreasing, cu_seqlens[0] >= 0; the run of
+ *               sequence b is rows [cu_seqlens[b], cu_seqlens[b + 1]) of the
+ *               token-major inputs and outputs.  A run may be empty.
+ *   total       rows those arrays have (cu_seqlens[B] <= total).  Rows of no
+ *               run are neither read nor written.
+ *   max_len     host upper bound of the run lengths, >= 0.
+ * A sequence whose entries are not 0 <= cu[b] <= cu[b+1] <= total with at most
+ * max_len tokens is skipped and sets KVQ_ERRBIT_BADLEN. */
+
+/* Arguments of kvq_append_chunk; zero-initialise the struct. */
+typedef struct {
+  const void* k;           /* fp16 device: element j of head h of row t at */
+  const void* v;           /*   t * kv_stride_token + h * kv_stride_head + j */
+  int64_t kv_stride_token; /* in elements, non-negative multiples of 8 */
+  int64_t kv_stride_head;
+  const void* q;           /* fp16 device queries to rotate, or NULL */
+  void* q_out;             /* fp16 device [total][Hq][d]; may be q itself when q is
+                              contiguous, and overlaps no input otherwise */
+  int64_t q_stride_token;
+  int64_t q_stride_head;
+  int32_t num_q_heads;     /* Hq (read only with q) */
+  const int32_t* cu_seqlens;
+  int32_t total;
+  int32_t max_len;
+  const float* rope;       /* fp32 device [rope_rows][rotary_dim / 2][2]: cos, sin of each
+                              position and pair; NULL when rotary_dim == 0 */
+  int32_t rope_rows;
+  int32_t rotary_dim;      /* leading elements of a head that are rotated: a multiple of 16,
+                              0..head_dim (0: keys and queries are taken as they are) */
+  int32_t interleaved;     /* pairs: 0 (i, i + rotary_dim / 2), 1 (2i, 2i + 1) */
+  const int32_t* positions; /* int32 device [total], or NULL: token i of a run is at the
+                              number of tokens its sequence held before the call + i */
+} kvq_append_args;
+
+/* Append a run of tokens to each sequence, rotating keys and queries to their
+ * positions on the way.
+ *   R1  a pair (a, b) at table entry (c, s) becomes fp16_rne(a*c - b*s) and
+ *       fp16_rne(b*c + a*s): fp32 products and one fp32 sum or difference, each
+ *       rounded to nearest even (no fused multiply-add).  Elements from
+ *       rotary_dim on, and values, are unchanged.
+ *   R2  the rotated keys and the values enter the cache exactly as successive
+ *       kvq_append calls of one token each would leave it: cache bytes, ring
+ *       slots, counters and KVQ_ERRBIT_CAPACITY (tokens that no longer fit are
+ *       dropped).  The sink is never written.
+ *   R3  with q, q_out[t] is row t's queries rotated to the same position; rows of
+ *       dropped tokens included.
+ * A position outside [0, rope_rows) sets KVQ_ERRBIT_BADPOS and uses the nearest
+ * row.  One launch for short runs (a block per sequence), two otherwise (the
+ * counters move in the second).  Asynchronous; needs no workspace. */
+kvq_status kvq_append_chunk(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                            const kvq_append_args* args, void* stream);
+
+/* Bytes of scratch kvq_chunk_attention and kvq_cross_attention need for
+ * num_q_heads query heads on the current device (any run lengths).  Returns 0
+ * for an invalid desc or head count. */
+size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* desc, int32_t num_q_heads);
+
+/* Causal attention of each sequence's newest tokens over its cache: the run of
+ * sequence b is its last T_b tokens (appended before the call), and token i of
+ * it attends over the first N_b - T_b + i + 1 of the sequence's N_b = sink_len +
+ * packed_len + res_len tokens, in the form in which the cache holds them.
+ *   q          fp16 device [total][Hq][d], 16-byte aligned (rotated, where positions are).
+ *   out        device [total][Hq][d], fp16 (fp32 with KVQ_OUT_F32 in flags), rounded
+ *              once from the fp32 result.
+ *   workspace  device scratch of ws_bytes >= kvq_chunk_workspace_bytes(desc, Hq),
+ *              16-byte aligned, zeroed before its first use; each completed call
+ *              leaves it ready for the next, whatever its shapes.  Zero it again
+ *              after a call that reported KVQ_ERR_TIMEOUT.  One workspace serves
+ *              one call at a time.
+ *   flags      0 or KVQ_OUT_F32; other bits return KVQ_ERR_INVALID_ARG.
+ * A row with no token to attend over gets zeros and sets KVQ_ERRBIT_EMPTY.
+ * Tokens a row does not attend over have no part in its output, whatever they
+ * hold.  Tokens in a page outside the pool are left out (KVQ_ERRBIT_BADPAGE).
+ * With one token for every sequence kvq_decode_attention is the faster call.
+ * Asynchronous; lengths are read on the device. */
+kvq_status kvq_chunk_attention(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                               const void* q, int32_t num_q_heads, const int32_t* cu_seqlens,
+                               int32_t total, int32_t max_len, void* out, void* workspace,
+                               size_t ws_bytes, uint32_t flags, void* stream);
+
+/* kvq_chunk_attention without the mask: every row of sequence b's run attends
+ * over all N_b cached tokens (cross attention of decoder tokens to an encoder's
+ * states, packed by kvq_quantize_pack; run and cache lengths are unrelated). */
+kvq_status kvq_cross_attention(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                               const void* q, int32_t num_q_heads, const int32_t* cu_seqlens,
+                               int32_t total, int32_t max_len, void* out, void* workspace,
+                               size_t ws_bytes, uint32_t flags, void* stream);
+
+/* Read tokens back as the values they stand for.
+ *   first      int32 device [B]: first token of each sequence, in the order sink,
+ *              packed, residual (oldest first); NULL reads from token 0.
+ *   count      tokens per sequence, >= 0.
+ *   k_out, v_out  device [B][Hkv][count][d] (the layout kvq_quantize_pack takes), fp16,
+ *              or fp32 with KVQ_OUT_F32 in flags; row j of sequence b is token
+ *              first[b] + j.  Packed values are min + code * scale in fp32, rounded
+ *              once to the output type; sink and residual values are exact.
+ * Rows past a sequence's end are zero.  A negative first[b] sets
+ * KVQ_ERRBIT_BADLEN and gives that sequence zero rows; a page outside the pool
+ * sets KVQ_ERRBIT_BADPAGE and gives its tokens zero rows.  Asynchronous. */
+kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                           const int32_t* first, int32_t count, void* k_out, void* v_out,
+                           uint32_t flags, void* stream);
 
 /* Synchronize `stream`, copy *err_word to *word_out (may be NULL), clear it, and
  * return KVQ_OK if it was 0, else the status of its lowest set bit. */

@@ -269,7 +269,7 @@ def _cache(s):
     cache.counters.copy_(torch.stack([s["packed_len"], s["res_len"], s["res_head"], s["sink_len"]]))
     s["counters"] = cache.counters.clone()
     if c["op"] != "read":
-        s["workspace"] = kvq.chunk_workspace_for(cache, c["hq"], s["total"], s["q_max"])
+        s["workspace"] = kvq.chunk_workspace_for(cache, c["hq"])
     return cache
 
 
