@@ -268,7 +268,7 @@ def _cache(s):
         cache.block_table.copy_(s["block_table"])
     cache.counters.copy_(torch.stack([s["packed_len"], s["res_len"], s["res_head"], s["sink_len"]]))
     s["counters"] = cache.counters.clone()
-    if c["op"] != "read":
+    if c["op"] in ("chunk", "cross"):
         s["workspace"] = kvq.chunk_workspace_for(cache, c["hq"])
     return cache
 
@@ -393,7 +393,7 @@ def _calls(s, op):
         if s["case"]["residual"]:
             torch._foreach_copy_([cache.k_res, cache.v_res], [s["k_res"], s["v_res"]])
         q = kvq.kvq_append_chunk(cache, s["k"], s["v"], s["cu"], s["q_max"], q=s["q"], rope=s.get("rope"),
-                                 interleaved=s["case"]["interleaved"], workspace=s["workspace"])
+                                 interleaved=s["case"]["interleaved"])
         k, v = kvq.kvq_read_tokens(cache, s["first"], s["case"]["residual"] + s["q_max"])
         return {"k": k, "v": v, "q": q, "counters": cache.counters}
     if op == "read":
