@@ -237,6 +237,95 @@ kvq_status kvq_decode_step_host(const kvq_cache_desc* desc, const kvq_cache_view
   return KVQ_OK;
 }
 
+kvq_status kvq_append_chunk(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                            const kvq_append_args* args, void* stream) {
+  kvq_status st = check_desc(desc);
+  if (st != KVQ_OK) return st;
+  if ((st = check_view(*desc, view)) != KVQ_OK) return st;
+  if (!args || !args->cu_seqlens || args->total < 0 || args->max_len < 0) return KVQ_ERR_INVALID_ARG;
+  const kvq_append_args& A = *args;
+  if (A.total > 0 && (!A.k || !A.v)) return KVQ_ERR_INVALID_ARG;
+  if (A.kv_stride_token < 0 || A.kv_stride_head < 0) return KVQ_ERR_INVALID_ARG;
+  if (A.q && (!A.q_out || A.num_q_heads < 1 || A.num_q_heads % desc->num_kv_heads ||
+              A.q_stride_token < 0 || A.q_stride_head < 0))
+    return KVQ_ERR_INVALID_ARG;
+  if (A.rotary_dim < 0 || A.rotary_dim > desc->head_dim || (A.interleaved != 0 && A.interleaved != 1))
+    return KVQ_ERR_INVALID_ARG;
+  if (A.rotary_dim % 16) return KVQ_ERR_UNSUPPORTED;
+  if (A.rotary_dim > 0 && (!A.rope || A.rope_rows < 1)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(A.k, 16) || !aligned(A.v, 16) || !aligned(A.q, 16) || !aligned(A.q_out, 16) ||
+      !aligned(A.rope, 16) || !aligned(A.cu_seqlens, 4) || !aligned(A.positions, 4))
+    return KVQ_ERR_MISALIGNED;
+  // every 8-value piece a lane loads must start on a 16-byte boundary
+  if (A.kv_stride_token % 8 || A.kv_stride_head % 8) return KVQ_ERR_MISALIGNED;
+  if (A.q && (A.q_stride_token % 8 || A.q_stride_head % 8)) return KVQ_ERR_MISALIGNED;
+  const Dims s = kvq::dims_of(*desc);
+  return from_cuda(kvq::launch_append_chunk(s, *view, A, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* desc, int32_t num_q_heads) {
+  if (check_desc(desc) != KVQ_OK || num_q_heads < 1 || num_q_heads % desc->num_kv_heads) return 0;
+  return kvq::chunk_workspace_bytes(kvq::dims_of(*desc), num_q_heads, kvq::device_sm_count());
+}
+
+namespace {
+kvq_status attend_runs(const kvq_cache_desc* desc, const kvq_cache_view* view, const void* q,
+                       int32_t num_q_heads, const int32_t* cu_seqlens, int32_t total, int32_t max_len,
+                       void* out, void* workspace, size_t ws_bytes, uint32_t flags, bool causal,
+                       void* stream) {
+  kvq_status st = check_desc(desc);
+  if (st != KVQ_OK) return st;
+  if ((st = check_view(*desc, view)) != KVQ_OK) return st;
+  if (!cu_seqlens || total < 0 || max_len < 0 || !workspace || num_q_heads < 1 ||
+      num_q_heads % desc->num_kv_heads || (flags & ~(uint32_t)KVQ_OUT_F32))
+    return KVQ_ERR_INVALID_ARG;
+  if (total > 0 && (!q || !out)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(cu_seqlens, 4))
+    return KVQ_ERR_MISALIGNED;
+  const Dims s = kvq::dims_of(*desc);
+  // rows of one KV head and tokens of one sequence are counted in 32 bits
+  const int64_t gq = num_q_heads / desc->num_kv_heads;
+  if ((int64_t)(max_len < total ? max_len : total) * gq > (1LL << 30) ||
+      (int64_t)s.cap + s.Nr + s.Ns > (1LL << 30))
+    return KVQ_ERR_UNSUPPORTED;
+  if (ws_bytes < kvq::chunk_workspace_bytes(s, num_q_heads, kvq::device_sm_count()))
+    return KVQ_ERR_INVALID_ARG;
+  return from_cuda(kvq::launch_chunk_attention(
+      s, *view, static_cast<const __half*>(q), num_q_heads, cu_seqlens, total, max_len, out, workspace,
+      causal, flags, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+kvq_status kvq_chunk_attention(const kvq_cache_desc* desc, const kvq_cache_view* view, const void* q,
+                               int32_t num_q_heads, const int32_t* cu_seqlens, int32_t total,
+                               int32_t max_len, void* out, void* workspace, size_t ws_bytes,
+                               uint32_t flags, void* stream) {
+  return attend_runs(desc, view, q, num_q_heads, cu_seqlens, total, max_len, out, workspace, ws_bytes,
+                     flags, true, stream);
+}
+
+kvq_status kvq_cross_attention(const kvq_cache_desc* desc, const kvq_cache_view* view, const void* q,
+                               int32_t num_q_heads, const int32_t* cu_seqlens, int32_t total,
+                               int32_t max_len, void* out, void* workspace, size_t ws_bytes,
+                               uint32_t flags, void* stream) {
+  return attend_runs(desc, view, q, num_q_heads, cu_seqlens, total, max_len, out, workspace, ws_bytes,
+                     flags, false, stream);
+}
+
+kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* view,
+                           const int32_t* first, int32_t count, void* k_out, void* v_out,
+                           uint32_t flags, void* stream) {
+  kvq_status st = check_desc(desc);
+  if (st != KVQ_OK) return st;
+  if ((st = check_view(*desc, view)) != KVQ_OK) return st;
+  if (count < 0 || (flags & ~(uint32_t)KVQ_OUT_F32)) return KVQ_ERR_INVALID_ARG;
+  if (count > 0 && (!k_out || !v_out)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(first, 4)) return KVQ_ERR_MISALIGNED;
+  const Dims s = kvq::dims_of(*desc);
+  return from_cuda(kvq::launch_read_tokens(s, *view, first, count, k_out, v_out, flags,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
 kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* stream) {
   if (!view || !view->err_word) return KVQ_ERR_INVALID_ARG;
   if (!aligned(view->err_word, 4)) return KVQ_ERR_MISALIGNED;
@@ -251,7 +340,7 @@ kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* 
   if (w & KVQ_ERRBIT_CAPACITY) return KVQ_ERR_CAPACITY;
   if (w & KVQ_ERRBIT_EMPTY) return KVQ_ERR_EMPTY;
   if (w & KVQ_ERRBIT_TIMEOUT) return KVQ_ERR_TIMEOUT;
-  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE)) return KVQ_ERR_INVALID_ARG;
+  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE | KVQ_ERRBIT_BADPOS)) return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
 

@@ -33,6 +33,7 @@ KVQ_ERRBIT_EMPTY = 0x2
 KVQ_ERRBIT_TIMEOUT = 0x4
 KVQ_ERRBIT_BADLEN = 0x8
 KVQ_ERRBIT_BADPAGE = 0x10
+KVQ_ERRBIT_BADPOS = 0x20
 
 KVQ_ARRAY_CODES = 0
 KVQ_ARRAY_PARAMS = 1
@@ -44,7 +45,8 @@ KVQ_ARRAY_MODE = 4
 EXPORTS = ("kvq_cache_bytes", "kvq_decode_workspace_bytes", "kvq_quantize_pack",
            "kvq_quantize_pack_strided", "kvq_append",
            "kvq_decode_attention", "kvq_decode_step", "kvq_decode_step_host", "kvq_step_io_bytes",
-           "kvq_decode_attention_noalloc",
+           "kvq_decode_attention_noalloc", "kvq_append_chunk", "kvq_chunk_workspace_bytes",
+           "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens",
            "kvq_read_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
            "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding")
 
@@ -62,6 +64,17 @@ class CacheView(ctypes.Structure):
         "k_codes", "v_codes", "k_params", "v_params", "k_res", "v_res",
         "packed_len", "res_len", "res_head", "err_word", "k_sink", "v_sink", "sink_len",
         "k_mode", "v_mode", "block_table")]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("kv_stride_token", ctypes.c_int64), ("kv_stride_head", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("num_q_heads", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+                ("total", ctypes.c_int32), ("max_len", ctypes.c_int32), ("rope", ctypes.c_void_p),
+                ("rope_rows", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
 
 
 class KvqError(RuntimeError):
@@ -110,6 +123,15 @@ def load(path: str | None = None):
             lib.kvq_decode_step_host.restype = ctypes.c_int
             lib.kvq_decode_attention_noalloc.argtypes = [DP, VP, P, i32, P, ctypes.c_uint32, P]
             lib.kvq_decode_attention_noalloc.restype = ctypes.c_int
+            lib.kvq_append_chunk.argtypes = [DP, VP, ctypes.POINTER(AppendArgs), P]
+            lib.kvq_append_chunk.restype = ctypes.c_int
+            lib.kvq_chunk_workspace_bytes.argtypes = [DP, i32]
+            lib.kvq_chunk_workspace_bytes.restype = sz
+            for fn in (lib.kvq_chunk_attention, lib.kvq_cross_attention):
+                fn.argtypes = [DP, VP, P, i32, P, i32, i32, P, P, sz, ctypes.c_uint32, P]
+                fn.restype = ctypes.c_int
+            lib.kvq_read_tokens.argtypes = [DP, VP, P, i32, P, P, ctypes.c_uint32, P]
+            lib.kvq_read_tokens.restype = ctypes.c_int
             lib.kvq_read_error.argtypes = [VP, ctypes.POINTER(ctypes.c_uint32), P]
             lib.kvq_read_error.restype = ctypes.c_int
             lib.kvq_status_string.argtypes = [ctypes.c_int]
@@ -398,6 +420,168 @@ def kvq_decode_attention_noalloc(cache: KVCache, q: torch.Tensor, out: torch.Ten
                                              _stream(stream, q.device))
     _check(st, "kvq_decode_attention_noalloc")
     return out
+
+
+# --------------------------------------------------- runs of several tokens ----
+
+
+def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0,
+               device="cuda") -> torch.Tensor:
+    """Cosine and sine of positions 0 .. num_positions - 1 for kvq_append_chunk, fp32
+    [num_positions][rotary_dim / 2][2]: angle = position * base^(-2i / rotary_dim),
+    worked out in 64 bits.  Made once; any table of that shape serves (scaled
+    frequencies, a magnitude factor)."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    angle = (torch.arange(num_positions, dtype=torch.float64, device=device).unsqueeze(1)
+             * base ** (-2.0 * i / rotary_dim))
+    return torch.stack([angle.cos(), angle.sin()], -1).float()
+
+
+def _run_args(cache: KVCache, cu_seqlens: torch.Tensor, what: str) -> None:
+    if (cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous()
+            or cu_seqlens.numel() != cache.desc.batch + 1):
+        raise ValueError(f"{what}: cu_seqlens must be a contiguous int32 CUDA tensor of B + 1 entries")
+
+
+def _run_tensor(t: torch.Tensor, heads: int, cache: KVCache, name: str, contiguous: bool) -> None:
+    if (t.dtype != torch.float16 or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads
+            or t.shape[2] != cache.desc.head_dim or (t.numel() and t.stride(2) != 1)
+            or (contiguous and not t.is_contiguous())):
+        raise ValueError(f"{name} must be a float16 CUDA tensor [total][{heads}][{cache.desc.head_dim}]"
+                         f"{', contiguous' if contiguous else ' with head_dim contiguous'}")
+    if t.device != cache.device and cache.device.index is not None:
+        raise ValueError(f"{name} must be on the cache's device")
+
+
+def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     max_len: int, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                     rope: torch.Tensor | None = None, interleaved: bool = False,
+                     positions: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Append a run of tokens to each sequence (ragged, concatenated: sequence b's run
+    is rows cu_seqlens[b] .. cu_seqlens[b+1]); k, v fp16 [total][Hkv][d] views with d
+    contiguous and equal strides.  With ``rope`` (fp32 [rows][rotary_dim / 2][2], see
+    rope_table) keys are rotated to their positions first: the tokens the sequence held
+    + the place in the run, or ``positions`` (int32 [total]).  ``q`` (fp16 [total][Hq][d])
+    is rotated too and returned (in ``q_out``, which may be q itself)."""
+    D = cache.desc
+    _run_args(cache, cu_seqlens, "kvq_append_chunk")
+    _run_tensor(k, D.num_kv_heads, cache, "k", False)
+    _run_tensor(v, D.num_kv_heads, cache, "v", False)
+    total = int(k.shape[0])
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    a = AppendArgs(k=k.data_ptr(), v=v.data_ptr(), kv_stride_token=k.stride(0),
+                   kv_stride_head=k.stride(1), cu_seqlens=cu_seqlens.data_ptr(), total=total,
+                   max_len=int(max_len), interleaved=int(interleaved))
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != total:
+            raise ValueError("q must be [total][Hq][d] with k's rows")
+        _run_tensor(q, q.shape[1], cache, "q", False)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        _run_tensor(q_out, q.shape[1], cache, "q_out", True)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q must be contiguous to be rotated in place")
+        a.q, a.q_out, a.num_q_heads = q.data_ptr(), q_out.data_ptr(), int(q.shape[1])
+        a.q_stride_token, a.q_stride_head = q.stride(0), q.stride(1)
+    if rope is not None:
+        if (rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 3 or rope.shape[2] != 2
+                or not rope.is_contiguous()):
+            raise ValueError("rope must be a contiguous float32 CUDA tensor [rows][rotary_dim / 2][2]")
+        a.rope, a.rope_rows, a.rotary_dim = rope.data_ptr(), int(rope.shape[0]), 2 * int(rope.shape[1])
+    if positions is not None:
+        if (positions.dtype != torch.int32 or not positions.is_cuda or not positions.is_contiguous()
+                or positions.numel() != total):
+            raise ValueError("positions must be a contiguous int32 CUDA tensor of `total` entries")
+        a.positions = positions.data_ptr()
+    st = load().kvq_append_chunk(ctypes.byref(D), ctypes.byref(cache.view), ctypes.byref(a),
+                                 _stream(stream, k.device))
+    _check(st, "kvq_append_chunk")
+    return q_out
+
+
+def kvq_chunk_workspace_bytes(desc: CacheDesc, num_q_heads: int) -> int:
+    return int(load().kvq_chunk_workspace_bytes(ctypes.byref(desc), int(num_q_heads)))
+
+
+def chunk_workspace_for(cache: KVCache, num_q_heads: int) -> torch.Tensor:
+    """A zeroed workspace for kvq_chunk_attention and kvq_cross_attention (zeroed
+    once; any run lengths)."""
+    n = kvq_chunk_workspace_bytes(cache.desc, num_q_heads)
+    if n == 0:
+        raise KvqError(KVQ_ERR_INVALID_ARG, "kvq_chunk_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspace, stream, flags):
+    if q.dim() != 3:
+        raise ValueError("q must be [total][Hq][d]")
+    _run_args(cache, cu_seqlens, name)
+    _run_tensor(q, q.shape[1], cache, "q", True)
+    out, flags = _out(q, out, flags)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = chunk_workspace_for(cache, q.shape[1])
+    st = getattr(load(), name)(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
+                               int(q.shape[1]), _ptr(cu_seqlens), int(q.shape[0]), int(max_len),
+                               _ptr(out), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), int(flags),
+                               _stream(stream, q.device))
+    _check(st, name)
+    return out
+
+
+def kvq_chunk_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None, flags: int = 0) -> torch.Tensor:
+    """Causal attention of each sequence's newest tokens over its cache: q fp16
+    [total][Hq][d], sequence b's run (rows cu_seqlens[b] .. cu_seqlens[b+1]) being its
+    last tokens, already appended.  out fp16, or fp32 as for kvq_decode_attention."""
+    return _attend_runs("kvq_chunk_attention", cache, q, cu_seqlens, max_len, out, workspace, stream,
+                        flags)
+
+
+def kvq_cross_attention(cache: KVCache, q: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None, flags: int = 0) -> torch.Tensor:
+    """Every row of each sequence's run attends over all its cached tokens (decoder
+    tokens over an encoder's states); arguments as for kvq_chunk_attention."""
+    return _attend_runs("kvq_cross_attention", cache, q, cu_seqlens, max_len, out, workspace, stream,
+                        flags)
+
+
+def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
+                    k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                    stream=None, flags: int = 0) -> tuple[torch.Tensor, torch.Tensor]:
+    """Tokens first[b] .. first[b] + count - 1 of each sequence (sink, packed, residual
+    order; first int32 [B] or None for 0) as values: (K, V) [B][Hkv][count][d], fp16 or
+    fp32 (KVQ_OUT_F32 in flags, or fp32 outputs).  Rows past the end are zero."""
+    D = cache.desc
+    if first is not None and (first.dtype != torch.int32 or not first.is_cuda
+                              or not first.is_contiguous() or first.numel() != D.batch):
+        raise ValueError("first must be a contiguous int32 CUDA tensor of B entries")
+    shape = (D.batch, D.num_kv_heads, int(count), D.head_dim)
+    given = k_out if k_out is not None else v_out
+    dtype = given.dtype if given is not None else (
+        torch.float32 if flags & KVQ_OUT_F32 else torch.float16)
+    if dtype not in (torch.float16, torch.float32):
+        raise ValueError("k_out and v_out must be float16 or float32")
+    outs = []
+    for t in (k_out, v_out):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=cache.device)
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("k_out and v_out must be contiguous CUDA tensors [B][Hkv][count][d] of one type")
+        outs.append(t)
+    flags = (flags | KVQ_OUT_F32) if dtype == torch.float32 else (flags & ~KVQ_OUT_F32)
+    st = load().kvq_read_tokens(ctypes.byref(D), ctypes.byref(cache.view), _ptr(first), int(count),
+                                _ptr(outs[0]), _ptr(outs[1]), int(flags),
+                                _stream(stream, cache.device))
+    _check(st, "kvq_read_tokens")
+    return outs[0], outs[1]
 
 
 def kvq_read_error(cache: KVCache, stream=None) -> tuple[int, int]:
