@@ -1,0 +1,10 @@
+// kvq_chunk_attn_d128.cu -- attention of runs, head_dim 128 (kvq_chunk_attn.cuh).
+#include "kvq_chunk_attn.cuh"
+
+namespace kvq {
+
+cudaError_t launch_chunk_attn_d128(const ChunkAttnArgs& a, int bits, int grid, cudaStream_t st) {
+  return chunk::launch_bits<128>(a, bits, grid, st);
+}
+
+}  // namespace kvq

@@ -1,0 +1,10 @@
+// kvq_chunk_attn_d64.cu -- attention of runs, head_dim 64 (kvq_chunk_attn.cuh).
+#include "kvq_chunk_attn.cuh"
+
+namespace kvq {
+
+cudaError_t launch_chunk_attn_d64(const ChunkAttnArgs& a, int bits, int grid, cudaStream_t st) {
+  return chunk::launch_bits<64>(a, bits, grid, st);
+}
+
+}  // namespace kvq
