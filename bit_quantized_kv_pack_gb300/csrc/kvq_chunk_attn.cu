@@ -58,6 +58,11 @@ cudaError_t launch_chunk_attention(const Dims& s, const kvq_cache_view& v, const
   a.Hkv = s.Hkv;
   a.Hq = Hq;
   a.gq = Hq / s.Hkv;
+  // gq_mul = ceil(2^(31 + k) / gq) with 2^k >= gq: exact for rows below 2^31
+  int k = 0;
+  while ((1 << k) < a.gq) ++k;
+  a.gq_shift = 31 + k;
+  a.gq_mul = (uint32_t)(((1ull << a.gq_shift) + a.gq - 1) / a.gq);
   a.cap = s.cap;
   a.Nr = s.Nr;
   a.Ns = s.Ns;

@@ -59,6 +59,7 @@ struct ChunkAttnArgs {
   float2* ml_part;    // [2 G][QB] {m, l}
   float4* o_part;     // [2 G][d / 4][QB]
   int B, Hkv, Hq, gq, cap, Nr, Ns, total, max_len, causal, out_f32;
+  uint32_t gq_mul, gq_shift;  // row / gq = row * gq_mul >> gq_shift for rows below 2^31
   uint32_t wait_limit_us;
   int fault;  // testing hook: one barrier of block 0 waits for an arrival that never comes
   float scale_log2;
@@ -111,38 +112,51 @@ struct Cfg {
   static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES : OFF_RAW + RAWN * RAWB;
   static constexpr int OFF_POISON = OFF_RAW + RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // int [2][3][D]
   static constexpr int OFF_BAR = OFF_POISON + 2 * 3 * D * 4;
-  static constexpr int SMEM = OFF_BAR + 512 + 1024;             // slack to align the base
+  static constexpr int OFF_SEG = OFF_BAR + 512;                 // Seg [kSegs]
+  static constexpr int SMEM = OFF_SEG + 512 + 1024;             // slack to align the base
+};
+
+// A segment: the block's tiles [lo, hi) of the unit (sequence b, KV head h, query block
+// qb).  One warp works the segments out, the others read them from a ring.
+constexpr int kSegs = 8;
+struct alignas(16) Seg {
+  int b, h, qb, lo;
+  int hi, npt, nt, alt;     // packed tiles and all tiles of the unit; alt: the lanes take alternate tiles
+  int c0, n, ns, npk;       // the run, and the sequence's lengths
+  int nres, head, first_b, last_b;  // blocks that hold the unit's first and last tile; b < 0: the end
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
 enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_EPI = 8, B_PAIR = 10, B_DRAIN = 11,
-       B_KFULL = 12, B_KEMPTY = 16, B_VFULL = 20, B_VEMPTY = 24, B_COUNT = 28 };
-enum { W_TMEM = 56, W_ABORT = 57, W_PFLAG = 58 /* [2] */, W_TICKET = 60, W_STARTB = 61, W_STARTQ = 62,
-       W_BASE = 64 /* int64 [2] */, W_SCAN = 68 /* int64 [16] */ };
+       B_KFULL = 12, B_KEMPTY = 16, B_VFULL = 20, B_VEMPTY = 24, B_SEGFULL = 28, B_SEGEMPTY = 36, B_COUNT = 44 };
+enum { W_TMEM = 88, W_ABORT = 89, W_PFLAG = 90 /* [2] */, W_TICKET = 92, W_STARTB = 93, W_STARTQ = 94,
+       W_BASE = 96 /* int64 [2] */ };
 
 // Bounded waits: all give up when one has.
+__device__ __forceinline__ bool wait_on(uint32_t b, uint32_t parity, volatile uint32_t* words, uint32_t* err_word,
+                                     uint32_t limit_us) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  for (uint32_t k = 1;; ++k) {
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    if ((k & 63u) == 0) {
+      if (words[W_ABORT]) return false;
+      if (ptx::global_timer_ns() - t0 > (uint64_t)limit_us * 1000u) {
+        words[W_ABORT] = 1;
+        set_error(err_word, KVQ_ERRBIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
 struct Waits {
   uint32_t bars;             // shared address of the barriers
   volatile uint32_t* words;  // the same as words
   uint32_t* err_word;
-  uint64_t limit_ns;
+  uint32_t limit_us;
 
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-    const uint32_t b = bar(i);
-    if (ptx::mbar_try_wait(b, parity)) return true;
-    const uint64_t t0 = ptx::global_timer_ns();
-    for (uint32_t k = 1;; ++k) {
-      if (ptx::mbar_try_wait(b, parity)) return true;
-      if ((k & 63u) == 0) {
-        if (words[W_ABORT]) return false;
-        if (ptx::global_timer_ns() - t0 > limit_ns) {
-          words[W_ABORT] = 1;
-          set_error(err_word, KVQ_ERRBIT_TIMEOUT);
-          return false;
-        }
-      }
-    }
+    return ptx::mbar_try_wait(bar(i), parity) || wait_on(bar(i), parity, words, err_word, limit_us);
   }
   // a whole warp waits; the same answer for all its lanes
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -154,6 +168,20 @@ struct Waits {
   }
 };
 
+__device__ __forceinline__ int token_of(const ChunkAttnArgs& a, int row) {
+  return (int)(((uint64_t)(uint32_t)row * a.gq_mul) >> a.gq_shift);
+}
+
+// Tokens that token `tok` of a run of n sees, of the packed ones and of the fp16 ones
+// (sink, then window): prefixes of both.
+__device__ __forceinline__ int seen_of(const ChunkAttnArgs& a, int n, int held, int tok) {
+  return a.causal ? max(0, held - n + tok + 1) : held;
+}
+__device__ __forceinline__ int seen_packed(int ns, int npk, int lim) { return min(max(lim - ns, 0), npk); }
+__device__ __forceinline__ int seen_f16(int ns, int npk, int lim) {
+  return min(lim, ns) + max(lim - ns - npk, 0);
+}
+
 // Where a block is in the line of tiles: the unit (b, qb, h), whose first tile starts
 // at `base`, and the block's tiles [lo, hi) of it.
 template <int D, int BITS>
@@ -163,21 +191,9 @@ struct Walk {
   int64_t base, x0, x1;
   Run run;
   SeqLens s;
-  int npt, nt, w;  // packed tiles, all tiles, cost of a tile
+  int npt, nt, w;  // packed tiles, all tiles, cost of a tile (1 or 2)
   int lo, hi;
 
-  // Tokens that a row of the run's token `tok` sees.
-  static __device__ __forceinline__ int seen(const ChunkAttnArgs& a, const Run& run, const SeqLens& s, int tok) {
-    const int n = s.ns + s.npk + s.nres;
-    return a.causal ? max(0, n - run.n + tok + 1) : n;
-  }
-  // ... of the packed ones, and of the fp16 ones (sink, then window): prefixes of both
-  static __device__ __forceinline__ int seen_packed(const SeqLens& s, int lim) {
-    return min(max(lim - s.ns, 0), s.npk);
-  }
-  static __device__ __forceinline__ int seen_f16(const SeqLens& s, int lim) {
-    return min(lim, s.ns) + max(lim - s.ns - s.npk, 0);
-  }
   static __device__ __forceinline__ int blocks(const ChunkAttnArgs& a, const Run& run) {
     return run.n > 0 ? (run.n * a.gq + C::QB - 1) / C::QB : 0;
   }
@@ -187,9 +203,9 @@ struct Walk {
                                                int qb, int& npt, int& nt, int& w) {
     const int rows = run.n * a.gq;
     const int last = min(rows, (qb + 1) * C::QB) - 1;
-    const int lim = seen(a, run, s, last / a.gq);
-    npt = (seen_packed(s, lim) + C::TN - 1) / C::TN;
-    nt = max(1, npt + (seen_f16(s, lim) + C::TN - 1) / C::TN);
+    const int lim = seen_of(a, run.n, s.ns + s.npk + s.nres, token_of(a, last));
+    npt = (seen_packed(s.ns, s.npk, lim) + C::TN - 1) / C::TN;
+    nt = max(1, npt + (seen_f16(s.ns, s.npk, lim) + C::TN - 1) / C::TN);
     w = C::LANES == 2 && last - qb * C::QB >= 128 ? 2 : 1;
   }
   static __device__ __forceinline__ int64_t seq_cost(const ChunkAttnArgs& a, int b) {
@@ -212,9 +228,9 @@ struct Walk {
   }
   __device__ __forceinline__ void range() {
     // tile k starts at base + k w and is the block's if that is in [x0, x1)
-    lo = x0 <= base ? 0 : (int)((x0 - base + w - 1) / w);
+    lo = x0 <= base ? 0 : (int)((x0 - base + w - 1) >> (w - 1));
     const int64_t e = x1 - base + w - 1;
-    hi = e <= 0 ? 0 : (int)min((int64_t)nt, e / w);
+    hi = e <= 0 ? 0 : (int)min((int64_t)nt, e >> (w - 1));
   }
   __device__ __forceinline__ void start(const ChunkAttnArgs& a, int b_, int qb_, int64_t base_, int64_t x0_,
                                         int64_t x1_) {
@@ -250,10 +266,45 @@ struct Walk {
     }
     range();
   }
-  __device__ __forceinline__ int block_rows(const ChunkAttnArgs& a) const {
-    return min(run.n * a.gq - qb * C::QB, C::QB);
+};
+
+// The warp that works out the segments.
+template <int D, int BITS>
+__device__ __forceinline__ void walk_role(const ChunkAttnArgs& a, const Waits& wt, Seg* ring, int b, int qb,
+                                          int64_t base, int64_t x0, int64_t x1, int64_t W, int64_t G) {
+  Walk<D, BITS> k;
+  k.start(a, b, qb, base, x0, x1);
+  for (uint32_t i = 0;; ++i) {
+    const int at = i % kSegs;
+    if (!wt.wait(B_SEGEMPTY + at, ((i / kSegs) & 1) ^ 1)) return;
+    Seg s;
+    s.b = -1;
+    if (k.valid(a)) {
+      s.b = k.b, s.h = k.h, s.qb = k.qb, s.lo = k.lo, s.hi = k.hi, s.npt = k.npt, s.nt = k.nt;
+      s.alt = Cfg<D, BITS>::LANES == 2 && k.w == 1;
+      s.c0 = k.run.c0, s.n = k.run.n, s.ns = k.s.ns, s.npk = k.s.npk, s.nres = k.s.nres, s.head = k.s.head;
+      s.first_b = s.last_b = 0;
+      if (k.lo > 0 || k.hi < k.nt) {
+        // block c has the starts from floor(c W / G) on
+        const int64_t end = k.base + (int64_t)(k.nt - 1) * k.w;
+        s.first_b = (int)(((k.base + 1) * G - 1) / W);
+        s.last_b = (int)(((end + 1) * G - 1) / W);
+      }
+    }
+    ring[at] = s;
+    ptx::mbar_arrive(wt.bar(B_SEGFULL + at));
+    if (s.b < 0) return;
+    k.next(a);
   }
-  __device__ __forceinline__ bool alternate() const { return C::LANES == 2 && w == 1; }  // lanes take alternate tiles
+}
+
+// A reader's place in the ring.
+struct SegReader {
+  uint32_t i = 0;
+  __device__ __forceinline__ bool wait(const Waits& wt) const {
+    return wt.wait(B_SEGFULL + i % kSegs, (i / kSegs) & 1);
+  }
+  __device__ __forceinline__ const Seg& get(const Seg* ring) const { return ring[i % kSegs]; }
 };
 
 // ------------------------------------------------------------- storage order ---
@@ -355,6 +406,7 @@ struct Deq {
   const Waits& wt;
   uint32_t smem;  // base of the block's shared memory
   int* poison;
+  const Seg* ring;
   int dt;         // thread of the warps that dequantize
   uint32_t seg;   // segments of the block so far
 
@@ -362,7 +414,7 @@ struct Deq {
   // zero would make them NaN in rows that do not see the token.  The first token of
   // the segment with +inf, -inf or NaN in a column is noted, and the epilogue gives
   // the rows that see it what the sum would be.  (Rare: one thread per element.)
-  __device__ __noinline__ bool note(int col, int token, uint32_t h) {
+  __device__ __forceinline__ bool note(int col, int token, uint32_t h) {
     // the notes of the segment before last are read before this one's are made
     if (seg >= 2 && !wt.wait(B_EPI + (seg & 1), ((seg >> 1) - 1) & 1)) return false;
     const int kind = (h & 0x3ffu) ? 2 : (h & 0x8000u) ? 1 : 0;
@@ -371,48 +423,96 @@ struct Deq {
     return true;
   }
 
-  // Raw copies of a half tile (w: 0 keys, 1 values) into ring slot `slot`; rows that
-  // are not there become zero codes with zero params, which stand for zeros.
-  __device__ __forceinline__ void fetch(const Walk<D, BITS>& k, int tile, int w, int slot) {
-    const uint32_t raw = smem + C::OFF_RAW + slot * C::RAWB;
+  // The cursor of the copies: a half tile of a segment.
+  struct Cursor {
+    SegReader at;
+    int tile = -1, w = 0, hi = 0, npt = 0, npk = 0, b = 0;
+    int64_t row0 = 0;  // contiguous: row of the head's token 0; paged: h * 32
+  };
+
+  // Raw copies of a half tile (keys, then values) into ring slot `slot`; rows that are
+  // not there become zero codes with zero params, which stand for zeros.  A head's groups
+  // lie one behind the other, so group gi of the tile is gi groups from its first.
+  __device__ __forceinline__ void fetch(const Cursor& c, int slot) {
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * C::CB;
+    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::GPT * C::CB + dt * 4;
+    const uint8_t* codes = a.codes[c.w];
+    const uint32_t* params = a.params[c.w];
+    const int left = c.npk - c.tile * C::TN;  // rows of the tile that there are
+    int64_t at = (c.row0 + c.tile * C::TN) * C::G + dt;
 #pragma unroll
     for (int i = 0; i < C::GPT; ++i) {
-      const int gi = i * kDeqThreads + dt;
-      const int p = tile * C::TN + gi / C::G, g = gi % C::G;
-      const uint32_t dc = raw + gi * C::CB, dp = raw + kDeqThreads * C::GPT * C::CB + gi * 4;
-      int64_t row = -1;
-      if (p < k.s.npk) {
-        row = a.rm.row(k.b, k.h, p);
-        if (row < 0) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+      const int r = (i * kDeqThreads + dt) / C::G;
+      bool there = r < left;
+      int64_t from = at + i * kDeqThreads;
+      if (a.rm.paged && there) {
+        const int p = c.tile * C::TN + r;
+        const int pg = a.rm.page_of(c.b, p / kPage);
+        there = pg >= 0 && pg < a.rm.npages;
+        if (!there) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+        from = ((int64_t)pg * a.Hkv * kPage + c.row0 + p % kPage) * C::G + dt % C::G;
       }
-      if (row >= 0) {
-        const int64_t at = row * C::G + g;
-        const uint8_t* src = a.codes[w] + at * C::CB;
+      const uint32_t d0 = dc + i * kDeqThreads * C::CB, d1 = dp + i * kDeqThreads * 4;
+      if (there) {
+        const uint8_t* src = codes + from * C::CB;
         if (BITS == 4) {
-          ptx::cp_async_16(dc, src, 16);
+          ptx::cp_async_16(d0, src, 16);
         } else if (BITS == 2) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dc), "l"(src) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d0), "l"(src) : "memory");
         } else {
 #pragma unroll
           for (int j = 0; j < 3; ++j)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dc + 4 * j), "l"(src + 4 * j)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d0 + 4 * j), "l"(src + 4 * j)
                          : "memory");
         }
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dp), "l"(a.params[w] + at) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d1), "l"(params + from) : "memory");
       } else {
 #pragma unroll
         for (int j = 0; j < C::CB / 4; ++j)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dc + 4 * j), "r"(0) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dp), "r"(0) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(d0 + 4 * j), "r"(0) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(d1), "r"(0) : "memory");
       }
     }
   }
 
+  // The pieces of one group with a value that is not finite in fp16, at `at` + pieces
+  // c0 ^ 0..3 (x: their code words, in the order of the pieces; col: the group's first
+  // column, xr: the order).
+  __device__ __forceinline__ bool rare_group(const uint32_t* x, uint32_t prm, int w, uint32_t at, uint32_t c0, int col,
+                                          int xr, int token) {
+    const uint32_t s2 = ptx::prmt(prm, prm, 0x1010), m2 = ptx::prmt(prm, prm, 0x3232);
+    const bool finite = !f16_nonfinite(prm) && !f16_nonfinite(prm >> 16);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t y[4];
+      codes_f16<BITS>(x[c], y);
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        uint32_t v = ptx::hfma2_u32(y[j], s2, m2);
+#pragma unroll 1
+        for (int sh = 0; sh < 32; sh += 16) {
+          const uint32_t hv = (v >> sh) & 0xffffu;
+          if (!f16_nonfinite(hv)) continue;
+          uint32_t to = hv;
+          if (finite) {
+            to = (hv & 0x8000u) | 0x7bffu;  // past fp16's largest value by the scale's rounding
+          } else if (w == 1) {
+            if (!note(col + (c ^ xr) * 8 + 2 * j + sh / 16, token, hv)) return false;
+            to = 0;
+          }
+          v = (v & ~(0xffffu << sh)) | (to << sh);
+        }
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + ((c0 ^ c) << 4) + 4 * j), "r"(v) : "memory");
+      }
+    }
+    return true;
+  }
+
   // A fetched half tile as fp16 at `dst`.
-  __device__ __forceinline__ bool packed_tile(const Walk<D, BITS>& k, int tile, int w, int slot, uint32_t dst) {
+  __device__ __forceinline__ bool packed_tile(const Seg& k, int tile, int w, int slot, uint32_t dst) {
     const uint32_t raw = smem + C::OFF_RAW + slot * C::RAWB;
     constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < C::GPT; ++i) {
       const int gi = i * kDeqThreads + dt;
       const int r = gi / C::G, g = gi % C::G;
@@ -436,51 +536,53 @@ struct Deq {
       const uint32_t at = dst + panel * C::KP + r * C::RB;
       const uint32_t c0 = C::RB == 128 ? (((g & 1) * 4) ^ xr ^ (r & 7)) : ((r >> 1) & 3);
       // the group's largest value; only where it is not finite can any value be so
-      const uint32_t top = ptx::hfma2_u32(kQmax2, s2, m2);
-      const bool rare = f16_nonfinite(top);
+      if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) {
+        const uint32_t xs[4] = {x[0], x[1], x[2], x[3]};
+        if (!rare_group(xs, prm, w, at, c0, panel * 64 + (g & 1) * 32, xr, k.ns + tile * C::TN + r)) return false;
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t f[4], y[4];
         codes_f16<BITS>(x[c], f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(f[j], s2, m2);
-        if (rare) {
-          const bool finite = !f16_nonfinite(prm) && !f16_nonfinite(prm >> 16);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int sh = 16 * (j & 1);
-            uint32_t hv = (y[j >> 1] >> sh) & 0xffffu;
-            if (!f16_nonfinite(hv)) continue;
-            uint32_t to = hv;
-            if (finite) {
-              to = (hv & 0x8000u) | 0x7bffu;  // past fp16's largest value by the scale's rounding
-            } else if (w == 1) {
-              const int col = panel * 64 + (g & 1) * 32 + ((c ^ xr) & 3) * 8 + j;
-              if (!note(col, k.s.ns + tile * C::TN + r, hv)) return false;
-              to = 0;
-            }
-            y[j >> 1] = (y[j >> 1] & ~(0xffffu << sh)) | (to << sh);
-          }
-        }
         st_shared_v4(at + ((c0 ^ c) << 4), make_uint4(y[0], y[1], y[2], y[3]));
       }
     }
     return true;
   }
 
+  // The 16 stored elements at p0 and p1, of columns col ..: what is not finite becomes
+  // zero and is noted.
+  __device__ __forceinline__ bool rare_pieces(uint32_t p0, uint32_t p1, int col, int token) {
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t at = (j < 8 ? p0 : p1) + 2 * (j & 7);
+      unsigned short hv;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(at) : "memory");
+      if (!f16_nonfinite(hv)) continue;
+      if (!note(col + j, token, hv)) return false;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ int ring_slot(int j) const { return j < a.Nr ? j : j - a.Nr; }  // j < 2 Nr
+
   // A half tile of fp16 tokens (sink, then window): rows f0 .. of their line.
-  __device__ __forceinline__ bool f16_tile(const Walk<D, BITS>& k, int f0, int w, uint32_t dst) {
+  __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, int w, uint32_t dst) {
     const int64_t bh = (int64_t)k.b * a.Hkv + k.h;
-    const int n = k.s.ns + k.s.nres;
+    const int n = k.ns + k.nres;
 #pragma unroll 1
     for (int i = 0; i < C::GPT; ++i) {
       const int gi = i * kDeqThreads + dt;
       const int r = gi / C::G, g = gi % C::G, f = f0 + r;
       const __half* src = a.q;  // (not read)
-      if (f < k.s.ns)
+      if (f < k.ns)
         src = a.sink[w] + (bh * a.Ns + f) * D + g * 32;
       else if (f < n)
-        src = a.res[w] + (bh * a.Nr + (k.s.head + f - k.s.ns) % a.Nr) * D + g * 32;
+        src = a.res[w] + (bh * a.Nr + ring_slot(k.head + f - k.ns)) * D + g * 32;
       const uint32_t at = dst + (g / 2) * C::KP;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -493,76 +595,82 @@ struct Deq {
       const int r = gi / C::G, g = gi % C::G, f = f0 + r;
       const uint32_t at = dst + (g / 2) * C::KP;
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
+      for (int c = 0; c < 4; c += 2) {  // (16 elements)
         const uint32_t p0 = at + swizzled<C::RB>(r, (g & 1) * 4 + c), p1 = at + swizzled<C::RB>(r, (g & 1) * 4 + c + 1);
         uint4 u[2] = {ld_shared_v4(p0), ld_shared_v4(p1)};
         to_storage<BITS>(u[0], u[1]);
+        st_shared_v4(p0, u[0]);
+        st_shared_v4(p1, u[1]);
         if (w == 1) {
-          uint32_t* y = reinterpret_cast<uint32_t*>(u);
+          const uint32_t* y = reinterpret_cast<const uint32_t*>(u);
           bool bad = false;
 #pragma unroll
           for (int j = 0; j < 8; ++j) bad |= f16_nonfinite(y[j]) || f16_nonfinite(y[j] >> 16);
-          if (bad) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int sh = 16 * (j & 1);
-              const uint32_t hv = (y[j >> 1] >> sh) & 0xffffu;
-              if (!f16_nonfinite(hv)) continue;
-              const int col = (g / 2) * 64 + (g & 1) * 32 + c * 8 + j;
-              if (!note(col, f < k.s.ns ? f : f + k.s.npk, hv)) return false;
-              y[j >> 1] &= ~(0xffffu << sh);
-            }
-          }
+          if (bad && !rare_pieces(p0, p1, (g / 2) * 64 + (g & 1) * 32 + c * 8, f < k.ns ? f : f + k.npk))
+            return false;
         }
-        st_shared_v4(p0, u[0]);
-        st_shared_v4(p1, u[1]);
       }
     }
     return true;
   }
 
-  __device__ __forceinline__ void run(const Walk<D, BITS>& first) {
-    Walk<D, BITS> k = first, ahead = first;
-    int atile = ahead.lo, ahalf = 0;
+  __device__ __forceinline__ void run() {
+    SegReader k;
+    Cursor c;
+    bool ok = true, more = true;
     // the next half tile of the line into its ring slot
     auto fetch_next = [&](int slot) {
-      if (ahead.valid(a)) {
-        if (atile < ahead.npt) fetch(ahead, atile, ahalf, slot);
-        ahalf ^= 1;
-        if (ahalf == 0 && ++atile == ahead.hi) {
-          ahead.next(a);
-          atile = ahead.lo;
+      if (more && c.tile < 0) {
+        ok = ok && __all_sync(0xffffffffu, c.at.wait(wt));
+        const Seg& s = c.at.get(ring);
+        more = ok && s.b >= 0;
+        if (more) {
+          c.tile = s.lo, c.hi = s.hi, c.npt = s.npt, c.npk = s.npk, c.b = s.b;
+          c.row0 = a.rm.paged ? (int64_t)s.h * kPage : ((int64_t)s.b * a.Hkv + s.h) * a.cap;
+        }
+      }
+      if (more) {
+        if (c.tile < c.npt) fetch(c, slot);
+        c.w ^= 1;
+        if (c.w == 0 && ++c.tile == c.hi) {
+          ++c.at.i;
+          c.tile = -1;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int i = 0; i < C::RAWN; ++i) fetch_next(i);
     uint32_t kv = 0;  // tiles so far
     int slot = 0;
-    bool ok = true;
-    for (; ok && k.valid(a); k.next(a), ++seg) {
-      for (int t = k.lo; ok && t < k.hi; ++t, ++kv) {
-        const int stage = kv % C::ST;
-        const uint32_t par = ((kv / C::ST) & 1) ^ 1;
+    // RAWN - 1 half tiles ahead: a free slot is filled before the oldest is taken
 #pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
-          ok = wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + stage, par);
-          if (!ok) break;
-          if (t < k.npt) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-            ok = packed_tile(k, t, w, slot, dst);
-          } else {
-            ok = f16_tile(k, (t - k.npt) * C::TN, w, dst);
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ptx::fence_proxy_async_shared();
-          wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
-          fetch_next(slot);
-          if (++slot == C::RAWN) slot = 0;
+    for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
+    for (; ok; ++k.i, ++seg) {
+      ok = ok && __all_sync(0xffffffffu, k.wait(wt));
+      if (!ok) break;
+      const Seg& s = k.get(ring);
+      if (s.b < 0) break;
+      const int lo = s.lo, hi = s.hi, npt = s.npt;
+      for (int h = 2 * lo; h < 2 * hi; ++h) {
+        fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
+        const int t = h >> 1, w = h & 1;
+        const int stage = kv % C::ST;
+        const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
+        ok = ok && wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + stage, ((kv / C::ST) & 1) ^ 1);
+        if (!ok) break;
+        if (t < npt) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
+          ok = packed_tile(s, t, w, slot, dst);
+        } else {
+          ok = f16_tile(s, (t - npt) * C::TN, w, dst);
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::fence_proxy_async_shared();
+        wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
+        if (++slot == C::RAWN) slot = 0;
+        kv += w;
       }
+      wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -572,17 +680,19 @@ struct Deq {
 
 template <int D, int BITS>
 __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt, uint32_t smem, uint32_t tmem,
-                                         const Walk<D, BITS>& first) {
+                                         const Seg* ring) {
   using C = Cfg<D, BITS>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
-  Walk<D, BITS> k = first;
+  SegReader k;
   uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
   uint32_t kv = 0;                          // tiles so far
   bool ok = true;
-  for (; ok && k.valid(a); k.next(a)) {
-    const bool alt = k.alternate();
-    const int n = k.hi - k.lo;
+  for (;; ++k.i) {
+    if (!k.wait(wt) || k.get(ring).b < 0) break;
+    const bool alt = k.get(ring).alt;
+    const int n = k.get(ring).hi - k.get(ring).lo;
+    ptx::mbar_arrive(wt.bar(B_SEGEMPTY + k.i % kSegs));
     const int U = C::LANES == 2 && !alt ? 2 * n : n;
     ok = wt.wait(B_QFULL, qn[0]++ & 1);
     if (ok && C::LANES == 2 && !alt) ok = wt.wait(B_QFULL + 1, qn[1]++ & 1);
@@ -628,6 +738,7 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
       else
         tc5::commit(wt.bar(B_ODONE + lane));
     }
+    if (!ok) break;
     kv += n;
   }
   // nothing of this thread's is in flight when TMEM is freed
@@ -651,6 +762,7 @@ struct Soft {
   uint32_t smem, tmem;  // tmem: with the warp's lanes
   int* poison;
   float* stage;         // [column][row]
+  const Seg* ring;
   int lane, r;          // accumulator, row in it
   uint32_t sn, on, pairn, seg;
 
@@ -660,12 +772,13 @@ struct Soft {
   }
 
   // The lane's 128 rows of Q, in storage order and swizzled.
-  __device__ __forceinline__ void load_q(const Walk<D, BITS>& k) {
-    if (k.alternate() && lane == 1) return;
+  __device__ __forceinline__ int block_rows(const Seg& k) const { return min(k.n * a.gq - k.qb * C::QB, C::QB); }
+  __device__ __forceinline__ void load_q(const Seg& k) {
+    if (k.alt && lane == 1) return;
     constexpr int LPR = D / 16;    // threads of a row, 32 bytes each
     constexpr int RPI = 32 / LPR;  // rows of a warp at a time
     const int w = r >> 5, l = r & 31;
-    const int rows = k.block_rows(a);
+    const int rows = block_rows(k);
     const int rb = k.qb * C::QB + lane * 128;
     const uint32_t base = smem + C::OFF_Q + lane * C::QBYTES;
 #pragma unroll 4
@@ -674,9 +787,9 @@ struct Soft {
       uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
       if (lane * 128 + row < rows) {
         const int R = rb + row;
-        const int tok = R / a.gq, g = R - tok * a.gq;
+        const int tok = token_of(a, R), g = R - tok * a.gq;
         const uint4* src = reinterpret_cast<const uint4*>(
-                               a.q + ((int64_t)(k.run.c0 + tok) * a.Hq + k.h * a.gq + g) * D) + c;
+                               a.q + ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + g) * D) + c;
         u0 = __ldg(src);
         u1 = __ldg(src + 1);
       }
@@ -695,24 +808,29 @@ struct Soft {
   __device__ __forceinline__ void tile(int visible, uint32_t bad, bool has_o, float& m, float& l) {
     const uint32_t sa = tmem + C::S0 + lane * C::TN;
     float s[C::TN];
+    float mx[4];
 #pragma unroll
-    for (int i = 0; i < C::TN; i += 32) tc5::ld32(sa + i, reinterpret_cast<uint32_t*>(s + i));
+    for (int i = 0; i < C::TN; i += 32) tc5::ld32_max(sa + i, reinterpret_cast<uint32_t*>(s + i), mx[i / 32]);
     tc5::wait_ld();
 #pragma unroll
-    for (int i = 0; i < C::TN; i += 32) tc5::pin32(reinterpret_cast<uint32_t*>(s + i));
+    for (int i = 0; i < C::TN; i += 32) {
+      tc5::pin32(reinterpret_cast<uint32_t*>(s + i));
+      asm volatile("" : "+f"(mx[i / 32]));
+    }
     if (__any_sync(0xffffffffu, visible < C::TN) || bad) {
 #pragma unroll
-      for (int i = 0; i < C::TN; ++i)
-        s[i] = i < visible && !((bad >> (i / kPage)) & 1u) ? s[i] : -INFINITY;
-    }
-    float mx[4] = {s[0], s[1], s[2], s[3]};
+      for (int i = 0; i < C::TN; i += kPage) {
+        const int v = (bad >> (i / kPage)) & 1u ? 0 : visible - i;
+        float x = -INFINITY;
 #pragma unroll
-    for (int i = 4; i < C::TN; i += 8) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        mx[j] = i + 4 + j < C::TN ? fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]) : fmaxf(mx[j], s[i + j]);
+        for (int j = 0; j < kPage; ++j) {
+          s[i + j] = j < v ? s[i + j] : -INFINITY;
+          x = fmaxf(x, s[i + j]);
+        }
+        mx[i / 32] = x;
+      }
     }
-    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    const float mt = C::TN == 128 ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) : fmaxf(mx[0], mx[1]);
     const float c = a.scale_log2;
     const float mn = fmaxf(m, mt);
     const bool moves = (mn - m) * c > 8.0f;
@@ -722,47 +840,59 @@ struct Soft {
       l *= f;
       if (has_o) {
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tc5::ld32(tmem + C::O0 + lane * C::OSTEP + i, o);
+        for (int i = 0; i < D; i += 16) {
+          uint32_t o[16];
+          tc5::ld16(tmem + C::O0 + lane * C::OSTEP + i, o);
           tc5::wait_ld();
-          tc5::pin32(o);
+          tc5::pin16(o);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tc5::st32(tmem + C::O0 + lane * C::OSTEP + i, o);
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc5::st16(tmem + C::O0 + lane * C::OSTEP + i, o);
         }
       }
     }
     const float off = m == -INFINITY ? 0.0f : -m * c;
     const uint64_t c2 = pack_f32x2(c, c), off2 = pack_f32x2(off, off);
     uint64_t sum2[4] = {0, 0, 0, 0};
-    uint32_t p[C::TN / 2];
 #pragma unroll
-    for (int i = 0; i < C::TN; i += 2) {
-      const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
-      const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
-      const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
-      sum2[(i / 2) & 3] = add_f32x2(sum2[(i / 2) & 3], pack_f32x2(e0, e1));
-      p[i / 2] = ptx::pack_h2(e0, e1);
+    for (int h = 0; h < C::TN; h += 32) {
+      uint32_t p[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t x = fma_f32x2(pack_f32x2(s[h + i], s[h + i + 1]), c2, off2);
+        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
+        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
+        sum2[(i / 2) & 3] = add_f32x2(sum2[(i / 2) & 3], pack_f32x2(e0, e1));
+        p[i / 2] = ptx::pack_h2(e0, e1);
+      }
+      tc5::st16(sa + h / 2, p);
     }
-#pragma unroll
-    for (int i = 0; i < C::TN / 2; i += 32) tc5::st32(sa + i, p + i);
     const uint64_t t2 = add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3]));
     l += __uint_as_float(lo_bits(t2)) + __uint_as_float(hi_bits(t2));
     tc5::wait_st();
   }
 
-  // Columns [c0, c0 + 32) of the row's O, with what the notes say of a row that sees
-  // `lim` tokens.
-  __device__ __forceinline__ void notes(float (&o)[32], int c0, int lim) {
-    const int* pn = poison + (seg & 1) * 3 * D + c0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const bool up = pn[j] < lim, down = pn[D + j] < lim, nan = pn[2 * D + j] < lim;
-      if (nan || (up && down))
-        o[j] = NAN;
-      else if (up || down)
-        o[j] = up ? INFINITY : -INFINITY;
+  // What the notes say of the row's outputs: the row sees `lim` tokens; written over the
+  // thread's own earlier stores, to the output (whole) or to the piece's O in `slot`.
+  __device__ __forceinline__ void notes(int lim, bool whole, int64_t at, int slot, int row) const {
+    const int* pn = poison + (seg & 1) * 3 * D;
+#pragma unroll 1
+    for (int c = 0; c < D; ++c) {
+      const bool up = pn[c] < lim, down = pn[D + c] < lim, nan = pn[2 * D + c] < lim;
+      if (!(up || down || nan)) continue;
+      const float v = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+      if (!whole) {
+        float4* dst = a.o_part + ((int64_t)slot * (D / 4) + c / 4) * C::QB + row;
+        __stcg(reinterpret_cast<float*>(dst) + (c & 3), v);
+        continue;
+      }
+      int e = 0;  // the element that is stored at this column
+      while (place<BITS>(e) != (c & 15)) ++e;
+      e += c & ~15;
+      if (a.out_f32)
+        static_cast<float*>(a.out)[at + e] = v;
+      else
+        static_cast<__half*>(a.out)[at + e] = __float2half(v);
     }
   }
 
@@ -783,10 +913,10 @@ struct Soft {
                             ptx::pack_h2(y[8 * e + 4], y[8 * e + 5]), ptx::pack_h2(y[8 * e + 6], y[8 * e + 7]));
     }
   }
-  __device__ __forceinline__ int64_t out_at(const Walk<D, BITS>& k, int row) const {
+  __device__ __forceinline__ int64_t out_at(const Seg& k, int row) const {
     const int R = k.qb * C::QB + row;
-    const int tok = R / a.gq;
-    return ((int64_t)(k.run.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
+    const int tok = token_of(a, R);
+    return ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
   }
 
   __device__ __forceinline__ float inverse(float l) const {
@@ -796,8 +926,8 @@ struct Soft {
 
   // The pieces of a cut unit, from their (O, m, l) in global memory: 16 columns of a row
   // at a time, all softmax threads.  first .. last: the blocks that hold the pieces.
-  __device__ __forceinline__ void join(const Walk<D, BITS>& k, int first, int last) {
-    const int rows = k.block_rows(a);
+  __device__ __forceinline__ void join(const Seg& k) const {
+    const int rows = block_rows(k), first = k.first_b, last = k.last_b;
     const int tid = lane * 128 + r;
     const float c = a.scale_log2;
     for (int it = tid; it < rows * (D / 16); it += C::SMT) {
@@ -829,28 +959,31 @@ struct Soft {
     }
   }
 
-  __device__ __forceinline__ bool run(const Walk<D, BITS>& first, int block, int64_t W, int64_t G) {
-    Walk<D, BITS> k = first;
-    if (!k.valid(a)) return true;
-    load_q(k);
+  __device__ __forceinline__ bool run(int block) {
+    SegReader at_seg;
+    if (!__all_sync(0xffffffffu, at_seg.wait(wt))) return false;
+    if (at_seg.get(ring).b < 0) return true;
+    load_q(at_seg.get(ring));
     while (true) {
-      const bool alt = k.alternate();
+      const Seg& k = at_seg.get(ring);
+      const bool alt = k.alt;
       const int row = (alt ? 0 : lane * 128) + r;  // of the block
-      const int rows = k.block_rows(a);
+      const int rows = block_rows(k);
       const bool warp_live = (row & ~31) < rows;
       int lim = 0;
-      if (row < rows) lim = Walk<D, BITS>::seen(a, k.run, k.s, (k.qb * C::QB + row) / a.gq);
-      const int plim = Walk<D, BITS>::seen_packed(k.s, lim), flim = Walk<D, BITS>::seen_f16(k.s, lim);
+      if (row < rows) lim = seen_of(a, k.n, k.ns + k.npk + k.nres, token_of(a, k.qb * C::QB + row));
+      const int plim = seen_packed(k.ns, k.npk, lim), flim = seen_f16(k.ns, k.npk, lim);
+      const int npt = k.npt, hi = k.hi;
       float m = -INFINITY, l = 0.0f;
       const int step = alt ? 2 : 1, t0 = k.lo + (alt ? lane : 0);
-      for (int t = t0; t < k.hi; t += step) {
-        const bool packed = t < k.npt;
-        const int visible = packed ? plim - t * C::TN : flim - (t - k.npt) * C::TN;
+      for (int t = t0; t < hi; t += step) {
+        const bool packed = t < npt;
+        const int visible = packed ? plim - t * C::TN : flim - (t - npt) * C::TN;
         uint32_t bad = 0;
         if (a.rm.paged && packed) {
           const int j = t * (C::TN / kPage) + (r & 31);
           bool out = false;
-          if ((r & 31) < C::TN / kPage && j * kPage < k.s.npk) {
+          if ((r & 31) < C::TN / kPage && j * kPage < k.npk) {
             const int pg = a.rm.page_of(k.b, j);
             out = pg < 0 || pg >= a.rm.npages;
           }
@@ -862,100 +995,86 @@ struct Soft {
         tc5::fence_before();
         wt.arrive_warp(B_PREADY + lane);
       }
-      const bool any = t0 < k.hi;
+      const bool any = t0 < hi;
       if (any && !wt.wait_warp(B_ODONE + lane, on++ & 1)) return false;
       tc5::fence_after();
 
-      const Walk<D, BITS> cur = k;
-      k.next(a);
-      const bool more = k.valid(a);
-      if (more && !alt) load_q(k);  // under the epilogue
+      SegReader after = at_seg;
+      ++after.i;
+      if (!__all_sync(0xffffffffu, after.wait(wt))) return false;
+      const bool more = after.get(ring).b >= 0;
+      if (more && !alt) load_q(after.get(ring));  // under the epilogue
 
       // with alternating lanes the other's tiles may still be on their way
       if (alt && !pair_sync()) return false;
       const bool noted = wt.words[W_PFLAG + (seg & 1)] != 0;
-      const bool whole = cur.lo == 0 && cur.hi == cur.nt;
-      const int slot = 2 * block + (cur.lo == 0);
+      const bool whole = k.lo == 0 && k.hi == k.nt;
+      const int slot = 2 * block + (k.lo == 0);
       const uint32_t oa = tmem + C::O0 + lane * C::OSTEP;
-      auto emit = [&](float (&o)[32], int c0, float inv, int64_t at) {
-        if (noted) notes(o, c0, lim);
-        if (row >= rows) return;
-        if (whole) {
-          store16(o, inv, at + c0);
-          store16(o + 16, inv, at + c0 + 16);
-        } else {
+      float inv = 0.0f;
+      int64_t at = 0;
+      // With alternating lanes, lane 1's accumulator goes through shared memory to lane
+      // 0, 32 columns at a time, with its rows' m and l.
+      const bool pass = alt && k.hi - k.lo > 1;
+      float* xm = stage + 32 * 128;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (pass) {
+        if (lane == 1 && warp_live) {
+          xm[r] = m;
+          xm[128 + r] = l;
+        }
+        if (!pair_sync()) return false;
+        const float m1 = xm[r], l1 = xm[128 + r], mm = fmaxf(m, m1), c = a.scale_log2;
+        if (lane == 0) {
+          // a lane that saw nothing has weight zero (NaN scores stay NaN through l)
+          f0 = m == -INFINITY ? 0.0f : ptx::ex2_ftz((m - mm) * c);
+          f1 = m1 == -INFINITY ? 0.0f : ptx::ex2_ftz((m1 - mm) * c);
+          if (l != l) f0 = l;
+          if (l1 != l1) f1 = l1;
+          l = l * f0 + l1 * f1;
+          m = mm;
+        }
+      }
+      const bool mine = row < rows && !(alt && lane == 1);
+      if (mine) {
+        at = out_at(k, row);
+        if (whole)
+          inv = inverse(l);
+        else
+          __stcg(a.ml_part + (int64_t)slot * C::QB + row, make_float2(m, l));
+      }
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float o[32];
+        if (warp_live && any) {
+          tc5::ld32(oa + c0, reinterpret_cast<uint32_t*>(o));
+          tc5::wait_ld();
+          tc5::pin32(reinterpret_cast<uint32_t*>(o));
+        }
+        if (pass) {
+          if (lane == 1 && warp_live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) stage[j * 128 + r] = o[j];
+          }
+          if (!pair_sync()) return false;
+          if (lane == 0 && warp_live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + stage[j * 128 + r] * f1;
+          }
+          if (!pair_sync()) return false;
+        }
+        if (mine && whole) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) store16(o + j, inv, at + c0 + j);
+        } else if (mine) {
           float4* dst = a.o_part + ((int64_t)slot * (D / 4) + c0 / 4) * C::QB + row;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             __stcg(dst + j * C::QB, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         }
-      };
-      if (!alt) {
-        if (warp_live) {
-          const float inv = whole && row < rows ? inverse(l) : 0.0f;
-          const int64_t at = row < rows ? out_at(cur, row) : 0;
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tc5::ld32(oa + c0, reinterpret_cast<uint32_t*>(o));
-            tc5::wait_ld();
-            tc5::pin32(reinterpret_cast<uint32_t*>(o));
-            emit(o, c0, inv, at);
-          }
-          if (!whole && row < rows) __stcg(a.ml_part + (int64_t)slot * C::QB + row, make_float2(m, l));
-        }
-      } else {
-        // Lane 1's accumulator goes through shared memory to lane 0, 32 columns at a time.
-        float* xm = stage + 32 * 128;
-        const bool both = cur.hi - cur.lo > 1;
-        float f0 = 1.0f, f1 = 0.0f, inv = 0.0f;
-        int64_t at = 0;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          if (warp_live && any) {
-            tc5::ld32(oa + c0, reinterpret_cast<uint32_t*>(o));
-            tc5::wait_ld();
-            tc5::pin32(reinterpret_cast<uint32_t*>(o));
-          }
-          if (lane == 1 && both && warp_live) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) stage[j * 128 + r] = o[j];
-            if (c0 == 0) {
-              xm[r] = m;
-              xm[128 + r] = l;
-            }
-          }
-          if (both && !pair_sync()) return false;
-          if (lane == 0 && warp_live) {
-            if (c0 == 0) {
-              if (both) {
-                const float m1 = xm[r], l1 = xm[128 + r], mm = fmaxf(m, m1), c = a.scale_log2;
-                // a lane that saw nothing has weight zero (NaN scores stay NaN through l)
-                f0 = m == -INFINITY ? 0.0f : ptx::ex2_ftz((m - mm) * c);
-                f1 = m1 == -INFINITY ? 0.0f : ptx::ex2_ftz((m1 - mm) * c);
-                if (l != l) f0 = l;
-                if (l1 != l1) f1 = l1;
-                l = l * f0 + l1 * f1;
-                m = mm;
-              }
-              if (row < rows) {
-                at = out_at(cur, row);
-                if (whole)
-                  inv = inverse(l);
-                else
-                  __stcg(a.ml_part + (int64_t)slot * C::QB + row, make_float2(m, l));
-              }
-            }
-            if (both) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + stage[j * 128 + r] * f1;
-            }
-            emit(o, c0, inv, at);
-          }
-          if (both && !pair_sync()) return false;
-        }
+        __syncwarp();
       }
+      if (noted && mine) notes(lim, whole, at, slot, row);
       // the notes have been read: clean them for the segment after next
       if (noted) {
         if (!pair_sync()) return false;
@@ -968,24 +1087,21 @@ struct Soft {
       ++seg;
 
       if (!whole) {
-        // the pieces lie in the blocks that own the unit's first to last tile
-        const int64_t base = cur.base, end = base + (int64_t)(cur.nt - 1) * cur.w;
-        const int first_b = (int)(((base + 1) * G - 1) / W), last_b = (int)(((end + 1) * G - 1) / W);
         __threadfence();
         if (!pair_sync()) return false;
-        if (lane * 128 + r == 0) wt.words[W_TICKET] = atomicAdd(a.tickets + first_b, 1u);
+        if (lane * 128 + r == 0) wt.words[W_TICKET] = atomicAdd(a.tickets + k.first_b, 1u);
         if (!pair_sync()) return false;
-        if (wt.words[W_TICKET] == (uint32_t)(last_b - first_b)) {
+        if (wt.words[W_TICKET] == (uint32_t)(k.last_b - k.first_b)) {
           __threadfence();
-          join(cur, first_b, last_b);
-          if (lane * 128 + r == 0) a.tickets[first_b] = 0;
+          join(k);
+          if (lane * 128 + r == 0) a.tickets[k.first_b] = 0;
         }
       }
+      wt.arrive_warp(B_SEGEMPTY + at_seg.i % kSegs);
       if (!more) return true;
-      if (alt) {
-        // lane 1's Q, if it has one, goes where the accumulator passed: after all have read it
-        load_q(k);
-      }
+      at_seg = after;
+      // with alternating lanes: Q goes where the accumulator passed, after all have read it
+      if (alt) load_q(at_seg.get(ring));
     }
   }
 };
@@ -1016,11 +1132,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
     if (lid >= o) scan += v;
   }
-  if (lid == 31) wide[W_SCAN / 2 + warp] = scan;
+  volatile int64_t* scans = reinterpret_cast<volatile int64_t*>(base + C::OFF_SEG);  // (the ring is not in use yet)
+  if (lid == 31) scans[warp] = scan;
   __syncthreads();
   int64_t before = 0, W = 0;
   for (int i = 0; i < kThreads / 32; ++i) {
-    const int64_t v = wide[W_SCAN / 2 + i];
+    const int64_t v = scans[i];
     if (i < warp) before += v;
     W += v;
   }
@@ -1048,6 +1165,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       init(B_PREADY + i, 4);
       init(B_ODONE + i, 1);
       init(B_EPI + i, 4 * C::LANES);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      init(B_SEGFULL + i, 1);
+      init(B_SEGEMPTY + i, 4 * C::LANES + 4 + 1);
     }
     init(B_PAIR, 4 * C::LANES);
     init(B_DRAIN, 1);
@@ -1098,7 +1219,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   __syncthreads();
   tc5::fence_after();
   const uint32_t tmem = words[W_TMEM];
-  const Waits wt = {smem + C::OFF_BAR, words, a.err_word, (uint64_t)a.wait_limit_us * 1000u};
+  const Waits wt = {smem + C::OFF_BAR, words, a.err_word, a.wait_limit_us};
+  Seg* ring = reinterpret_cast<Seg*>(base + C::OFF_SEG);
   const int sb = words[W_STARTB], sq = words[W_STARTQ];
   const int64_t sbase = wide[W_BASE / 2 + 1];
 
@@ -1106,26 +1228,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   if (warp < 8) {
     tc5::regs_inc<184>();
     if (warp < 4 * C::LANES) {
-      Walk<D, BITS> k;
-      k.start(a, sb, sq, sbase, x0, x1);
       Soft<D, BITS> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21), poison,
-                            reinterpret_cast<float*>(base + C::OFF_STAGE),
+                            reinterpret_cast<float*>(base + C::OFF_STAGE), ring,
                             warp >> 2, tid & 127, 0, 0, 0, 0};
-      soft.run(k, blockIdx.x, W, G);
+      soft.run(blockIdx.x);
     }
   } else if (warp < 12) {
     tc5::regs_dec<96>();
-    Walk<D, BITS> k;
-    k.start(a, sb, sq, sbase, x0, x1);
-    Deq<D, BITS> deq = {a, wt, smem, poison, tid - 256, 0};
-    deq.run(k);
+    Deq<D, BITS> deq = {a, wt, smem, poison, ring, tid - 256, 0};
+    deq.run();
   } else {
     tc5::regs_dec<48>();
-    if (tid == 12 * 32) {
-      Walk<D, BITS> k;
-      k.start(a, sb, sq, sbase, x0, x1);
-      mma_role<D, BITS>(a, wt, smem, tmem, k);
-    }
+    if (tid == 12 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
+    if (tid == 13 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     __syncwarp();
   }
   tc5::fence_before();
