@@ -286,7 +286,7 @@ kvq_status attend_runs(const kvq_cache_desc* desc, const kvq_cache_view* view, c
   // rows of one KV head and tokens of one sequence are counted in 32 bits
   const int64_t gq = num_q_heads / desc->num_kv_heads;
   if ((int64_t)(max_len < total ? max_len : total) * gq > (1LL << 30) ||
-      (int64_t)s.cap + s.Nr + s.Ns > (1LL << 30))
+      (int64_t)s.cap + s.Nr + s.Ns > (1LL << 28))
     return KVQ_ERR_UNSUPPORTED;
   if (ws_bytes < kvq::chunk_workspace_bytes(s, num_q_heads, kvq::device_sm_count()))
     return KVQ_ERR_INVALID_ARG;

@@ -10,14 +10,17 @@
 // Roundings: the dequantized keys and values min + code * scale are rounded to fp16 once
 // (operands of the MMA), the weights P to fp16 once; scores, m, l and O are fp32.
 //
-// A block (one per SM, persistent) has 16 warps:
-//   0-7   softmax: one thread per query row, S from TMEM, P back to TMEM (it takes S's
-//         place and is the A operand of the second MMA), the epilogue.  Two groups of
-//         four warps, one for each of the block's two accumulators (lanes 0 and 1).
-//   8-11  dequantize: codes come by cp.async into a ring that is private to each thread
-//         (no barrier), become fp16 in registers and go to shared memory in the MMA's
-//         128-byte swizzle, K as the K-major and V as the MN-major B operand.
-//   12    issues the MMAs.
+// A block (one per SM, persistent) has 24 warps:
+//   0-15   softmax: S from TMEM, P back to TMEM (it takes S's place and is the A operand
+//          of the second MMA), the epilogue.  Four groups of four warps: two for each of
+//          the block's two accumulators (lanes 0 and 1), each with half of the tile's
+//          tokens and half of O's columns, a thread per query row.  (One group per
+//          accumulator left the chain S -> P -> next S as the bound: 42 % of the issue
+//          slots used.)
+//   16-19  dequantize: a row of codes comes by cp.async into a ring that is private to
+//          its thread (no barrier), becomes fp16 in registers and goes to shared memory
+//          in the MMA's 128-byte swizzle, K as the K-major and V as the MN-major B operand.
+//   20     issues the MMAs; 21 works out the segments.
 // A unit of work is (sequence, block of query rows, KV head).  With more than 128 rows in
 // the block the two lanes are its two halves and share each tile; with fewer they take
 // alternate tiles of the same rows and are joined at the end, so that the softmax of one
@@ -75,7 +78,7 @@ __host__ __device__ constexpr int chunk_rows(int d) { return d == 256 ? 128 : 25
 
 namespace chunk {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kDeqThreads = 128;
 
 template <int D, int BITS>
@@ -92,28 +95,35 @@ struct Cfg {
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int KBYTES = TN * D * 2;
   static constexpr int ST = D <= 64 ? 4 : 2;        // K and V stages
-  static constexpr int GPT = TN * G / kDeqThreads;  // groups per dequantizing thread and half tile
+  static constexpr int HC = TN / 2;                 // a softmax group's columns of S
+  static constexpr int HD = D / 2;                  // ... and of O
+  static constexpr int TPR = TN == 64 ? 2 : 1;      // dequantizing threads of a row
+  static constexpr int GPT = G / TPR;               // groups of each
   static constexpr int CB = 4 * BITS;               // code bytes of a group
-  static constexpr int RAWB = kDeqThreads * GPT * (CB + 4);
-  static constexpr int RAWN = D == 256 ? 2 : D == 128 ? 3 : 6;
-  static constexpr int SMT = 128 * LANES;           // softmax threads
+  static constexpr int TB = GPT * CB;               // code bytes of a thread, contiguous
+  static constexpr int UN = (TB + 15) / 16;         // 16-byte units of them in the ring
+  static constexpr int PB = GPT * 4;                // param bytes of a thread
+  static constexpr int RAWB = kDeqThreads * (UN * 16 + PB);
+  static constexpr int RAWN = D == 256 ? 2 : D == 128 ? 3 : 6;  // half tiles of the ring
+  static constexpr int SMW = 8 * LANES;             // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
   static constexpr int O0 = 256;
-  static constexpr int OSTEP = D < 32 ? 32 : D;
+  static constexpr int OSTEP = D;
   // shared memory
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + LANES * QBYTES;
   static constexpr int OFF_V = OFF_K + ST * KBYTES;
   static constexpr int OFF_RAW = OFF_V + ST * KBYTES;
-  // where lane 1's accumulator passes to lane 0: 32 columns, m and l of 128 rows.  Lane 1's
-  // Q is free then, and large enough from head_dim 128 on
-  static constexpr int STAGE = 34 * 128 * 4;
-  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES : OFF_RAW + RAWN * RAWB;
-  static constexpr int OFF_POISON = OFF_RAW + RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // int [2][3][D]
-  static constexpr int OFF_BAR = OFF_POISON + 2 * 3 * D * 4;
+  // where lane 1's accumulator passes to lane 0: 16 columns of 128 rows of each half.  Lane
+  // 1's Q (but for its first KiB) is free then, and large enough from head_dim 128 on
+  static constexpr int STAGE = 2 * 16 * 128 * 4;
+  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES + 1024 : OFF_RAW + RAWN * RAWB;
+  static constexpr int OFF_POISON = OFF_RAW + RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // int [3][D]
+  static constexpr int OFF_MAX = OFF_POISON + 3 * D * 4;        // float [LANES][2][128]
+  static constexpr int OFF_BAR = OFF_MAX + LANES * 1024;
   static constexpr int OFF_SEG = OFF_BAR + 512;                 // Seg [kSegs]
-  static constexpr int SMEM = OFF_SEG + 512 + 1024;             // slack to align the base
+  static constexpr int SMEM = OFF_SEG + 512;
 };
 
 // A segment: the block's tiles [lo, hi) of the unit (sequence b, KV head h, query block
@@ -127,36 +137,58 @@ struct alignas(16) Seg {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_EPI = 8, B_PAIR = 10, B_DRAIN = 11,
-       B_KFULL = 12, B_KEMPTY = 16, B_VFULL = 20, B_VEMPTY = 24, B_SEGFULL = 28, B_SEGEMPTY = 36, B_COUNT = 44 };
-enum { W_TMEM = 88, W_ABORT = 89, W_PFLAG = 90 /* [2] */, W_TICKET = 92, W_STARTB = 93, W_STARTQ = 94,
-       W_BASE = 96 /* int64 [2] */ };
+enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_PAIR = 8, B_DRAIN = 9, B_KFULL = 10,
+       B_KEMPTY = 14, B_VFULL = 18, B_VEMPTY = 22, B_SEGFULL = 26, B_SEGEMPTY = 34, B_MAX = 42, B_COUNT = 50 };
+enum { W_TMEM = 100, W_ABORT = 101, W_PFLAG = 102, W_EPI = 103, W_TICKET = 104, W_STARTB = 105,
+       W_STARTQ = 106, W_BASE = 108 /* int64 [2] */ };
 
-// Bounded waits: all give up when one has.
-__device__ __forceinline__ bool wait_on(uint32_t b, uint32_t parity, volatile uint32_t* words, uint32_t* err_word,
-                                     uint32_t limit_us) {
-  const uint64_t t0 = ptx::global_timer_ns();
-  for (uint32_t k = 1;; ++k) {
-    if (ptx::mbar_try_wait(b, parity)) return true;
-    if ((k & 63u) == 0) {
-      if (words[W_ABORT]) return false;
-      if (ptx::global_timer_ns() - t0 > (uint64_t)limit_us * 1000u) {
-        words[W_ABORT] = 1;
-        set_error(err_word, KVQ_ERRBIT_TIMEOUT);
-        return false;
-      }
-    }
-  }
+__device__ __forceinline__ uint32_t lds(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float ldsf(uint32_t addr) { return __uint_as_float(lds(addr)); }
+__device__ __forceinline__ void stsf(uint32_t addr, float v) { sts(addr, __float_as_uint(v)); }
+__device__ __forceinline__ uint32_t timer_lo() {  // nanoseconds, modulo 2^32
+  uint32_t t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+// Bounded waits (at most a second: the timer's 32 bits do): all give up when one has.
+// Few registers: most waits stand between registers full of scores.
 struct Waits {
-  uint32_t bars;             // shared address of the barriers
-  volatile uint32_t* words;  // the same as words
-  uint32_t* err_word;
-  uint32_t limit_us;
+  const ChunkAttnArgs& a;
+  uint32_t bars;  // shared address of the barriers and words
 
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+  // (volatile in PTX too: a plain load may be taken out of a loop that polls)
+  __device__ __forceinline__ uint32_t word(int i) const {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(bars + 4 * i) : "memory");
+    return v;
+  }
+  __device__ __forceinline__ void set_word(int i, uint32_t v) const {
+    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(bars + 4 * i), "r"(v) : "memory");
+  }
+  __device__ __forceinline__ bool late(uint32_t t0) const {
+    if (word(W_ABORT)) return true;
+    if (timer_lo() - t0 <= a.wait_limit_us * 1000u) return false;
+    set_word(W_ABORT, 1);
+    set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
+    return true;
+  }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-    return ptx::mbar_try_wait(bar(i), parity) || wait_on(bar(i), parity, words, err_word, limit_us);
+    const uint32_t b = bar(i);
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    const uint32_t t0 = timer_lo();
+#pragma unroll 1
+    for (uint32_t k = 1; !ptx::mbar_try_wait(b, parity); ++k)
+      if ((k & 63u) == 0 && late(t0)) return false;
+    return true;
   }
   // a whole warp waits; the same answer for all its lanes
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -377,28 +409,30 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&f)[4]) {
   }
 }
 
-// The four 8-code words of a group in raw code memory.
+// The four 8-code words of group g, from a thread's raw words.
 template <int BITS>
-__device__ __forceinline__ void code_words(uint32_t addr, uint32_t (&x)[4]) {
+__device__ __forceinline__ void code_words(const uint32_t* raw, int g, uint32_t (&x)[4]) {
   if (BITS == 4) {
-    const uint4 v = ld_shared_v4(addr);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-  } else if (BITS == 2) {
-    uint32_t w0, w1;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(addr) : "memory");
-    x[0] = w0, x[1] = w0 >> 8, x[2] = w1, x[3] = w1 >> 8;
-  } else {
-    uint32_t w[3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i) : "memory");
+    for (int i = 0; i < 4; ++i) x[i] = raw[4 * g + i];
+  } else if (BITS == 2) {
+    x[0] = raw[2 * g], x[1] = raw[2 * g] >> 8, x[2] = raw[2 * g + 1], x[3] = raw[2 * g + 1] >> 8;
+  } else {
+    const uint32_t* w = raw + 3 * g;
     const uint32_t v[4] = {w[0], __funnelshift_r(w[0], w[1], 24), __funnelshift_r(w[1], w[2], 16), w[2] >> 8};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = (v[i] & 0xfffu) | ((v[i] & 0xfff000u) << 4);
   }
 }
 
-// What the dequantizing warps share.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// What the dequantizing warps share.  Thread dt has row dt of a tile (head_dim 256: half
+// of row dt / 2): its codes are contiguous, and 8 neighbouring lanes store the same piece
+// of 8 rows, which the swizzle puts into 8 different banks' groups.
 template <int D, int BITS>
 struct Deq {
   using C = Cfg<D, BITS>;
@@ -410,16 +444,18 @@ struct Deq {
   int dt;         // thread of the warps that dequantize
   uint32_t seg;   // segments of the block so far
 
-  // Values of the fp16 format that are not finite take no part in the MMA: a weight of
-  // zero would make them NaN in rows that do not see the token.  The first token of
-  // the segment with +inf, -inf or NaN in a column is noted, and the epilogue gives
-  // the rows that see it what the sum would be.  (Rare: one thread per element.)
+  // Values that fp16 does not hold as finite ones take no part in the MMA: a weight of
+  // zero would make them NaN in rows that do not see the token.  The first token of the
+  // segment with +inf, -inf or NaN in a column is noted, and the epilogue gives the rows
+  // that see it what the sum would be.  (Rare: one thread per element.)
   __device__ __forceinline__ bool note(int col, int token, uint32_t h) {
-    // the notes of the segment before last are read before this one's are made
-    if (seg >= 2 && !wt.wait(B_EPI + (seg & 1), ((seg >> 1) - 1) & 1)) return false;
+    // the notes of earlier segments have been read before this one's are made
+    const uint32_t t0 = timer_lo();
+    while (wt.word(W_EPI) < seg * C::SMW)
+      if (wt.late(t0)) return false;
     const int kind = (h & 0x3ffu) ? 2 : (h & 0x8000u) ? 1 : 0;
-    atomicMin(poison + ((seg & 1) * 3 + kind) * D + col, token);
-    wt.words[W_PFLAG + (seg & 1)] = 1;
+    atomicMin(poison + kind * D + col, token);
+    wt.set_word(W_PFLAG, 1);
     return true;
   }
 
@@ -430,140 +466,97 @@ struct Deq {
     int64_t row0 = 0;  // contiguous: row of the head's token 0; paged: h * 32
   };
 
-  // Raw copies of a half tile (keys, then values) into ring slot `slot`; rows that are
-  // not there become zero codes with zero params, which stand for zeros.  A head's groups
-  // lie one behind the other, so group gi of the tile is gi groups from its first.
+  // The thread's raw row of a half tile (keys, then values) into ring slot `slot`; a row
+  // that is not there becomes zero codes with zero params, which stand for zeros.
   __device__ __forceinline__ void fetch(const Cursor& c, int slot) {
-    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * C::CB;
-    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::GPT * C::CB + dt * 4;
-    const uint8_t* codes = a.codes[c.w];
-    const uint32_t* params = a.params[c.w];
-    const int left = c.npk - c.tile * C::TN;  // rows of the tile that there are
-    int64_t at = (c.row0 + c.tile * C::TN) * C::G + dt;
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
+    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+    const int p = c.tile * C::TN + dt / C::TPR;
+    bool there = p < c.npk;
+    int64_t row = c.row0 + p;
+    if (a.rm.paged && there) {
+      const int pg = a.rm.page_of(c.b, p / kPage);
+      there = pg >= 0 && pg < a.rm.npages;
+      if (!there) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+      row = (int64_t)pg * a.Hkv * kPage + c.row0 + p % kPage;
+    }
+    if (there) {
+      const uint8_t* src = a.codes[c.w] + row * (C::G * C::CB) + (dt % C::TPR) * C::TB;
+      constexpr int N = C::TB % 16 == 0 ? 16 : C::TB % 8 == 0 ? 8 : 4;
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i) {
-      const int r = (i * kDeqThreads + dt) / C::G;
-      bool there = r < left;
-      int64_t from = at + i * kDeqThreads;
-      if (a.rm.paged && there) {
-        const int p = c.tile * C::TN + r;
-        const int pg = a.rm.page_of(c.b, p / kPage);
-        there = pg >= 0 && pg < a.rm.npages;
-        if (!there) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
-        from = ((int64_t)pg * a.Hkv * kPage + c.row0 + p % kPage) * C::G + dt % C::G;
-      }
-      const uint32_t d0 = dc + i * kDeqThreads * C::CB, d1 = dp + i * kDeqThreads * 4;
-      if (there) {
-        const uint8_t* src = codes + from * C::CB;
-        if (BITS == 4) {
-          ptx::cp_async_16(d0, src, 16);
-        } else if (BITS == 2) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d0), "l"(src) : "memory");
-        } else {
+      for (int i = 0; i < C::TB / N; ++i)
+        cp_async<N>(dc + (i * N / 16) * (kDeqThreads * 16) + i * N % 16, src + i * N);
+      cp_async<C::PB>(dp, a.params[c.w] + row * C::G + (dt % C::TPR) * C::GPT);
+    } else {
 #pragma unroll
-          for (int j = 0; j < 3; ++j)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d0 + 4 * j), "l"(src + 4 * j)
-                         : "memory");
-        }
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d1), "l"(params + from) : "memory");
-      } else {
+      for (int i = 0; i < C::UN; ++i) st_shared_v4(dc + i * (kDeqThreads * 16), make_uint4(0, 0, 0, 0));
 #pragma unroll
-        for (int j = 0; j < C::CB / 4; ++j)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(d0 + 4 * j), "r"(0) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(d1), "r"(0) : "memory");
-      }
+      for (int i = 0; i < C::GPT; ++i) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dp + 4 * i), "r"(0) : "memory");
     }
   }
 
-  // The pieces of one group with a value that is not finite in fp16, at `at` + pieces
-  // c0 ^ 0..3 (x: their code words, in the order of the pieces; col: the group's first
-  // column, xr: the order).
-  __device__ __forceinline__ bool rare_group(const uint32_t* x, uint32_t prm, int w, uint32_t at, uint32_t c0, int col,
-                                          int xr, int token) {
-    const uint32_t s2 = ptx::prmt(prm, prm, 0x1010), m2 = ptx::prmt(prm, prm, 0x3232);
-    const bool finite = !f16_nonfinite(prm) && !f16_nonfinite(prm >> 16);
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t y[4];
-      codes_f16<BITS>(x[c], y);
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        uint32_t v = ptx::hfma2_u32(y[j], s2, m2);
-#pragma unroll 1
-        for (int sh = 0; sh < 32; sh += 16) {
-          const uint32_t hv = (v >> sh) & 0xffffu;
-          if (!f16_nonfinite(hv)) continue;
-          uint32_t to = hv;
-          if (finite) {
-            to = (hv & 0x8000u) | 0x7bffu;  // past fp16's largest value by the scale's rounding
-          } else if (w == 1) {
-            if (!note(col + (c ^ xr) * 8 + 2 * j + sh / 16, token, hv)) return false;
-            to = 0;
-          }
-          v = (v & ~(0xffffu << sh)) | (to << sh);
-        }
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + ((c0 ^ c) << 4) + 4 * j), "r"(v) : "memory");
-      }
-    }
-    return true;
+  // Shared address of the thread's row in a tile at dst, with the row's swizzle in its
+  // low bits: piece c of panel p is at (this ^ (c << 4)) + p * KP.
+  __device__ __forceinline__ uint32_t row_addr(uint32_t dst) const {
+    const int r = dt / C::TPR;
+    return dst + (dt % C::TPR) * (C::GPT / 2) * C::KP + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
   }
+  __device__ __forceinline__ int column(int g, int c) const { return ((dt % C::TPR) * C::GPT + g) * 32 + c * 8; }
 
-  // A fetched half tile as fp16 at `dst`.
-  __device__ __forceinline__ bool packed_tile(const Seg& k, int tile, int w, int slot, uint32_t dst) {
-    const uint32_t raw = smem + C::OFF_RAW + slot * C::RAWB;
+  // A fetched half tile as fp16 at `dst`.  first: logical place of the tile's first token.
+  __device__ __forceinline__ bool packed_tile(int first, int w, int slot, uint32_t dst) {
     constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
-#pragma unroll 2
-    for (int i = 0; i < C::GPT; ++i) {
-      const int gi = i * kDeqThreads + dt;
-      const int r = gi / C::G, g = gi % C::G;
-      const int panel = g / 2;
-      uint32_t x[4], prm;
-      code_words<BITS>(raw + gi * C::CB, x);
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(prm) : "r"(raw + kDeqThreads * C::GPT * C::CB + gi * 4) : "memory");
-      const uint32_t s2 = ptx::prmt(prm, prm, 0x1010), m2 = ptx::prmt(prm, prm, 0x3232);
-      // the lanes of a store phase take different pieces first, so that they differ in
-      // banks: two panels of a row lie a multiple of 128 bytes apart
-      const int xr = D == 256 ? panel : D == 128 ? 2 * panel : 0;
-      if (D >= 128 && (xr & 2)) {
-        const uint32_t t0 = x[0], t1 = x[1];
-        x[0] = x[2], x[1] = x[3], x[2] = t0, x[3] = t1;
-      }
-      if (D == 256 && (xr & 1)) {
-        const uint32_t t0 = x[0], t2 = x[2];
-        x[0] = x[1], x[2] = x[3], x[1] = t0, x[3] = t2;
-      }
-      const uint32_t at = dst + panel * C::KP + r * C::RB;
-      const uint32_t c0 = C::RB == 128 ? (((g & 1) * 4) ^ xr ^ (r & 7)) : ((r >> 1) & 3);
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
+    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+    uint32_t raw[C::UN * 4], prm[C::GPT];
+#pragma unroll
+    for (int i = 0; i < C::UN; ++i) {
+      const uint4 v = ld_shared_v4(dc + i * (kDeqThreads * 16));
+      raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < C::GPT; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(prm[i]) : "r"(dp + 4 * i) : "memory");
+    const uint32_t at = row_addr(dst);
+    uint32_t rare = 0;
+#pragma unroll
+    for (int g = 0; g < C::GPT; ++g) {
+      const uint32_t s2 = ptx::prmt(prm[g], prm[g], 0x1010), m2 = ptx::prmt(prm[g], prm[g], 0x3232);
       // the group's largest value; only where it is not finite can any value be so
-      if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) {
-        const uint32_t xs[4] = {x[0], x[1], x[2], x[3]};
-        if (!rare_group(xs, prm, w, at, c0, panel * 64 + (g & 1) * 32, xr, k.ns + tile * C::TN + r)) return false;
-        continue;
-      }
+      if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) rare |= 1u << g;
+      uint32_t x[4];
+      code_words<BITS>(raw, g, x);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t f[4], y[4];
-        codes_f16<BITS>(x[c], f);
+        uint32_t y[4];
+        codes_f16<BITS>(x[c], y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(f[j], s2, m2);
-        st_shared_v4(at + ((c0 ^ c) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+        for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(y[j], s2, m2);
+        st_shared_v4((at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP, make_uint4(y[0], y[1], y[2], y[3]));
       }
     }
-    return true;
-  }
-
-  // The 16 stored elements at p0 and p1, of columns col ..: what is not finite becomes
-  // zero and is noted.
-  __device__ __forceinline__ bool rare_pieces(uint32_t p0, uint32_t p1, int col, int token) {
+    if (rare == 0) return true;
+    // what is not finite among the stored values: past fp16's largest value by the
+    // scale's rounding, or meant (params that are not finite)
 #pragma unroll 1
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t at = (j < 8 ? p0 : p1) + 2 * (j & 7);
+    for (int e = 0; e < 32 * C::GPT; ++e) {
+      const int g = e >> 5;
+      if (!((rare >> g) & 1u)) continue;
+      uint32_t pg;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pg) : "r"(dp + 4 * g) : "memory");
+      const uint32_t ea = (at ^ (((g & 1) * 4 + ((e >> 3) & 3)) << 4)) + (g / 2) * C::KP + 2 * (e & 7);
       unsigned short hv;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(at) : "memory");
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
       if (!f16_nonfinite(hv)) continue;
-      if (!note(col + j, token, hv)) return false;
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+      if (!f16_nonfinite(pg) && !f16_nonfinite(pg >> 16))
+        hv = (hv & 0x8000u) | 0x7bffu;
+      else if (w == 0)
+        continue;
+      else if (note(column(g, 0) + (e & 31), first + dt / C::TPR, hv))
+        hv = 0;
+      else
+        return false;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(ea), "h"(hv) : "memory");
     }
     return true;
   }
@@ -573,42 +566,40 @@ struct Deq {
   // A half tile of fp16 tokens (sink, then window): rows f0 .. of their line.
   __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, int w, uint32_t dst) {
     const int64_t bh = (int64_t)k.b * a.Hkv + k.h;
-    const int n = k.ns + k.nres;
-#pragma unroll 1
-    for (int i = 0; i < C::GPT; ++i) {
-      const int gi = i * kDeqThreads + dt;
-      const int r = gi / C::G, g = gi % C::G, f = f0 + r;
-      const __half* src = a.q;  // (not read)
-      if (f < k.ns)
-        src = a.sink[w] + (bh * a.Ns + f) * D + g * 32;
-      else if (f < n)
-        src = a.res[w] + (bh * a.Nr + ring_slot(k.head + f - k.ns)) * D + g * 32;
-      const uint32_t at = dst + (g / 2) * C::KP;
+    const int f = f0 + dt / C::TPR, n = k.ns + k.nres;
+    const __half* src = a.q;  // (not read)
+    if (f < k.ns)
+      src = a.sink[w] + (bh * a.Ns + f) * D;
+    else if (f < n)
+      src = a.res[w] + (bh * a.Nr + ring_slot(k.head + f - k.ns)) * D;
+    if (f < n) src += column(0, 0);
+    const uint32_t at = row_addr(dst);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        ptx::cp_async_16(at + swizzled<C::RB>(r, (g & 1) * 4 + c), src + (f < n ? c * 8 : 0), f < n ? 16 : 0);
-    }
+    for (int i = 0; i < 4 * C::GPT; ++i)
+      ptx::cp_async_16((at ^ ((i & 7) << 4)) + (i / 8) * C::KP, src + (f < n ? i * 8 : 0), f < n ? 16 : 0);
     ptx::cp_async_wait_all();
+    const int token = f < k.ns ? f : f + k.npk;
+#pragma unroll 2
+    for (int i = 0; i < 4 * C::GPT; i += 2) {  // 16 elements
+      const uint32_t p0 = (at ^ ((i & 7) << 4)) + (i / 8) * C::KP, p1 = (at ^ (((i & 7) + 1) << 4)) + (i / 8) * C::KP;
+      uint4 u[2] = {ld_shared_v4(p0), ld_shared_v4(p1)};
+      to_storage<BITS>(u[0], u[1]);
+      st_shared_v4(p0, u[0]);
+      st_shared_v4(p1, u[1]);
+      if (w == 0) continue;
+      const uint32_t* y = reinterpret_cast<const uint32_t*>(u);
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bad |= f16_nonfinite(y[j]) || f16_nonfinite(y[j] >> 16);
+      if (!bad) continue;
 #pragma unroll 1
-    for (int i = 0; i < C::GPT; ++i) {
-      const int gi = i * kDeqThreads + dt;
-      const int r = gi / C::G, g = gi % C::G, f = f0 + r;
-      const uint32_t at = dst + (g / 2) * C::KP;
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {  // (16 elements)
-        const uint32_t p0 = at + swizzled<C::RB>(r, (g & 1) * 4 + c), p1 = at + swizzled<C::RB>(r, (g & 1) * 4 + c + 1);
-        uint4 u[2] = {ld_shared_v4(p0), ld_shared_v4(p1)};
-        to_storage<BITS>(u[0], u[1]);
-        st_shared_v4(p0, u[0]);
-        st_shared_v4(p1, u[1]);
-        if (w == 1) {
-          const uint32_t* y = reinterpret_cast<const uint32_t*>(u);
-          bool bad = false;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) bad |= f16_nonfinite(y[j]) || f16_nonfinite(y[j] >> 16);
-          if (bad && !rare_pieces(p0, p1, (g / 2) * 64 + (g & 1) * 32 + c * 8, f < k.ns ? f : f + k.npk))
-            return false;
-        }
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t ea = (j < 8 ? p0 : p1) + 2 * (j & 7);
+        unsigned short hv;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
+        if (!f16_nonfinite(hv)) continue;
+        if (!note(column(0, i) + j, token, hv)) return false;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(ea), "h"((unsigned short)0) : "memory");
       }
     }
     return true;
@@ -649,7 +640,7 @@ struct Deq {
       if (!ok) break;
       const Seg& s = k.get(ring);
       if (s.b < 0) break;
-      const int lo = s.lo, hi = s.hi, npt = s.npt;
+      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns;
       for (int h = 2 * lo; h < 2 * hi; ++h) {
         fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
         const int t = h >> 1, w = h & 1;
@@ -659,7 +650,7 @@ struct Deq {
         if (!ok) break;
         if (t < npt) {
           asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-          ok = packed_tile(s, t, w, slot, dst);
+          ok = packed_tile(ns + t * C::TN, w, slot, dst);
         } else {
           ok = f16_tile(s, (t - npt) * C::TN, w, dst);
         }
@@ -706,13 +697,14 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
       const int stage = t % C::ST, lane = lane_of(u);
       if ((C::LANES == 1 || alt || lane == 0) && !wt.wait(B_KFULL + stage, (t / C::ST) & 1)) return false;
       tc5::fence_after();
-      const uint32_t q = smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES);
-      const uint32_t kb = smem + C::OFF_K + stage * C::KBYTES;
+      const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
+      const uint64_t kd = tc5::smem_desc(smem + C::OFF_K + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
-        tc5::mma_ss(tmem + C::S0 + lane * C::TN, tc5::smem_desc(q + panel * C::QP + in, 16, 8 * C::RB, C::SWZ),
-                    tc5::smem_desc(kb + panel * C::KP + in, 16, 8 * C::RB, C::SWZ), kIdescQK, j > 0);
+        constexpr int PW = C::PW;
+        const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
+        tc5::mma_ss(tmem + C::S0 + lane * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+                    kIdescQK, j > 0);
       }
       tc5::commit(wt.bar(B_SFULL + lane));
       if (releases(u)) tc5::commit(wt.bar(B_KEMPTY + stage));
@@ -726,12 +718,15 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
       if (ok && (C::LANES == 1 || alt || lane == 0)) ok = wt.wait(B_VFULL + stage, (t / C::ST) & 1);
       if (!ok) break;
       tc5::fence_after();
-      const uint32_t vb = smem + C::OFF_V + stage * C::KBYTES;
+      const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
       const bool acc = u >= C::LANES;  // the lane's first tile of the segment starts O
 #pragma unroll
-      for (int j = 0; j < C::TN / 16; ++j)
-        tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + j * 8,
-                    tc5::smem_desc(vb + j * 16 * C::RB, C::KP, 8 * C::RB, C::SWZ), kIdescPV, acc || j > 0);
+      for (int j = 0; j < C::TN / 16; ++j) {
+        // P of each half of the tokens lies at the start of that half of S
+        const int col = j * 16 / C::HC * C::HC + (j * 16 % C::HC) / 2;
+        tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + col,
+                    vd + ((j * 16 * C::RB) >> 4), kIdescPV, acc || j > 0);
+      }
       if (releases(u)) tc5::commit(wt.bar(B_VEMPTY + stage));
       if (u + C::LANES < U)
         ok = qk(u + C::LANES);  // after PV(u) in the tensor cores' order: S may take P's place
@@ -759,37 +754,85 @@ struct Soft {
   using C = Cfg<D, BITS>;
   const ChunkAttnArgs& a;
   const Waits& wt;
-  uint32_t smem, tmem;  // tmem: with the warp's lanes
-  int* poison;
-  float* stage;         // [column][row]
-  const Seg* ring;
-  int lane, r;          // accumulator, row in it
-  uint32_t sn, on, pairn, seg;
+  const uint32_t smem, tmem;  // tmem: with the warp's lanes
+  uint32_t phases;            // parity bits of the barriers that the thread waits on
+  uint32_t at_seg, seg;       // place in the ring of segments, segments so far
 
+  enum { P_S = 0, P_O = 1, P_PAIR = 2, P_MAX = 3, P_STARTED = 4 };
+
+  // Accumulator, half of its columns, and row: by the thread.
+  static __device__ __forceinline__ int lane() { return threadIdx.x >> 8; }
+  static __device__ __forceinline__ int half() { return (threadIdx.x >> 7) & 1; }
+  static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
+
+  __device__ __forceinline__ bool wait(int bar, int bit) {
+    const bool ok = wt.wait_warp(bar, (phases >> bit) & 1);
+    phases ^= 1u << bit;
+    return ok;
+  }
   __device__ __forceinline__ bool pair_sync() {
     wt.arrive_warp(B_PAIR);
-    return wt.wait_warp(B_PAIR, pairn++ & 1);
+    return wait(B_PAIR, P_PAIR);
+  }
+  // with the warp that has the same rows and the other half of the columns
+  __device__ __forceinline__ bool row_sync() {
+    const int b = B_MAX + lane() * 4 + (r() >> 5);
+    wt.arrive_warp(b);
+    return wait(b, P_MAX);
+  }
+  __device__ __forceinline__ uint32_t xmax() const { return smem + C::OFF_MAX + lane() * 1024; }
+
+  // The current segment, read field by field.
+  struct Ref {
+    uint32_t at;
+#define KVQ_SEG_FIELD(name) \
+  __device__ __forceinline__ int name() const { return (int)lds(at + (uint32_t)offsetof(Seg, name)); }
+    KVQ_SEG_FIELD(b)
+    KVQ_SEG_FIELD(h)
+    KVQ_SEG_FIELD(qb)
+    KVQ_SEG_FIELD(lo)
+    KVQ_SEG_FIELD(hi)
+    KVQ_SEG_FIELD(npt)
+    KVQ_SEG_FIELD(nt)
+    KVQ_SEG_FIELD(alt)
+    KVQ_SEG_FIELD(c0)
+    KVQ_SEG_FIELD(n)
+    KVQ_SEG_FIELD(ns)
+    KVQ_SEG_FIELD(npk)
+    KVQ_SEG_FIELD(nres)
+    KVQ_SEG_FIELD(first_b)
+    KVQ_SEG_FIELD(last_b)
+#undef KVQ_SEG_FIELD
+  };
+  __device__ __forceinline__ Ref ref() const { return {smem + C::OFF_SEG + (at_seg % kSegs) * (uint32_t)sizeof(Seg)}; }
+  __device__ __forceinline__ bool wait_seg() const {
+    return wt.wait_warp(B_SEGFULL + at_seg % kSegs, (at_seg / kSegs) & 1);
+  }
+
+  __device__ __forceinline__ int block_rows(const Ref& k) const { return min(k.n() * a.gq - k.qb() * C::QB, C::QB); }
+  __device__ __forceinline__ int block_row(const Ref& k) const { return (k.alt() ? 0 : lane() * 128) + r(); }
+  // Where query row `row` of the block is, in q and in the output.
+  __device__ __forceinline__ int64_t row_at(const Ref& k, int row) const {
+    const int R = k.qb() * C::QB + row;
+    const int tok = token_of(a, R);
+    return ((int64_t)(k.c0() + tok) * a.Hq + k.h() * a.gq + (R - tok * a.gq)) * D;
   }
 
   // The lane's 128 rows of Q, in storage order and swizzled.
-  __device__ __forceinline__ int block_rows(const Seg& k) const { return min(k.n * a.gq - k.qb * C::QB, C::QB); }
-  __device__ __forceinline__ void load_q(const Seg& k) {
-    if (k.alt && lane == 1) return;
+  __device__ __forceinline__ void load_q() {
+    const Ref k = ref();
+    if (k.alt() && lane() == 1) return;
     constexpr int LPR = D / 16;    // threads of a row, 32 bytes each
     constexpr int RPI = 32 / LPR;  // rows of a warp at a time
-    const int w = r >> 5, l = r & 31;
-    const int rows = block_rows(k);
-    const int rb = k.qb * C::QB + lane * 128;
-    const uint32_t base = smem + C::OFF_Q + lane * C::QBYTES;
-#pragma unroll 4
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int row = w * 32 + i * RPI + l / LPR, c = (l % LPR) * 2;  // c: 16-byte piece of the row
+    const int w = half() * 4 + (r() >> 5), l = r() & 31;  // a warp loads 16 rows
+    const int rows = block_rows(k) - lane() * 128;
+    const uint32_t base = smem + C::OFF_Q + lane() * C::QBYTES;
+#pragma unroll 2
+    for (int i = 0; i < 16 / RPI; ++i) {
+      const int row = w * 16 + i * RPI + l / LPR, c = (l % LPR) * 2;  // c: 16-byte piece of the row
       uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-      if (lane * 128 + row < rows) {
-        const int R = rb + row;
-        const int tok = token_of(a, R), g = R - tok * a.gq;
-        const uint4* src = reinterpret_cast<const uint4*>(
-                               a.q + ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + g) * D) + c;
+      if (row < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + row_at(k, lane() * 128 + row)) + c;
         u0 = __ldg(src);
         u1 = __ldg(src + 1);
       }
@@ -800,85 +843,101 @@ struct Soft {
       st_shared_v4(at + swizzled<C::RB>(row, cc + 1), u1);
     }
     ptx::fence_proxy_async_shared();
-    wt.arrive_warp(B_QFULL + lane);
+    wt.arrive_warp(B_QFULL + lane());
   }
 
-  // One tile: the weights of S's row into TMEM, m and l brought up to date.
-  // visible: tokens of the tile that the row sees (a prefix); bad: pages left out.
-  __device__ __forceinline__ void tile(int visible, uint32_t bad, bool has_o, float& m, float& l) {
-    const uint32_t sa = tmem + C::S0 + lane * C::TN;
-    float s[C::TN];
-    float mx[4];
+  // Hides what the row does not see of 32 tokens (a page: `bad` all of them); the largest
+  // score that is left.
+  static __device__ __forceinline__ float mask(float (&s)[32], int visible, uint32_t bad) {
+    const int v = bad ? 0 : visible;
+    float x = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < C::TN; i += 32) tc5::ld32_max(sa + i, reinterpret_cast<uint32_t*>(s + i), mx[i / 32]);
-    tc5::wait_ld();
-#pragma unroll
-    for (int i = 0; i < C::TN; i += 32) {
-      tc5::pin32(reinterpret_cast<uint32_t*>(s + i));
-      asm volatile("" : "+f"(mx[i / 32]));
+    for (int j = 0; j < 32; ++j) {
+      s[j] = j < v ? s[j] : -INFINITY;
+      x = fmaxf(x, s[j]);
     }
-    if (__any_sync(0xffffffffu, visible < C::TN) || bad) {
+    return x;
+  }
+
+  // One tile: the weights of the group's half of S's row into TMEM, m (the same in both
+  // groups) and l (each group's own) brought up to date.  visible: columns of the half
+  // that the row sees (a prefix); bad: pages of it left out.
+  __device__ __forceinline__ bool tile(int visible, uint32_t bad, float& m, float& l) {
+    const uint32_t sa = tmem + C::S0 + lane() * C::TN + half() * C::HC;
+    // 32 scores at a time, read again after the maximum is known: 64 at once and what
+    // else lives do not fit the registers, and the small L1 beside the tiles makes a
+    // spilled register a trip to L2
+    float s[32];
+    const bool masked = __any_sync(0xffffffffu, visible < C::HC) || bad;
+    float mine = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < C::TN; i += kPage) {
-        const int v = (bad >> (i / kPage)) & 1u ? 0 : visible - i;
-        float x = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kPage; ++j) {
-          s[i + j] = j < v ? s[i + j] : -INFINITY;
-          x = fmaxf(x, s[i + j]);
-        }
-        mx[i / 32] = x;
-      }
+    for (int h = C::HC - 32; h >= 0; h -= 32) {
+      float mx;
+      tc5::ld32_max(sa + h, reinterpret_cast<uint32_t*>(s), mx);
+      tc5::wait_ld();
+      tc5::pin32(reinterpret_cast<uint32_t*>(s));
+      asm volatile("" : "+f"(mx));
+      if (masked) mx = mask(s, visible - h, (bad >> (h / 32)) & 1u);
+      mine = fmaxf(mine, mx);
     }
-    const float mt = C::TN == 128 ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) : fmaxf(mx[0], mx[1]);
-    const float c = a.scale_log2;
-    const float mn = fmaxf(m, mt);
-    const bool moves = (mn - m) * c > 8.0f;
+    // the row's maximum: of this half and of the other group's
+    stsf(xmax() + half() * 512 + r() * 4, mine);
+    if (!row_sync()) return false;
+    const float mn = fmaxf(m, fmaxf(mine, ldsf(xmax() + (half() ^ 1) * 512 + r() * 4)));
+    const bool moves = (mn - m) * a.scale_log2 > 8.0f;
     if (__any_sync(0xffffffffu, moves)) {
-      const float f = moves ? ptx::ex2_ftz((m - mn) * c) : 1.0f;
+      const float f = moves ? ptx::ex2_ftz((m - mn) * a.scale_log2) : 1.0f;
       if (moves) m = mn;
       l *= f;
-      if (has_o) {
+      if (phases & (1u << P_STARTED)) {
+        const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP + half() * C::HD;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 16) {
-          uint32_t o[16];
-          tc5::ld16(tmem + C::O0 + lane * C::OSTEP + i, o);
+        for (int i = 0; i < C::HD; i += 8) {
+          uint32_t o[8];
+          tc5::ld8(oa + i, o);
           tc5::wait_ld();
-          tc5::pin16(o);
+          tc5::pin8(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tc5::st16(tmem + C::O0 + lane * C::OSTEP + i, o);
+          for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc5::st8(oa + i, o);
         }
       }
     }
-    const float off = m == -INFINITY ? 0.0f : -m * c;
-    const uint64_t c2 = pack_f32x2(c, c), off2 = pack_f32x2(off, off);
-    uint64_t sum2[4] = {0, 0, 0, 0};
+    const float off = m == -INFINITY ? 0.0f : -m * a.scale_log2;
+    const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
+    uint64_t sum2 = pack_f32x2(l, 0.0f);
 #pragma unroll
-    for (int h = 0; h < C::TN; h += 32) {
+    for (int h = 0; h < C::HC; h += 32) {
+      if (h > 0) {
+        tc5::ld32(sa + h, reinterpret_cast<uint32_t*>(s));
+        tc5::wait_ld();
+        tc5::pin32(reinterpret_cast<uint32_t*>(s));
+        if (masked) mask(s, visible - h, (bad >> (h / 32)) & 1u);
+      }
       uint32_t p[16];
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const uint64_t x = fma_f32x2(pack_f32x2(s[h + i], s[h + i + 1]), c2, off2);
+        const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
         const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
         const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
-        sum2[(i / 2) & 3] = add_f32x2(sum2[(i / 2) & 3], pack_f32x2(e0, e1));
+        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
         p[i / 2] = ptx::pack_h2(e0, e1);
       }
       tc5::st16(sa + h / 2, p);
     }
-    const uint64_t t2 = add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3]));
-    l += __uint_as_float(lo_bits(t2)) + __uint_as_float(hi_bits(t2));
+    l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
     tc5::wait_st();
+    return true;
   }
 
-  // What the notes say of the row's outputs: the row sees `lim` tokens; written over the
+  // What the notes say of the group's columns of the row: it sees `lim` tokens; written over the
   // thread's own earlier stores, to the output (whole) or to the piece's O in `slot`.
   __device__ __forceinline__ void notes(int lim, bool whole, int64_t at, int slot, int row) const {
-    const int* pn = poison + (seg & 1) * 3 * D;
+    const uint32_t pn = smem + C::OFF_POISON;
 #pragma unroll 1
-    for (int c = 0; c < D; ++c) {
-      const bool up = pn[c] < lim, down = pn[D + c] < lim, nan = pn[2 * D + c] < lim;
+    for (int c = half() * C::HD; c < (half() + 1) * C::HD; ++c) {
+      const bool up = (int)lds(pn + 4 * c) < lim, down = (int)lds(pn + 4 * (D + c)) < lim,
+                 nan = (int)lds(pn + 4 * (2 * D + c)) < lim;
       if (!(up || down || nan)) continue;
       const float v = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
       if (!whole) {
@@ -913,24 +972,16 @@ struct Soft {
                             ptx::pack_h2(y[8 * e + 4], y[8 * e + 5]), ptx::pack_h2(y[8 * e + 6], y[8 * e + 7]));
     }
   }
-  __device__ __forceinline__ int64_t out_at(const Seg& k, int row) const {
-    const int R = k.qb * C::QB + row;
-    const int tok = token_of(a, R);
-    return ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
-  }
-
   __device__ __forceinline__ float inverse(float l) const {
     if (l == 0.0f) set_error(a.err_word, KVQ_ERRBIT_EMPTY);  // nothing seen
     return l == 0.0f ? 0.0f : 1.0f / l;
   }
 
   // The pieces of a cut unit, from their (O, m, l) in global memory: 16 columns of a row
-  // at a time, all softmax threads.  first .. last: the blocks that hold the pieces.
-  __device__ __forceinline__ void join(const Seg& k) const {
-    const int rows = block_rows(k), first = k.first_b, last = k.last_b;
-    const int tid = lane * 128 + r;
-    const float c = a.scale_log2;
-    for (int it = tid; it < rows * (D / 16); it += C::SMT) {
+  // at a time, all softmax threads.
+  __device__ __forceinline__ void join(const Ref& k) const {
+    const int rows = block_rows(k), first = k.first_b(), last = k.last_b();
+    for (int it = threadIdx.x; it < rows * (D / 16); it += C::SMW * 32) {
       const int cg = it / rows, row = it - cg * rows;
       float m = -INFINITY;
 #pragma unroll 4
@@ -943,7 +994,7 @@ struct Soft {
       for (int p = first; p <= last; ++p) {
         const int64_t slot = 2 * p + (p == first);
         const float2 ml = __ldcg(a.ml_part + slot * C::QB + row);
-        const float f = ml.x == -INFINITY ? (ml.y != ml.y ? NAN : 0.0f) : ptx::ex2_ftz((ml.x - m) * c);
+        const float f = ml.x == -INFINITY ? (ml.y != ml.y ? NAN : 0.0f) : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
         l += ml.y * f;
         const float4* src = a.o_part + (slot * (D / 4) + cg * 4) * C::QB + row;
 #pragma unroll
@@ -955,153 +1006,189 @@ struct Soft {
           o[4 * e + 3] += v.w * f;
         }
       }
-      store16(o, inverse(l), out_at(k, row) + cg * 16);
+      store16(o, inverse(l), row_at(k, row) + cg * 16);
     }
   }
 
-  __device__ __forceinline__ bool run(int block) {
-    SegReader at_seg;
-    if (!__all_sync(0xffffffffu, at_seg.wait(wt))) return false;
-    if (at_seg.get(ring).b < 0) return true;
-    load_q(at_seg.get(ring));
-    while (true) {
-      const Seg& k = at_seg.get(ring);
-      const bool alt = k.alt;
-      const int row = (alt ? 0 : lane * 128) + r;  // of the block
-      const int rows = block_rows(k);
-      const bool warp_live = (row & ~31) < rows;
-      int lim = 0;
-      if (row < rows) lim = seen_of(a, k.n, k.ns + k.npk + k.nres, token_of(a, k.qb * C::QB + row));
-      const int plim = seen_packed(k.ns, k.npk, lim), flim = seen_f16(k.ns, k.npk, lim);
-      const int npt = k.npt, hi = k.hi;
-      float m = -INFINITY, l = 0.0f;
-      const int step = alt ? 2 : 1, t0 = k.lo + (alt ? lane : 0);
-      for (int t = t0; t < hi; t += step) {
-        const bool packed = t < npt;
-        const int visible = packed ? plim - t * C::TN : flim - (t - npt) * C::TN;
+  // The tiles of a segment: m and l of the row's columns.
+  __device__ __forceinline__ bool tiles(float& m, float& l) {
+    m = -INFINITY;
+    l = 0.0f;
+    phases &= ~(1u << P_STARTED);
+    // packed tiles, then fp16 ones: t and its end, and the tokens that the row sees from t on
+#pragma unroll 1
+    for (int f16 = 0; f16 < 2; ++f16) {
+      int t, end, visible;
+      bool live;
+      {
+        const Ref k = ref();
+        const int row = block_row(k), rows = block_rows(k), npt = k.npt(), alt = k.alt();
+        t = k.lo() + (alt ? lane() : 0);
+        // (the lane's first tile that is not packed)
+        if (f16 && t < npt) t += alt ? (npt - t + 1) & ~1 : npt - t;
+        end = f16 ? k.hi() : min(k.hi(), npt);
+        live = (row & ~31) < rows;
+        visible = 1 << 30;  // rows that are not there need no mask
+        if (row < rows) {
+          const int ns = k.ns(), npk = k.npk();
+          const int lim = seen_of(a, k.n(), ns + npk + k.nres(), token_of(a, k.qb() * C::QB + row));
+          visible = (f16 ? seen_f16(ns, npk, lim) + npt * C::TN : seen_packed(ns, npk, lim)) - t * C::TN;
+          visible -= half() * C::HC;
+        }
+      }
+#pragma unroll 1
+      while (t < end) {
         uint32_t bad = 0;
-        if (a.rm.paged && packed) {
-          const int j = t * (C::TN / kPage) + (r & 31);
+        if (a.rm.paged && !f16) {
+          const Ref k = ref();
+          const int j = (t * C::TN + half() * C::HC) / kPage + (r() & 31);
           bool out = false;
-          if ((r & 31) < C::TN / kPage && j * kPage < k.npk) {
-            const int pg = a.rm.page_of(k.b, j);
+          if ((r() & 31) < C::HC / kPage && j * kPage < k.npk()) {
+            const int pg = a.rm.page_of(k.b(), j);
             out = pg < 0 || pg >= a.rm.npages;
           }
           bad = __ballot_sync(0xffffffffu, out);
         }
-        if (!wt.wait_warp(B_SFULL + lane, sn++ & 1)) return false;
+        if (!wait(B_SFULL + lane(), P_S)) return false;
         tc5::fence_after();
-        if (warp_live) tile(visible, bad, t > t0, m, l);
+        if (live && !tile(visible, bad, m, l)) return false;
         tc5::fence_before();
-        wt.arrive_warp(B_PREADY + lane);
+        wt.arrive_warp(B_PREADY + lane());
+        phases |= 1u << P_STARTED;
+        const int step = ref().alt() ? 2 : 1;
+        t += step;
+        if (visible < (1 << 29)) visible -= step * C::TN;
       }
-      const bool any = t0 < hi;
-      if (any && !wt.wait_warp(B_ODONE + lane, on++ & 1)) return false;
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ bool run(int block) {
+    if (!wait_seg()) return false;
+    if (ref().b() < 0) return true;
+    load_q();
+    while (true) {
+      float m, l;
+      if (!tiles(m, l)) return false;
+      const bool any = (phases >> P_STARTED) & 1;
+      if (any && !wait(B_ODONE + lane(), P_O)) return false;
       tc5::fence_after();
 
-      SegReader after = at_seg;
-      ++after.i;
-      if (!__all_sync(0xffffffffu, after.wait(wt))) return false;
-      const bool more = after.get(ring).b >= 0;
-      if (more && !alt) load_q(after.get(ring));  // under the epilogue
-
-      // with alternating lanes the other's tiles may still be on their way
+      const Ref k = ref();
+      const bool alt = k.alt();
+      const int row = block_row(k), rows = block_rows(k);
+      const bool live = (row & ~31) < rows;
+      // l of both groups, through the first KiB of the lane's Q, which no MMA reads any more
+      // (with alternating lanes once the other lane is done too)
       if (alt && !pair_sync()) return false;
-      const bool noted = wt.words[W_PFLAG + (seg & 1)] != 0;
-      const bool whole = k.lo == 0 && k.hi == k.nt;
-      const int slot = 2 * block + (k.lo == 0);
-      const uint32_t oa = tmem + C::O0 + lane * C::OSTEP;
+      if (live) {
+        const uint32_t xl = smem + C::OFF_Q + lane() * C::QBYTES + r() * 4;
+        stsf(xl + half() * 512, l);
+        if (!row_sync()) return false;
+        l += ldsf(xl + (half() ^ 1) * 512);
+      }
+      const bool noted = wt.word(W_PFLAG) != 0;
+      const bool whole = k.lo() == 0 && k.hi() == k.nt();
+      const int slot = 2 * block + (k.lo() == 0);
       float inv = 0.0f;
       int64_t at = 0;
       // With alternating lanes, lane 1's accumulator goes through shared memory to lane
-      // 0, 32 columns at a time, with its rows' m and l.
-      const bool pass = alt && k.hi - k.lo > 1;
-      float* xm = stage + 32 * 128;
+      // 0, 16 columns of each half at a time, with its rows' m and l.
+      const bool pass = alt && k.hi() - k.lo() > 1;
       float f0 = 1.0f, f1 = 0.0f;
       if (pass) {
-        if (lane == 1 && warp_live) {
-          xm[r] = m;
-          xm[128 + r] = l;
+        const uint32_t x1 = smem + C::OFF_MAX + (C::LANES - 1) * 1024 + r() * 4;
+        if (lane() == 1 && half() == 0 && live) {
+          stsf(x1, m);
+          stsf(x1 + 512, l);
         }
         if (!pair_sync()) return false;
-        const float m1 = xm[r], l1 = xm[128 + r], mm = fmaxf(m, m1), c = a.scale_log2;
-        if (lane == 0) {
+        if (lane() == 0) {
+          const float m1 = ldsf(x1), l1 = ldsf(x1 + 512), mm = fmaxf(m, m1);
           // a lane that saw nothing has weight zero (NaN scores stay NaN through l)
-          f0 = m == -INFINITY ? 0.0f : ptx::ex2_ftz((m - mm) * c);
-          f1 = m1 == -INFINITY ? 0.0f : ptx::ex2_ftz((m1 - mm) * c);
+          f0 = m == -INFINITY ? 0.0f : ptx::ex2_ftz((m - mm) * a.scale_log2);
+          f1 = m1 == -INFINITY ? 0.0f : ptx::ex2_ftz((m1 - mm) * a.scale_log2);
           if (l != l) f0 = l;
           if (l1 != l1) f1 = l1;
           l = l * f0 + l1 * f1;
           m = mm;
         }
       }
-      const bool mine = row < rows && !(alt && lane == 1);
+      const bool mine = row < rows && !(alt && lane() == 1);
       if (mine) {
-        at = out_at(k, row);
+        at = row_at(k, row);
         if (whole)
           inv = inverse(l);
-        else
+        else if (half() == 0)
           __stcg(a.ml_part + (int64_t)slot * C::QB + row, make_float2(m, l));
       }
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float o[32];
-        if (warp_live && any) {
-          tc5::ld32(oa + c0, reinterpret_cast<uint32_t*>(o));
+      for (int c0 = 0; c0 < C::HD; c0 += 16) {
+        float o[16];
+        if (live && any) {
+          tc5::ld16(tmem + C::O0 + lane() * C::OSTEP + half() * C::HD + c0, reinterpret_cast<uint32_t*>(o));
           tc5::wait_ld();
-          tc5::pin32(reinterpret_cast<uint32_t*>(o));
+          tc5::pin16(reinterpret_cast<uint32_t*>(o));
         }
         if (pass) {
-          if (lane == 1 && warp_live) {
+          const uint32_t st = smem + C::OFF_STAGE + half() * (16 * 128 * 4) + r() * 4;
+          if (lane() == 1 && live) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) stage[j * 128 + r] = o[j];
+            for (int j = 0; j < 16; ++j) stsf(st + j * 512, o[j]);
           }
           if (!pair_sync()) return false;
-          if (lane == 0 && warp_live) {
+          if (lane() == 0 && live) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + stage[j * 128 + r] * f1;
+            for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + ldsf(st + j * 512) * f1;
           }
           if (!pair_sync()) return false;
         }
+        const int col = half() * C::HD + c0;
         if (mine && whole) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 16) store16(o + j, inv, at + c0 + j);
+          store16(o, inv, at + col);
         } else if (mine) {
-          float4* dst = a.o_part + ((int64_t)slot * (D / 4) + c0 / 4) * C::QB + row;
+          float4* dst = a.o_part + ((int64_t)slot * (D / 4) + col / 4) * C::QB + row;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 4; ++j)
             __stcg(dst + j * C::QB, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         }
         __syncwarp();
       }
-      if (noted && mine) notes(lim, whole, at, slot, row);
-      // the notes have been read: clean them for the segment after next
       if (noted) {
+        if (mine) {
+          const int lim = seen_of(a, k.n(), k.ns() + k.npk() + k.nres(), token_of(a, k.qb() * C::QB + row));
+          notes(lim, whole, at, slot, row);
+        }
+        // the notes have been read: clean them
         if (!pair_sync()) return false;
-        for (int i = lane * 128 + r; i < 3 * D; i += C::SMT) poison[(seg & 1) * 3 * D + i] = 0x7fffffff;
-        if (lane * 128 + r == 0) wt.words[W_PFLAG + (seg & 1)] = 0;
+        for (int i = threadIdx.x; i < 3 * D; i += C::SMW * 32) sts(smem + C::OFF_POISON + 4 * i, 0x7fffffff);
+        if (threadIdx.x == 0) wt.set_word(W_PFLAG, 0);
         if (!pair_sync()) return false;
       }
       tc5::fence_before();
-      wt.arrive_warp(B_EPI + (seg & 1));
-      ++seg;
+      __threadfence_block();
+      __syncwarp();
+      if ((r() & 31) == 0)
+        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(wt.bars + 4 * W_EPI) : "memory");
 
       if (!whole) {
         __threadfence();
         if (!pair_sync()) return false;
-        if (lane * 128 + r == 0) wt.words[W_TICKET] = atomicAdd(a.tickets + k.first_b, 1u);
+        if (threadIdx.x == 0) wt.set_word(W_TICKET, atomicAdd(a.tickets + k.first_b(), 1u));
         if (!pair_sync()) return false;
-        if (wt.words[W_TICKET] == (uint32_t)(k.last_b - k.first_b)) {
+        if (wt.word(W_TICKET) == (uint32_t)(k.last_b() - k.first_b())) {
           __threadfence();
           join(k);
-          if (lane * 128 + r == 0) a.tickets[k.first_b] = 0;
+          if (threadIdx.x == 0) a.tickets[k.first_b()] = 0;
         }
       }
-      wt.arrive_warp(B_SEGEMPTY + at_seg.i % kSegs);
-      if (!more) return true;
-      at_seg = after;
-      // with alternating lanes: Q goes where the accumulator passed, after all have read it
-      if (alt) load_q(at_seg.get(ring));
+      wt.arrive_warp(B_SEGEMPTY + at_seg % kSegs);
+      ++at_seg;
+      if (!wait_seg()) return false;
+      if (ref().b() < 0) return true;
+      // Q goes where l and the accumulator passed: after all have read them
+      if (!pair_sync()) return false;
+      load_q();
     }
   }
 };
@@ -1111,9 +1198,13 @@ struct Soft {
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkAttnArgs a) {
   using C = Cfg<D, BITS>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw;
   const uint32_t smem = ptx::smem_u32(base);
+  if (smem & 1023u) {  // the swizzles count on it (a block without static shared memory has it)
+    set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
+    return;
+  }
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(base + C::OFF_BAR);
   volatile int64_t* wide = reinterpret_cast<volatile int64_t*>(base + C::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lid = tid & 31;
@@ -1160,17 +1251,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   if (tid == 0) {
     auto init = [&](int i, uint32_t n) { ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n); };
     for (int i = 0; i < 2; ++i) {
-      init(B_QFULL + i, 4);
+      init(B_QFULL + i, 8);
       init(B_SFULL + i, 1 + (a.fault && blockIdx.x == 0 ? 1 : 0));
-      init(B_PREADY + i, 4);
+      init(B_PREADY + i, 8);
       init(B_ODONE + i, 1);
-      init(B_EPI + i, 4 * C::LANES);
     }
+    for (int i = 0; i < 8; ++i) init(B_MAX + i, 2);
     for (int i = 0; i < kSegs; ++i) {
       init(B_SEGFULL + i, 1);
-      init(B_SEGEMPTY + i, 4 * C::LANES + 4 + 1);
+      init(B_SEGEMPTY + i, C::SMW + 4 + 1);
     }
-    init(B_PAIR, 4 * C::LANES);
+    init(B_PAIR, C::SMW);
     init(B_DRAIN, 1);
     for (int i = 0; i < C::ST; ++i) {
       init(B_KFULL + i, 4);
@@ -1179,11 +1270,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       init(B_VEMPTY + i, 1);
     }
     words[W_ABORT] = 0;
-    words[W_PFLAG] = words[W_PFLAG + 1] = 0;
+    words[W_PFLAG] = words[W_EPI] = 0;
     ptx::fence_mbar_init();
   }
   int* poison = reinterpret_cast<int*>(base + C::OFF_POISON);
-  for (int i = tid; i < 2 * 3 * D; i += kThreads) poison[i] = 0x7fffffff;
+  for (int i = tid; i < 3 * D; i += kThreads) poison[i] = 0x7fffffff;
   __syncthreads();
   if (warp == 0) {
     // the query block that holds x0, 32 at a time
@@ -1214,39 +1305,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       at += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
-  if (warp == 12) tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
+  if (warp == 20) tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
   const uint32_t tmem = words[W_TMEM];
-  const Waits wt = {smem + C::OFF_BAR, words, a.err_word, a.wait_limit_us};
+  const Waits wt = {a, smem + C::OFF_BAR};
   Seg* ring = reinterpret_cast<Seg*>(base + C::OFF_SEG);
   const int sb = words[W_STARTB], sq = words[W_STARTQ];
   const int64_t sbase = wide[W_BASE / 2 + 1];
 
-  // Registers: 128 a thread at launch (65536 in all) = 256 x 184 + 128 x 96 + 128 x 48.
-  if (warp < 8) {
-    tc5::regs_inc<184>();
-    if (warp < 4 * C::LANES) {
-      Soft<D, BITS> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21), poison,
-                            reinterpret_cast<float*>(base + C::OFF_STAGE), ring,
-                            warp >> 2, tid & 127, 0, 0, 0, 0};
+  // Registers: 80 a thread at launch (61440 in all) = 512 x 88 + 128 x 88 + 128 x 40.
+  if (warp < 16) {
+    tc5::regs_inc<88>();
+    if (warp < C::SMW) {
+      Soft<D, BITS> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21), 0, 0, 0};
       soft.run(blockIdx.x);
     }
-  } else if (warp < 12) {
-    tc5::regs_dec<96>();
-    Deq<D, BITS> deq = {a, wt, smem, poison, ring, tid - 256, 0};
+  } else if (warp < 20) {
+    tc5::regs_inc<88>();
+    Deq<D, BITS> deq = {a, wt, smem, poison, ring, tid - 512, 0};
     deq.run();
   } else {
-    tc5::regs_dec<48>();
-    if (tid == 12 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
-    if (tid == 13 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
+    tc5::regs_dec<40>();
+    if (tid == 20 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
+    if (tid == 21 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     __syncwarp();
   }
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  if (warp == 12) tc5::dealloc(tmem, 512);
+  if (warp == 20) tc5::dealloc(tmem, 512);
 }
 
 template <int D, int BITS>
@@ -1257,7 +1346,7 @@ cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   cudaError_t e = cudaFuncGetAttributes(&at, kernel);
   if (e != cudaSuccess) return e;
   // the warps' shares (setmaxnreg) come out of what the block is launched with
-  if (at.numRegs != 65536 / kThreads) return cudaErrorInvalidConfiguration;
+  if (at.numRegs != 80) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, Cfg<D, BITS>::SMEM, st>>>(a);
