@@ -3,24 +3,30 @@
 //
 // The mathematics.  The query rows of one (sequence, KV head) are its run's tokens times
 // the gq heads that share the KV head, row = token * gq + head: one pass over K and V
-// serves them all.  For a tile of tokens S = Q K^T, P = exp2(S c - m c) with the row's
+// serves them all.  For a tile of 64 tokens S = Q K^T, P = exp2(S c - m c) with the row's
 // reference maximum m, O += P V, l += sum P; c = log2(e) / sqrt(d).  m follows the
 // running maximum lazily: it moves (and O, l are rescaled) only when the maximum has
 // passed it by 2^8, so weights stay below 256 and the sums lose nothing in fp32.
 // Roundings: the dequantized keys and values min + code * scale are rounded to fp16 once
 // (operands of the MMA), the weights P to fp16 once; scores, m, l and O are fp32.
 //
-// A block (one per SM, persistent) has 24 warps:
+// A block (one per SM, persistent) has 28 warps:
 //   0-15   softmax: S from TMEM, P back to TMEM (it takes S's place and is the A operand
 //          of the second MMA), the epilogue.  Four groups of four warps: two for each of
-//          the block's two accumulators (lanes 0 and 1), each with half of the tile's
-//          tokens and half of O's columns, a thread per query row.  (One group per
-//          accumulator left the chain S -> P -> next S as the bound: 42 % of the issue
-//          slots used.)
-//   16-19  dequantize: a row of codes comes by cp.async into a ring that is private to
-//          its thread (no barrier), becomes fp16 in registers and goes to shared memory
-//          in the MMA's 128-byte swizzle, K as the K-major and V as the MN-major B operand.
-//   20     issues the MMAs; 21 works out the segments.
+//          the block's two accumulators (lanes 0 and 1), which take its tiles in turns; a
+//          thread per query row.
+//   16-23  dequantize, four warps the keys and four the values: a piece of a row of codes
+//          comes by cp.async into a ring that is private to its thread (no barrier),
+//          becomes fp16 in registers and goes to shared memory in the MMA's swizzle, K as
+//          the K-major and V as the MN-major B operand.
+//   24, 25 issue the MMAs, one thread for each lane; 26 works out the segments.
+// What the shape answers to (head_dim 128): a tile's chain S -> P -> PV -> next S takes
+// longer than its MMAs, so each lane has two S buffers and the next S is made while the
+// softmax works on this one.  TMEM (2 lanes x 2 x 64 columns of S, 2 x 128 of O) then
+// holds tiles of 64 tokens; their QK^T runs at 0.6 of the rate of 128 (measured 861
+// against 520 cycles for 128 x 128 x 128), which the overlap outweighs.  An MMA takes its
+// issuer about 55 cycles and a commit 85 (measured), hence a thread for each lane.
+//
 // A unit of work is (sequence, block of query rows, KV head).  With more than 128 rows in
 // the block the two lanes are its two halves and share each tile; with fewer they take
 // alternate tiles of the same rows and are joined at the end, so that the softmax of one
@@ -78,14 +84,15 @@ __host__ __device__ constexpr int chunk_rows(int d) { return d == 256 ? 128 : 25
 
 namespace chunk {
 
-constexpr int kThreads = 768;
-constexpr int kDeqThreads = 128;
+constexpr int kThreads = 896;
+constexpr int kDeqThreads = 128;  // of the keys, and of the values
+constexpr int kTile = 64;         // tokens of a tile
 
 template <int D, int BITS>
 struct Cfg {
   static constexpr int LANES = D == 256 ? 1 : 2;    // accumulators
   static constexpr int QB = chunk_rows(D);
-  static constexpr int TN = D == 256 ? 64 : 128;    // tokens of a tile
+  static constexpr int TN = kTile;
   static constexpr int G = D / 32;                  // groups of a row
   static constexpr int PW = D < 64 ? D : 64;        // elements of a panel's row
   static constexpr int RB = PW * 2;                 // bytes of it
@@ -94,17 +101,16 @@ struct Cfg {
   static constexpr int KP = TN * RB;                // of a panel of K or V
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int KBYTES = TN * D * 2;
-  static constexpr int ST = D <= 64 ? 4 : 2;        // K and V stages
-  static constexpr int HC = TN / 2;                 // a softmax group's columns of S
-  static constexpr int HD = D / 2;                  // ... and of O
-  static constexpr int TPR = TN == 64 ? 2 : 1;      // dequantizing threads of a row
+  static constexpr int ST = D == 256 ? 2 : 4;       // K and V stages
+  static constexpr int HD = D / 2;                  // a softmax group's columns of O
+  static constexpr int TPR = G > 1 ? 2 : 1;         // dequantizing threads of a row
   static constexpr int GPT = G / TPR;               // groups of each
   static constexpr int CB = 4 * BITS;               // code bytes of a group
   static constexpr int TB = GPT * CB;               // code bytes of a thread, contiguous
   static constexpr int UN = (TB + 15) / 16;         // 16-byte units of them in the ring
   static constexpr int PB = GPT * 4;                // param bytes of a thread
   static constexpr int RAWB = kDeqThreads * (UN * 16 + PB);
-  static constexpr int RAWN = D == 256 ? 2 : D == 128 ? 3 : 6;  // half tiles of the ring
+  static constexpr int RAWN = D == 256 ? 1 : D == 128 ? 3 : 6;  // tiles of the ring, of keys and of values
   static constexpr int SMW = 8 * LANES;             // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
@@ -116,13 +122,14 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + ST * KBYTES;
   static constexpr int OFF_RAW = OFF_V + ST * KBYTES;
   // where lane 1's accumulator passes to lane 0: 16 columns of 128 rows of each half.  Lane
-  // 1's Q (but for its first KiB) is free then, and large enough from head_dim 128 on
+  // 1's Q (but for its first 2 KiB) is free then, and large enough from head_dim 128 on
   static constexpr int STAGE = 2 * 16 * 128 * 4;
-  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES + 1024 : OFF_RAW + RAWN * RAWB;
-  static constexpr int OFF_POISON = OFF_RAW + RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // int [3][D]
-  static constexpr int OFF_MAX = OFF_POISON + 3 * D * 4;        // float [LANES][2][128]
-  static constexpr int OFF_BAR = OFF_MAX + LANES * 1024;
-  static constexpr int OFF_SEG = OFF_BAR + 512;                 // Seg [kSegs]
+  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES + 2048 : OFF_RAW + 2 * RAWN * RAWB;
+  static constexpr int OFF_MAX = OFF_RAW + 2 * RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // float [LANES][2][128]
+  static_assert(OFF_MAX % 1024 == 0, "a thread finds the other group's value by one bit of the address");
+  static constexpr int OFF_POISON = OFF_MAX + LANES * 1024;     // int [3][D]
+  static constexpr int OFF_BAR = OFF_POISON + 3 * D * 4;
+  static constexpr int OFF_SEG = OFF_BAR + 640;                 // Seg [kSegs]
   static constexpr int SMEM = OFF_SEG + 512;
 };
 
@@ -137,10 +144,13 @@ struct alignas(16) Seg {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_PAIR = 8, B_DRAIN = 9, B_KFULL = 10,
-       B_KEMPTY = 14, B_VFULL = 18, B_VEMPTY = 22, B_SEGFULL = 26, B_SEGEMPTY = 34, B_MAX = 42, B_COUNT = 50 };
-enum { W_TMEM = 100, W_ABORT = 101, W_PFLAG = 102, W_EPI = 103, W_TICKET = 104, W_STARTB = 105,
-       W_STARTQ = 106, W_BASE = 108 /* int64 [2] */ };
+// Of two: of each lane; S and P: of each lane and S buffer; REF: of each lane, 32 rows and
+// S buffer; free stages: of each stage and lane.
+enum { B_QFULL = 0, B_ODONE = 2, B_PVDONE = 4, B_DRAIN = 6, B_SFULL = 8, B_PREADY = 12, B_REF = 16,
+       B_KFULL = 32, B_VFULL = 36, B_KEMPTY = 40, B_VEMPTY = 48, B_SEGFULL = 56, B_SEGEMPTY = 64, B_PAIR = 72,
+       B_COUNT = 73 };
+enum { W_TMEM = 146, W_ABORT = 147, W_PFLAG = 148, W_EPI = 149, W_TICKET = 150, W_STARTB = 151,
+       W_STARTQ = 152, W_BASE = 154 /* int64 [2] */ };
 
 __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   uint32_t v;
@@ -181,8 +191,7 @@ struct Waits {
     set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
     return true;
   }
-  __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-    const uint32_t b = bar(i);
+  __device__ __forceinline__ bool wait_at(uint32_t b, uint32_t parity) const {
     if (ptx::mbar_try_wait(b, parity)) return true;
     const uint32_t t0 = timer_lo();
 #pragma unroll 1
@@ -190,13 +199,18 @@ struct Waits {
       if ((k & 63u) == 0 && late(t0)) return false;
     return true;
   }
+  __device__ __forceinline__ bool wait(int i, uint32_t parity) const { return wait_at(bar(i), parity); }
   // a whole warp waits; the same answer for all its lanes
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait(i, parity));
+    return wait_warp_at(bar(i), parity);
   }
-  __device__ __forceinline__ void arrive_warp(int i) const {
+  __device__ __forceinline__ bool wait_warp_at(uint32_t b, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait_at(b, parity));
+  }
+  __device__ __forceinline__ void arrive_warp(int i) const { arrive_warp_at(bar(i)); }
+  static __device__ __forceinline__ void arrive_warp_at(uint32_t b) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar(i));
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(b);
   }
 };
 
@@ -430,9 +444,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-// What the dequantizing warps share.  Thread dt has row dt of a tile (head_dim 256: half
-// of row dt / 2): its codes are contiguous, and 8 neighbouring lanes store the same piece
-// of 8 rows, which the swizzle puts into 8 different banks' groups.
+// What four dequantizing warps share, those of the keys (w 0) or of the values (1).
+// Thread dt has part dt / 64 of row dt % 64 of a tile (head_dim 32: all of row dt, half of
+// the threads have none): its codes are contiguous, and 8 neighbouring lanes store the
+// same piece of 8 rows, which the swizzle puts into 8 different groups of banks.
 template <int D, int BITS>
 struct Deq {
   using C = Cfg<D, BITS>;
@@ -441,8 +456,13 @@ struct Deq {
   uint32_t smem;  // base of the block's shared memory
   int* poison;
   const Seg* ring;
-  int dt;         // thread of the warps that dequantize
+  int w;
+  int dt;         // thread of the four warps
   uint32_t seg;   // segments of the block so far
+
+  __device__ __forceinline__ int row() const { return dt % kTile; }
+  __device__ __forceinline__ int part() const { return dt / kTile; }
+  __device__ __forceinline__ bool has_row() const { return C::TPR == 2 || dt < kTile; }
 
   // Values that fp16 does not hold as finite ones take no part in the MMA: a weight of
   // zero would make them NaN in rows that do not see the token.  The first token of the
@@ -459,55 +479,72 @@ struct Deq {
     return true;
   }
 
-  // The cursor of the copies: a half tile of a segment.
+  // The cursor of the copies: a tile of a segment.
   struct Cursor {
-    SegReader at;
-    int tile = -1, w = 0, hi = 0, npt = 0, npk = 0, b = 0;
-    int64_t row0 = 0;  // contiguous: row of the head's token 0; paged: h * 32
+    SegReader seg;
+    int tile = -1, hi = 0, npt = 0;
+    int left = 0;              // packed tokens from the thread's row of the tile on
+    int64_t at = 0;            // contiguous: that row; paged: row of the head in a page
+    const int32_t* pages = nullptr;  // paged: the entry of the thread's row
+    int page = 0;              // ... and what it says, read a tile ahead
   };
 
-  // The thread's raw row of a half tile (keys, then values) into ring slot `slot`; a row
-  // that is not there becomes zero codes with zero params, which stand for zeros.
-  __device__ __forceinline__ void fetch(const Cursor& c, int slot) {
-    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
-    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
-    const int p = c.tile * C::TN + dt / C::TPR;
-    bool there = p < c.npk;
-    int64_t row = c.row0 + p;
+  __device__ __forceinline__ uint32_t raw_codes(int slot) const {
+    return smem + C::OFF_RAW + (w * C::RAWN + slot) * C::RAWB + dt * 16;
+  }
+  __device__ __forceinline__ uint32_t raw_params(int slot) const {
+    return smem + C::OFF_RAW + (w * C::RAWN + slot) * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+  }
+
+  // The thread's raw piece of a tile into ring slot `slot`; a row that is not there
+  // becomes zero codes with zero params, which stand for zeros.
+  __device__ __forceinline__ void fetch(Cursor& c, int slot) {
+    const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
+    bool there = c.left > 0 && has_row();
+    int64_t at = c.at;
     if (a.rm.paged && there) {
-      const int pg = a.rm.page_of(c.b, p / kPage);
-      there = pg >= 0 && pg < a.rm.npages;
+      there = c.page >= 0 && c.page < a.rm.npages;
       if (!there) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
-      row = (int64_t)pg * a.Hkv * kPage + c.row0 + p % kPage;
+      at += (int64_t)c.page * a.Hkv * kPage;
     }
     if (there) {
-      const uint8_t* src = a.codes[c.w] + row * (C::G * C::CB) + (dt % C::TPR) * C::TB;
+      const uint8_t* src = a.codes[w] + at * (C::G * C::CB) + part() * C::TB;
       constexpr int N = C::TB % 16 == 0 ? 16 : C::TB % 8 == 0 ? 8 : 4;
 #pragma unroll
       for (int i = 0; i < C::TB / N; ++i)
         cp_async<N>(dc + (i * N / 16) * (kDeqThreads * 16) + i * N % 16, src + i * N);
-      cp_async<C::PB>(dp, a.params[c.w] + row * C::G + (dt % C::TPR) * C::GPT);
+      cp_async<C::PB>(dp, a.params[w] + at * C::G + part() * C::GPT);
     } else {
 #pragma unroll
       for (int i = 0; i < C::UN; ++i) st_shared_v4(dc + i * (kDeqThreads * 16), make_uint4(0, 0, 0, 0));
 #pragma unroll
-      for (int i = 0; i < C::GPT; ++i) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dp + 4 * i), "r"(0) : "memory");
+      for (int i = 0; i < C::GPT; ++i) sts(dp + 4 * i, 0);
+    }
+    // on to the next tile
+    c.left -= C::TN;
+    if (a.rm.paged) {
+      c.pages += C::TN / kPage;
+      if (c.left > 0) c.page = __ldg(c.pages);
+    } else {
+      c.at += C::TN;
     }
   }
 
   // Shared address of the thread's row in a tile at dst, with the row's swizzle in its
-  // low bits: piece c of panel p is at (this ^ (c << 4)) + p * KP.
+  // low bits: piece c of the thread's panel p is at (this ^ (c << 4)) + p * KP (a thread
+  // with one group has half a panel's row, pieces 4 part .. 4 part + 3).
   __device__ __forceinline__ uint32_t row_addr(uint32_t dst) const {
-    const int r = dt / C::TPR;
-    return dst + (dt % C::TPR) * (C::GPT / 2) * C::KP + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
+    const int r = row();
+    const uint32_t at = dst + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
+    return C::GPT == 1 ? at ^ (part() << 6) : at + part() * (C::GPT / 2) * C::KP;
   }
-  __device__ __forceinline__ int column(int g, int c) const { return ((dt % C::TPR) * C::GPT + g) * 32 + c * 8; }
+  __device__ __forceinline__ int column(int g, int c) const { return (part() * C::GPT + g) * 32 + c * 8; }
 
-  // A fetched half tile as fp16 at `dst`.  first: logical place of the tile's first token.
-  __device__ __forceinline__ bool packed_tile(int first, int w, int slot, uint32_t dst) {
+  // A fetched tile as fp16 at `dst`.  first: logical place of the tile's first token.
+  __device__ __forceinline__ bool packed_tile(int first, int slot, uint32_t dst) {
     constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
-    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
-    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+    const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
+    if (!has_row()) return true;
     uint32_t raw[C::UN * 4], prm[C::GPT];
 #pragma unroll
     for (int i = 0; i < C::UN; ++i) {
@@ -515,8 +552,7 @@ struct Deq {
       raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i)
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(prm[i]) : "r"(dp + 4 * i) : "memory");
+    for (int i = 0; i < C::GPT; ++i) prm[i] = lds(dp + 4 * i);
     const uint32_t at = row_addr(dst);
     uint32_t rare = 0;
 #pragma unroll
@@ -542,8 +578,7 @@ struct Deq {
     for (int e = 0; e < 32 * C::GPT; ++e) {
       const int g = e >> 5;
       if (!((rare >> g) & 1u)) continue;
-      uint32_t pg;
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pg) : "r"(dp + 4 * g) : "memory");
+      const uint32_t pg = lds(dp + 4 * g);
       const uint32_t ea = (at ^ (((g & 1) * 4 + ((e >> 3) & 3)) << 4)) + (g / 2) * C::KP + 2 * (e & 7);
       unsigned short hv;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
@@ -552,7 +587,7 @@ struct Deq {
         hv = (hv & 0x8000u) | 0x7bffu;
       else if (w == 0)
         continue;
-      else if (note(column(g, 0) + (e & 31), first + dt / C::TPR, hv))
+      else if (note(column(g, 0) + (e & 31), first + row(), hv))
         hv = 0;
       else
         return false;
@@ -563,10 +598,10 @@ struct Deq {
 
   __device__ __forceinline__ int ring_slot(int j) const { return j < a.Nr ? j : j - a.Nr; }  // j < 2 Nr
 
-  // A half tile of fp16 tokens (sink, then window): rows f0 .. of their line.
-  __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, int w, uint32_t dst) {
+  // A tile of fp16 tokens (sink, then window): rows f0 .. of their line.
+  __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, uint32_t dst) {
     const int64_t bh = (int64_t)k.b * a.Hkv + k.h;
-    const int f = f0 + dt / C::TPR, n = k.ns + k.nres;
+    const int f = f0 + row(), n = k.ns + k.nres;
     const __half* src = a.q;  // (not read)
     if (f < k.ns)
       src = a.sink[w] + (bh * a.Ns + f) * D;
@@ -574,6 +609,7 @@ struct Deq {
       src = a.res[w] + (bh * a.Nr + ring_slot(k.head + f - k.ns)) * D;
     if (f < n) src += column(0, 0);
     const uint32_t at = row_addr(dst);
+    if (!has_row()) return true;
 #pragma unroll
     for (int i = 0; i < 4 * C::GPT; ++i)
       ptx::cp_async_16((at ^ ((i & 7) << 4)) + (i / 8) * C::KP, src + (f < n ? i * 8 : 0), f < n ? 16 : 0);
@@ -609,30 +645,38 @@ struct Deq {
     SegReader k;
     Cursor c;
     bool ok = true, more = true;
-    // the next half tile of the line into its ring slot
+    // the next tile of the line into its ring slot
     auto fetch_next = [&](int slot) {
       if (more && c.tile < 0) {
-        ok = ok && __all_sync(0xffffffffu, c.at.wait(wt));
-        const Seg& s = c.at.get(ring);
+        ok = ok && __all_sync(0xffffffffu, c.seg.wait(wt));
+        const Seg& s = c.seg.get(ring);
         more = ok && s.b >= 0;
         if (more) {
-          c.tile = s.lo, c.hi = s.hi, c.npt = s.npt, c.npk = s.npk, c.b = s.b;
-          c.row0 = a.rm.paged ? (int64_t)s.h * kPage : ((int64_t)s.b * a.Hkv + s.h) * a.cap;
+          c.tile = s.lo, c.hi = s.hi, c.npt = s.npt;
+          const int p = s.lo * C::TN + row();
+          c.left = s.npk - p;
+          if (a.rm.paged) {
+            c.at = (int64_t)s.h * kPage + p % kPage;
+            c.pages = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + p / kPage;
+            if (c.left > 0) c.page = __ldg(c.pages);
+          } else {
+            c.at = ((int64_t)s.b * a.Hkv + s.h) * a.cap + p;
+          }
         }
       }
       if (more) {
         if (c.tile < c.npt) fetch(c, slot);
-        c.w ^= 1;
-        if (c.w == 0 && ++c.tile == c.hi) {
-          ++c.at.i;
+        if (++c.tile == c.hi) {
+          ++c.seg.i;
           c.tile = -1;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint32_t kv = 0;  // tiles so far
+    uint32_t kv = 0;             // tiles so far
+    uint32_t used = 0, par = 0;  // by stage and lane: the lane has the stage; parity of its release
     int slot = 0;
-    // RAWN - 1 half tiles ahead: a free slot is filled before the oldest is taken
+    // RAWN - 1 tiles ahead: a free slot is filled before the oldest is taken
 #pragma unroll 1
     for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
     for (; ok; ++k.i, ++seg) {
@@ -640,26 +684,34 @@ struct Deq {
       if (!ok) break;
       const Seg& s = k.get(ring);
       if (s.b < 0) break;
-      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns;
-      for (int h = 2 * lo; h < 2 * hi; ++h) {
+      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns, alt = s.alt;
+      for (int t = lo; t < hi; ++t, ++kv) {
         fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
-        const int t = h >> 1, w = h & 1;
         const int stage = kv % C::ST;
         const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
-        ok = ok && wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + stage, ((kv / C::ST) & 1) ^ 1);
+        // the lanes that had the stage before have read it
+#pragma unroll
+        for (int l = 0; l < C::LANES; ++l) {
+          const int bit = 2 * stage + l;
+          if (ok && ((used >> bit) & 1u)) {
+            ok = wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + bit, (par >> bit) & 1u);
+            par ^= 1u << bit;
+          }
+        }
         if (!ok) break;
+        used &= ~(3u << (2 * stage));
+        used |= (alt ? 1u << ((t - lo) & 1) : C::LANES == 2 ? 3u : 1u) << (2 * stage);
         if (t < npt) {
           asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-          ok = packed_tile(ns + t * C::TN, w, slot, dst);
+          ok = packed_tile(ns + t * C::TN, slot, dst);
         } else {
-          ok = f16_tile(s, (t - npt) * C::TN, w, dst);
+          ok = f16_tile(s, (t - npt) * C::TN, dst);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::fence_proxy_async_shared();
         wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
         if (++slot == C::RAWN) slot = 0;
-        kv += w;
       }
       wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
     }
@@ -671,74 +723,70 @@ struct Deq {
 
 template <int D, int BITS>
 __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt, uint32_t smem, uint32_t tmem,
-                                         const Seg* ring) {
+                                         const Seg* ring, int lane) {
   using C = Cfg<D, BITS>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
+  const uint32_t s_at = tmem + C::S0 + lane * 2 * C::TN, o_at = tmem + C::O0 + lane * C::OSTEP;
   SegReader k;
-  uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
-  uint32_t kv = 0;                          // tiles so far
+  uint32_t qn = 0;           // phases of the lane's barrier of Q
+  uint32_t nqk = 0, npv = 0; // the lane's QK^T and PV so far: S buffers take turns
+  uint32_t kv = 0;           // tiles so far
   bool ok = true;
   for (;; ++k.i) {
     if (!k.wait(wt) || k.get(ring).b < 0) break;
     const bool alt = k.get(ring).alt;
     const int n = k.get(ring).hi - k.get(ring).lo;
     ptx::mbar_arrive(wt.bar(B_SEGEMPTY + k.i % kSegs));
-    const int U = C::LANES == 2 && !alt ? 2 * n : n;
-    ok = wt.wait(B_QFULL, qn[0]++ & 1);
-    if (ok && C::LANES == 2 && !alt) ok = wt.wait(B_QFULL + 1, qn[1]++ & 1);
-    if (!ok) break;
-    auto tile = [&](int u) { return C::LANES == 2 && !alt ? u >> 1 : u; };
-    auto lane_of = [&](int u) { return C::LANES == 2 ? u & 1 : 0; };
-    // the step's tile is read by no later step
-    auto releases = [&](int u) { return C::LANES == 1 || alt || (u & 1); };
-    auto qk = [&](int u) -> bool {
-      const uint32_t t = kv + tile(u);
-      const int stage = t % C::ST, lane = lane_of(u);
-      if ((C::LANES == 1 || alt || lane == 0) && !wt.wait(B_KFULL + stage, (t / C::ST) & 1)) return false;
+    // the lane's tiles: all, or every second one (with Q of lane 0)
+    const int step = alt ? 2 : 1, t0 = alt ? lane : 0;
+    // (the barrier of lane 1 completes in the segments that have tiles for it, and is
+    // waited on in just these: no phase is passed over)
+    if (t0 < n) ok = wt.wait(B_QFULL + lane, qn++ & 1);
+    const uint64_t qd =
+        tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
+    auto qk = [&](int t) -> bool {
+      const int stage = (kv + t) % C::ST, buf = nqk & 1;
+      if (!wt.wait(B_KFULL + stage, ((kv + t) / C::ST) & 1)) return false;
       tc5::fence_after();
-      const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
       const uint64_t kd = tc5::smem_desc(smem + C::OFF_K + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         constexpr int PW = C::PW;
         const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
-        tc5::mma_ss(tmem + C::S0 + lane * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+        tc5::mma_ss(s_at + buf * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
                     kIdescQK, j > 0);
       }
-      tc5::commit(wt.bar(B_SFULL + lane));
-      if (releases(u)) tc5::commit(wt.bar(B_KEMPTY + stage));
+      tc5::commit(wt.bar(B_SFULL + 2 * lane + buf));
+      tc5::commit(wt.bar(B_KEMPTY + 2 * stage + lane));
+      ++nqk;
       return true;
     };
-    for (int u = 0; ok && u < C::LANES && u < U; ++u) ok = qk(u);
-    for (int u = 0; ok && u < U; ++u) {
-      const uint32_t t = kv + tile(u);
-      const int stage = t % C::ST, lane = lane_of(u);
-      ok = wt.wait(B_PREADY + lane, pn[lane]++ & 1);
-      if (ok && (C::LANES == 1 || alt || lane == 0)) ok = wt.wait(B_VFULL + stage, (t / C::ST) & 1);
+    for (int t = t0; ok && t < n && t < t0 + 2 * step; t += step) ok = qk(t);
+    for (int t = t0; ok && t < n; t += step) {
+      const int stage = (kv + t) % C::ST, buf = npv & 1;
+      const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+      ok = wt.wait(B_VFULL + stage, ((kv + t) / C::ST) & 1) && wt.wait(B_PREADY + 2 * lane + buf, (npv >> 1) & 1);
       if (!ok) break;
       tc5::fence_after();
-      const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
-      const bool acc = u >= C::LANES;  // the lane's first tile of the segment starts O
 #pragma unroll
       for (int j = 0; j < C::TN / 16; ++j) {
-        // P of each half of the tokens lies at the start of that half of S
-        const int col = j * 16 / C::HC * C::HC + (j * 16 % C::HC) / 2;
-        tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + col,
-                    vd + ((j * 16 * C::RB) >> 4), kIdescPV, acc || j > 0);
+        // the lane's first tile of the segment starts O
+        tc5::mma_ts(o_at, s_at + buf * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, t > t0 || j > 0);
       }
-      if (releases(u)) tc5::commit(wt.bar(B_VEMPTY + stage));
-      if (u + C::LANES < U)
-        ok = qk(u + C::LANES);  // after PV(u) in the tensor cores' order: S may take P's place
-      else
-        tc5::commit(wt.bar(B_ODONE + lane));
+      tc5::commit(wt.bar(B_PVDONE + lane));
+      if (t + step >= n) tc5::commit(wt.bar(B_ODONE + lane));
+      // into the buffer of this tile's P: after PV in the tensor cores' order
+      if (t + 2 * step < n) ok = qk(t + 2 * step);
+      tc5::commit(wt.bar(B_VEMPTY + 2 * stage + lane));
+      ++npv;
     }
     if (!ok) break;
     kv += n;
   }
   // nothing of this thread's is in flight when TMEM is freed
-  tc5::commit(wt.bar(B_DRAIN));
-  wt.wait(B_DRAIN, 0);
+  tc5::commit(wt.bar(B_DRAIN + lane));
+  wt.wait(B_DRAIN + lane, 0);
 }
 
 // ------------------------------------------------------------------ softmax ---
@@ -756,14 +804,18 @@ struct Soft {
   const Waits& wt;
   const uint32_t smem, tmem;  // tmem: with the warp's lanes
   uint32_t phases;            // parity bits of the barriers that the thread waits on
-  uint32_t at_seg, seg;       // place in the ring of segments, segments so far
+  const uint32_t tid;
+  const uint32_t s_tm;        // TMEM: the group's S buffer
+  const uint32_t ref_at;      // shared: the thread's reference maximum (^ 512: the other group's)
+  uint32_t at_seg;            // place in the ring of segments
+  uint32_t nt;                // tiles of the lane so far: its two groups take turns
 
-  enum { P_S = 0, P_O = 1, P_PAIR = 2, P_MAX = 3, P_STARTED = 4 };
+  enum { P_O = 1, P_PAIR = 2 };
 
-  // Accumulator, half of its columns, and row: by the thread.
-  static __device__ __forceinline__ int lane() { return threadIdx.x >> 8; }
-  static __device__ __forceinline__ int half() { return (threadIdx.x >> 7) & 1; }
-  static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
+  // Accumulator, group (and half of O's columns), and row: by the thread.
+  __device__ __forceinline__ int lane() const { return tid >> 8; }
+  __device__ __forceinline__ int half() const { return (tid >> 7) & 1; }
+  __device__ __forceinline__ int r() const { return tid & 127; }
 
   __device__ __forceinline__ bool wait(int bar, int bit) {
     const bool ok = wt.wait_warp(bar, (phases >> bit) & 1);
@@ -774,14 +826,6 @@ struct Soft {
     wt.arrive_warp(B_PAIR);
     return wait(B_PAIR, P_PAIR);
   }
-  // with the warp that has the same rows and the other half of the columns
-  __device__ __forceinline__ bool row_sync() {
-    const int b = B_MAX + lane() * 4 + (r() >> 5);
-    wt.arrive_warp(b);
-    return wait(b, P_MAX);
-  }
-  __device__ __forceinline__ uint32_t xmax() const { return smem + C::OFF_MAX + lane() * 1024; }
-
   // The current segment, read field by field.
   struct Ref {
     uint32_t at;
@@ -844,88 +888,97 @@ struct Soft {
     }
     ptx::fence_proxy_async_shared();
     wt.arrive_warp(B_QFULL + lane());
+    // with alternating lanes the rows are lane 1's too, if there is a tile for it
+    if (k.alt() && k.hi() - k.lo() > 1) wt.arrive_warp(B_QFULL + 1);
   }
 
-  // Hides what the row does not see of 32 tokens (a page: `bad` all of them); the largest
-  // score that is left.
-  static __device__ __forceinline__ float mask(float (&s)[32], int visible, uint32_t bad) {
-    const int v = bad ? 0 : visible;
-    float x = -INFINITY;
+  // The weights of 16 scores (the visible ones) against the reference (off = -m c), two to a
+  // register, and their sum on top of `sum`.
+  __device__ __forceinline__ void weights(float (&s)[16], uint32_t (&p)[8], uint64_t c2, uint64_t off2,
+                                          uint64_t& sum, bool masked, int visible) const {
+    if (masked) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      s[j] = j < v ? s[j] : -INFINITY;
-      x = fmaxf(x, s[j]);
+      for (int j = 0; j < 16; ++j) s[j] = j < visible ? s[j] : -INFINITY;
     }
-    return x;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
+      const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x))), e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
+      sum = add_f32x2(sum, pack_f32x2(e0, e1));
+      p[i / 2] = ptx::pack_h2(e0, e1);
+    }
   }
 
-  // One tile: the weights of the group's half of S's row into TMEM, m (the same in both
-  // groups) and l (each group's own) brought up to date.  visible: columns of the half
-  // that the row sees (a prefix); bad: pages of it left out.
-  __device__ __forceinline__ bool tile(int visible, uint32_t bad, float& m, float& l) {
-    const uint32_t sa = tmem + C::S0 + lane() * C::TN + half() * C::HC;
-    // 32 scores at a time, read again after the maximum is known: 64 at once and what
-    // else lives do not fit the registers, and the small L1 beside the tiles makes a
-    // spilled register a trip to L2
-    float s[32];
-    const bool masked = __any_sync(0xffffffffu, visible < C::HC) || bad;
-    float mine = -INFINITY;
+  // One tile, the lane's n-th: P in S's place, m and l brought up to date.  visible:
+  // tokens of the tile that the row sees (a prefix); bad: pages (halves) left out.
+  // S is read twice, for its maximum and for the weights: 64 scores at once do not fit the
+  // registers, and beside the tiles L1 is so small that a spilled register is a trip to
+  // L2.  The reference is the lane's: the group that has tile n takes it over from the
+  // other, which had n - 1, and passes it on before it works out its weights.
+  __device__ __forceinline__ bool tile(int visible, uint32_t bad, bool first, float& m, float& l) {
+    const bool masked = __any_sync(0xffffffffu, visible < C::TN) || bad;
+    float mt = -INFINITY;
 #pragma unroll
-    for (int h = C::HC - 32; h >= 0; h -= 32) {
-      float mx;
-      tc5::ld32_max(sa + h, reinterpret_cast<uint32_t*>(s), mx);
+    for (int h = 0; h < C::TN; h += 32) {
+      float s[32], mx;
+      tc5::ld32_max(s_tm + h, reinterpret_cast<uint32_t*>(s), mx);
       tc5::wait_ld();
       tc5::pin32(reinterpret_cast<uint32_t*>(s));
       asm volatile("" : "+f"(mx));
-      if (masked) mx = mask(s, visible - h, (bad >> (h / 32)) & 1u);
-      mine = fmaxf(mine, mx);
-    }
-    // the row's maximum: of this half and of the other group's
-    stsf(xmax() + half() * 512 + r() * 4, mine);
-    if (!row_sync()) return false;
-    const float mn = fmaxf(m, fmaxf(mine, ldsf(xmax() + (half() ^ 1) * 512 + r() * 4)));
-    const bool moves = (mn - m) * a.scale_log2 > 8.0f;
-    if (__any_sync(0xffffffffu, moves)) {
-      const float f = moves ? ptx::ex2_ftz((m - mn) * a.scale_log2) : 1.0f;
-      if (moves) m = mn;
-      l *= f;
-      if (phases & (1u << P_STARTED)) {
-        const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP + half() * C::HD;
-#pragma unroll 1
-        for (int i = 0; i < C::HD; i += 8) {
-          uint32_t o[8];
-          tc5::ld8(oa + i, o);
-          tc5::wait_ld();
-          tc5::pin8(o);
+      if (masked) {
+        const int v = (bad >> (h / 32)) & 1u ? 0 : visible - h;
+        mx = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tc5::st8(oa + i, o);
-        }
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, j < v ? s[j] : -INFINITY);
+      }
+      mt = fmaxf(mt, mx);
+    }
+    const uint32_t bar = wt.bar(B_REF) + (lane() * 4 + (r() >> 5)) * 16;
+    float was = -INFINITY;  // the lane's reference
+    if (!first) {
+      if (!wt.wait_warp_at(bar + 8 * (half() ^ 1), ((nt - 1) >> 1) & 1)) return false;
+      was = ldsf(ref_at ^ 512);
+    }
+    const bool moves = (mt - was) * a.scale_log2 > 8.0f;
+    const float mn = moves ? mt : was;
+    stsf(ref_at, mn);
+    wt.arrive_warp_at(bar + 8 * half());
+    if (__any_sync(0xffffffffu, moves) && !first) {
+      const float f = moves ? ptx::ex2_ftz((was - mn) * a.scale_log2) : 1.0f;
+      // O is still while the last tile's PV is done and this one's P is not there
+      if (!wt.wait_warp(B_PVDONE + lane(), (nt - 1) & 1)) return false;
+      tc5::fence_after();
+      const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP;
+#pragma unroll 1
+      for (int i = 0; i < D; i += 16) {
+        uint32_t o[16];
+        tc5::ld16(oa + i, o);
+        tc5::wait_ld();
+        tc5::pin16(o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+        tc5::st16(oa + i, o);
       }
     }
+    if (m != mn) l *= ptx::ex2_ftz((m - mn) * a.scale_log2);  // (m below mn)
+    m = mn;
     const float off = m == -INFINITY ? 0.0f : -m * a.scale_log2;
     const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
-    uint64_t sum2 = pack_f32x2(l, 0.0f);
+    uint64_t sum = pack_f32x2(l, 0.0f);
+    float s[2][16];
+    tc5::ld16(s_tm, reinterpret_cast<uint32_t*>(s[0]));
 #pragma unroll
-    for (int h = 0; h < C::HC; h += 32) {
-      if (h > 0) {
-        tc5::ld32(sa + h, reinterpret_cast<uint32_t*>(s));
-        tc5::wait_ld();
-        tc5::pin32(reinterpret_cast<uint32_t*>(s));
-        if (masked) mask(s, visible - h, (bad >> (h / 32)) & 1u);
-      }
-      uint32_t p[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
-        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
-        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
-        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
-        p[i / 2] = ptx::pack_h2(e0, e1);
-      }
-      tc5::st16(sa + h / 2, p);
+    for (int h = 0; h < C::TN; h += 16) {
+      float (&now)[16] = s[(h / 16) & 1];
+      uint32_t p[8];
+      tc5::wait_ld();
+      tc5::pin16(reinterpret_cast<uint32_t*>(now));
+      if (h + 16 < C::TN) tc5::ld16(s_tm + h + 16, reinterpret_cast<uint32_t*>(s[(h / 16 + 1) & 1]));
+      weights(now, p, c2, off2, sum, masked, (bad >> (h / 32)) & 1u ? 0 : visible - h);
+      // P's columns lie below those of the scores that are still to be read
+      tc5::st8(s_tm + h / 2, p);
     }
-    l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
+    l = __uint_as_float(lo_bits(sum)) + __uint_as_float(hi_bits(sum));
     tc5::wait_st();
     return true;
   }
@@ -981,7 +1034,7 @@ struct Soft {
   // at a time, all softmax threads.
   __device__ __forceinline__ void join(const Ref& k) const {
     const int rows = block_rows(k), first = k.first_b(), last = k.last_b();
-    for (int it = threadIdx.x; it < rows * (D / 16); it += C::SMW * 32) {
+    for (int it = tid; it < rows * (D / 16); it += C::SMW * 32) {
       const int cg = it / rows, row = it - cg * rows;
       float m = -INFINITY;
 #pragma unroll 4
@@ -1010,56 +1063,66 @@ struct Soft {
     }
   }
 
-  // The tiles of a segment: m and l of the row's columns.
-  __device__ __forceinline__ bool tiles(float& m, float& l) {
+  // The group's tiles of a segment: the reference m of the last of them and l.
+  __device__ __forceinline__ bool tiles(float& m, float& l, bool& any) {
     m = -INFINITY;
     l = 0.0f;
-    phases &= ~(1u << P_STARTED);
-    // packed tiles, then fp16 ones: t and its end, and the tokens that the row sees from t on
+    int t, end, npt, step, row;
+    bool live, mine;
+    {
+      const Ref k = ref();
+      row = block_row(k);
+      live = (row & ~31) < block_rows(k);
+      mine = row < block_rows(k);
+      step = k.alt() ? 2 : 1;
+      t = k.lo() + (k.alt() ? lane() : 0);
+      end = k.hi();
+      npt = k.npt();
+    }
+    any = t < end;
+    const int t0 = t;
+    const uint32_t nt0 = nt;
+    if ((nt & 1) != (uint32_t)half()) t += step, ++nt;
+    int visible = 0, left = 0;  // tokens that the row sees from t on; tiles to go with it
 #pragma unroll 1
-    for (int f16 = 0; f16 < 2; ++f16) {
-      int t, end, visible;
-      bool live;
-      {
+    for (; t < end; t += 2 * step, nt += 2) {
+      if (--left < 0) {
+        // the first packed tile, then the first fp16 one
         const Ref k = ref();
-        const int row = block_row(k), rows = block_rows(k), npt = k.npt(), alt = k.alt();
-        t = k.lo() + (alt ? lane() : 0);
-        // (the lane's first tile that is not packed)
-        if (f16 && t < npt) t += alt ? (npt - t + 1) & ~1 : npt - t;
-        end = f16 ? k.hi() : min(k.hi(), npt);
-        live = (row & ~31) < rows;
+        const bool f16 = t >= npt;
+        left = ((f16 ? end : min(npt, end)) - t - 1) / (2 * step);
         visible = 1 << 30;  // rows that are not there need no mask
-        if (row < rows) {
+        if (mine) {
           const int ns = k.ns(), npk = k.npk();
           const int lim = seen_of(a, k.n(), ns + npk + k.nres(), token_of(a, k.qb() * C::QB + row));
           visible = (f16 ? seen_f16(ns, npk, lim) + npt * C::TN : seen_packed(ns, npk, lim)) - t * C::TN;
-          visible -= half() * C::HC;
         }
+      } else if (mine) {
+        visible -= 2 * step * C::TN;
       }
-#pragma unroll 1
-      while (t < end) {
-        uint32_t bad = 0;
-        if (a.rm.paged && !f16) {
-          const Ref k = ref();
-          const int j = (t * C::TN + half() * C::HC) / kPage + (r() & 31);
-          bool out = false;
-          if ((r() & 31) < C::HC / kPage && j * kPage < k.npk()) {
-            const int pg = a.rm.page_of(k.b(), j);
-            out = pg < 0 || pg >= a.rm.npages;
-          }
-          bad = __ballot_sync(0xffffffffu, out);
+      uint32_t bad = 0;
+      if (a.rm.paged && t < npt) {
+        const Ref k = ref();
+        const int j = t * (C::TN / kPage) + (r() & 1);
+        bool out = false;
+        if ((r() & 31) < C::TN / kPage && j * kPage < k.npk()) {
+          const int pg = a.rm.page_of(k.b(), j);
+          out = pg < 0 || pg >= a.rm.npages;
         }
-        if (!wait(B_SFULL + lane(), P_S)) return false;
-        tc5::fence_after();
-        if (live && !tile(visible, bad, m, l)) return false;
-        tc5::fence_before();
-        wt.arrive_warp(B_PREADY + lane());
-        phases |= 1u << P_STARTED;
-        const int step = ref().alt() ? 2 : 1;
-        t += step;
-        if (visible < (1 << 29)) visible -= step * C::TN;
+        bad = __ballot_sync(0xffffffffu, out);
       }
+      const uint32_t bar = wt.bar(B_SFULL) + 16 * lane() + 8 * half();
+      if (!wt.wait_warp_at(bar, (nt >> 1) & 1)) return false;
+      tc5::fence_after();
+      if (live) {
+        if (!tile(visible, bad, t == t0, m, l)) return false;
+      } else {
+        wt.arrive_warp_at(wt.bar(B_REF) + (lane() * 4 + (r() >> 5)) * 16 + 8 * half());
+      }
+      tc5::fence_before();
+      wt.arrive_warp_at(bar + 8 * (B_PREADY - B_SFULL));
     }
+    nt = nt0 + (any ? (end - t0 + step - 1) / step : 0);
     return true;
   }
 
@@ -1069,8 +1132,8 @@ struct Soft {
     load_q();
     while (true) {
       float m, l;
-      if (!tiles(m, l)) return false;
-      const bool any = (phases >> P_STARTED) & 1;
+      bool any;
+      if (!tiles(m, l, any)) return false;
       if (any && !wait(B_ODONE + lane(), P_O)) return false;
       tc5::fence_after();
 
@@ -1078,14 +1141,19 @@ struct Soft {
       const bool alt = k.alt();
       const int row = block_row(k), rows = block_rows(k);
       const bool live = (row & ~31) < rows;
-      // l of both groups, through the first KiB of the lane's Q, which no MMA reads any more
-      // (with alternating lanes once the other lane is done too)
-      if (alt && !pair_sync()) return false;
-      if (live) {
-        const uint32_t xl = smem + C::OFF_Q + lane() * C::QBYTES + r() * 4;
-        stsf(xl + half() * 512, l);
-        if (!row_sync()) return false;
-        l += ldsf(xl + (half() ^ 1) * 512);
+      // m and l of both groups; l through the first KiB of the lane's Q, which no MMA reads
+      // once both lanes are done.  The lane's reference is the later one, the larger.
+      const uint32_t xl = smem + C::OFF_Q + lane() * C::QBYTES + r() * 4;
+      if (!pair_sync()) return false;
+      stsf(ref_at, m);
+      stsf(xl + half() * 512, l);
+      if (!pair_sync()) return false;
+      {
+        const float mo = ldsf(ref_at ^ 512), lo = ldsf(xl + (half() ^ 1) * 512), mm = fmaxf(m, mo);
+        const float fa = m == mm ? 1.0f : ptx::ex2_ftz((m - mm) * a.scale_log2);
+        const float fb = mo == mm ? 1.0f : ptx::ex2_ftz((mo - mm) * a.scale_log2);
+        l = l * fa + lo * fb;
+        m = mm;
       }
       const bool noted = wt.word(W_PFLAG) != 0;
       const bool whole = k.lo() == 0 && k.hi() == k.nt();
@@ -1097,7 +1165,7 @@ struct Soft {
       const bool pass = alt && k.hi() - k.lo() > 1;
       float f0 = 1.0f, f1 = 0.0f;
       if (pass) {
-        const uint32_t x1 = smem + C::OFF_MAX + (C::LANES - 1) * 1024 + r() * 4;
+        const uint32_t x1 = smem + C::OFF_Q + (C::LANES - 1) * C::QBYTES + 1024 + r() * 4;
         if (lane() == 1 && half() == 0 && live) {
           stsf(x1, m);
           stsf(x1 + 512, l);
@@ -1161,8 +1229,8 @@ struct Soft {
         }
         // the notes have been read: clean them
         if (!pair_sync()) return false;
-        for (int i = threadIdx.x; i < 3 * D; i += C::SMW * 32) sts(smem + C::OFF_POISON + 4 * i, 0x7fffffff);
-        if (threadIdx.x == 0) wt.set_word(W_PFLAG, 0);
+        for (int i = tid; i < 3 * D; i += C::SMW * 32) sts(smem + C::OFF_POISON + 4 * i, 0x7fffffff);
+        if (tid == 0) wt.set_word(W_PFLAG, 0);
         if (!pair_sync()) return false;
       }
       tc5::fence_before();
@@ -1174,12 +1242,12 @@ struct Soft {
       if (!whole) {
         __threadfence();
         if (!pair_sync()) return false;
-        if (threadIdx.x == 0) wt.set_word(W_TICKET, atomicAdd(a.tickets + k.first_b(), 1u));
+        if (tid == 0) wt.set_word(W_TICKET, atomicAdd(a.tickets + k.first_b(), 1u));
         if (!pair_sync()) return false;
         if (wt.word(W_TICKET) == (uint32_t)(k.last_b() - k.first_b())) {
           __threadfence();
           join(k);
-          if (threadIdx.x == 0) a.tickets[k.first_b()] = 0;
+          if (tid == 0) a.tickets[k.first_b()] = 0;
         }
       }
       wt.arrive_warp(B_SEGEMPTY + at_seg % kSegs);
@@ -1252,23 +1320,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     auto init = [&](int i, uint32_t n) { ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n); };
     for (int i = 0; i < 2; ++i) {
       init(B_QFULL + i, 8);
-      init(B_SFULL + i, 1 + (a.fault && blockIdx.x == 0 ? 1 : 0));
-      init(B_PREADY + i, 8);
       init(B_ODONE + i, 1);
+      init(B_PVDONE + i, 1);
+      init(B_DRAIN + i, 1);
     }
-    for (int i = 0; i < 8; ++i) init(B_MAX + i, 2);
-    for (int i = 0; i < kSegs; ++i) {
-      init(B_SEGFULL + i, 1);
-      init(B_SEGEMPTY + i, C::SMW + 4 + 1);
-    }
-    init(B_PAIR, C::SMW);
-    init(B_DRAIN, 1);
-    for (int i = 0; i < C::ST; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      init(B_SFULL + i, 1 + (a.fault && blockIdx.x == 0 ? 1 : 0));
+      init(B_PREADY + i, 4);
       init(B_KFULL + i, 4);
-      init(B_KEMPTY + i, 1);
       init(B_VFULL + i, 4);
+    }
+    for (int i = 0; i < 8; ++i) {
+      init(B_KEMPTY + i, 1);
       init(B_VEMPTY + i, 1);
     }
+    for (int i = 0; i < 16; ++i) init(B_REF + i, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      init(B_SEGFULL + i, 1);
+      init(B_SEGEMPTY + i, C::SMW + 8 + C::LANES);
+    }
+    init(B_PAIR, C::SMW);
     words[W_ABORT] = 0;
     words[W_PFLAG] = words[W_EPI] = 0;
     ptx::fence_mbar_init();
@@ -1305,7 +1376,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       at += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
-  if (warp == 20) tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
+  if (warp == 24) tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
@@ -1315,39 +1386,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   const int sb = words[W_STARTB], sq = words[W_STARTQ];
   const int64_t sbase = wide[W_BASE / 2 + 1];
 
-  // Registers: 80 a thread at launch (61440 in all) = 512 x 88 + 128 x 88 + 128 x 40.
   if (warp < 16) {
-    tc5::regs_inc<88>();
     if (warp < C::SMW) {
-      Soft<D, BITS> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21), 0, 0, 0};
+      const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);
+      Soft<D, BITS> soft = {a, wt, smem, tm, 0, (uint32_t)tid,
+                            tm + C::S0 + (tid >> 7) * C::TN,
+                            smem + C::OFF_MAX + tid * 4, 0, 0};
       soft.run(blockIdx.x);
     }
-  } else if (warp < 20) {
-    tc5::regs_inc<88>();
-    Deq<D, BITS> deq = {a, wt, smem, poison, ring, tid - 512, 0};
+  } else if (warp < 24) {
+    const int w = (warp - 16) / 4;
+    Deq<D, BITS> deq = {a, wt, smem, poison, ring, w, (tid - 512) % kDeqThreads, 0};
     deq.run();
   } else {
-    tc5::regs_dec<40>();
-    if (tid == 20 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
-    if (tid == 21 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
+    if (lid == 0 && warp - 24 < C::LANES) mma_role<D, BITS>(a, wt, smem, tmem, ring, warp - 24);
+    if (tid == 26 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     __syncwarp();
   }
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  if (warp == 20) tc5::dealloc(tmem, 512);
+  if (warp == 24) tc5::dealloc(tmem, 512);
 }
 
 template <int D, int BITS>
 cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   static_assert(Cfg<D, BITS>::SMEM <= 227 * 1024, "shared memory of a block");
   auto kernel = chunk_attn_kernel<D, BITS>;
-  cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, kernel);
-  if (e != cudaSuccess) return e;
-  // the warps' shares (setmaxnreg) come out of what the block is launched with
-  if (at.numRegs != 80) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, Cfg<D, BITS>::SMEM, st>>>(a);
   return cudaGetLastError();
