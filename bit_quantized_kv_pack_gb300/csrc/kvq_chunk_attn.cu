@@ -12,7 +12,7 @@ Layout layout_of(int d, int grid) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   const size_t rows = (size_t)2 * grid * chunk_rows(d);
   Layout l;
-  l.ml = up((size_t)grid * sizeof(uint32_t));  // tickets first
+  l.ml = up((size_t)grid * 64);  // heads first
   l.o = up(l.ml + rows * sizeof(float2));
   l.total = l.o + rows * d * sizeof(float);
   return l;
@@ -51,7 +51,7 @@ cudaError_t launch_chunk_attention(const Dims& s, const kvq_cache_view& v, const
   a.q = q;
   a.out = out;
   a.cu = cu;
-  a.tickets = reinterpret_cast<uint32_t*>(ws);
+  a.heads = reinterpret_cast<int4*>(ws);
   a.ml_part = reinterpret_cast<float2*>(ws + l.ml);
   a.o_part = reinterpret_cast<float4*>(ws + l.o);
   a.B = s.B;

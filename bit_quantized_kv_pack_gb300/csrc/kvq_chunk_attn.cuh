@@ -34,8 +34,9 @@
 //
 // Balance.  All units' tiles lie in one line, and each of the G blocks takes an equal
 // piece of it (the line is cut by cost, so a unit may be cut, into two pieces or, with
-// few units, into many).  Pieces of a unit write (O, m, l) and the last to arrive joins
-// them in the order of the tiles: results do not depend on timing.
+// few units, into many).  Pieces of a unit write (O, m, l), with alternating lanes each
+// lane its own, and a second kernel joins them in a fixed order: results do not depend
+// on timing.
 //
 // Storage order.  Codes come out of a word in pairs (k, k + 4) (INT4, INT3) or (k, k + 8)
 // (INT2).  Instead of sorting them, Q's and the fp16 tokens' elements are put in the same
@@ -64,7 +65,7 @@ struct ChunkAttnArgs {
   const __half* q;  // [total][Hq][d]
   void* out;        // [total][Hq][d]
   const int32_t* cu;
-  uint32_t* tickets;  // [G], zero between calls
+  int4* heads;        // [G][4]: the Seg of the unit that block g begins and does not end (b < 0: none)
   float2* ml_part;    // [2 G][QB] {m, l}
   float4* o_part;     // [2 G][d / 4][QB]
   int B, Hkv, Hq, gq, cap, Nr, Ns, total, max_len, causal, out_f32;
@@ -87,6 +88,7 @@ namespace chunk {
 constexpr int kThreads = 896;
 constexpr int kDeqThreads = 128;  // of the keys, and of the values
 constexpr int kTile = 64;         // tokens of a tile
+constexpr int kSegs = 8;          // ring of segments
 
 template <int D, int BITS>
 struct Cfg {
@@ -103,14 +105,16 @@ struct Cfg {
   static constexpr int KBYTES = TN * D * 2;
   static constexpr int ST = D == 256 ? 2 : 4;       // K and V stages
   static constexpr int HD = D / 2;                  // a softmax group's columns of O
-  static constexpr int TPR = G > 1 ? 2 : 1;         // dequantizing threads of a row
-  static constexpr int GPT = G / TPR;               // groups of each
+  static constexpr int TPR = D == 256 ? 2 : 1;      // dequantizing threads of a row
+  static constexpr int NP = 2 / TPR;                // tiles that four dequantizing warps work on at a time
+  static constexpr int GPT = G / TPR;               // groups of a thread
   static constexpr int CB = 4 * BITS;               // code bytes of a group
   static constexpr int TB = GPT * CB;               // code bytes of a thread, contiguous
   static constexpr int UN = (TB + 15) / 16;         // 16-byte units of them in the ring
   static constexpr int PB = GPT * 4;                // param bytes of a thread
   static constexpr int RAWB = kDeqThreads * (UN * 16 + PB);
-  static constexpr int RAWN = D == 256 ? 1 : D == 128 ? 3 : 6;  // tiles of the ring, of keys and of values
+  static constexpr int RAWN = D >= 128 ? 1 : 3;     // rows of the thread's ring
+  static_assert(RAWN * NP < kSegs - 1, "the cursor of the copies stays within the ring of segments");
   static constexpr int SMW = 8 * LANES;             // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
@@ -135,7 +139,6 @@ struct Cfg {
 
 // A segment: the block's tiles [lo, hi) of the unit (sequence b, KV head h, query block
 // qb).  One warp works the segments out, the others read them from a ring.
-constexpr int kSegs = 8;
 struct alignas(16) Seg {
   int b, h, qb, lo;
   int hi, npt, nt, alt;     // packed tiles and all tiles of the unit; alt: the lanes take alternate tiles
@@ -144,12 +147,13 @@ struct alignas(16) Seg {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-// Of two: of each lane; S and P: of each lane and S buffer; REF: of each lane, 32 rows and
-// S buffer; free stages: of each stage and lane.
-enum { B_QFULL = 0, B_ODONE = 2, B_PVDONE = 4, B_DRAIN = 6, B_SFULL = 8, B_PREADY = 12, B_REF = 16,
+// Of two: of each lane (PVLAST: all PV of a segment but the last); S and P: of each lane
+// and S buffer; REF: of each lane, 32 rows and S buffer; EMPTY: of each stage and lane.
+// Every phase of a barrier is waited on by whoever waits there at all: parities count.
+enum { B_QFULL = 0, B_ODONE = 2, B_PVLAST = 4, B_DRAIN = 6, B_SFULL = 8, B_PREADY = 12, B_REF = 16,
        B_KFULL = 32, B_VFULL = 36, B_KEMPTY = 40, B_VEMPTY = 48, B_SEGFULL = 56, B_SEGEMPTY = 64, B_PAIR = 72,
        B_COUNT = 73 };
-enum { W_TMEM = 146, W_ABORT = 147, W_PFLAG = 148, W_EPI = 149, W_TICKET = 150, W_STARTB = 151,
+enum { W_TMEM = 146, W_ABORT = 147, W_PFLAG = 148, W_EPI = 149, W_STARTB = 151,
        W_STARTQ = 152, W_BASE = 154 /* int64 [2] */ };
 
 __device__ __forceinline__ uint32_t lds(uint32_t addr) {
@@ -159,6 +163,14 @@ __device__ __forceinline__ uint32_t lds(uint32_t addr) {
 }
 __device__ __forceinline__ void sts(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int4 lds_v4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ float ldsf(uint32_t addr) { return __uint_as_float(lds(addr)); }
 __device__ __forceinline__ void stsf(uint32_t addr, float v) { sts(addr, __float_as_uint(v)); }
@@ -444,10 +456,12 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-// What four dequantizing warps share, those of the keys (w 0) or of the values (1).
-// Thread dt has part dt / 64 of row dt % 64 of a tile (head_dim 32: all of row dt, half of
-// the threads have none): its codes are contiguous, and 8 neighbouring lanes store the
-// same piece of 8 rows, which the swizzle puts into 8 different groups of banks.
+// What four dequantizing warps share, those of the keys (w 0) or of the values (1).  Two
+// warps have a tile, a row to a thread (head_dim 256: four warps, half a row), and the two
+// pairs take the tiles in turns.  A thread's codes are contiguous, and 8 neighbouring
+// lanes store the same piece of 8 rows, which the swizzle puts into 8 different groups of
+// banks.  The raw row goes to registers before its turn, and the next one is on its way
+// while this one is worked on.
 template <int D, int BITS>
 struct Deq {
   using C = Cfg<D, BITS>;
@@ -461,8 +475,8 @@ struct Deq {
   uint32_t seg;   // segments of the block so far
 
   __device__ __forceinline__ int row() const { return dt % kTile; }
-  __device__ __forceinline__ int part() const { return dt / kTile; }
-  __device__ __forceinline__ bool has_row() const { return C::TPR == 2 || dt < kTile; }
+  __device__ __forceinline__ int part() const { return C::TPR == 2 ? dt / kTile : 0; }
+  __device__ __forceinline__ int pair() const { return C::NP == 2 ? dt / kTile : 0; }
 
   // Values that fp16 does not hold as finite ones take no part in the MMA: a weight of
   // zero would make them NaN in rows that do not see the token.  The first token of the
@@ -482,7 +496,8 @@ struct Deq {
   // The cursor of the copies: a tile of a segment.
   struct Cursor {
     SegReader seg;
-    int tile = -1, hi = 0, npt = 0;
+    int tile = 0, hi = 0, npt = 0;
+    bool open = false;         // seg has been looked at
     int left = 0;              // packed tokens from the thread's row of the tile on
     int64_t at = 0;            // contiguous: that row; paged: row of the head in a page
     const int32_t* pages = nullptr;  // paged: the entry of the thread's row
@@ -500,7 +515,7 @@ struct Deq {
   // becomes zero codes with zero params, which stand for zeros.
   __device__ __forceinline__ void fetch(Cursor& c, int slot) {
     const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
-    bool there = c.left > 0 && has_row();
+    bool there = c.left > 0;
     int64_t at = c.at;
     if (a.rm.paged && there) {
       there = c.page >= 0 && c.page < a.rm.npages;
@@ -520,52 +535,60 @@ struct Deq {
 #pragma unroll
       for (int i = 0; i < C::GPT; ++i) sts(dp + 4 * i, 0);
     }
-    // on to the next tile
-    c.left -= C::TN;
+    // on to the pair's next tile; contiguous rows further on are called into L2
+    c.left -= C::NP * C::TN;
     if (a.rm.paged) {
-      c.pages += C::TN / kPage;
+      c.pages += C::NP * C::TN / kPage;
       if (c.left > 0) c.page = __ldg(c.pages);
     } else {
-      c.at += C::TN;
+      c.at += C::NP * C::TN;
+      if (c.left > C::TN * C::NP) {
+        const int64_t far = c.at + C::NP * C::TN;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes[w] + far * (C::G * C::CB) + part() * C::TB));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.params[w] + far * C::G));
+      }
     }
   }
 
   // Shared address of the thread's row in a tile at dst, with the row's swizzle in its
-  // low bits: piece c of the thread's panel p is at (this ^ (c << 4)) + p * KP (a thread
-  // with one group has half a panel's row, pieces 4 part .. 4 part + 3).
+  // low bits: piece c of the thread's panel p is at (this ^ (c << 4)) + p * KP.
   __device__ __forceinline__ uint32_t row_addr(uint32_t dst) const {
     const int r = row();
-    const uint32_t at = dst + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
-    return C::GPT == 1 ? at ^ (part() << 6) : at + part() * (C::GPT / 2) * C::KP;
+    return dst + part() * (C::GPT / 2) * C::KP + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
   }
   __device__ __forceinline__ int column(int g, int c) const { return (part() * C::GPT + g) * 32 + c * 8; }
 
-  // A fetched tile as fp16 at `dst`.  first: logical place of the tile's first token.
-  __device__ __forceinline__ bool packed_tile(int first, int slot, uint32_t dst) {
-    constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
+  // The thread's raw row in registers.
+  struct Raw {
+    uint32_t code[C::UN * 4], prm[C::GPT];
+  };
+  __device__ __forceinline__ void take(Raw& x, int slot) const {
     const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
-    if (!has_row()) return true;
-    uint32_t raw[C::UN * 4], prm[C::GPT];
 #pragma unroll
     for (int i = 0; i < C::UN; ++i) {
       const uint4 v = ld_shared_v4(dc + i * (kDeqThreads * 16));
-      raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+      x.code[4 * i] = v.x, x.code[4 * i + 1] = v.y, x.code[4 * i + 2] = v.z, x.code[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i) prm[i] = lds(dp + 4 * i);
+    for (int i = 0; i < C::GPT; ++i) x.prm[i] = lds(dp + 4 * i);
+  }
+
+  // A raw row as fp16 at `dst`.  token: its logical place.
+  __device__ __forceinline__ bool packed_row(const Raw& x, int token, uint32_t dst) {
+    constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
     const uint32_t at = row_addr(dst);
     uint32_t rare = 0;
 #pragma unroll
     for (int g = 0; g < C::GPT; ++g) {
-      const uint32_t s2 = ptx::prmt(prm[g], prm[g], 0x1010), m2 = ptx::prmt(prm[g], prm[g], 0x3232);
+      const uint32_t s2 = ptx::prmt(x.prm[g], x.prm[g], 0x1010), m2 = ptx::prmt(x.prm[g], x.prm[g], 0x3232);
       // the group's largest value; only where it is not finite can any value be so
       if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) rare |= 1u << g;
-      uint32_t x[4];
-      code_words<BITS>(raw, g, x);
+      uint32_t c8[4];
+      code_words<BITS>(x.code, g, c8);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t y[4];
-        codes_f16<BITS>(x[c], y);
+        codes_f16<BITS>(c8[c], y);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(y[j], s2, m2);
         st_shared_v4((at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP, make_uint4(y[0], y[1], y[2], y[3]));
@@ -578,7 +601,9 @@ struct Deq {
     for (int e = 0; e < 32 * C::GPT; ++e) {
       const int g = e >> 5;
       if (!((rare >> g) & 1u)) continue;
-      const uint32_t pg = lds(dp + 4 * g);
+      uint32_t pg = x.prm[0];
+#pragma unroll
+      for (int i = 1; i < C::GPT; ++i) pg = g == i ? x.prm[i] : pg;
       const uint32_t ea = (at ^ (((g & 1) * 4 + ((e >> 3) & 3)) << 4)) + (g / 2) * C::KP + 2 * (e & 7);
       unsigned short hv;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
@@ -587,7 +612,7 @@ struct Deq {
         hv = (hv & 0x8000u) | 0x7bffu;
       else if (w == 0)
         continue;
-      else if (note(column(g, 0) + (e & 31), first + row(), hv))
+      else if (note(column(g, 0) + (e & 31), token, hv))
         hv = 0;
       else
         return false;
@@ -609,7 +634,6 @@ struct Deq {
       src = a.res[w] + (bh * a.Nr + ring_slot(k.head + f - k.ns)) * D;
     if (f < n) src += column(0, 0);
     const uint32_t at = row_addr(dst);
-    if (!has_row()) return true;
 #pragma unroll
     for (int i = 0; i < 4 * C::GPT; ++i)
       ptx::cp_async_16((at ^ ((i & 7) << 4)) + (i / 8) * C::KP, src + (f < n ? i * 8 : 0), f < n ? 16 : 0);
@@ -644,51 +668,57 @@ struct Deq {
   __device__ __forceinline__ void run() {
     SegReader k;
     Cursor c;
+    c.tile = pair();
     bool ok = true, more = true;
-    // the next tile of the line into its ring slot
+    // The pair's next tile into ring slot `slot`.  c.tile is its place in segment c.seg, or
+    // past that segment's end by as many tiles as there are to skip in the next.
     auto fetch_next = [&](int slot) {
-      if (more && c.tile < 0) {
+      while (more && c.tile >= c.hi) {
+        if (c.open) ++c.seg.i;
+        c.open = true;
         ok = ok && __all_sync(0xffffffffu, c.seg.wait(wt));
         const Seg& s = c.seg.get(ring);
         more = ok && s.b >= 0;
-        if (more) {
-          c.tile = s.lo, c.hi = s.hi, c.npt = s.npt;
-          const int p = s.lo * C::TN + row();
-          c.left = s.npk - p;
-          if (a.rm.paged) {
-            c.at = (int64_t)s.h * kPage + p % kPage;
-            c.pages = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + p / kPage;
-            if (c.left > 0) c.page = __ldg(c.pages);
-          } else {
-            c.at = ((int64_t)s.b * a.Hkv + s.h) * a.cap + p;
-          }
+        if (!more) break;
+        c.tile += s.lo - c.hi, c.hi = s.hi, c.npt = s.npt;
+        const int p = c.tile * C::TN + row();
+        c.left = s.npk - p;
+        if (a.rm.paged) {
+          c.at = (int64_t)s.h * kPage + p % kPage;
+          c.pages = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + p / kPage;
+          if (c.left > 0) c.page = __ldg(c.pages);
+        } else {
+          c.at = ((int64_t)s.b * a.Hkv + s.h) * a.cap + p;
         }
       }
       if (more) {
         if (c.tile < c.npt) fetch(c, slot);
-        if (++c.tile == c.hi) {
-          ++c.seg.i;
-          c.tile = -1;
-        }
+        c.tile += C::NP;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     uint32_t kv = 0;             // tiles so far
     uint32_t used = 0, par = 0;  // by stage and lane: the lane has the stage; parity of its release
     int slot = 0;
-    // RAWN - 1 tiles ahead: a free slot is filled before the oldest is taken
 #pragma unroll 1
-    for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
+    for (int i = 0; i < C::RAWN; ++i) fetch_next(i);
     for (; ok; ++k.i, ++seg) {
       ok = ok && __all_sync(0xffffffffu, k.wait(wt));
       if (!ok) break;
       const Seg& s = k.get(ring);
       if (s.b < 0) break;
       const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns, alt = s.alt;
-      for (int t = lo; t < hi; ++t, ++kv) {
-        fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
-        const int stage = kv % C::ST;
+      for (int t = lo + (C::NP == 2 ? (pair() ^ kv) & 1 : 0); t < hi; t += C::NP) {
+        const uint32_t x = kv + (t - lo);
+        const int stage = x % C::ST;
         const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
+        Raw raw;
+        if (t < npt) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
+          take(raw, slot);
+        }
+        fetch_next(slot);
+        if (++slot == C::RAWN) slot = 0;
         // the lanes that had the stage before have read it
 #pragma unroll
         for (int l = 0; l < C::LANES; ++l) {
@@ -701,18 +731,13 @@ struct Deq {
         if (!ok) break;
         used &= ~(3u << (2 * stage));
         used |= (alt ? 1u << ((t - lo) & 1) : C::LANES == 2 ? 3u : 1u) << (2 * stage);
-        if (t < npt) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-          ok = packed_tile(ns + t * C::TN, slot, dst);
-        } else {
-          ok = f16_tile(s, (t - npt) * C::TN, dst);
-        }
+        ok = t < npt ? packed_row(raw, ns + t * C::TN + row(), dst) : f16_tile(s, (t - npt) * C::TN, dst);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::fence_proxy_async_shared();
         wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
-        if (++slot == C::RAWN) slot = 0;
       }
+      kv += hi - lo;
       wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -728,6 +753,8 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
   const uint32_t s_at = tmem + C::S0 + lane * 2 * C::TN, o_at = tmem + C::O0 + lane * C::OSTEP;
+  const uint64_t kd0 = tc5::smem_desc(smem + C::OFF_K, 16, 8 * C::RB, C::SWZ);
+  const uint64_t vd0 = tc5::smem_desc(smem + C::OFF_V, C::KP, 8 * C::RB, C::SWZ);
   SegReader k;
   uint32_t qn = 0;           // phases of the lane's barrier of Q
   uint32_t nqk = 0, npv = 0; // the lane's QK^T and PV so far: S buffers take turns
@@ -745,40 +772,56 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
     if (t0 < n) ok = wt.wait(B_QFULL + lane, qn++ & 1);
     const uint64_t qd =
         tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
-    auto qk = [&](int t) -> bool {
-      const int stage = (kv + t) % C::ST, buf = nqk & 1;
-      if (!wt.wait(B_KFULL + stage, ((kv + t) / C::ST) & 1)) return false;
-      tc5::fence_after();
-      const uint64_t kd = tc5::smem_desc(smem + C::OFF_K + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+    // tile x of the line (of all the block's segments) is in stage x % ST
+    auto qk = [&](uint32_t x) {
+      const uint32_t buf = nqk & 1;
+      const uint64_t kd = kd0 + (x % C::ST) * (C::KBYTES >> 4);
+      const uint32_t to = s_at + buf * C::TN;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         constexpr int PW = C::PW;
         const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
-        tc5::mma_ss(s_at + buf * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
-                    kIdescQK, j > 0);
+        tc5::mma_ss(to, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4), kIdescQK, j > 0);
       }
-      tc5::commit(wt.bar(B_SFULL + 2 * lane + buf));
-      tc5::commit(wt.bar(B_KEMPTY + 2 * stage + lane));
+      tc5::commit(wt.bar(B_SFULL + 2 * lane) + 8 * buf);
+      tc5::commit(wt.bar(B_KEMPTY + lane) + 16 * (x % C::ST));
       ++nqk;
-      return true;
     };
-    for (int t = t0; ok && t < n && t < t0 + 2 * step; t += step) ok = qk(t);
-    for (int t = t0; ok && t < n; t += step) {
-      const int stage = (kv + t) % C::ST, buf = npv & 1;
-      const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
-      ok = wt.wait(B_VFULL + stage, ((kv + t) / C::ST) & 1) && wt.wait(B_PREADY + 2 * lane + buf, (npv >> 1) & 1);
+    const uint32_t end = kv + n;
+    for (uint32_t x = kv + t0; ok && x < end && x < kv + t0 + 2 * step; x += step) {
+      ok = wt.wait_at(wt.bar(B_KFULL) + 8 * (x % C::ST), (x / C::ST) & 1);
       if (!ok) break;
       tc5::fence_after();
+      qk(x);
+    }
+#pragma unroll 1
+    for (uint32_t x = kv + t0; ok && x < end; x += step) {
+      // V and P of this tile, and K of the one whose S comes after: asked for at once (the
+      // tensor cores idle while this thread waits)
+      const uint32_t y = x + 2 * step, buf = npv & 1;
+      const uint32_t vb = wt.bar(B_VFULL) + 8 * (x % C::ST), kb = wt.bar(B_KFULL) + 8 * (y % C::ST),
+                     pb = wt.bar(B_PREADY + 2 * lane) + 8 * buf;
+      const uint32_t vp = (x / C::ST) & 1, kp = (y / C::ST) & 1, pp = (npv >> 1) & 1;
+      const bool more = y < end;
+      const bool v_ok = ptx::mbar_try_wait(vb, vp), k_ok = !more || ptx::mbar_try_wait(kb, kp),
+                 p_ok = ptx::mbar_try_wait(pb, pp);
+      if (!(v_ok && k_ok && p_ok))
+        ok = wt.wait_at(vb, vp) && (!more || wt.wait_at(kb, kp)) && wt.wait_at(pb, pp);
+      if (!ok) break;
+      tc5::fence_after();
+      const uint64_t vd = vd0 + (x % C::ST) * (C::KBYTES >> 4);
+      const uint32_t from = s_at + buf * C::TN;
+      // the lane's first tile of the segment starts O
+      tc5::mma_ts(o_at, from, vd, kIdescPV, x != kv + t0);
 #pragma unroll
-      for (int j = 0; j < C::TN / 16; ++j) {
-        // the lane's first tile of the segment starts O
-        tc5::mma_ts(o_at, s_at + buf * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, t > t0 || j > 0);
-      }
-      tc5::commit(wt.bar(B_PVDONE + lane));
-      if (t + step >= n) tc5::commit(wt.bar(B_ODONE + lane));
+      for (int j = 1; j < C::TN / 16; ++j)
+        tc5::mma_ts(o_at, from + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, true);
       // into the buffer of this tile's P: after PV in the tensor cores' order
-      if (t + 2 * step < n) ok = qk(t + 2 * step);
-      tc5::commit(wt.bar(B_VEMPTY + 2 * stage + lane));
+      if (more)
+        qk(y);
+      else
+        tc5::commit(wt.bar((x + step < end ? B_PVLAST : B_ODONE) + lane));
+      tc5::commit(wt.bar(B_VEMPTY + lane) + 16 * (x % C::ST));
       ++npv;
     }
     if (!ok) break;
@@ -810,7 +853,7 @@ struct Soft {
   uint32_t at_seg;            // place in the ring of segments
   uint32_t nt;                // tiles of the lane so far: its two groups take turns
 
-  enum { P_O = 1, P_PAIR = 2 };
+  enum { P_O = 1, P_PAIR = 2, P_LAST = 3 };
 
   // Accumulator, group (and half of O's columns), and row: by the thread.
   __device__ __forceinline__ int lane() const { return tid >> 8; }
@@ -915,7 +958,7 @@ struct Soft {
   // registers, and beside the tiles L1 is so small that a spilled register is a trip to
   // L2.  The reference is the lane's: the group that has tile n takes it over from the
   // other, which had n - 1, and passes it on before it works out its weights.
-  __device__ __forceinline__ bool tile(int visible, uint32_t bad, bool first, float& m, float& l) {
+  __device__ __forceinline__ bool tile(int visible, uint32_t bad, bool first, bool last, float& m, float& l) {
     const bool masked = __any_sync(0xffffffffu, visible < C::TN) || bad;
     float mt = -INFINITY;
 #pragma unroll
@@ -945,8 +988,11 @@ struct Soft {
     wt.arrive_warp_at(bar + 8 * half());
     if (__any_sync(0xffffffffu, moves) && !first) {
       const float f = moves ? ptx::ex2_ftz((was - mn) * a.scale_log2) : 1.0f;
-      // O is still while the last tile's PV is done and this one's P is not there
-      if (!wt.wait_warp(B_PVDONE + lane(), (nt - 1) & 1)) return false;
+      // O is still when the last tile's PV is done (the next tile's S is made after it) and
+      // this one's P is not there
+      if (!(last ? wt.wait_warp(B_PVLAST + lane(), (phases >> P_LAST) & 1)
+                 : wt.wait_warp_at(wt.bar(B_SFULL) + 16 * lane() + 8 * (half() ^ 1), ((nt + 1) >> 1) & 1)))
+        return false;
       tc5::fence_after();
       const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP;
 #pragma unroll 1
@@ -1030,39 +1076,6 @@ struct Soft {
     return l == 0.0f ? 0.0f : 1.0f / l;
   }
 
-  // The pieces of a cut unit, from their (O, m, l) in global memory: 16 columns of a row
-  // at a time, all softmax threads.
-  __device__ __forceinline__ void join(const Ref& k) const {
-    const int rows = block_rows(k), first = k.first_b(), last = k.last_b();
-    for (int it = tid; it < rows * (D / 16); it += C::SMW * 32) {
-      const int cg = it / rows, row = it - cg * rows;
-      float m = -INFINITY;
-#pragma unroll 4
-      for (int p = first; p <= last; ++p)
-        m = fmaxf(m, __ldcg(a.ml_part + (int64_t)(2 * p + (p == first)) * C::QB + row).x);
-      float l = 0.0f, o[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = 0.0f;
-#pragma unroll 2
-      for (int p = first; p <= last; ++p) {
-        const int64_t slot = 2 * p + (p == first);
-        const float2 ml = __ldcg(a.ml_part + slot * C::QB + row);
-        const float f = ml.x == -INFINITY ? (ml.y != ml.y ? NAN : 0.0f) : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
-        l += ml.y * f;
-        const float4* src = a.o_part + (slot * (D / 4) + cg * 4) * C::QB + row;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = __ldcg(src + e * C::QB);
-          o[4 * e] += v.x * f;
-          o[4 * e + 1] += v.y * f;
-          o[4 * e + 2] += v.z * f;
-          o[4 * e + 3] += v.w * f;
-        }
-      }
-      store16(o, inverse(l), row_at(k, row) + cg * 16);
-    }
-  }
-
   // The group's tiles of a segment: the reference m of the last of them and l.
   __device__ __forceinline__ bool tiles(float& m, float& l, bool& any) {
     m = -INFINITY;
@@ -1115,14 +1128,16 @@ struct Soft {
       if (!wt.wait_warp_at(bar, (nt >> 1) & 1)) return false;
       tc5::fence_after();
       if (live) {
-        if (!tile(visible, bad, t == t0, m, l)) return false;
+        if (!tile(visible, bad, t == t0, t + step >= end, m, l)) return false;
       } else {
         wt.arrive_warp_at(wt.bar(B_REF) + (lane() * 4 + (r() >> 5)) * 16 + 8 * half());
       }
       tc5::fence_before();
       wt.arrive_warp_at(bar + 8 * (B_PREADY - B_SFULL));
     }
-    nt = nt0 + (any ? (end - t0 + step - 1) / step : 0);
+    const int n = any ? (end - t0 + step - 1) / step : 0;
+    nt = nt0 + n;
+    if (n > 1) phases ^= 1u << P_LAST;
     return true;
   }
 
@@ -1160,9 +1175,9 @@ struct Soft {
       const int slot = 2 * block + (k.lo() == 0);
       float inv = 0.0f;
       int64_t at = 0;
-      // With alternating lanes, lane 1's accumulator goes through shared memory to lane
-      // 0, 16 columns of each half at a time, with its rows' m and l.
-      const bool pass = alt && k.hi() - k.lo() > 1;
+      // With alternating lanes, lane 1's accumulator of a whole unit goes through shared
+      // memory to lane 0, 16 columns of each half at a time, with its rows' m and l.
+      const bool pass = alt && whole && k.hi() - k.lo() > 1;
       float f0 = 1.0f, f1 = 0.0f;
       if (pass) {
         const uint32_t x1 = smem + C::OFF_Q + (C::LANES - 1) * C::QBYTES + 1024 + r() * 4;
@@ -1182,13 +1197,14 @@ struct Soft {
           m = mm;
         }
       }
-      const bool mine = row < rows && !(alt && lane() == 1);
+      const bool mine = row < rows && !(alt && whole && lane() == 1);
+      const int prow = lane() * 128 + r();  // row in a piece
       if (mine) {
         at = row_at(k, row);
         if (whole)
           inv = inverse(l);
         else if (half() == 0)
-          __stcg(a.ml_part + (int64_t)slot * C::QB + row, make_float2(m, l));
+          __stcg(a.ml_part + (int64_t)slot * C::QB + prow, make_float2(m, l));
       }
 #pragma unroll 1
       for (int c0 = 0; c0 < C::HD; c0 += 16) {
@@ -1215,7 +1231,7 @@ struct Soft {
         if (mine && whole) {
           store16(o, inv, at + col);
         } else if (mine) {
-          float4* dst = a.o_part + ((int64_t)slot * (D / 4) + col / 4) * C::QB + row;
+          float4* dst = a.o_part + ((int64_t)slot * (D / 4) + col / 4) * C::QB + prow;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             __stcg(dst + j * C::QB, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
@@ -1225,7 +1241,7 @@ struct Soft {
       if (noted) {
         if (mine) {
           const int lim = seen_of(a, k.n(), k.ns() + k.npk() + k.nres(), token_of(a, k.qb() * C::QB + row));
-          notes(lim, whole, at, slot, row);
+          notes(lim, whole, at, slot, prow);
         }
         // the notes have been read: clean them
         if (!pair_sync()) return false;
@@ -1239,17 +1255,7 @@ struct Soft {
       if ((r() & 31) == 0)
         asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(wt.bars + 4 * W_EPI) : "memory");
 
-      if (!whole) {
-        __threadfence();
-        if (!pair_sync()) return false;
-        if (tid == 0) wt.set_word(W_TICKET, atomicAdd(a.tickets + k.first_b(), 1u));
-        if (!pair_sync()) return false;
-        if (wt.word(W_TICKET) == (uint32_t)(k.last_b() - k.first_b())) {
-          __threadfence();
-          join(k);
-          if (tid == 0) a.tickets[k.first_b()] = 0;
-        }
-      }
+      if (!whole && k.lo() == 0 && tid < 4) a.heads[block * 4 + tid] = lds_v4(k.at + 16 * tid);
       wt.arrive_warp(B_SEGEMPTY + at_seg % kSegs);
       ++at_seg;
       if (!wait_seg()) return false;
@@ -1276,6 +1282,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(base + C::OFF_BAR);
   volatile int64_t* wide = reinterpret_cast<volatile int64_t*>(base + C::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lid = tid & 31;
+  if (tid == 0) a.heads[blockIdx.x * 4].x = -1;  // (a later head is this thread's store too)
+  asm volatile("griddepcontrol.launch_dependents;");
 
   // The line of tiles: each thread sums up some sequences, then the block scans.
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -1321,14 +1329,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     for (int i = 0; i < 2; ++i) {
       init(B_QFULL + i, 8);
       init(B_ODONE + i, 1);
-      init(B_PVDONE + i, 1);
+      init(B_PVLAST + i, 1);
       init(B_DRAIN + i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       init(B_SFULL + i, 1 + (a.fault && blockIdx.x == 0 ? 1 : 0));
       init(B_PREADY + i, 4);
-      init(B_KFULL + i, 4);
-      init(B_VFULL + i, 4);
+      init(B_KFULL + i, 2 * C::TPR);
+      init(B_VFULL + i, 2 * C::TPR);
     }
     for (int i = 0; i < 8; ++i) {
       init(B_KEMPTY + i, 1);
@@ -1387,6 +1395,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   const int64_t sbase = wide[W_BASE / 2 + 1];
 
   if (warp < 16) {
+    tc5::regs_inc<80>();
     if (warp < C::SMW) {
       const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);
       Soft<D, BITS> soft = {a, wt, smem, tm, 0, (uint32_t)tid,
@@ -1395,10 +1404,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       soft.run(blockIdx.x);
     }
   } else if (warp < 24) {
+    tc5::regs_dec<64>();
     const int w = (warp - 16) / 4;
     Deq<D, BITS> deq = {a, wt, smem, poison, ring, w, (tid - 512) % kDeqThreads, 0};
     deq.run();
   } else {
+    tc5::regs_dec<56>();
     if (lid == 0 && warp - 24 < C::LANES) mma_role<D, BITS>(a, wt, smem, tmem, ring, warp - 24);
     if (tid == 26 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     __syncwarp();
@@ -1409,14 +1420,101 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   if (warp == 24) tc5::dealloc(tmem, 512);
 }
 
+// The pieces of the units that were cut, in the order of the tiles.  A block looks at the
+// unit that block x of the other kernel began; a warp has 16 columns of a row: eight
+// lanes' worth of pieces at a time, four columns to a lane.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 8;
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAttnArgs a) {
+  constexpr int QB = chunk_rows(D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  union {
+    int4 v[4];
+    Seg s;
+  } u;
+  u.v[0] = __ldcg(a.heads + blockIdx.x * 4);
+  if (u.v[0].x < 0) return;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) u.v[i] = __ldcg(a.heads + blockIdx.x * 4 + i);
+  const Seg& k = u.s;
+  const int rows = min(k.n * a.gq - k.qb * QB, QB), lane = threadIdx.x & 31, e = lane & 3;
+  const int subs = (k.last_b - k.first_b + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
+  const int warps = kJoinBlocks * kJoinThreads / 32;
+  for (int it = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); it < rows * (D / 16); it += warps) {
+    const int row = it / (D / 16), cg = it % (D / 16);
+    auto ml_at = [&](int s, int64_t& slot, int& prow) {
+      const int p = k.first_b + (k.alt ? s >> 1 : s);
+      slot = 2 * (int64_t)p + (p == k.first_b);
+      prow = row + (k.alt ? (s & 1) * 128 : 0);
+      return __ldcg(a.ml_part + slot * QB + prow);
+    };
+    int64_t slot;
+    int prow;
+    float m = -INFINITY;
+    for (int s = lane >> 2; s < subs; s += 8) m = fmaxf(m, ml_at(s, slot, prow).x);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = lane >> 2; s < subs; s += 8) {
+      const float2 ml = ml_at(s, slot, prow);
+      if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // saw nothing (and may have written nothing)
+      const float f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
+      const float4 v = __ldcg(a.o_part + (slot * (D / 4) + cg * 4 + e) * QB + prow);
+      l += ml.y * f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
+    }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, x);
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    }
+    if (lane >= 4) continue;
+    if (l == 0.0f) set_error(a.err_word, KVQ_ERRBIT_EMPTY);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int R = k.qb * QB + row;
+    const int tok = token_of(a, R);
+    const int64_t at = ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D + cg * 16;
+    const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = 4 * e + j;  // the element that is stored at this column
+      const int el = BITS == 2 ? (c & 1) * 8 + (c >> 3) * 4 + ((c & 7) >> 1) : (c & 8) + ((c & 7) >> 1) + 4 * (c & 1);
+      if (a.out_f32)
+        static_cast<float*>(a.out)[at + el] = y[j];
+      else
+        static_cast<__half*>(a.out)[at + el] = __float2half_rn(y[j]);
+    }
+  }
+}
+
 template <int D, int BITS>
 cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   static_assert(Cfg<D, BITS>::SMEM <= 227 * 1024, "shared memory of a block");
   auto kernel = chunk_attn_kernel<D, BITS>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, Cfg<D, BITS>::SMEM, st>>>(a);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, kJoinBlocks);
+  cfg.blockDim = kJoinThreads;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];  // its blocks may come as the others leave; they wait for all of them
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, BITS>, a);
 }
 
 template <int D>
