@@ -23,14 +23,15 @@ Layout layout_of(int d, int grid) {
 // Two pieces of units to each block (its first and its last), whatever the lengths.
 size_t chunk_workspace_bytes(const Dims& s, int num_q_heads, int sm_count) {
   (void)num_q_heads;
-  return layout_of(s.d, sm_count).total;
+  return layout_of(s.d, sm_count < 256 ? sm_count : 256).total;
 }
 
 cudaError_t launch_chunk_attention(const Dims& s, const kvq_cache_view& v, const __half* q, int Hq,
                                    const int32_t* cu, int total, int max_len, void* out,
                                    void* workspace, bool causal, uint32_t flags, cudaStream_t st) {
   if (total == 0 || max_len == 0) return cudaSuccess;
-  const int grid = device_sm_count();  // one block per SM
+  const int sms = device_sm_count();
+  const int grid = sms < 256 ? sms : 256;  // one block per SM
   const Layout l = layout_of(s.d, grid);
   char* ws = static_cast<char*>(workspace);
   ChunkAttnArgs a;

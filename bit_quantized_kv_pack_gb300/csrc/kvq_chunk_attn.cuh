@@ -3,30 +3,24 @@
 //
 // The mathematics.  The query rows of one (sequence, KV head) are its run's tokens times
 // the gq heads that share the KV head, row = token * gq + head: one pass over K and V
-// serves them all.  For a tile of 64 tokens S = Q K^T, P = exp2(S c - m c) with the row's
+// serves them all.  For a tile of tokens S = Q K^T, P = exp2(S c - m c) with the row's
 // reference maximum m, O += P V, l += sum P; c = log2(e) / sqrt(d).  m follows the
 // running maximum lazily: it moves (and O, l are rescaled) only when the maximum has
 // passed it by 2^8, so weights stay below 256 and the sums lose nothing in fp32.
 // Roundings: the dequantized keys and values min + code * scale are rounded to fp16 once
 // (operands of the MMA), the weights P to fp16 once; scores, m, l and O are fp32.
 //
-// A block (one per SM, persistent) has 28 warps:
+// A block (one per SM, persistent) has 24 warps:
 //   0-15   softmax: S from TMEM, P back to TMEM (it takes S's place and is the A operand
 //          of the second MMA), the epilogue.  Four groups of four warps: two for each of
-//          the block's two accumulators (lanes 0 and 1), which take its tiles in turns; a
-//          thread per query row.
-//   16-23  dequantize, four warps the keys and four the values: a piece of a row of codes
-//          comes by cp.async into a ring that is private to its thread (no barrier),
-//          becomes fp16 in registers and goes to shared memory in the MMA's swizzle, K as
-//          the K-major and V as the MN-major B operand.
-//   24, 25 issue the MMAs, one thread for each lane; 26 works out the segments.
-// What the shape answers to (head_dim 128): a tile's chain S -> P -> PV -> next S takes
-// longer than its MMAs, so each lane has two S buffers and the next S is made while the
-// softmax works on this one.  TMEM (2 lanes x 2 x 64 columns of S, 2 x 128 of O) then
-// holds tiles of 64 tokens; their QK^T runs at 0.6 of the rate of 128 (measured 861
-// against 520 cycles for 128 x 128 x 128), which the overlap outweighs.  An MMA takes its
-// issuer about 55 cycles and a commit 85 (measured), hence a thread for each lane.
-//
+//          the block's two accumulators (lanes 0 and 1), each with half of the tile's
+//          tokens and half of O's columns, a thread per query row.  (One group per
+//          accumulator left the chain S -> P -> next S as the bound: 42 % of the issue
+//          slots used.)
+//   16-19  dequantize: a row of codes comes by cp.async into a ring that is private to
+//          its thread (no barrier), becomes fp16 in registers and goes to shared memory
+//          in the MMA's 128-byte swizzle, K as the K-major and V as the MN-major B operand.
+//   20     issues the MMAs; 21 works out the segments.
 // A unit of work is (sequence, block of query rows, KV head).  With more than 128 rows in
 // the block the two lanes are its two halves and share each tile; with fewer they take
 // alternate tiles of the same rows and are joined at the end, so that the softmax of one
@@ -67,7 +61,7 @@ struct ChunkAttnArgs {
   const int32_t* cu;
   int4* heads;        // [G][4]: the Seg of the unit that block g begins and does not end (b < 0: none)
   float2* ml_part;    // [2 G][QB] {m, l}
-  float4* o_part;     // [2 G][d / 4][QB]
+  float4* o_part;     // [2 G][QB][d / 4]
   int B, Hkv, Hq, gq, cap, Nr, Ns, total, max_len, causal, out_f32;
   uint32_t gq_mul, gq_shift;  // row / gq = row * gq_mul >> gq_shift for rows below 2^31
   uint32_t wait_limit_us;
@@ -85,16 +79,18 @@ __host__ __device__ constexpr int chunk_rows(int d) { return d == 256 ? 128 : 25
 
 namespace chunk {
 
-constexpr int kThreads = 896;
-constexpr int kDeqThreads = 128;  // of the keys, and of the values
-constexpr int kTile = 64;         // tokens of a tile
-constexpr int kSegs = 8;          // ring of segments
+constexpr int kThreads = 768;
+constexpr int kDeqThreads = 128;
+// What the line of tiles is cut by, in quarters of a shared tile's time (128 tokens x 256
+// rows): a shared tile 2.0 us, a lane's own 1.5 us, a unit's begin and end about 5 us
+// (head_dim 128; measured).
+constexpr int kCostShared = 4, kCostOwn = 3, kCostUnit = 10;
 
 template <int D, int BITS>
 struct Cfg {
   static constexpr int LANES = D == 256 ? 1 : 2;    // accumulators
   static constexpr int QB = chunk_rows(D);
-  static constexpr int TN = kTile;
+  static constexpr int TN = D == 256 ? 64 : 128;    // tokens of a tile
   static constexpr int G = D / 32;                  // groups of a row
   static constexpr int PW = D < 64 ? D : 64;        // elements of a panel's row
   static constexpr int RB = PW * 2;                 // bytes of it
@@ -103,18 +99,17 @@ struct Cfg {
   static constexpr int KP = TN * RB;                // of a panel of K or V
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int KBYTES = TN * D * 2;
-  static constexpr int ST = D == 256 ? 2 : 4;       // K and V stages
-  static constexpr int HD = D / 2;                  // a softmax group's columns of O
-  static constexpr int TPR = D == 256 ? 2 : 1;      // dequantizing threads of a row
-  static constexpr int NP = 2 / TPR;                // tiles that four dequantizing warps work on at a time
-  static constexpr int GPT = G / TPR;               // groups of a thread
+  static constexpr int ST = D <= 64 ? 4 : 2;        // K and V stages
+  static constexpr int HC = TN / 2;                 // a softmax group's columns of S
+  static constexpr int HD = D / 2;                  // ... and of O
+  static constexpr int TPR = TN == 64 ? 2 : 1;      // dequantizing threads of a row
+  static constexpr int GPT = G / TPR;               // groups of each
   static constexpr int CB = 4 * BITS;               // code bytes of a group
   static constexpr int TB = GPT * CB;               // code bytes of a thread, contiguous
   static constexpr int UN = (TB + 15) / 16;         // 16-byte units of them in the ring
   static constexpr int PB = GPT * 4;                // param bytes of a thread
   static constexpr int RAWB = kDeqThreads * (UN * 16 + PB);
-  static constexpr int RAWN = D >= 128 ? 1 : 3;     // rows of the thread's ring
-  static_assert(RAWN * NP < kSegs - 1, "the cursor of the copies stays within the ring of segments");
+  static constexpr int RAWN = D == 256 ? 2 : D == 128 ? 3 : 6;  // half tiles of the ring
   static constexpr int SMW = 8 * LANES;             // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
@@ -126,19 +121,19 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + ST * KBYTES;
   static constexpr int OFF_RAW = OFF_V + ST * KBYTES;
   // where lane 1's accumulator passes to lane 0: 16 columns of 128 rows of each half.  Lane
-  // 1's Q (but for its first 2 KiB) is free then, and large enough from head_dim 128 on
+  // 1's Q (but for its first KiB) is free then, and large enough from head_dim 128 on
   static constexpr int STAGE = 2 * 16 * 128 * 4;
-  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES + 2048 : OFF_RAW + 2 * RAWN * RAWB;
-  static constexpr int OFF_MAX = OFF_RAW + 2 * RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // float [LANES][2][128]
-  static_assert(OFF_MAX % 1024 == 0, "a thread finds the other group's value by one bit of the address");
-  static constexpr int OFF_POISON = OFF_MAX + LANES * 1024;     // int [3][D]
-  static constexpr int OFF_BAR = OFF_POISON + 3 * D * 4;
-  static constexpr int OFF_SEG = OFF_BAR + 640;                 // Seg [kSegs]
+  static constexpr int OFF_STAGE = D >= 128 ? OFF_Q + (LANES - 1) * QBYTES + 1024 : OFF_RAW + RAWN * RAWB;
+  static constexpr int OFF_POISON = OFF_RAW + RAWN * RAWB + (D >= 128 ? 0 : STAGE);  // int [3][D]
+  static constexpr int OFF_MAX = OFF_POISON + 3 * D * 4;        // float [LANES][2][128]
+  static constexpr int OFF_BAR = OFF_MAX + LANES * 1024;
+  static constexpr int OFF_SEG = OFF_BAR + 512;                 // Seg [kSegs]
   static constexpr int SMEM = OFF_SEG + 512;
 };
 
 // A segment: the block's tiles [lo, hi) of the unit (sequence b, KV head h, query block
 // qb).  One warp works the segments out, the others read them from a ring.
+constexpr int kSegs = 8;
 struct alignas(16) Seg {
   int b, h, qb, lo;
   int hi, npt, nt, alt;     // packed tiles and all tiles of the unit; alt: the lanes take alternate tiles
@@ -147,14 +142,10 @@ struct alignas(16) Seg {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-// Of two: of each lane (PVLAST: all PV of a segment but the last); S and P: of each lane
-// and S buffer; REF: of each lane, 32 rows and S buffer; EMPTY: of each stage and lane.
-// Every phase of a barrier is waited on by whoever waits there at all: parities count.
-enum { B_QFULL = 0, B_ODONE = 2, B_PVLAST = 4, B_DRAIN = 6, B_SFULL = 8, B_PREADY = 12, B_REF = 16,
-       B_KFULL = 32, B_VFULL = 36, B_KEMPTY = 40, B_VEMPTY = 48, B_SEGFULL = 56, B_SEGEMPTY = 64, B_PAIR = 72,
-       B_COUNT = 73 };
-enum { W_TMEM = 146, W_ABORT = 147, W_PFLAG = 148, W_EPI = 149, W_STARTB = 151,
-       W_STARTQ = 152, W_BASE = 154 /* int64 [2] */ };
+enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_PAIR = 8, B_DRAIN = 9, B_KFULL = 10,
+       B_KEMPTY = 14, B_VFULL = 18, B_VEMPTY = 22, B_SEGFULL = 26, B_SEGEMPTY = 34, B_MAX = 42, B_COUNT = 50 };
+enum { W_TMEM = 100, W_ABORT = 101, W_PFLAG = 102, W_EPI = 103, W_STARTB = 105,
+       W_STARTQ = 106, W_BASE = 108 /* int64 */ };
 
 __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   uint32_t v;
@@ -203,7 +194,8 @@ struct Waits {
     set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
     return true;
   }
-  __device__ __forceinline__ bool wait_at(uint32_t b, uint32_t parity) const {
+  __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+    const uint32_t b = bar(i);
     if (ptx::mbar_try_wait(b, parity)) return true;
     const uint32_t t0 = timer_lo();
 #pragma unroll 1
@@ -211,18 +203,13 @@ struct Waits {
       if ((k & 63u) == 0 && late(t0)) return false;
     return true;
   }
-  __device__ __forceinline__ bool wait(int i, uint32_t parity) const { return wait_at(bar(i), parity); }
   // a whole warp waits; the same answer for all its lanes
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
-    return wait_warp_at(bar(i), parity);
+    return __all_sync(0xffffffffu, wait(i, parity));
   }
-  __device__ __forceinline__ bool wait_warp_at(uint32_t b, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait_at(b, parity));
-  }
-  __device__ __forceinline__ void arrive_warp(int i) const { arrive_warp_at(bar(i)); }
-  static __device__ __forceinline__ void arrive_warp_at(uint32_t b) {
+  __device__ __forceinline__ void arrive_warp(int i) const {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(b);
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar(i));
   }
 };
 
@@ -249,7 +236,7 @@ struct Walk {
   int64_t base, x0, x1;
   Run run;
   SeqLens s;
-  int npt, nt, w;  // packed tiles, all tiles, cost of a tile (1 or 2)
+  int npt, nt, w;  // packed tiles, all tiles, cost of a tile
   int lo, hi;
 
   static __device__ __forceinline__ int blocks(const ChunkAttnArgs& a, const Run& run) {
@@ -264,18 +251,18 @@ struct Walk {
     const int lim = seen_of(a, run.n, s.ns + s.npk + s.nres, token_of(a, last));
     npt = (seen_packed(s.ns, s.npk, lim) + C::TN - 1) / C::TN;
     nt = max(1, npt + (seen_f16(s.ns, s.npk, lim) + C::TN - 1) / C::TN);
-    w = C::LANES == 2 && last - qb * C::QB >= 128 ? 2 : 1;
+    w = C::LANES == 2 && last - qb * C::QB >= 128 ? kCostShared : kCostOwn;
   }
+  static __device__ __forceinline__ int64_t unit_cost(int nt, int w) { return (int64_t)nt * w + kCostUnit; }
   static __device__ __forceinline__ int64_t seq_cost(const ChunkAttnArgs& a, int b) {
     const Run run = run_of(a.cu, b, a.total, a.max_len);
-    const int nq = blocks(a, run);
-    if (nq == 0) return 0;
     const SeqLens s = seq_lens_of(a.sink_len, a.packed_len, a.res_len, a.res_head, b, a.Ns, a.cap, a.Nr);
+    const int nq = blocks(a, run);
     int64_t c = 0;
     for (int qb = 0; qb < nq; ++qb) {
       int npt, nt, w;
       tiles(a, run, s, qb, npt, nt, w);
-      c += (int64_t)nt * w;
+      c += unit_cost(nt, w);
     }
     return c * a.Hkv;
   }
@@ -285,10 +272,15 @@ struct Walk {
     s = seq_lens_of(a.sink_len, a.packed_len, a.res_len, a.res_head, b, a.Ns, a.cap, a.Nr);
   }
   __device__ __forceinline__ void range() {
-    // tile k starts at base + k w and is the block's if that is in [x0, x1)
-    lo = x0 <= base ? 0 : (int)((x0 - base + w - 1) >> (w - 1));
-    const int64_t e = x1 - base + w - 1;
-    hi = e <= 0 ? 0 : (int)min((int64_t)nt, e >> (w - 1));
+    // tile k starts at base + kCostUnit + k w and is the block's if that is in [x0, x1)
+    lo = count_below(x0 - base - kCostUnit);
+    hi = count_below(x1 - base - kCostUnit);
+  }
+  // tiles of the unit that start before e
+  __device__ __forceinline__ int count_below(int64_t e) const {
+    if (e <= 0) return 0;
+    if (e >= (int64_t)nt * w) return nt;
+    return (int)(((uint32_t)e + w - 1) / (uint32_t)w);  // (a unit's cost is below 2^31)
   }
   __device__ __forceinline__ void start(const ChunkAttnArgs& a, int b_, int qb_, int64_t base_, int64_t x0_,
                                         int64_t x1_) {
@@ -298,15 +290,15 @@ struct Walk {
     x1 = x1_;
     load_seq(a);
     tiles(a, run, s, qb, npt, nt, w);
-    const int64_t unit = (int64_t)nt * w;
+    const int64_t unit = unit_cost(nt, w);
     h = (int)((x0 - base_) / unit);
     base = base_ + h * unit;
     range();
-    if (lo >= hi) next(a);
+    while (b < a.B && base < x1 && lo >= hi) next(a);
   }
-  __device__ __forceinline__ bool valid(const ChunkAttnArgs& a) const { return b < a.B && base < x1; }
+  __device__ __forceinline__ bool valid(const ChunkAttnArgs& a) const { return b < a.B && base < x1 && lo < hi; }
   __device__ __forceinline__ void next(const ChunkAttnArgs& a) {
-    base += (int64_t)nt * w;
+    base += unit_cost(nt, w);
     if (++h == a.Hkv) {
       h = 0;
       if (++qb >= blocks(a, run)) {
@@ -339,13 +331,13 @@ __device__ __forceinline__ void walk_role(const ChunkAttnArgs& a, const Waits& w
     s.b = -1;
     if (k.valid(a)) {
       s.b = k.b, s.h = k.h, s.qb = k.qb, s.lo = k.lo, s.hi = k.hi, s.npt = k.npt, s.nt = k.nt;
-      s.alt = Cfg<D, BITS>::LANES == 2 && k.w == 1;
+      s.alt = Cfg<D, BITS>::LANES == 2 && k.w == kCostOwn;
       s.c0 = k.run.c0, s.n = k.run.n, s.ns = k.s.ns, s.npk = k.s.npk, s.nres = k.s.nres, s.head = k.s.head;
       s.first_b = s.last_b = 0;
       if (k.lo > 0 || k.hi < k.nt) {
         // block c has the starts from floor(c W / G) on
-        const int64_t end = k.base + (int64_t)(k.nt - 1) * k.w;
-        s.first_b = (int)(((k.base + 1) * G - 1) / W);
+        const int64_t begin = k.base + kCostUnit, end = begin + (int64_t)(k.nt - 1) * k.w;
+        s.first_b = (int)(((begin + 1) * G - 1) / W);
         s.last_b = (int)(((end + 1) * G - 1) / W);
       }
     }
@@ -456,12 +448,9 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-// What four dequantizing warps share, those of the keys (w 0) or of the values (1).  Two
-// warps have a tile, a row to a thread (head_dim 256: four warps, half a row), and the two
-// pairs take the tiles in turns.  A thread's codes are contiguous, and 8 neighbouring
-// lanes store the same piece of 8 rows, which the swizzle puts into 8 different groups of
-// banks.  The raw row goes to registers before its turn, and the next one is on its way
-// while this one is worked on.
+// What the dequantizing warps share.  Thread dt has row dt of a tile (head_dim 256: half
+// of row dt / 2): its codes are contiguous, and 8 neighbouring lanes store the same piece
+// of 8 rows, which the swizzle puts into 8 different banks' groups.
 template <int D, int BITS>
 struct Deq {
   using C = Cfg<D, BITS>;
@@ -470,13 +459,8 @@ struct Deq {
   uint32_t smem;  // base of the block's shared memory
   int* poison;
   const Seg* ring;
-  int w;
-  int dt;         // thread of the four warps
+  int dt;         // thread of the warps that dequantize
   uint32_t seg;   // segments of the block so far
-
-  __device__ __forceinline__ int row() const { return dt % kTile; }
-  __device__ __forceinline__ int part() const { return C::TPR == 2 ? dt / kTile : 0; }
-  __device__ __forceinline__ int pair() const { return C::NP == 2 ? dt / kTile : 0; }
 
   // Values that fp16 does not hold as finite ones take no part in the MMA: a weight of
   // zero would make them NaN in rows that do not see the token.  The first token of the
@@ -493,102 +477,77 @@ struct Deq {
     return true;
   }
 
-  // The cursor of the copies: a tile of a segment.
+  // The cursor of the copies: a half tile of a segment.
   struct Cursor {
-    SegReader seg;
-    int tile = 0, hi = 0, npt = 0;
-    bool open = false;         // seg has been looked at
-    int left = 0;              // packed tokens from the thread's row of the tile on
-    int64_t at = 0;            // contiguous: that row; paged: row of the head in a page
-    const int32_t* pages = nullptr;  // paged: the entry of the thread's row
-    int page = 0;              // ... and what it says, read a tile ahead
+    SegReader at;
+    int tile = -1, w = 0, hi = 0, npt = 0, npk = 0, b = 0;
+    int64_t row0 = 0;  // contiguous: row of the head's token 0; paged: h * 32
   };
 
-  __device__ __forceinline__ uint32_t raw_codes(int slot) const {
-    return smem + C::OFF_RAW + (w * C::RAWN + slot) * C::RAWB + dt * 16;
-  }
-  __device__ __forceinline__ uint32_t raw_params(int slot) const {
-    return smem + C::OFF_RAW + (w * C::RAWN + slot) * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
-  }
-
-  // The thread's raw piece of a tile into ring slot `slot`; a row that is not there
-  // becomes zero codes with zero params, which stand for zeros.
-  __device__ __forceinline__ void fetch(Cursor& c, int slot) {
-    const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
-    bool there = c.left > 0;
-    int64_t at = c.at;
+  // The thread's raw row of a half tile (keys, then values) into ring slot `slot`; a row
+  // that is not there becomes zero codes with zero params, which stand for zeros.
+  __device__ __forceinline__ void fetch(const Cursor& c, int slot) {
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
+    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+    const int p = c.tile * C::TN + dt / C::TPR;
+    bool there = p < c.npk;
+    int64_t row = c.row0 + p;
     if (a.rm.paged && there) {
-      there = c.page >= 0 && c.page < a.rm.npages;
+      const int pg = a.rm.page_of(c.b, p / kPage);
+      there = pg >= 0 && pg < a.rm.npages;
       if (!there) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
-      at += (int64_t)c.page * a.Hkv * kPage;
+      row = (int64_t)pg * a.Hkv * kPage + c.row0 + p % kPage;
     }
     if (there) {
-      const uint8_t* src = a.codes[w] + at * (C::G * C::CB) + part() * C::TB;
+      const uint8_t* src = a.codes[c.w] + row * (C::G * C::CB) + (dt % C::TPR) * C::TB;
       constexpr int N = C::TB % 16 == 0 ? 16 : C::TB % 8 == 0 ? 8 : 4;
 #pragma unroll
       for (int i = 0; i < C::TB / N; ++i)
         cp_async<N>(dc + (i * N / 16) * (kDeqThreads * 16) + i * N % 16, src + i * N);
-      cp_async<C::PB>(dp, a.params[w] + at * C::G + part() * C::GPT);
+      cp_async<C::PB>(dp, a.params[c.w] + row * C::G + (dt % C::TPR) * C::GPT);
     } else {
 #pragma unroll
       for (int i = 0; i < C::UN; ++i) st_shared_v4(dc + i * (kDeqThreads * 16), make_uint4(0, 0, 0, 0));
 #pragma unroll
-      for (int i = 0; i < C::GPT; ++i) sts(dp + 4 * i, 0);
-    }
-    // on to the pair's next tile; contiguous rows further on are called into L2
-    c.left -= C::NP * C::TN;
-    if (a.rm.paged) {
-      c.pages += C::NP * C::TN / kPage;
-      if (c.left > 0) c.page = __ldg(c.pages);
-    } else {
-      c.at += C::NP * C::TN;
-      if (c.left > C::TN * C::NP) {
-        const int64_t far = c.at + C::NP * C::TN;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes[w] + far * (C::G * C::CB) + part() * C::TB));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.params[w] + far * C::G));
-      }
+      for (int i = 0; i < C::GPT; ++i) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dp + 4 * i), "r"(0) : "memory");
     }
   }
 
   // Shared address of the thread's row in a tile at dst, with the row's swizzle in its
-  // low bits: piece c of the thread's panel p is at (this ^ (c << 4)) + p * KP.
+  // low bits: piece c of panel p is at (this ^ (c << 4)) + p * KP.
   __device__ __forceinline__ uint32_t row_addr(uint32_t dst) const {
-    const int r = row();
-    return dst + part() * (C::GPT / 2) * C::KP + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
+    const int r = dt / C::TPR;
+    return dst + (dt % C::TPR) * (C::GPT / 2) * C::KP + r * C::RB + ((C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4);
   }
-  __device__ __forceinline__ int column(int g, int c) const { return (part() * C::GPT + g) * 32 + c * 8; }
+  __device__ __forceinline__ int column(int g, int c) const { return ((dt % C::TPR) * C::GPT + g) * 32 + c * 8; }
 
-  // The thread's raw row in registers.
-  struct Raw {
-    uint32_t code[C::UN * 4], prm[C::GPT];
-  };
-  __device__ __forceinline__ void take(Raw& x, int slot) const {
-    const uint32_t dc = raw_codes(slot), dp = raw_params(slot);
+  // A fetched half tile as fp16 at `dst`.  first: logical place of the tile's first token.
+  __device__ __forceinline__ bool packed_tile(int first, int w, int slot, uint32_t dst) {
+    constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
+    const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
+    uint32_t raw[C::UN * 4], prm[C::GPT];
 #pragma unroll
     for (int i = 0; i < C::UN; ++i) {
       const uint4 v = ld_shared_v4(dc + i * (kDeqThreads * 16));
-      x.code[4 * i] = v.x, x.code[4 * i + 1] = v.y, x.code[4 * i + 2] = v.z, x.code[4 * i + 3] = v.w;
+      raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i) x.prm[i] = lds(dp + 4 * i);
-  }
-
-  // A raw row as fp16 at `dst`.  token: its logical place.
-  __device__ __forceinline__ bool packed_row(const Raw& x, int token, uint32_t dst) {
-    constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
+    for (int i = 0; i < C::GPT; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(prm[i]) : "r"(dp + 4 * i) : "memory");
     const uint32_t at = row_addr(dst);
     uint32_t rare = 0;
 #pragma unroll
     for (int g = 0; g < C::GPT; ++g) {
-      const uint32_t s2 = ptx::prmt(x.prm[g], x.prm[g], 0x1010), m2 = ptx::prmt(x.prm[g], x.prm[g], 0x3232);
+      const uint32_t s2 = ptx::prmt(prm[g], prm[g], 0x1010), m2 = ptx::prmt(prm[g], prm[g], 0x3232);
       // the group's largest value; only where it is not finite can any value be so
       if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) rare |= 1u << g;
-      uint32_t c8[4];
-      code_words<BITS>(x.code, g, c8);
+      uint32_t x[4];
+      code_words<BITS>(raw, g, x);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t y[4];
-        codes_f16<BITS>(c8[c], y);
+        codes_f16<BITS>(x[c], y);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(y[j], s2, m2);
         st_shared_v4((at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP, make_uint4(y[0], y[1], y[2], y[3]));
@@ -601,9 +560,8 @@ struct Deq {
     for (int e = 0; e < 32 * C::GPT; ++e) {
       const int g = e >> 5;
       if (!((rare >> g) & 1u)) continue;
-      uint32_t pg = x.prm[0];
-#pragma unroll
-      for (int i = 1; i < C::GPT; ++i) pg = g == i ? x.prm[i] : pg;
+      uint32_t pg;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pg) : "r"(dp + 4 * g) : "memory");
       const uint32_t ea = (at ^ (((g & 1) * 4 + ((e >> 3) & 3)) << 4)) + (g / 2) * C::KP + 2 * (e & 7);
       unsigned short hv;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
@@ -612,7 +570,7 @@ struct Deq {
         hv = (hv & 0x8000u) | 0x7bffu;
       else if (w == 0)
         continue;
-      else if (note(column(g, 0) + (e & 31), token, hv))
+      else if (note(column(g, 0) + (e & 31), first + dt / C::TPR, hv))
         hv = 0;
       else
         return false;
@@ -623,10 +581,10 @@ struct Deq {
 
   __device__ __forceinline__ int ring_slot(int j) const { return j < a.Nr ? j : j - a.Nr; }  // j < 2 Nr
 
-  // A tile of fp16 tokens (sink, then window): rows f0 .. of their line.
-  __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, uint32_t dst) {
+  // A half tile of fp16 tokens (sink, then window): rows f0 .. of their line.
+  __device__ __forceinline__ bool f16_tile(const Seg& k, int f0, int w, uint32_t dst) {
     const int64_t bh = (int64_t)k.b * a.Hkv + k.h;
-    const int f = f0 + row(), n = k.ns + k.nres;
+    const int f = f0 + dt / C::TPR, n = k.ns + k.nres;
     const __half* src = a.q;  // (not read)
     if (f < k.ns)
       src = a.sink[w] + (bh * a.Ns + f) * D;
@@ -668,76 +626,59 @@ struct Deq {
   __device__ __forceinline__ void run() {
     SegReader k;
     Cursor c;
-    c.tile = pair();
     bool ok = true, more = true;
-    // The pair's next tile into ring slot `slot`.  c.tile is its place in segment c.seg, or
-    // past that segment's end by as many tiles as there are to skip in the next.
+    // the next half tile of the line into its ring slot
     auto fetch_next = [&](int slot) {
-      while (more && c.tile >= c.hi) {
-        if (c.open) ++c.seg.i;
-        c.open = true;
-        ok = ok && __all_sync(0xffffffffu, c.seg.wait(wt));
-        const Seg& s = c.seg.get(ring);
+      if (more && c.tile < 0) {
+        ok = ok && __all_sync(0xffffffffu, c.at.wait(wt));
+        const Seg& s = c.at.get(ring);
         more = ok && s.b >= 0;
-        if (!more) break;
-        c.tile += s.lo - c.hi, c.hi = s.hi, c.npt = s.npt;
-        const int p = c.tile * C::TN + row();
-        c.left = s.npk - p;
-        if (a.rm.paged) {
-          c.at = (int64_t)s.h * kPage + p % kPage;
-          c.pages = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + p / kPage;
-          if (c.left > 0) c.page = __ldg(c.pages);
-        } else {
-          c.at = ((int64_t)s.b * a.Hkv + s.h) * a.cap + p;
+        if (more) {
+          c.tile = s.lo, c.hi = s.hi, c.npt = s.npt, c.npk = s.npk, c.b = s.b;
+          c.row0 = a.rm.paged ? (int64_t)s.h * kPage : ((int64_t)s.b * a.Hkv + s.h) * a.cap;
         }
       }
       if (more) {
         if (c.tile < c.npt) fetch(c, slot);
-        c.tile += C::NP;
+        c.w ^= 1;
+        if (c.w == 0 && ++c.tile == c.hi) {
+          ++c.at.i;
+          c.tile = -1;
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint32_t kv = 0;             // tiles so far
-    uint32_t used = 0, par = 0;  // by stage and lane: the lane has the stage; parity of its release
+    uint32_t kv = 0;  // tiles so far
     int slot = 0;
+    // RAWN - 1 half tiles ahead: a free slot is filled before the oldest is taken
 #pragma unroll 1
-    for (int i = 0; i < C::RAWN; ++i) fetch_next(i);
+    for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
     for (; ok; ++k.i, ++seg) {
       ok = ok && __all_sync(0xffffffffu, k.wait(wt));
       if (!ok) break;
       const Seg& s = k.get(ring);
       if (s.b < 0) break;
-      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns, alt = s.alt;
-      for (int t = lo + (C::NP == 2 ? (pair() ^ kv) & 1 : 0); t < hi; t += C::NP) {
-        const uint32_t x = kv + (t - lo);
-        const int stage = x % C::ST;
+      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns;
+      for (int h = 2 * lo; h < 2 * hi; ++h) {
+        fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
+        const int t = h >> 1, w = h & 1;
+        const int stage = kv % C::ST;
         const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
-        Raw raw;
+        ok = ok && wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + stage, ((kv / C::ST) & 1) ^ 1);
+        if (!ok) break;
         if (t < npt) {
           asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-          take(raw, slot);
+          ok = packed_tile(ns + t * C::TN, w, slot, dst);
+        } else {
+          ok = f16_tile(s, (t - npt) * C::TN, w, dst);
         }
-        fetch_next(slot);
-        if (++slot == C::RAWN) slot = 0;
-        // the lanes that had the stage before have read it
-#pragma unroll
-        for (int l = 0; l < C::LANES; ++l) {
-          const int bit = 2 * stage + l;
-          if (ok && ((used >> bit) & 1u)) {
-            ok = wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + bit, (par >> bit) & 1u);
-            par ^= 1u << bit;
-          }
-        }
-        if (!ok) break;
-        used &= ~(3u << (2 * stage));
-        used |= (alt ? 1u << ((t - lo) & 1) : C::LANES == 2 ? 3u : 1u) << (2 * stage);
-        ok = t < npt ? packed_row(raw, ns + t * C::TN + row(), dst) : f16_tile(s, (t - npt) * C::TN, dst);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::fence_proxy_async_shared();
         wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
+        if (++slot == C::RAWN) slot = 0;
+        kv += w;
       }
-      kv += hi - lo;
       wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -748,88 +689,74 @@ struct Deq {
 
 template <int D, int BITS>
 __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt, uint32_t smem, uint32_t tmem,
-                                         const Seg* ring, int lane) {
+                                         const Seg* ring) {
   using C = Cfg<D, BITS>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
-  const uint32_t s_at = tmem + C::S0 + lane * 2 * C::TN, o_at = tmem + C::O0 + lane * C::OSTEP;
-  const uint64_t kd0 = tc5::smem_desc(smem + C::OFF_K, 16, 8 * C::RB, C::SWZ);
-  const uint64_t vd0 = tc5::smem_desc(smem + C::OFF_V, C::KP, 8 * C::RB, C::SWZ);
   SegReader k;
-  uint32_t qn = 0;           // phases of the lane's barrier of Q
-  uint32_t nqk = 0, npv = 0; // the lane's QK^T and PV so far: S buffers take turns
-  uint32_t kv = 0;           // tiles so far
+  uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
+  uint32_t kv = 0;                          // tiles so far
   bool ok = true;
   for (;; ++k.i) {
     if (!k.wait(wt) || k.get(ring).b < 0) break;
     const bool alt = k.get(ring).alt;
     const int n = k.get(ring).hi - k.get(ring).lo;
     ptx::mbar_arrive(wt.bar(B_SEGEMPTY + k.i % kSegs));
-    // the lane's tiles: all, or every second one (with Q of lane 0)
-    const int step = alt ? 2 : 1, t0 = alt ? lane : 0;
-    // (the barrier of lane 1 completes in the segments that have tiles for it, and is
-    // waited on in just these: no phase is passed over)
-    if (t0 < n) ok = wt.wait(B_QFULL + lane, qn++ & 1);
-    const uint64_t qd =
-        tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
-    // tile x of the line (of all the block's segments) is in stage x % ST
-    auto qk = [&](uint32_t x) {
-      const uint32_t buf = nqk & 1;
-      const uint64_t kd = kd0 + (x % C::ST) * (C::KBYTES >> 4);
-      const uint32_t to = s_at + buf * C::TN;
+    const int U = C::LANES == 2 && !alt ? 2 * n : n;
+    ok = wt.wait(B_QFULL, qn[0]++ & 1);
+    if (ok && C::LANES == 2 && !alt) ok = wt.wait(B_QFULL + 1, qn[1]++ & 1);
+    if (!ok) break;
+    auto tile = [&](int u) { return C::LANES == 2 && !alt ? u >> 1 : u; };
+    auto lane_of = [&](int u) { return C::LANES == 2 ? u & 1 : 0; };
+    // the step's tile is read by no later step
+    auto releases = [&](int u) { return C::LANES == 1 || alt || (u & 1); };
+    auto qk = [&](int u) -> bool {
+      const uint32_t t = kv + tile(u);
+      const int stage = t % C::ST, lane = lane_of(u);
+      if ((C::LANES == 1 || alt || lane == 0) && !wt.wait(B_KFULL + stage, (t / C::ST) & 1)) return false;
+      tc5::fence_after();
+      const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
+      const uint64_t kd = tc5::smem_desc(smem + C::OFF_K + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         constexpr int PW = C::PW;
         const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
-        tc5::mma_ss(to, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4), kIdescQK, j > 0);
+        tc5::mma_ss(tmem + C::S0 + lane * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+                    kIdescQK, j > 0);
       }
-      tc5::commit(wt.bar(B_SFULL + 2 * lane) + 8 * buf);
-      tc5::commit(wt.bar(B_KEMPTY + lane) + 16 * (x % C::ST));
-      ++nqk;
+      tc5::commit(wt.bar(B_SFULL + lane));
+      if (releases(u)) tc5::commit(wt.bar(B_KEMPTY + stage));
+      return true;
     };
-    const uint32_t end = kv + n;
-    for (uint32_t x = kv + t0; ok && x < end && x < kv + t0 + 2 * step; x += step) {
-      ok = wt.wait_at(wt.bar(B_KFULL) + 8 * (x % C::ST), (x / C::ST) & 1);
+    for (int u = 0; ok && u < C::LANES && u < U; ++u) ok = qk(u);
+    for (int u = 0; ok && u < U; ++u) {
+      const uint32_t t = kv + tile(u);
+      const int stage = t % C::ST, lane = lane_of(u);
+      ok = wt.wait(B_PREADY + lane, pn[lane]++ & 1);
+      if (ok && (C::LANES == 1 || alt || lane == 0)) ok = wt.wait(B_VFULL + stage, (t / C::ST) & 1);
       if (!ok) break;
       tc5::fence_after();
-      qk(x);
-    }
-#pragma unroll 1
-    for (uint32_t x = kv + t0; ok && x < end; x += step) {
-      // V and P of this tile, and K of the one whose S comes after: asked for at once (the
-      // tensor cores idle while this thread waits)
-      const uint32_t y = x + 2 * step, buf = npv & 1;
-      const uint32_t vb = wt.bar(B_VFULL) + 8 * (x % C::ST), kb = wt.bar(B_KFULL) + 8 * (y % C::ST),
-                     pb = wt.bar(B_PREADY + 2 * lane) + 8 * buf;
-      const uint32_t vp = (x / C::ST) & 1, kp = (y / C::ST) & 1, pp = (npv >> 1) & 1;
-      const bool more = y < end;
-      const bool v_ok = ptx::mbar_try_wait(vb, vp), k_ok = !more || ptx::mbar_try_wait(kb, kp),
-                 p_ok = ptx::mbar_try_wait(pb, pp);
-      if (!(v_ok && k_ok && p_ok))
-        ok = wt.wait_at(vb, vp) && (!more || wt.wait_at(kb, kp)) && wt.wait_at(pb, pp);
-      if (!ok) break;
-      tc5::fence_after();
-      const uint64_t vd = vd0 + (x % C::ST) * (C::KBYTES >> 4);
-      const uint32_t from = s_at + buf * C::TN;
-      // the lane's first tile of the segment starts O
-      tc5::mma_ts(o_at, from, vd, kIdescPV, x != kv + t0);
+      const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+      const bool acc = u >= C::LANES;  // the lane's first tile of the segment starts O
 #pragma unroll
-      for (int j = 1; j < C::TN / 16; ++j)
-        tc5::mma_ts(o_at, from + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, true);
-      // into the buffer of this tile's P: after PV in the tensor cores' order
-      if (more)
-        qk(y);
+      for (int j = 0; j < C::TN / 16; ++j) {
+        // P of each half of the tokens lies at the start of that half of S
+        const int col = j * 16 / C::HC * C::HC + (j * 16 % C::HC) / 2;
+        tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + col,
+                    vd + ((j * 16 * C::RB) >> 4), kIdescPV, acc || j > 0);
+      }
+      if (releases(u)) tc5::commit(wt.bar(B_VEMPTY + stage));
+      if (u + C::LANES < U)
+        ok = qk(u + C::LANES);  // after PV(u) in the tensor cores' order: S may take P's place
       else
-        tc5::commit(wt.bar((x + step < end ? B_PVLAST : B_ODONE) + lane));
-      tc5::commit(wt.bar(B_VEMPTY + lane) + 16 * (x % C::ST));
-      ++npv;
+        tc5::commit(wt.bar(B_ODONE + lane));
     }
     if (!ok) break;
     kv += n;
   }
   // nothing of this thread's is in flight when TMEM is freed
-  tc5::commit(wt.bar(B_DRAIN + lane));
-  wt.wait(B_DRAIN + lane, 0);
+  tc5::commit(wt.bar(B_DRAIN));
+  wt.wait(B_DRAIN, 0);
 }
 
 // ------------------------------------------------------------------ softmax ---
@@ -847,18 +774,14 @@ struct Soft {
   const Waits& wt;
   const uint32_t smem, tmem;  // tmem: with the warp's lanes
   uint32_t phases;            // parity bits of the barriers that the thread waits on
-  const uint32_t tid;
-  const uint32_t s_tm;        // TMEM: the group's S buffer
-  const uint32_t ref_at;      // shared: the thread's reference maximum (^ 512: the other group's)
-  uint32_t at_seg;            // place in the ring of segments
-  uint32_t nt;                // tiles of the lane so far: its two groups take turns
+  uint32_t at_seg, seg;       // place in the ring of segments, segments so far
 
-  enum { P_O = 1, P_PAIR = 2, P_LAST = 3 };
+  enum { P_S = 0, P_O = 1, P_PAIR = 2, P_MAX = 3, P_STARTED = 4 };
 
-  // Accumulator, group (and half of O's columns), and row: by the thread.
-  __device__ __forceinline__ int lane() const { return tid >> 8; }
-  __device__ __forceinline__ int half() const { return (tid >> 7) & 1; }
-  __device__ __forceinline__ int r() const { return tid & 127; }
+  // Accumulator, half of its columns, and row: by the thread.
+  static __device__ __forceinline__ int lane() { return threadIdx.x >> 8; }
+  static __device__ __forceinline__ int half() { return (threadIdx.x >> 7) & 1; }
+  static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
 
   __device__ __forceinline__ bool wait(int bar, int bit) {
     const bool ok = wt.wait_warp(bar, (phases >> bit) & 1);
@@ -869,6 +792,14 @@ struct Soft {
     wt.arrive_warp(B_PAIR);
     return wait(B_PAIR, P_PAIR);
   }
+  // with the warp that has the same rows and the other half of the columns
+  __device__ __forceinline__ bool row_sync() {
+    const int b = B_MAX + lane() * 4 + (r() >> 5);
+    wt.arrive_warp(b);
+    return wait(b, P_MAX);
+  }
+  __device__ __forceinline__ uint32_t xmax() const { return smem + C::OFF_MAX + lane() * 1024; }
+
   // The current segment, read field by field.
   struct Ref {
     uint32_t at;
@@ -931,100 +862,88 @@ struct Soft {
     }
     ptx::fence_proxy_async_shared();
     wt.arrive_warp(B_QFULL + lane());
-    // with alternating lanes the rows are lane 1's too, if there is a tile for it
-    if (k.alt() && k.hi() - k.lo() > 1) wt.arrive_warp(B_QFULL + 1);
   }
 
-  // The weights of 16 scores (the visible ones) against the reference (off = -m c), two to a
-  // register, and their sum on top of `sum`.
-  __device__ __forceinline__ void weights(float (&s)[16], uint32_t (&p)[8], uint64_t c2, uint64_t off2,
-                                          uint64_t& sum, bool masked, int visible) const {
-    if (masked) {
+  // Hides what the row does not see of 32 tokens (a page: `bad` all of them); the largest
+  // score that is left.
+  static __device__ __forceinline__ float mask(float (&s)[32], int visible, uint32_t bad) {
+    const int v = bad ? 0 : visible;
+    float x = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] = j < visible ? s[j] : -INFINITY;
+    for (int j = 0; j < 32; ++j) {
+      s[j] = j < v ? s[j] : -INFINITY;
+      x = fmaxf(x, s[j]);
     }
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
-      const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x))), e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
-      sum = add_f32x2(sum, pack_f32x2(e0, e1));
-      p[i / 2] = ptx::pack_h2(e0, e1);
-    }
+    return x;
   }
 
-  // One tile, the lane's n-th: P in S's place, m and l brought up to date.  visible:
-  // tokens of the tile that the row sees (a prefix); bad: pages (halves) left out.
-  // S is read twice, for its maximum and for the weights: 64 scores at once do not fit the
-  // registers, and beside the tiles L1 is so small that a spilled register is a trip to
-  // L2.  The reference is the lane's: the group that has tile n takes it over from the
-  // other, which had n - 1, and passes it on before it works out its weights.
-  __device__ __forceinline__ bool tile(int visible, uint32_t bad, bool first, bool last, float& m, float& l) {
-    const bool masked = __any_sync(0xffffffffu, visible < C::TN) || bad;
-    float mt = -INFINITY;
+  // One tile: the weights of the group's half of S's row into TMEM, m (the same in both
+  // groups) and l (each group's own) brought up to date.  visible: columns of the half
+  // that the row sees (a prefix); bad: pages of it left out.
+  __device__ __forceinline__ bool tile(int visible, uint32_t bad, float& m, float& l) {
+    const uint32_t sa = tmem + C::S0 + lane() * C::TN + half() * C::HC;
+    // 32 scores at a time, read again after the maximum is known: 64 at once and what
+    // else lives do not fit the registers, and the small L1 beside the tiles makes a
+    // spilled register a trip to L2
+    float s[32];
+    const bool masked = __any_sync(0xffffffffu, visible < C::HC) || bad;
+    float mine = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < C::TN; h += 32) {
-      float s[32], mx;
-      tc5::ld32_max(s_tm + h, reinterpret_cast<uint32_t*>(s), mx);
+    for (int h = C::HC - 32; h >= 0; h -= 32) {
+      float mx;
+      tc5::ld32_max(sa + h, reinterpret_cast<uint32_t*>(s), mx);
       tc5::wait_ld();
       tc5::pin32(reinterpret_cast<uint32_t*>(s));
       asm volatile("" : "+f"(mx));
-      if (masked) {
-        const int v = (bad >> (h / 32)) & 1u ? 0 : visible - h;
-        mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, j < v ? s[j] : -INFINITY);
-      }
-      mt = fmaxf(mt, mx);
+      if (masked) mx = mask(s, visible - h, (bad >> (h / 32)) & 1u);
+      mine = fmaxf(mine, mx);
     }
-    const uint32_t bar = wt.bar(B_REF) + (lane() * 4 + (r() >> 5)) * 16;
-    float was = -INFINITY;  // the lane's reference
-    if (!first) {
-      if (!wt.wait_warp_at(bar + 8 * (half() ^ 1), ((nt - 1) >> 1) & 1)) return false;
-      was = ldsf(ref_at ^ 512);
-    }
-    const bool moves = (mt - was) * a.scale_log2 > 8.0f;
-    const float mn = moves ? mt : was;
-    stsf(ref_at, mn);
-    wt.arrive_warp_at(bar + 8 * half());
-    if (__any_sync(0xffffffffu, moves) && !first) {
-      const float f = moves ? ptx::ex2_ftz((was - mn) * a.scale_log2) : 1.0f;
-      // O is still when the last tile's PV is done (the next tile's S is made after it) and
-      // this one's P is not there
-      if (!(last ? wt.wait_warp(B_PVLAST + lane(), (phases >> P_LAST) & 1)
-                 : wt.wait_warp_at(wt.bar(B_SFULL) + 16 * lane() + 8 * (half() ^ 1), ((nt + 1) >> 1) & 1)))
-        return false;
-      tc5::fence_after();
-      const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP;
+    // the row's maximum: of this half and of the other group's
+    stsf(xmax() + half() * 512 + r() * 4, mine);
+    if (!row_sync()) return false;
+    const float mn = fmaxf(m, fmaxf(mine, ldsf(xmax() + (half() ^ 1) * 512 + r() * 4)));
+    const bool moves = (mn - m) * a.scale_log2 > 8.0f;
+    if (__any_sync(0xffffffffu, moves)) {
+      const float f = moves ? ptx::ex2_ftz((m - mn) * a.scale_log2) : 1.0f;
+      if (moves) m = mn;
+      l *= f;
+      if (phases & (1u << P_STARTED)) {
+        const uint32_t oa = tmem + C::O0 + lane() * C::OSTEP + half() * C::HD;
 #pragma unroll 1
-      for (int i = 0; i < D; i += 16) {
-        uint32_t o[16];
-        tc5::ld16(oa + i, o);
-        tc5::wait_ld();
-        tc5::pin16(o);
+        for (int i = 0; i < C::HD; i += 8) {
+          uint32_t o[8];
+          tc5::ld8(oa + i, o);
+          tc5::wait_ld();
+          tc5::pin8(o);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-        tc5::st16(oa + i, o);
+          for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc5::st8(oa + i, o);
+        }
       }
     }
-    if (m != mn) l *= ptx::ex2_ftz((m - mn) * a.scale_log2);  // (m below mn)
-    m = mn;
     const float off = m == -INFINITY ? 0.0f : -m * a.scale_log2;
     const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
-    uint64_t sum = pack_f32x2(l, 0.0f);
-    float s[2][16];
-    tc5::ld16(s_tm, reinterpret_cast<uint32_t*>(s[0]));
+    uint64_t sum2 = pack_f32x2(l, 0.0f);
 #pragma unroll
-    for (int h = 0; h < C::TN; h += 16) {
-      float (&now)[16] = s[(h / 16) & 1];
-      uint32_t p[8];
-      tc5::wait_ld();
-      tc5::pin16(reinterpret_cast<uint32_t*>(now));
-      if (h + 16 < C::TN) tc5::ld16(s_tm + h + 16, reinterpret_cast<uint32_t*>(s[(h / 16 + 1) & 1]));
-      weights(now, p, c2, off2, sum, masked, (bad >> (h / 32)) & 1u ? 0 : visible - h);
-      // P's columns lie below those of the scores that are still to be read
-      tc5::st8(s_tm + h / 2, p);
+    for (int h = 0; h < C::HC; h += 32) {
+      if (h > 0) {
+        tc5::ld32(sa + h, reinterpret_cast<uint32_t*>(s));
+        tc5::wait_ld();
+        tc5::pin32(reinterpret_cast<uint32_t*>(s));
+        if (masked) mask(s, visible - h, (bad >> (h / 32)) & 1u);
+      }
+      uint32_t p[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t x = fma_f32x2(pack_f32x2(s[i], s[i + 1]), c2, off2);
+        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
+        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
+        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
+        p[i / 2] = ptx::pack_h2(e0, e1);
+      }
+      tc5::st16(sa + h / 2, p);
     }
-    l = __uint_as_float(lo_bits(sum)) + __uint_as_float(hi_bits(sum));
+    l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
     tc5::wait_st();
     return true;
   }
@@ -1040,8 +959,7 @@ struct Soft {
       if (!(up || down || nan)) continue;
       const float v = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
       if (!whole) {
-        float4* dst = a.o_part + ((int64_t)slot * (D / 4) + c / 4) * C::QB + row;
-        __stcg(reinterpret_cast<float*>(dst) + (c & 3), v);
+        __stcg(reinterpret_cast<float*>(a.o_part) + ((int64_t)slot * C::QB + row) * D + c, v);
         continue;
       }
       int e = 0;  // the element that is stored at this column
@@ -1076,68 +994,56 @@ struct Soft {
     return l == 0.0f ? 0.0f : 1.0f / l;
   }
 
-  // The group's tiles of a segment: the reference m of the last of them and l.
-  __device__ __forceinline__ bool tiles(float& m, float& l, bool& any) {
+  // The tiles of a segment: m and l of the row's columns.
+  __device__ __forceinline__ bool tiles(float& m, float& l) {
     m = -INFINITY;
     l = 0.0f;
-    int t, end, npt, step, row;
-    bool live, mine;
-    {
-      const Ref k = ref();
-      row = block_row(k);
-      live = (row & ~31) < block_rows(k);
-      mine = row < block_rows(k);
-      step = k.alt() ? 2 : 1;
-      t = k.lo() + (k.alt() ? lane() : 0);
-      end = k.hi();
-      npt = k.npt();
-    }
-    any = t < end;
-    const int t0 = t;
-    const uint32_t nt0 = nt;
-    if ((nt & 1) != (uint32_t)half()) t += step, ++nt;
-    int visible = 0, left = 0;  // tokens that the row sees from t on; tiles to go with it
+    phases &= ~(1u << P_STARTED);
+    // packed tiles, then fp16 ones: t and its end, and the tokens that the row sees from t on
 #pragma unroll 1
-    for (; t < end; t += 2 * step, nt += 2) {
-      if (--left < 0) {
-        // the first packed tile, then the first fp16 one
+    for (int f16 = 0; f16 < 2; ++f16) {
+      int t, end, visible;
+      bool live;
+      {
         const Ref k = ref();
-        const bool f16 = t >= npt;
-        left = ((f16 ? end : min(npt, end)) - t - 1) / (2 * step);
+        const int row = block_row(k), rows = block_rows(k), npt = k.npt(), alt = k.alt();
+        t = k.lo() + (alt ? lane() : 0);
+        // (the lane's first tile that is not packed)
+        if (f16 && t < npt) t += alt ? (npt - t + 1) & ~1 : npt - t;
+        end = f16 ? k.hi() : min(k.hi(), npt);
+        live = (row & ~31) < rows;
         visible = 1 << 30;  // rows that are not there need no mask
-        if (mine) {
+        if (row < rows) {
           const int ns = k.ns(), npk = k.npk();
           const int lim = seen_of(a, k.n(), ns + npk + k.nres(), token_of(a, k.qb() * C::QB + row));
           visible = (f16 ? seen_f16(ns, npk, lim) + npt * C::TN : seen_packed(ns, npk, lim)) - t * C::TN;
+          visible -= half() * C::HC;
         }
-      } else if (mine) {
-        visible -= 2 * step * C::TN;
       }
-      uint32_t bad = 0;
-      if (a.rm.paged && t < npt) {
-        const Ref k = ref();
-        const int j = t * (C::TN / kPage) + (r() & 1);
-        bool out = false;
-        if ((r() & 31) < C::TN / kPage && j * kPage < k.npk()) {
-          const int pg = a.rm.page_of(k.b(), j);
-          out = pg < 0 || pg >= a.rm.npages;
+#pragma unroll 1
+      while (t < end) {
+        uint32_t bad = 0;
+        if (a.rm.paged && !f16) {
+          const Ref k = ref();
+          const int j = (t * C::TN + half() * C::HC) / kPage + (r() & 31);
+          bool out = false;
+          if ((r() & 31) < C::HC / kPage && j * kPage < k.npk()) {
+            const int pg = a.rm.page_of(k.b(), j);
+            out = pg < 0 || pg >= a.rm.npages;
+          }
+          bad = __ballot_sync(0xffffffffu, out);
         }
-        bad = __ballot_sync(0xffffffffu, out);
+        if (!wait(B_SFULL + lane(), P_S)) return false;
+        tc5::fence_after();
+        if (live && !tile(visible, bad, m, l)) return false;
+        tc5::fence_before();
+        wt.arrive_warp(B_PREADY + lane());
+        phases |= 1u << P_STARTED;
+        const int step = ref().alt() ? 2 : 1;
+        t += step;
+        if (visible < (1 << 29)) visible -= step * C::TN;
       }
-      const uint32_t bar = wt.bar(B_SFULL) + 16 * lane() + 8 * half();
-      if (!wt.wait_warp_at(bar, (nt >> 1) & 1)) return false;
-      tc5::fence_after();
-      if (live) {
-        if (!tile(visible, bad, t == t0, t + step >= end, m, l)) return false;
-      } else {
-        wt.arrive_warp_at(wt.bar(B_REF) + (lane() * 4 + (r() >> 5)) * 16 + 8 * half());
-      }
-      tc5::fence_before();
-      wt.arrive_warp_at(bar + 8 * (B_PREADY - B_SFULL));
     }
-    const int n = any ? (end - t0 + step - 1) / step : 0;
-    nt = nt0 + n;
-    if (n > 1) phases ^= 1u << P_LAST;
     return true;
   }
 
@@ -1147,8 +1053,8 @@ struct Soft {
     load_q();
     while (true) {
       float m, l;
-      bool any;
-      if (!tiles(m, l, any)) return false;
+      if (!tiles(m, l)) return false;
+      const bool any = (phases >> P_STARTED) & 1;
       if (any && !wait(B_ODONE + lane(), P_O)) return false;
       tc5::fence_after();
 
@@ -1156,31 +1062,30 @@ struct Soft {
       const bool alt = k.alt();
       const int row = block_row(k), rows = block_rows(k);
       const bool live = (row & ~31) < rows;
-      // m and l of both groups; l through the first KiB of the lane's Q, which no MMA reads
-      // once both lanes are done.  The lane's reference is the later one, the larger.
-      const uint32_t xl = smem + C::OFF_Q + lane() * C::QBYTES + r() * 4;
-      if (!pair_sync()) return false;
-      stsf(ref_at, m);
-      stsf(xl + half() * 512, l);
-      if (!pair_sync()) return false;
-      {
-        const float mo = ldsf(ref_at ^ 512), lo = ldsf(xl + (half() ^ 1) * 512), mm = fmaxf(m, mo);
-        const float fa = m == mm ? 1.0f : ptx::ex2_ftz((m - mm) * a.scale_log2);
-        const float fb = mo == mm ? 1.0f : ptx::ex2_ftz((mo - mm) * a.scale_log2);
-        l = l * fa + lo * fb;
-        m = mm;
+      const bool whole = k.lo() == 0 && k.hi() == k.nt();
+      // With alternating lanes, lane 1's accumulator of a whole unit goes through shared
+      // memory (its Q) to lane 0, 16 columns of each half at a time, with its rows' m and l.
+      const bool pass = alt && whole && k.hi() - k.lo() > 1;
+      // no MMA reads Q any more (with alternating lanes once the other lane is done too): the
+      // next segment's, under this one's epilogue
+      if (alt && !pair_sync()) return false;
+      ++at_seg;
+      if (!wait_seg()) return false;
+      const bool more = ref().b() >= 0;
+      if (more && !pass) load_q();
+      // l of both groups
+      if (live) {
+        stsf(xmax() + half() * 512 + r() * 4, l);
+        if (!row_sync()) return false;
+        l += ldsf(xmax() + (half() ^ 1) * 512 + r() * 4);
       }
       const bool noted = wt.word(W_PFLAG) != 0;
-      const bool whole = k.lo() == 0 && k.hi() == k.nt();
       const int slot = 2 * block + (k.lo() == 0);
       float inv = 0.0f;
       int64_t at = 0;
-      // With alternating lanes, lane 1's accumulator of a whole unit goes through shared
-      // memory to lane 0, 16 columns of each half at a time, with its rows' m and l.
-      const bool pass = alt && whole && k.hi() - k.lo() > 1;
       float f0 = 1.0f, f1 = 0.0f;
       if (pass) {
-        const uint32_t x1 = smem + C::OFF_Q + (C::LANES - 1) * C::QBYTES + 1024 + r() * 4;
+        const uint32_t x1 = smem + C::OFF_Q + (C::LANES - 1) * C::QBYTES + r() * 4;
         if (lane() == 1 && half() == 0 && live) {
           stsf(x1, m);
           stsf(x1 + 512, l);
@@ -1231,10 +1136,10 @@ struct Soft {
         if (mine && whole) {
           store16(o, inv, at + col);
         } else if (mine) {
-          float4* dst = a.o_part + ((int64_t)slot * (D / 4) + col / 4) * C::QB + prow;
+          float4* dst = a.o_part + ((int64_t)slot * C::QB + prow) * (D / 4) + col / 4;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            __stcg(dst + j * C::QB, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+            __stcg(dst + j, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         }
         __syncwarp();
       }
@@ -1245,8 +1150,8 @@ struct Soft {
         }
         // the notes have been read: clean them
         if (!pair_sync()) return false;
-        for (int i = tid; i < 3 * D; i += C::SMW * 32) sts(smem + C::OFF_POISON + 4 * i, 0x7fffffff);
-        if (tid == 0) wt.set_word(W_PFLAG, 0);
+        for (int i = threadIdx.x; i < 3 * D; i += C::SMW * 32) sts(smem + C::OFF_POISON + 4 * i, 0x7fffffff);
+        if (threadIdx.x == 0) wt.set_word(W_PFLAG, 0);
         if (!pair_sync()) return false;
       }
       tc5::fence_before();
@@ -1255,14 +1160,11 @@ struct Soft {
       if ((r() & 31) == 0)
         asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(wt.bars + 4 * W_EPI) : "memory");
 
-      if (!whole && k.lo() == 0 && tid < 4) a.heads[block * 4 + tid] = lds_v4(k.at + 16 * tid);
-      wt.arrive_warp(B_SEGEMPTY + at_seg % kSegs);
-      ++at_seg;
-      if (!wait_seg()) return false;
-      if (ref().b() < 0) return true;
-      // Q goes where l and the accumulator passed: after all have read them
-      if (!pair_sync()) return false;
-      load_q();
+      if (!whole && k.lo() == 0 && threadIdx.x < 4) a.heads[block * 4 + threadIdx.x] = lds_v4(k.at + 16 * threadIdx.x);
+      wt.arrive_warp(B_SEGEMPTY + (at_seg - 1) % kSegs);
+      if (!more) return true;
+      // (the last read of what passed through Q was followed by a barrier of all)
+      if (pass) load_q();
     }
   }
 };
@@ -1282,8 +1184,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(base + C::OFF_BAR);
   volatile int64_t* wide = reinterpret_cast<volatile int64_t*>(base + C::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lid = tid & 31;
-  if (tid == 0) a.heads[blockIdx.x * 4].x = -1;  // (a later head is this thread's store too)
+  // nothing is read or written before the kernel before this one is done
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) a.heads[blockIdx.x * 4].x = -1;  // (a later head is this thread's store too)
 
   // The line of tiles: each thread sums up some sequences, then the block scans.
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -1308,66 +1212,52 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     if (i < warp) before += v;
     W += v;
   }
-  // at least four units of cost (two tiles of each lane) to a block
-  const int64_t G = max((int64_t)1, min((int64_t)gridDim.x, W / 4));
+  // at least two shared tiles, or nearly three of the lanes' own, to a block
+  const int64_t G = max((int64_t)1, min((int64_t)gridDim.x, W / (2 * kCostShared)));
   if (W == 0 || (int64_t)blockIdx.x >= G) return;
   const int64_t x0 = (int64_t)blockIdx.x * W / G, x1 = ((int64_t)blockIdx.x + 1) * W / G;
   before += scan - mine;
-  if (before <= x0 && x0 < before + mine) {
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t c = Walk<D, BITS>::seq_cost(a, b);
-      if (x0 < before + c) {
-        words[W_STARTB] = b;
-        wide[W_BASE / 2] = before;
-        break;
-      }
-      before += c;
+  if (warp == 20) {
+    tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
+  } else if (warp == 21) {
+    for (int i = lid; i < B_COUNT; i += 32) {
+      int n = 1;  // arrivals of a phase
+      if (i == B_QFULL || i == B_QFULL + 1 || i == B_PREADY || i == B_PREADY + 1) n = 8;
+      if (i == B_SFULL || i == B_SFULL + 1) n = 1 + (a.fault && blockIdx.x == 0 ? 1 : 0);
+      if (i >= B_MAX && i < B_MAX + 8) n = 2;
+      if (i >= B_SEGEMPTY && i < B_SEGEMPTY + kSegs) n = C::SMW + 4 + 1;
+      if (i == B_PAIR) n = C::SMW;
+      if ((i >= B_KFULL && i < B_KFULL + 4) || (i >= B_VFULL && i < B_VFULL + 4)) n = 4;
+      ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n);
     }
-  }
-  if (tid == 0) {
-    auto init = [&](int i, uint32_t n) { ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n); };
-    for (int i = 0; i < 2; ++i) {
-      init(B_QFULL + i, 8);
-      init(B_ODONE + i, 1);
-      init(B_PVLAST + i, 1);
-      init(B_DRAIN + i, 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      init(B_SFULL + i, 1 + (a.fault && blockIdx.x == 0 ? 1 : 0));
-      init(B_PREADY + i, 4);
-      init(B_KFULL + i, 2 * C::TPR);
-      init(B_VFULL + i, 2 * C::TPR);
-    }
-    for (int i = 0; i < 8; ++i) {
-      init(B_KEMPTY + i, 1);
-      init(B_VEMPTY + i, 1);
-    }
-    for (int i = 0; i < 16; ++i) init(B_REF + i, 1);
-    for (int i = 0; i < kSegs; ++i) {
-      init(B_SEGFULL + i, 1);
-      init(B_SEGEMPTY + i, C::SMW + 8 + C::LANES);
-    }
-    init(B_PAIR, C::SMW);
-    words[W_ABORT] = 0;
-    words[W_PFLAG] = words[W_EPI] = 0;
+    if (lid == 0) words[W_ABORT] = words[W_PFLAG] = words[W_EPI] = 0;
     ptx::fence_mbar_init();
   }
   int* poison = reinterpret_cast<int*>(base + C::OFF_POISON);
   for (int i = tid; i < 3 * D; i += kThreads) poison[i] = 0x7fffffff;
-  __syncthreads();
-  if (warp == 0) {
-    // the query block that holds x0, 32 at a time
-    const int b = words[W_STARTB];
+  // The warp whose sequences hold x0 finds the sequence, then the query block, 32 at a time.
+  const uint32_t holds = __ballot_sync(0xffffffffu, before <= x0 && x0 < before + mine);
+  if (holds) {
+    int b = b_lo;
+    if (before <= x0 && x0 < before + mine) {
+      for (; b < b_hi; ++b) {
+        const int64_t c = b_hi - b_lo == 1 ? mine : Walk<D, BITS>::seq_cost(a, b);
+        if (x0 < before + c) break;
+        before += c;
+      }
+    }
+    const int src = __ffs(holds) - 1;
+    b = __shfl_sync(0xffffffffu, b, src);
+    int64_t at = __shfl_sync(0xffffffffu, before, src);
     const Run run = run_of(a.cu, b, a.total, a.max_len);
     const SeqLens s = seq_lens_of(a.sink_len, a.packed_len, a.res_len, a.res_head, b, a.Ns, a.cap, a.Nr);
     const int nq = Walk<D, BITS>::blocks(a, run);
-    int64_t at = wide[W_BASE / 2];
     for (int q0 = 0; q0 < nq; q0 += 32) {
       int64_t c = 0;
       if (q0 + lid < nq) {
         int npt, nt, w;
         Walk<D, BITS>::tiles(a, run, s, q0 + lid, npt, nt, w);
-        c = (int64_t)nt * w * a.Hkv;
+        c = Walk<D, BITS>::unit_cost(nt, w) * a.Hkv;
       }
       int64_t sum = c;
 #pragma unroll
@@ -1377,14 +1267,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       }
       const bool here = at + sum - c <= x0 && x0 < at + sum;
       if (here) {
+        words[W_STARTB] = b;
         words[W_STARTQ] = q0 + lid;
-        wide[W_BASE / 2 + 1] = at + sum - c;
+        wide[W_BASE / 2] = at + sum - c;
       }
       if (__any_sync(0xffffffffu, here)) break;
       at += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
-  if (warp == 24) tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
@@ -1392,107 +1282,182 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   const Waits wt = {a, smem + C::OFF_BAR};
   Seg* ring = reinterpret_cast<Seg*>(base + C::OFF_SEG);
   const int sb = words[W_STARTB], sq = words[W_STARTQ];
-  const int64_t sbase = wide[W_BASE / 2 + 1];
+  const int64_t sbase = wide[W_BASE / 2];
 
+  // Registers: 80 a thread at launch (61440 in all) = 512 x 88 + 128 x 88 + 128 x 40.
   if (warp < 16) {
-    tc5::regs_inc<80>();
+    tc5::regs_inc<88>();
     if (warp < C::SMW) {
-      const uint32_t tm = tmem + ((uint32_t)(warp & 3) << 21);
-      Soft<D, BITS> soft = {a, wt, smem, tm, 0, (uint32_t)tid,
-                            tm + C::S0 + (tid >> 7) * C::TN,
-                            smem + C::OFF_MAX + tid * 4, 0, 0};
+      Soft<D, BITS> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21), 0, 0, 0};
       soft.run(blockIdx.x);
     }
-  } else if (warp < 24) {
-    tc5::regs_dec<64>();
-    const int w = (warp - 16) / 4;
-    Deq<D, BITS> deq = {a, wt, smem, poison, ring, w, (tid - 512) % kDeqThreads, 0};
+  } else if (warp < 20) {
+    tc5::regs_inc<88>();
+    Deq<D, BITS> deq = {a, wt, smem, poison, ring, tid - 512, 0};
     deq.run();
   } else {
-    tc5::regs_dec<56>();
-    if (lid == 0 && warp - 24 < C::LANES) mma_role<D, BITS>(a, wt, smem, tmem, ring, warp - 24);
-    if (tid == 26 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
+    tc5::regs_dec<40>();
+    if (tid == 20 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
+    if (tid == 21 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     __syncwarp();
   }
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  if (warp == 24) tc5::dealloc(tmem, 512);
+  if (warp == 20) tc5::dealloc(tmem, 512);
 }
 
-// The pieces of the units that were cut, in the order of the tiles.  A block looks at the
-// unit that block x of the other kernel began; a warp has 16 columns of a row: eight
-// lanes' worth of pieces at a time, four columns to a lane.
+// The pieces of the units that were cut.  All their rows lie in one line, which the warps
+// share out; with fewer rows than blocks a block has a row, and its warps every eighth
+// piece of it.  The weights of up to 32 pieces are in a warp's lanes, then the pieces'
+// rows are read one after the other, each as a whole (head_dim 64 and 32: two and four at a
+// time, head_dim 256: in two halves).  The order is fixed.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 8;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kMaxBlocks = 256;  // of the kernel above
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAttnArgs a, int blocks) {
   constexpr int QB = chunk_rows(D);
+  constexpr int LPR = D >= 128 ? 32 : D / 4;  // lanes of a row
+  constexpr int V = D / 4 / LPR;              // float4 of a lane
+  __shared__ int ends[kMaxBlocks];            // rows of the units that blocks 0 .. i began
+  __shared__ int sums[kJoinWarps];
+  __shared__ float part[kJoinWarps][D + 1];   // a block's row: O and l of each warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  union {
+  asm volatile("griddepcontrol.launch_dependents;");
+  union Head {
     int4 v[4];
     Seg s;
-  } u;
-  u.v[0] = __ldcg(a.heads + blockIdx.x * 4);
-  if (u.v[0].x < 0) return;
+  };
+  {
+    int rows = 0;
+    if (tid < blocks) {
+      Head u;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) u.v[i] = __ldcg(a.heads + blockIdx.x * 4 + i);
-  const Seg& k = u.s;
-  const int rows = min(k.n * a.gq - k.qb * QB, QB), lane = threadIdx.x & 31, e = lane & 3;
-  const int subs = (k.last_b - k.first_b + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
-  const int warps = kJoinBlocks * kJoinThreads / 32;
-  for (int it = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); it < rows * (D / 16); it += warps) {
-    const int row = it / (D / 16), cg = it % (D / 16);
-    auto ml_at = [&](int s, int64_t& slot, int& prow) {
+      for (int i = 0; i < 3; ++i) u.v[i] = __ldcg(a.heads + tid * 4 + i);
+      if (u.s.b >= 0) rows = min(u.s.n * a.gq - u.s.qb * QB, QB);
+    }
+    int sum = rows;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) sum += sums[i];
+    ends[tid] = sum;
+    __syncthreads();
+  }
+  const int total = ends[kJoinThreads - 1];
+  const bool team = total <= (int)gridDim.x;  // a block to a row
+  const int step = team ? gridDim.x : gridDim.x * kJoinWarps;
+  for (int it = team ? blockIdx.x : blockIdx.x * kJoinWarps + warp; it < total; it += step) {
+    int head = 0;  // the first block with ends > it
+#pragma unroll
+    for (int o = kMaxBlocks / 2; o > 0; o >>= 1)
+      if (ends[head + o - 1] <= it) head += o;
+    const int row = it - (head > 0 ? ends[head - 1] : 0);
+    Head u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.v[i] = __ldcg(a.heads + head * 4 + i);
+    const Seg& k = u.s;
+    const int subs = (k.last_b - k.first_b + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
+    // where piece s of the row is
+    auto piece = [&](int s) {
       const int p = k.first_b + (k.alt ? s >> 1 : s);
-      slot = 2 * (int64_t)p + (p == k.first_b);
-      prow = row + (k.alt ? (s & 1) * 128 : 0);
-      return __ldcg(a.ml_part + slot * QB + prow);
+      return (2 * (int64_t)p + (p == k.first_b)) * QB + row + (k.alt ? (s & 1) * 128 : 0);
     };
-    int64_t slot;
-    int prow;
-    float m = -INFINITY;
-    for (int s = lane >> 2; s < subs; s += 8) m = fmaxf(m, ml_at(s, slot, prow).x);
+    const float2 ml0 = lane < subs ? __ldcg(a.ml_part + piece(lane)) : make_float2(-INFINITY, 0.0f);
+    float m = ml0.x;
+    for (int s = lane + 32; s < subs; s += 32) m = fmaxf(m, __ldcg(a.ml_part + piece(s)).x);
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < subs; s0 += 32) {
+      // the weight of the lane's piece; one that saw nothing may have written nothing
+      float f = 0.0f;
+      bool seen = false;
+      if (s0 + lane < subs) {
+        const float2 ml = s0 == 0 ? ml0 : __ldcg(a.ml_part + piece(s0 + lane));
+        seen = !(ml.x == -INFINITY && ml.y == 0.0f);
+        if (seen) {
+          f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
+          l += ml.y * f;
+        }
+      }
+      const uint32_t all = __ballot_sync(0xffffffffu, seen);
+      const int n = min(32, subs - s0);
+      constexpr int AT = 32 / LPR;  // pieces at a time
+      const int first = team ? warp * AT : 0, stride = team ? kJoinWarps * AT : AT;
 #pragma unroll 4
-    for (int s = lane >> 2; s < subs; s += 8) {
-      const float2 ml = ml_at(s, slot, prow);
-      if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // saw nothing (and may have written nothing)
-      const float f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
-      const float4 v = __ldcg(a.o_part + (slot * (D / 4) + cg * 4 + e) * QB + prow);
-      l += ml.y * f;
-      o.x += v.x * f;
-      o.y += v.y * f;
-      o.z += v.z * f;
-      o.w += v.w * f;
+      for (int i = first; i < n; i += stride) {
+        const int s = i + lane / LPR;
+        const float fs = __shfl_sync(0xffffffffu, f, s & 31);
+        if (s < n && ((all >> s) & 1u)) {
+          const float4* src = a.o_part + piece(s0 + s) * (D / 4) + lane % LPR;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float4 x = __ldcg(src + v * LPR);
+            o[v].x += x.x * fs;
+            o[v].y += x.y * fs;
+            o[v].z += x.z * fs;
+            o[v].w += x.w * fs;
+          }
+        }
+      }
     }
 #pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, x);
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+#pragma unroll
+    for (int x = LPR; x < 32; x <<= 1) {
+      o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, x);
+      o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, x);
+      o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, x);
+      o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, x);
     }
-    if (lane >= 4) continue;
-    if (l == 0.0f) set_error(a.err_word, KVQ_ERRBIT_EMPTY);
+    if (l == 0.0f && lane == 0 && (!team || warp == 0)) set_error(a.err_word, KVQ_ERRBIT_EMPTY);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int R = k.qb * QB + row;
     const int tok = token_of(a, R);
-    const int64_t at = ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D + cg * 16;
-    const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = 4 * e + j;  // the element that is stored at this column
-      const int el = BITS == 2 ? (c & 1) * 8 + (c >> 3) * 4 + ((c & 7) >> 1) : (c & 8) + ((c & 7) >> 1) + 4 * (c & 1);
+    const int64_t at = ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
+    auto store = [&](int c, float y) {  // to the element that is stored at column c
+      const int c16 = c & 15;
+      const int el = (c & ~15) + (BITS == 2 ? (c16 & 1) * 8 + (c16 >> 3) * 4 + ((c16 & 7) >> 1)
+                                            : (c16 & 8) + ((c16 & 7) >> 1) + 4 * (c16 & 1));
       if (a.out_f32)
-        static_cast<float*>(a.out)[at + el] = y[j];
+        static_cast<float*>(a.out)[at + el] = y * inv;
       else
-        static_cast<__half*>(a.out)[at + el] = __float2half_rn(y[j]);
+        static_cast<__half*>(a.out)[at + el] = __float2half_rn(y * inv);
+    };
+    if (team) {  // (uniform over the block)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (lane < LPR) {
+          float* to = &part[warp][4 * (lane + v * LPR)];
+          to[0] = o[v].x, to[1] = o[v].y, to[2] = o[v].z, to[3] = o[v].w;
+        }
+      }
+      __syncthreads();
+      for (int c = tid; c < D; c += kJoinThreads) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) y += part[w][c];
+        store(c, y);
+      }
+      __syncthreads();
+    } else if (lane < LPR) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float y[4] = {o[v].x, o[v].y, o[v].z, o[v].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) store(4 * (lane + v * LPR) + j, y[j]);
+      }
     }
   }
 }
@@ -1500,21 +1465,35 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAtt
 template <int D, int BITS>
 cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   static_assert(Cfg<D, BITS>::SMEM <= 227 * 1024, "shared memory of a block");
+  if (grid > kMaxBlocks) return cudaErrorInvalidConfiguration;
   auto kernel = chunk_attn_kernel<D, BITS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
+  auto join = chunk_join_kernel<D, BITS>;
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, kernel);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, Cfg<D, BITS>::SMEM, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the warps' shares (setmaxnreg) come out of what the block is launched with
+  if (at.numRegs != 80) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
+  if (e != cudaSuccess) return e;
+  // the same split of L1 and shared memory: an SM that changes it drains first
+  e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  // each may be launched while the kernel before it ends, and waits for it
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kJoinBlocks);
-  cfg.blockDim = kJoinThreads;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = Cfg<D, BITS>::SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];  // its blocks may come as the others leave; they wait for all of them
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, BITS>, a);
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(5 * grid);  // as many as an SM has registers for
+  cfg.blockDim = kJoinThreads;
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join, a, grid);
 }
 
 template <int D>
