@@ -11,17 +11,20 @@
 //
 // Mapping.  A lane holds 8 values of a row (16 bytes), a row is d / 8 neighbouring
 // lanes of one warp, a quad of lanes is one quantization group.  A warp takes
-// 256 / d tokens and a group of heads of one kind (keys, values or queries), four
-// rows' loads in flight at a time, so that a token's cosines and sines are loaded
-// once for the heads of a group.  The rotation's partner elements (rotary_dim / 2
-// away) are a second load of the same row, which L1 answers.  Bytes bound it.
+// 256 / d tokens and up to four heads of one kind (keys, values or queries), whose
+// rows are loaded together before anything about the sequence is known; the warps
+// of a block share their tokens, so that cosines and sines come from L1 after the
+// first.  The rotation's partner values (rotary_dim / 2 away) are in a lane of the
+// same row and come by shuffles.
 #include "kvq_internal.cuh"
+#include "kvq_ptx.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kRows = 4;  // rows in flight per lane
+constexpr int kRunThreads = 384;  // at most
+constexpr int kRowThreads = 128;  // small: a block lives as long as its slowest warp (a packing one)
+constexpr int kHeads = 4;            // heads of a unit: rows in flight per lane
 
 struct ChunkAppendArgs {
   const __half* x[3];  // keys, values, queries: element j of head h of row t at x + t * st + h * sh + j
@@ -42,8 +45,7 @@ struct ChunkAppendArgs {
   uint32_t* err_word;
   int B, Hkv, Hq, d, Ng, row_bytes, cap, Nr, Ns;
   int total, max_len, rope_rows, rd, interleaved;
-  int hpg;         // heads per group
-  int gkv, gq;     // groups of KV heads and of query heads
+  int gkv, groups;  // head groups of the keys (as many of the values), and of all
 };
 
 // How a sequence's run enters the cache: tokens taken and tokens packed.
@@ -106,16 +108,39 @@ __device__ __forceinline__ uint4 rotate8(const uint4& own, const uint4& partner,
   return r;
 }
 
+// A unit's head group: its kind (0 keys, 1 values, 2 queries), first head and heads.
+struct Group {
+  int kind, h0, nh;
+};
+__device__ __forceinline__ Group group_of(const ChunkAppendArgs& a, int grp) {
+  Group g;
+  g.kind = grp < a.gkv ? 0 : grp < 2 * a.gkv ? 1 : 2;
+  g.h0 = (grp - g.kind * a.gkv) * kHeads;
+  g.nh = min(kHeads, (g.kind == 2 ? a.Hq : a.Hkv) - g.h0);
+  return g;
+}
+
+// The lane's piece of row t of the group's heads.  Plain loads: with q rotated in
+// place the same lane writes these bytes below.
+__device__ __forceinline__ void load_rows(const ChunkAppendArgs& a, const Group& g, int t, bool there,
+                                          uint4 (&own)[kHeads]) {
+  const int e = (threadIdx.x & ((a.d >> 3) - 1)) * 8;
+  const __half* src = a.x[g.kind] + (int64_t)t * a.st[g.kind] + (int64_t)g.h0 * a.sh[g.kind] + e;
+#pragma unroll
+  for (int u = 0; u < kHeads; ++u) {
+    own[u] = make_uint4(0, 0, 0, 0);
+    if (there && u < g.nh) own[u] = *reinterpret_cast<const uint4*>(src + u * a.sh[g.kind]);
+  }
+}
+
 // One warp's unit: the lane's row t of sequence b (live: the lane has one) and
-// head group `grp`.  All lanes of the warp take part.
+// head group g, its values in `own`.  All lanes of the warp take part.
 template <int BITS, bool HYB>
-__device__ __forceinline__ void append_unit(const ChunkAppendArgs& a, int t, int b, bool live, int grp) {
+__device__ __forceinline__ void append_unit(const ChunkAppendArgs& a, const Group& g, int t, int b, bool live,
+                                            const uint4 (&own)[kHeads]) {
   const int lane = threadIdx.x & 31;
-  const int lpr = a.d >> 3;              // lanes per row
-  const int e = (lane & (lpr - 1)) * 8;  // first element of the lane
-  const int kind = grp < a.gkv ? 0 : grp < 2 * a.gkv ? 1 : 2;
-  const int h0 = (grp - (kind == 0 ? 0 : kind == 1 ? a.gkv : 2 * a.gkv)) * a.hpg;
-  const int nh = min(a.hpg, (kind == 2 ? a.Hq : a.Hkv) - h0);
+  const int e = (lane & ((a.d >> 3) - 1)) * 8;  // first element of the lane
+  const int kind = g.kind;
 
   Run run = {0, -1};
   SeqLens s = {0, 0, 0, 0};
@@ -124,17 +149,7 @@ __device__ __forceinline__ void append_unit(const ChunkAppendArgs& a, int t, int
     live = run.n > 0 && t >= run.c0 && t - run.c0 < run.n;
     if (live) s = lens_of(a, b);
   }
-  const Plan plan = plan_of(s, max(run.n, 0), a.cap, a.Nr);
   const int i = t - run.c0;
-  const int j = s.nres + i;  // place in the line
-  const bool taken = live && kind != 2 && i < plan.taken;
-  const bool direct = taken && j < plan.packed;             // packed straight from the input
-  const bool ring = taken && !direct;                       // goes to a window slot
-  const bool oust = ring && a.Nr > 0 && j >= a.Nr && j % max(a.Nr, 1) < s.nres;  // a window token leaves it
-  const int slot = a.Nr > 0 ? (int)(((int64_t)s.head + j) % a.Nr) : 0;
-  const int pack_at = s.npk + (direct ? j : j % max(a.Nr, 1));
-  const bool packs = direct || oust;
-  const bool any_pack = __any_sync(0xffffffffu, packs);
 
   // the position's cosines and sines
   float2 cs[8];
@@ -157,56 +172,71 @@ __device__ __forceinline__ void append_unit(const ChunkAppendArgs& a, int t, int
       cs[2 * u + 1] = make_float2(f.z, f.w);
     }
   }
-  const __half* src = a.x[kind] + (int64_t)t * a.st[kind] + (int64_t)h0 * a.sh[kind] + e;
-  const int away = second ? -half : half;
-  const int64_t row = packs ? a.rm.row(b, 0, pack_at) : -1;  // of KV head 0
-  const int64_t row_step = a.rm.paged ? kPage : a.cap;       // to the next head's row
-  if (packs && row < 0) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
-  const int w = kind & 1;
+  const int partner = lane + (second ? -(half >> 3) : half >> 3);
+  auto rotated = [&](const uint4& x) {
+    uint4 y = x;
+    if (a.rd > 0 && kind != 1 && !a.interleaved) {
+      y.x = __shfl_sync(0xffffffffu, x.x, partner);
+      y.y = __shfl_sync(0xffffffffu, x.y, partner);
+      y.z = __shfl_sync(0xffffffffu, x.z, partner);
+      y.w = __shfl_sync(0xffffffffu, x.w, partner);
+    }
+    return rot ? rotate8(x, y, cs, a.interleaved, second) : x;
+  };
 
-  for (int r0 = 0; r0 < nh; r0 += kRows) {
-    uint4 own[kRows], other[kRows];
+  if (kind == 2) {
+    __half* dst = a.q_out + ((int64_t)t * a.Hq + g.h0) * a.d + e;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      own[u] = other[u] = make_uint4(0, 0, 0, 0);
-      if (live && r0 + u < nh) {
-        // plain loads: with q rotated in place these rows are written below
-        const __half* p = src + (int64_t)(r0 + u) * a.sh[kind];
-        own[u] = *reinterpret_cast<const uint4*>(p);
-        if (rot && !a.interleaved) {
-          other[u] = *reinterpret_cast<const uint4*>(p + away);
-        } else if (oust && kind == 1) {
-          other[u] = *reinterpret_cast<const uint4*>(
-              a.res[1] + (((int64_t)b * a.Hkv + h0 + r0 + u) * a.Nr + slot) * a.d + e);
-        }
-      }
+    for (int u = 0; u < kHeads; ++u) {
+      if (u >= g.nh) break;  // warp-uniform
+      const uint4 x = rotated(own[u]);
+      if (live) *reinterpret_cast<uint4*>(dst + u * a.d) = x;
     }
-    __syncwarp();  // every lane has read its rows before any is written
+    return;
+  }
+
+  const Plan plan = plan_of(s, max(run.n, 0), a.cap, a.Nr);
+  const int j = s.nres + i;  // place in the line
+  const bool taken = live && i < plan.taken;
+  const bool direct = taken && j < plan.packed;  // packed straight from the input
+  const bool ring = taken && !direct;            // goes to a window slot
+  int lap = j, slot = 0;
+  if (ring) {
+    lap = j % a.Nr;  // ring: the window has slots
+    slot = (int)(((int64_t)s.head + j) % a.Nr);
+  }
+  const bool oust = ring && j >= a.Nr && lap < s.nres;  // a window token leaves the slot
+  const bool packs = direct || oust;
+  const bool any_pack = __any_sync(0xffffffffu, packs);
+  const bool any_oust = __any_sync(0xffffffffu, oust);
+  const int64_t row = packs ? a.rm.row(b, 0, s.npk + lap) : -1;  // of KV head 0
+  const int64_t row_step = a.rm.paged ? kPage : a.cap;           // to the next head's row
+  if (packs && row < 0) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+  const bool ok = packs && row >= 0;
+  const int w = kind & 1;
+  __half* slot_row = a.res[w] + (((int64_t)b * a.Hkv + g.h0) * a.Nr + slot) * a.d + e;
+  const int64_t slot_step = (int64_t)a.Nr * a.d;
+  uint4 old[kHeads];
+  if (any_oust) {  // warp-uniform
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (r0 + u >= nh) break;  // warp-uniform
-      const int h = h0 + r0 + u;
-      const uint4 x = rot ? rotate8(own[u], other[u], cs, a.interleaved, second) : own[u];
-      if (kind == 2) {
-        if (live) *reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * a.Hq + h) * a.d + e) = x;
-        continue;
-      }
-      __half* slot_row = a.res[w] + (((int64_t)b * a.Hkv + h) * a.Nr + slot) * a.d + e;
-      if (any_pack) {
-        uint4 y = x;
-        if (oust) y = kind == 1 ? other[u] : *reinterpret_cast<const uint4*>(slot_row);
-        uint32_t prm, asym = 1;
-        const uint32_t packed = quantize_quad<BITS>(y, prm, HYB, &asym);
-        const uint32_t modes = HYB ? __ballot_sync(0xffffffffu, (lane & 3) == 0 && asym) : 0u;
-        const bool ok = packs && row >= 0;
-        const int64_t hr = row + (int64_t)h * row_step;
-        store_group_codes<BITS>(ok ? a.codes[w] + hr * a.row_bytes + (e >> 5) * (4 * BITS) : nullptr,
-                                packed, lane & 3, ok);
-        if (ok && (lane & 3) == 0) a.params[w][hr * a.Ng + (e >> 5)] = prm;
-        if (HYB && ok && e == 0) a.modes[w][hr] = mode_byte(modes, lane >> 2, a.Ng);
-      }
-      if (ring) *reinterpret_cast<uint4*>(slot_row) = x;
+    for (int u = 0; u < kHeads; ++u)
+      if (oust && u < g.nh) old[u] = *reinterpret_cast<const uint4*>(slot_row + u * slot_step);
+  }
+#pragma unroll
+  for (int u = 0; u < kHeads; ++u) {
+    if (u >= g.nh) break;  // warp-uniform
+    const uint4 x = rotated(own[u]);
+    if (any_pack) {
+      uint32_t prm, asym = 1;
+      const uint32_t packed = quantize_quad<BITS>(oust ? old[u] : x, prm, HYB, &asym);
+      const uint32_t modes = HYB ? __ballot_sync(0xffffffffu, (lane & 3) == 0 && asym) : 0u;
+      const int64_t hr = row + (int64_t)(g.h0 + u) * row_step;
+      store_group_codes<BITS>(ok ? a.codes[w] + hr * a.row_bytes + (e >> 5) * (4 * BITS) : nullptr, packed,
+                              lane & 3, ok);
+      if (ok && (lane & 3) == 0) a.params[w][hr * a.Ng + (e >> 5)] = prm;
+      if (HYB && ok && e == 0) a.modes[w][hr] = mode_byte(modes, lane >> 2, a.Ng);
     }
+    if (ring) *reinterpret_cast<uint4*>(slot_row + u * slot_step) = x;
   }
 }
 
@@ -226,39 +256,48 @@ __device__ __forceinline__ void finish_seq(const ChunkAppendArgs& a, int b) {
   if (a.Nr > 0) a.res_head[b] = (int)(((int64_t)s.head + p.packed) % a.Nr);
 }
 
-// Short runs: one block per sequence, which also moves its counters.
+// Short runs: one cluster of blocks per sequence, which also moves its counters
+// once all its blocks have read them.
 template <int BITS, bool HYB>
-__global__ void __launch_bounds__(1024) append_run_kernel(ChunkAppendArgs a) {
+__global__ void __launch_bounds__(kRunThreads) append_run_kernel(ChunkAppendArgs a, int blocks) {
   asm volatile("griddepcontrol.launch_dependents;");
-  const int b = blockIdx.x;
+  const int b = blockIdx.x / blocks, rank = blockIdx.x % blocks;
   const int lane = threadIdx.x & 31;
   const int tpw = 256 / a.d;  // tokens per warp
   const Run run = run_of(a.cu, b, a.total, a.max_len);
-  const int groups = 2 * a.gkv + a.gq;
-  const int64_t units = (int64_t)((max(run.n, 0) + tpw - 1) / tpw) * groups;
-  for (int64_t u = threadIdx.x >> 5; u < units; u += blockDim.x >> 5) {
-    const int i = (int)(u / groups) * tpw + lane / (a.d >> 3);
-    append_unit<BITS, HYB>(a, run.c0 + i, b, i < run.n, (int)(u % groups));
+  const int units = (max(run.n, 0) + tpw - 1) / tpw * a.groups;
+  const int warps = blockDim.x >> 5;
+  for (int u = rank * warps + (threadIdx.x >> 5); u < units; u += blocks * warps) {
+    const Group g = group_of(a, u % a.groups);
+    const int i = u / a.groups * tpw + lane / (a.d >> 3);
+    uint4 own[kHeads];
+    load_rows(a, g, run.c0 + i, i < run.n, own);
+    append_unit<BITS, HYB>(a, g, run.c0 + i, b, i < run.n, own);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) finish_seq(a, b);
+  if (blocks > 1) {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) finish_seq(a, b);
 }
 
-// Long runs: the rows of all runs in one line.
+// Long runs: the rows of all runs in one line, a block for 256 / d of them.
 template <int BITS, bool HYB>
-__global__ void __launch_bounds__(kAppendThreads) append_rows_kernel(ChunkAppendArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 6) append_rows_kernel(ChunkAppendArgs a) {
   const int lane = threadIdx.x & 31;
-  const int tpw = 256 / a.d;
-  const int groups = 2 * a.gkv + a.gq;
-  const int64_t u = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t0 = (u / groups) * tpw;
-  if (t0 >= a.total) return;  // warp-uniform
-  int b = find_seq(a.cu, a.B, (int)t0);
+  const int grp = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (grp >= a.groups) return;  // warp-uniform
+  const int64_t t0 = (int64_t)blockIdx.x * (256 / a.d);
   const int64_t t = t0 + lane / (a.d >> 3);
   const bool live = t < a.total;
+  const Group g = group_of(a, grp);
+  uint4 own[kHeads];
+  load_rows(a, g, (int)(live ? t : t0), live, own);
+  int b = find_seq(a.cu, a.B, (int)t0);
   if (live)
     while (b + 1 < a.B && __ldg(a.cu + b + 1) <= t) ++b;
-  append_unit<BITS, HYB>(a, (int)(live ? t : t0), b, live, (int)(u % groups));
+  append_unit<BITS, HYB>(a, g, (int)(live ? t : t0), b, live, own);
 }
 
 __global__ void append_finish_kernel(ChunkAppendArgs a) {
@@ -269,7 +308,7 @@ __global__ void append_finish_kernel(ChunkAppendArgs a) {
 // ------------------------------------------------------------------- read ---
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 4;  // pieces of 8 values per thread, one grid stride apart
+constexpr int kReadRows = 8;  // pieces of 8 values per thread, one block's width apart, at most
 
 struct ReadArgs {
   const uint8_t* codes[2];
@@ -285,6 +324,7 @@ struct ReadArgs {
   const int32_t* sink_len;
   uint32_t* err_word;
   int Hkv, d, Ng, row_bytes, cap, Nr, Ns, count, lpr_shift;
+  int rows;  // pieces per thread
 };
 
 // Codes 8q .. 8q + 7 of a group (its first byte at grp), packed in 8 * BITS bits.
@@ -297,8 +337,45 @@ __device__ __forceinline__ uint32_t load_codes8(const uint8_t* grp, int q) {
   return __funnelshift_r(__ldg(w + i), __ldg(w + min(i + 1, 2)), 8 * ((3 * q) & 3)) & 0xffffffu;
 }
 
+// Eight codes (load_codes8) as values min + code * scale; the product is exact in
+// fp32, so the fused form rounds as the sum does.
+template <int BITS>
+__device__ __forceinline__ void values8(uint32_t codes, uint32_t prm, float (&x)[8]) {
+  const float sc = __half2float(__ushort_as_half((unsigned short)(prm & 0xffffu)));
+  const float mn = __half2float(__ushort_as_half((unsigned short)(prm >> 16)));
+  // codes 0-3 in the low half word, 4-7 in the high one
+  const uint32_t y = BITS == 4   ? codes
+                     : BITS == 3 ? (codes & 0xfffu) | ((codes & 0xfff000u) << 4)
+                                 : (codes & 0xffu) | ((codes & 0xff00u) << 8);
+  constexpr uint32_t m = (1u << BITS) - 1u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // the bits in the mantissa of 1024, less 1024
+    const uint32_t c = ptx::hadd2_u32(ptx::and_or(y >> (BITS * k), m << 16 | m, 0x64006400u), 0xe400e400u);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c));
+    x[k] = __fmaf_rn(f.x, sc, mn);
+    x[k + 4] = __fmaf_rn(f.y, sc, mn);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_piece(void* out, int64_t at, const float (&x)[8]) {
+  if (F32) {
+    float4* dst = static_cast<float4*>(out) + 2 * at;
+    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint4 r;
+    __half2* hh = reinterpret_cast<__half2*>(&r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hh[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+    static_cast<uint4*>(out)[at] = r;
+  }
+}
+
 // A quad of lanes per group: each lane turns 8 codes into 8 values, so that the
-// quad's stores are the group's contiguous 64 (or 128) bytes.  Output bytes bound it.
+// quad's stores are the group's contiguous 64 (or 128) bytes.  Output bytes bound
+// it.  A block whose tokens are all packed has the loads of all its pieces in
+// flight together; the others go piece by piece.
 template <int BITS, bool F32>
 __global__ void __launch_bounds__(kReadThreads) read_tokens_kernel(ReadArgs a) {
   const int bh = blockIdx.y, w = blockIdx.z;
@@ -309,79 +386,88 @@ __global__ void __launch_bounds__(kReadThreads) read_tokens_kernel(ReadArgs a) {
     set_error(a.err_word, KVQ_ERRBIT_BADLEN);
   const int64_t n = first < 0 ? 0 : (int64_t)s.ns + s.npk + s.nres;
   const int64_t pieces = (int64_t)a.count << a.lpr_shift;
-  const int64_t p0 = (int64_t)blockIdx.x * (kReadThreads * kReadRows) + threadIdx.x;
-  const __half* sink = a.sink[w] + (int64_t)bh * a.Ns * a.d;
-  const __half* res = a.res[w] + (int64_t)bh * a.Nr * a.d;
+  const int64_t block0 = (int64_t)blockIdx.x * (kReadThreads * a.rows);
+  const int64_t p0 = block0 + threadIdx.x;
+  const int64_t at = ((int64_t)bh << a.lpr_shift) * a.count + p0;  // pieces of 8 values
+  const int e = (int)(p0 & ((1 << a.lpr_shift) - 1)) * 8;          // the same in all the thread's pieces
+  const int64_t t0 = max(first, 0) + (p0 >> a.lpr_shift);          // a negative first has n = 0
+  const int tstep = kReadThreads >> a.lpr_shift;
+  const uint8_t* codes = a.codes[w] + (e >> 5) * (4 * BITS);
+  const uint32_t* params = a.params[w] + (e >> 5);
 
-  uint4 raw[kReadRows];      // fp16 tokens: the values; packed ones: codes and params
-  int kind[kReadRows];       // 0 zero, 1 fp16, 2 packed
+  const int64_t tb = max(first, 0) + (block0 >> a.lpr_shift);
+  if (a.rows == kReadRows && tb >= s.ns && tb + kReadRows * tstep <= min(n, (int64_t)s.ns + s.npk) &&
+      block0 + kReadRows * kReadThreads <= pieces) {
+    int64_t row[kReadRows];
+    uint32_t c[kReadRows], prm[kReadRows];
 #pragma unroll
-  for (int u = 0; u < kReadRows; ++u) {
-    const int64_t p = p0 + u * kReadThreads;
-    const int64_t t = max(first, 0) + (p >> a.lpr_shift);  // a negative first has n = 0
-    const int e = (int)(p & ((1 << a.lpr_shift) - 1)) * 8;
-    kind[u] = 0;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (p >= pieces || t >= n) continue;
-    if (t < s.ns) {
-      kind[u] = 1;
-      raw[u] = __ldg(reinterpret_cast<const uint4*>(sink + t * a.d + e));
-    } else if (t < s.ns + s.npk) {
-      const int64_t row = a.rm.row(b, h, (int)(t - s.ns));
-      if (row < 0) {
-        set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
-        continue;
+    for (int u = 0; u < kReadRows; ++u) row[u] = a.rm.row(b, h, (int)(t0 - s.ns) + u * tstep);
+#pragma unroll
+    for (int u = 0; u < kReadRows; ++u) {
+      c[u] = prm[u] = 0;
+      if (row[u] >= 0) {
+        c[u] = load_codes8<BITS>(codes + row[u] * a.row_bytes, (e >> 3) & 3);
+        prm[u] = __ldg(params + row[u] * a.Ng);
       }
-      kind[u] = 2;
-      raw[u].x = load_codes8<BITS>(a.codes[w] + row * a.row_bytes + (e >> 5) * (4 * BITS), (e >> 3) & 3);
-      raw[u].y = __ldg(a.params[w] + row * a.Ng + (e >> 5));
-    } else {
-      kind[u] = 1;
-      const int64_t j = (t - s.ns - s.npk + s.head) % a.Nr;
-      raw[u] = __ldg(reinterpret_cast<const uint4*>(res + j * a.d + e));
     }
+#pragma unroll
+    for (int u = 0; u < kReadRows; ++u) {
+      if (row[u] < 0) set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+      float x[8];
+      values8<BITS>(c[u], prm[u], x);
+      store_piece<F32>(a.out[w], at + u * kReadThreads, x);
+    }
+    return;
   }
-#pragma unroll
-  for (int u = 0; u < kReadRows; ++u) {
-    const int64_t p = p0 + u * kReadThreads;
-    if (p >= pieces) break;
-    const int64_t at = ((int64_t)bh << a.lpr_shift) * a.count + p;  // pieces of 8 values
-    float x[8];
-    if (kind[u] == 2) {
-      const float sc = __half2float(__ushort_as_half((unsigned short)(raw[u].y & 0xffffu)));
-      const float mn = __half2float(__ushort_as_half((unsigned short)(raw[u].y >> 16)));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        x[j] = __fadd_rn(mn, __fmul_rn((float)((raw[u].x >> (BITS * j)) & ((1u << BITS) - 1u)), sc));
-    }
-    if (F32) {
-      if (kind[u] != 2) unpack8_f16(raw[u], x);
-      float4* dst = reinterpret_cast<float4*>(a.out[w]) + 2 * at;
-      dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-      dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      uint4 r = raw[u];
-      if (kind[u] == 2) {
-        __half2* hh = reinterpret_cast<__half2*>(&r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hh[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+
+  const __half* sink = a.sink[w] + (int64_t)bh * a.Ns * a.d + e;
+  const __half* res = a.res[w] + (int64_t)bh * a.Nr * a.d + e;
+#pragma unroll 1
+  for (int u = 0; u < a.rows; ++u) {
+    if (p0 + u * kReadThreads >= pieces) break;
+    const int64_t t = t0 + u * tstep;
+    float x[8] = {};
+    if (t < n) {
+      if (t >= s.ns && t < s.ns + s.npk) {
+        const int64_t row = a.rm.row(b, h, (int)(t - s.ns));
+        if (row < 0)
+          set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+        else
+          values8<BITS>(load_codes8<BITS>(codes + row * a.row_bytes, (e >> 3) & 3), __ldg(params + row * a.Ng), x);
+      } else {
+        const __half* src = t < s.ns ? sink + t * a.d : res + (t - s.ns - s.npk + s.head) % a.Nr * a.d;
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(src));
+        if (!F32) {  // as they are, whatever they hold
+          static_cast<uint4*>(a.out[w])[at + u * kReadThreads] = raw;
+          continue;
+        }
+        unpack8_f16(raw, x);
       }
-      reinterpret_cast<uint4*>(a.out[w])[at] = r;
     }
+    store_piece<F32>(a.out[w], at + u * kReadThreads, x);
   }
 }
 
+// blocks: per sequence for short runs, 0 for long ones.
 template <int BITS, bool HYB>
-cudaError_t launch_append_bits(const ChunkAppendArgs& a, bool by_seq, int threads, cudaStream_t st) {
-  if (by_seq) {
-    append_run_kernel<BITS, HYB><<<a.B, threads, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_append_bits(const ChunkAppendArgs& a, int blocks, int threads, cudaStream_t st) {
+  if (blocks > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * blocks));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)blocks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, append_run_kernel<BITS, HYB>, a, blocks);
   }
-  const int tpw = 256 / a.d;
-  const int64_t warps = (((int64_t)a.total + tpw - 1) / tpw) * (2 * a.gkv + a.gq);
-  const int64_t blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  if (blocks > 2147483647LL) return cudaErrorInvalidConfiguration;
-  append_rows_kernel<BITS, HYB><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
+  const int per = 256 / a.d;
+  constexpr int kWarps = kRowThreads / 32;
+  const dim3 grid((unsigned)((a.total + per - 1) / per), (unsigned)((a.groups + kWarps - 1) / kWarps));
+  append_rows_kernel<BITS, HYB><<<grid, kRowThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   append_finish_kernel<<<(a.B + 127) / 128, 128, 0, st>>>(a);
@@ -432,32 +518,27 @@ cudaError_t launch_append_chunk(const Dims& s, const kvq_cache_view& v, const kv
   a.rope_rows = A.rope_rows;
   a.rd = A.rotary_dim;
   a.interleaved = A.interleaved;
-  // A block per sequence saves the second launch; it is the shorter way while
-  // one block's warps take at most a few units each.
+  a.gkv = (a.Hkv + kHeads - 1) / kHeads;
+  a.groups = 2 * a.gkv + (a.Hq + kHeads - 1) / kHeads;
+  // Blocks per sequence save the second launch; they are the shorter way while a
+  // cluster's warps take few units each.
   const int tpw = 256 / s.d;
   const int64_t len = A.max_len < A.total ? A.max_len : A.total;
-  const int64_t tiles = (len + tpw - 1) / tpw;
-  auto groups = [&](int hpg) {
-    a.hpg = hpg;
-    a.gkv = (a.Hkv + hpg - 1) / hpg;
-    a.gq = (a.Hq + hpg - 1) / hpg;
-    return 2 * a.gkv + a.gq;
-  };
-  const int64_t units = tiles * groups(4);
-  const bool by_seq = units <= 128;
-  int threads = 0;
-  if (by_seq)
-    threads = 32 * (int)(units < 1 ? 1 : units < 32 ? units : 32);
-  else
-    groups(8);
+  const int64_t units = (len + tpw - 1) / tpw * a.groups;
+  int blocks = 0, threads = 0;
+  constexpr int kWarps = kRunThreads / 32;
+  if (units <= 16 * kWarps && s.B < (1 << 28)) {
+    blocks = units <= kWarps ? 1 : units <= 2 * kWarps ? 2 : units <= 4 * kWarps ? 4 : 8;
+    threads = 32 * (int)(units < 1 ? 1 : units < kWarps ? units : kWarps);
+  }
   if (s.bits == 4)
-    return s.hybrid ? launch_append_bits<4, true>(a, by_seq, threads, st)
-                    : launch_append_bits<4, false>(a, by_seq, threads, st);
+    return s.hybrid ? launch_append_bits<4, true>(a, blocks, threads, st)
+                    : launch_append_bits<4, false>(a, blocks, threads, st);
   if (s.bits == 3)
-    return s.hybrid ? launch_append_bits<3, true>(a, by_seq, threads, st)
-                    : launch_append_bits<3, false>(a, by_seq, threads, st);
-  return s.hybrid ? launch_append_bits<2, true>(a, by_seq, threads, st)
-                  : launch_append_bits<2, false>(a, by_seq, threads, st);
+    return s.hybrid ? launch_append_bits<3, true>(a, blocks, threads, st)
+                    : launch_append_bits<3, false>(a, blocks, threads, st);
+  return s.hybrid ? launch_append_bits<2, true>(a, blocks, threads, st)
+                  : launch_append_bits<2, false>(a, blocks, threads, st);
 }
 
 cudaError_t launch_read_tokens(const Dims& s, const kvq_cache_view& v, const int32_t* first, int count,
@@ -491,8 +572,11 @@ cudaError_t launch_read_tokens(const Dims& s, const kvq_cache_view& v, const int
   a.count = count;
   a.lpr_shift = __builtin_ctz((unsigned)s.d / 8);
   const int64_t pieces = (int64_t)count << a.lpr_shift;
-  const int64_t per = kReadThreads * kReadRows;
-  const dim3 grid((unsigned)((pieces + per - 1) / per), (unsigned)(s.B * s.Hkv), 2);
+  // few pieces: spread over the SMs, one to a thread, before threads take several
+  auto blocks = [&](int rows) { return (pieces + kReadThreads * rows - 1) / (kReadThreads * rows); };
+  a.rows = kReadRows;
+  while (a.rows > 1 && blocks(a.rows) * s.B * s.Hkv * 2 < 4 * device_sm_count()) a.rows /= 2;
+  const dim3 grid((unsigned)blocks(a.rows), (unsigned)(s.B * s.Hkv), 2);
   const bool f32 = (flags & KVQ_OUT_F32) != 0;
   if (s.bits == 4)
     f32 ? read_tokens_kernel<4, true><<<grid, kReadThreads, 0, st>>>(a)

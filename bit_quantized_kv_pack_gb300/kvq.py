@@ -437,20 +437,36 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0,
     return torch.stack([angle.cos(), angle.sin()], -1).float()
 
 
-def _run_args(cache: KVCache, cu_seqlens: torch.Tensor, what: str) -> None:
-    if (cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous()
-            or cu_seqlens.numel() != cache.desc.batch + 1):
-        raise ValueError(f"{what}: cu_seqlens must be a contiguous int32 CUDA tensor of B + 1 entries")
+def _run_int(t: torch.Tensor, n: int, device: torch.device, name: str) -> int:
+    if (t.dtype != torch.int32 or not t.is_cuda or t.device != device or not t.is_contiguous()
+            or t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} entries on the cache's device")
+    return t.data_ptr()
 
 
-def _run_tensor(t: torch.Tensor, heads: int, cache: KVCache, name: str, contiguous: bool) -> None:
-    if (t.dtype != torch.float16 or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads
-            or t.shape[2] != cache.desc.head_dim or (t.numel() and t.stride(2) != 1)
-            or (contiguous and not t.is_contiguous())):
-        raise ValueError(f"{name} must be a float16 CUDA tensor [total][{heads}][{cache.desc.head_dim}]"
-                         f"{', contiguous' if contiguous else ' with head_dim contiguous'}")
-    if t.device != cache.device and cache.device.index is not None:
-        raise ValueError(f"{name} must be on the cache's device")
+def _run_tensor(t: torch.Tensor, heads: int, cache: KVCache, device: torch.device, name: str,
+                contiguous: bool) -> int:
+    d = cache.desc.head_dim
+    if (t.dtype != torch.float16 or not t.is_cuda or t.device != device or t.dim() != 3 or t.shape[1] != heads
+            or t.shape[2] != d or not (t.is_contiguous() if contiguous else t.stride(2) == 1)):
+        raise ValueError(f"{name} must be a float16 CUDA tensor [total][{heads}][{d}] on the cache's device, "
+                         f"{'contiguous' if contiguous else 'with head_dim contiguous'}")
+    return t.data_ptr()
+
+
+def _run_call(fn: str, cache: KVCache, device: torch.device, stream, *args) -> None:
+    """One library call on the cache's device, whichever is current."""
+    f = getattr(_lib or load(), fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = f(ctypes.byref(cache.desc), ctypes.byref(cache.view), *args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(ctypes.byref(cache.desc), ctypes.byref(cache.view), *args, stream)
+    _check(st, fn)
 
 
 def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -464,41 +480,38 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     + the place in the run, or ``positions`` (int32 [total]).  ``q`` (fp16 [total][Hq][d])
     is rotated too and returned (in ``q_out``, which may be q itself)."""
     D = cache.desc
-    _run_args(cache, cu_seqlens, "kvq_append_chunk")
-    _run_tensor(k, D.num_kv_heads, cache, "k", False)
-    _run_tensor(v, D.num_kv_heads, cache, "v", False)
-    total = int(k.shape[0])
+    device = cache.counters.device
+    total = k.shape[0]
+    cu = _run_int(cu_seqlens, D.batch + 1, device, "cu_seqlens")
+    a = AppendArgs(k=_run_tensor(k, D.num_kv_heads, cache, device, "k", False),
+                   v=_run_tensor(v, D.num_kv_heads, cache, device, "v", False),
+                   cu_seqlens=cu, total=total, max_len=int(max_len), interleaved=int(interleaved))
+    a.kv_stride_token, a.kv_stride_head, _ = k.stride()
     if k.shape != v.shape or k.stride() != v.stride():
         raise ValueError("k and v must have the same shape and strides")
-    a = AppendArgs(k=k.data_ptr(), v=v.data_ptr(), kv_stride_token=k.stride(0),
-                   kv_stride_head=k.stride(1), cu_seqlens=cu_seqlens.data_ptr(), total=total,
-                   max_len=int(max_len), interleaved=int(interleaved))
     if q is not None:
         if q.dim() != 3 or q.shape[0] != total:
             raise ValueError("q must be [total][Hq][d] with k's rows")
-        _run_tensor(q, q.shape[1], cache, "q", False)
+        heads = q.shape[1]
+        a.q = _run_tensor(q, heads, cache, device, "q", False)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-        _run_tensor(q_out, q.shape[1], cache, "q_out", True)
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=device)
+        a.q_out = _run_tensor(q_out, heads, cache, device, "q_out", True)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        if a.q_out == a.q and not q.is_contiguous():
             raise ValueError("q must be contiguous to be rotated in place")
-        a.q, a.q_out, a.num_q_heads = q.data_ptr(), q_out.data_ptr(), int(q.shape[1])
-        a.q_stride_token, a.q_stride_head = q.stride(0), q.stride(1)
+        a.num_q_heads = heads
+        a.q_stride_token, a.q_stride_head, _ = q.stride()
     if rope is not None:
-        if (rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 3 or rope.shape[2] != 2
-                or not rope.is_contiguous()):
-            raise ValueError("rope must be a contiguous float32 CUDA tensor [rows][rotary_dim / 2][2]")
-        a.rope, a.rope_rows, a.rotary_dim = rope.data_ptr(), int(rope.shape[0]), 2 * int(rope.shape[1])
+        if (rope.dtype != torch.float32 or not rope.is_cuda or rope.device != device
+                or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous()):
+            raise ValueError("rope must be a contiguous float32 CUDA tensor [rows][rotary_dim / 2][2] "
+                             "on the cache's device")
+        a.rope, a.rope_rows, a.rotary_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
     if positions is not None:
-        if (positions.dtype != torch.int32 or not positions.is_cuda or not positions.is_contiguous()
-                or positions.numel() != total):
-            raise ValueError("positions must be a contiguous int32 CUDA tensor of `total` entries")
-        a.positions = positions.data_ptr()
-    st = load().kvq_append_chunk(ctypes.byref(D), ctypes.byref(cache.view), ctypes.byref(a),
-                                 _stream(stream, k.device))
-    _check(st, "kvq_append_chunk")
+        a.positions = _run_int(positions, total, device, "positions")
+    _run_call("kvq_append_chunk", cache, device, stream, ctypes.byref(a))
     return q_out
 
 
@@ -518,19 +531,17 @@ def chunk_workspace_for(cache: KVCache, num_q_heads: int) -> torch.Tensor:
 def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspace, stream, flags):
     if q.dim() != 3:
         raise ValueError("q must be [total][Hq][d]")
-    _run_args(cache, cu_seqlens, name)
-    _run_tensor(q, q.shape[1], cache, "q", True)
+    device = cache.counters.device
+    total, heads, _ = q.shape
+    cu = _run_int(cu_seqlens, cache.desc.batch + 1, device, "cu_seqlens")
+    qp = _run_tensor(q, heads, cache, device, "q", True)
     out, flags = _out(q, out, flags)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = chunk_workspace_for(cache, q.shape[1])
-    st = getattr(load(), name)(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
-                               int(q.shape[1]), _ptr(cu_seqlens), int(q.shape[0]), int(max_len),
-                               _ptr(out), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), int(flags),
-                               _stream(stream, q.device))
-    _check(st, name)
+        workspace = chunk_workspace_for(cache, heads)
+    if out.shape != q.shape or out.device != device or workspace.device != device:
+        raise ValueError("out must have q's shape; out and workspace must be on the cache's device")
+    _run_call(name, cache, device, stream, qp, heads, cu, total, int(max_len), out.data_ptr(),
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(), flags)
     return out
 
 
@@ -560,27 +571,23 @@ def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
     order; first int32 [B] or None for 0) as values: (K, V) [B][Hkv][count][d], fp16 or
     fp32 (KVQ_OUT_F32 in flags, or fp32 outputs).  Rows past the end are zero."""
     D = cache.desc
-    if first is not None and (first.dtype != torch.int32 or not first.is_cuda
-                              or not first.is_contiguous() or first.numel() != D.batch):
-        raise ValueError("first must be a contiguous int32 CUDA tensor of B entries")
+    device = cache.counters.device
+    first_ptr = None if first is None else _run_int(first, D.batch, device, "first")
     shape = (D.batch, D.num_kv_heads, int(count), D.head_dim)
     given = k_out if k_out is not None else v_out
     dtype = given.dtype if given is not None else (
         torch.float32 if flags & KVQ_OUT_F32 else torch.float16)
     if dtype not in (torch.float16, torch.float32):
         raise ValueError("k_out and v_out must be float16 or float32")
-    outs = []
+    outs = [torch.empty(shape, dtype=dtype, device=device) if t is None else t for t in (k_out, v_out)]
     for t in (k_out, v_out):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=cache.device)
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-            raise ValueError("k_out and v_out must be contiguous CUDA tensors [B][Hkv][count][d] of one type")
-        outs.append(t)
+        if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_cuda or t.device != device
+                              or not t.is_contiguous()):
+            raise ValueError("k_out and v_out must be contiguous tensors [B][Hkv][count][d] of one type "
+                             "on the cache's device")
     flags = (flags | KVQ_OUT_F32) if dtype == torch.float32 else (flags & ~KVQ_OUT_F32)
-    st = load().kvq_read_tokens(ctypes.byref(D), ctypes.byref(cache.view), _ptr(first), int(count),
-                                _ptr(outs[0]), _ptr(outs[1]), int(flags),
-                                _stream(stream, cache.device))
-    _check(st, "kvq_read_tokens")
+    _run_call("kvq_read_tokens", cache, device, stream, first_ptr, int(count), outs[0].data_ptr(),
+              outs[1].data_ptr(), flags)
     return outs[0], outs[1]
 
 

@@ -34,7 +34,8 @@ def _append(lib, desc=None, view=None, **kw):
                 interleaved=0, positions=0)
     base.update(kw)
     a = kvq.AppendArgs(**base)
-    return lib.kvq_append_chunk(ctypes.byref(desc or _desc()), ctypes.byref(view or _view()),
+    view = kvq.CacheView() if view == 0 else _view()
+    return lib.kvq_append_chunk(ctypes.byref(_desc(**(desc or {}))), ctypes.byref(view),
                                 ctypes.byref(a), None)
 
 
@@ -53,8 +54,8 @@ def _append(lib, desc=None, view=None, **kw):
     (dict(q=0x300004), kvq.KVQ_ERR_MISALIGNED), (dict(q_out=0x400008), kvq.KVQ_ERR_MISALIGNED),
     (dict(rope=0x600008), kvq.KVQ_ERR_MISALIGNED), (dict(cu_seqlens=0x500002), kvq.KVQ_ERR_MISALIGNED),
     (dict(positions=0x700002), kvq.KVQ_ERR_MISALIGNED),
-    (dict(desc=_desc(bits=5)), kvq.KVQ_ERR_UNSUPPORTED), (dict(desc=_desc(batch=0)), kvq.KVQ_ERR_INVALID_ARG),
-    (dict(view=kvq.CacheView()), kvq.KVQ_ERR_INVALID_ARG),
+    (dict(desc=dict(bits=5)), kvq.KVQ_ERR_UNSUPPORTED), (dict(desc=dict(batch=0)), kvq.KVQ_ERR_INVALID_ARG),
+    (dict(view=0), kvq.KVQ_ERR_INVALID_ARG),
 ])
 def test_append_chunk_refuses(lib, kw, expect):
     assert _append(lib, **kw) == expect
