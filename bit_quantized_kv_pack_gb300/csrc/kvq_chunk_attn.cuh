@@ -138,7 +138,7 @@ struct alignas(16) Seg {
   int b, h, qb, lo;
   int hi, npt, nt, alt;     // packed tiles and all tiles of the unit; alt: the lanes take alternate tiles
   int c0, n, ns, npk;       // the run, and the sequence's lengths
-  int nres, head, first_b, last_b;  // blocks that hold the unit's first and last tile; b < 0: the end
+  int nres, head, last_b, pad;  // last_b: of a unit that the block begins, the block that ends it; b < 0: the end
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
@@ -191,7 +191,6 @@ struct Waits {
     if (word(W_ABORT)) return true;
     if (timer_lo() - t0 <= a.wait_limit_us * 1000u) return false;
     set_word(W_ABORT, 1);
-    set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
     return true;
   }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
@@ -294,9 +293,8 @@ struct Walk {
     h = (int)((x0 - base_) / unit);
     base = base_ + h * unit;
     range();
-    while (b < a.B && base < x1 && lo >= hi) next(a);
   }
-  __device__ __forceinline__ bool valid(const ChunkAttnArgs& a) const { return b < a.B && base < x1 && lo < hi; }
+  __device__ __forceinline__ bool more(const ChunkAttnArgs& a) const { return b < a.B && base < x1; }
   __device__ __forceinline__ void next(const ChunkAttnArgs& a) {
     base += unit_cost(nt, w);
     if (++h == a.Hkv) {
@@ -324,27 +322,25 @@ __device__ __forceinline__ void walk_role(const ChunkAttnArgs& a, const Waits& w
                                           int64_t base, int64_t x0, int64_t x1, int64_t W, int64_t G) {
   Walk<D, BITS> k;
   k.start(a, b, qb, base, x0, x1);
-  for (uint32_t i = 0;; ++i) {
+  for (uint32_t i = 0;; k.next(a)) {
+    const bool more = k.more(a);
+    if (more && k.lo >= k.hi) continue;  // the unit's begin is the block's, no tile of it
     const int at = i % kSegs;
     if (!wt.wait(B_SEGEMPTY + at, ((i / kSegs) & 1) ^ 1)) return;
     Seg s;
     s.b = -1;
-    if (k.valid(a)) {
+    if (more) {
       s.b = k.b, s.h = k.h, s.qb = k.qb, s.lo = k.lo, s.hi = k.hi, s.npt = k.npt, s.nt = k.nt;
       s.alt = Cfg<D, BITS>::LANES == 2 && k.w == kCostOwn;
       s.c0 = k.run.c0, s.n = k.run.n, s.ns = k.s.ns, s.npk = k.s.npk, s.nres = k.s.nres, s.head = k.s.head;
-      s.first_b = s.last_b = 0;
-      if (k.lo > 0 || k.hi < k.nt) {
-        // block c has the starts from floor(c W / G) on
-        const int64_t begin = k.base + kCostUnit, end = begin + (int64_t)(k.nt - 1) * k.w;
-        s.first_b = (int)(((begin + 1) * G - 1) / W);
-        s.last_b = (int)(((end + 1) * G - 1) / W);
-      }
+      s.last_b = 0;
+      if (k.lo == 0 && k.hi < k.nt)  // block c has the starts from floor(c W / G) on
+        s.last_b = (int)(((k.base + kCostUnit + (int64_t)(k.nt - 1) * k.w + 1) * G - 1) / W);
     }
     ring[at] = s;
     ptx::mbar_arrive(wt.bar(B_SEGFULL + at));
-    if (s.b < 0) return;
-    k.next(a);
+    if (!more) return;
+    ++i;
   }
 }
 
@@ -818,8 +814,6 @@ struct Soft {
     KVQ_SEG_FIELD(ns)
     KVQ_SEG_FIELD(npk)
     KVQ_SEG_FIELD(nres)
-    KVQ_SEG_FIELD(first_b)
-    KVQ_SEG_FIELD(last_b)
 #undef KVQ_SEG_FIELD
   };
   __device__ __forceinline__ Ref ref() const { return {smem + C::OFF_SEG + (at_seg % kSegs) * (uint32_t)sizeof(Seg)}; }
@@ -1304,6 +1298,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
+  if (tid == 0 && words[W_ABORT]) set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
   if (warp == 20) tc5::dealloc(tmem, 512);
 }
 
@@ -1323,21 +1318,19 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAtt
   constexpr int V = D / 4 / LPR;              // float4 of a lane
   __shared__ int ends[kMaxBlocks];            // rows of the units that blocks 0 .. i began
   __shared__ int sums[kJoinWarps];
+  __shared__ Seg heads[kMaxBlocks];           // ... and those units
   __shared__ float part[kJoinWarps][D + 1];   // a block's row: O and l of each warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  union Head {
-    int4 v[4];
-    Seg s;
-  };
   {
     int rows = 0;
     if (tid < blocks) {
-      Head u;
+      int4* to = reinterpret_cast<int4*>(heads + tid);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) u.v[i] = __ldcg(a.heads + tid * 4 + i);
-      if (u.s.b >= 0) rows = min(u.s.n * a.gq - u.s.qb * QB, QB);
+      for (int i = 0; i < 4; ++i) to[i] = __ldcg(a.heads + tid * 4 + i);
+      const Seg& k = heads[tid];
+      if (k.b >= 0) rows = min(k.n * a.gq - k.qb * QB, QB);
     }
     int sum = rows;
 #pragma unroll
@@ -1360,15 +1353,12 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAtt
     for (int o = kMaxBlocks / 2; o > 0; o >>= 1)
       if (ends[head + o - 1] <= it) head += o;
     const int row = it - (head > 0 ? ends[head - 1] : 0);
-    Head u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u.v[i] = __ldcg(a.heads + head * 4 + i);
-    const Seg& k = u.s;
-    const int subs = (k.last_b - k.first_b + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
+    const Seg k = heads[head];
+    const int subs = (k.last_b - head + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
     // where piece s of the row is
     auto piece = [&](int s) {
-      const int p = k.first_b + (k.alt ? s >> 1 : s);
-      return (2 * (int64_t)p + (p == k.first_b)) * QB + row + (k.alt ? (s & 1) * 128 : 0);
+      const int p = head + (k.alt ? s >> 1 : s);
+      return (2 * (int64_t)p + (p == head)) * QB + row + (k.alt ? (s & 1) * 128 : 0);
     };
     const float2 ml0 = lane < subs ? __ldcg(a.ml_part + piece(lane)) : make_float2(-INFINITY, 0.0f);
     float m = ml0.x;
