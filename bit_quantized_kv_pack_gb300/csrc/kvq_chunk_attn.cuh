@@ -1302,24 +1302,90 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   if (warp == 20) tc5::dealloc(tmem, 512);
 }
 
-// The pieces of the units that were cut.  All their rows lie in one line, which the warps
-// share out; with fewer rows than blocks a block has a row, and its warps every eighth
-// piece of it.  The weights of up to 32 pieces are in a warp's lanes, then the pieces'
-// rows are read one after the other, each as a whole (head_dim 64 and 32: two and four at a
-// time, head_dim 256: in two halves).  The order is fixed.
+// The pieces of the units that were cut.  All their rows lie in one line; a row is a
+// group of D / 4 lanes (head_dim 128 and 256: a warp), which reads its pieces four at a
+// time, maxima, sums and values together, and has two rows in flight.  With fewer rows
+// than blocks a block has a row, whose pieces its groups share.  The order is fixed.
+// Latency bounds it: before the first piece there are only the ends of the units.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinBlocks = 3;   // of an SM
 constexpr int kMaxBlocks = 256;  // of the kernel above
 
+template <int D>
+struct Joined {
+  static constexpr int LPR = D >= 128 ? 32 : D / 4;  // lanes of a row
+  static constexpr int V = D / 4 / LPR;              // float4 of a lane
+  static constexpr int P = 4 / V;                    // pieces at a time
+  float m = -INFINITY, l = 0.0f;
+  float4 o[V];
+
+  __device__ __forceinline__ Joined() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  // Where piece s of row `row` of block `head`'s unit is (alt: pieces and lanes in turn).
+  static __device__ __forceinline__ int64_t piece(int head, int alt, int row, int s) {
+    const int p = head + (alt ? s >> 1 : s);
+    return (2 * (int64_t)p + (p == head)) * chunk_rows(D) + row + (alt ? (s & 1) * 128 : 0);
+  }
+  struct Loads {
+    float2 ml[P];
+    float4 x[P][V];
+  };
+  static __device__ __forceinline__ void load(const ChunkAttnArgs& a, Loads& in, int head, int alt, int row,
+                                              int subs, int s, int stride) {
+    const int col = threadIdx.x % LPR;
+#pragma unroll
+    for (int i = 0; i < P; ++i, s += stride) {
+      in.ml[i] = make_float2(-INFINITY, 0.0f);
+      if (s < subs) {
+        const int64_t at = piece(head, alt, row, s);
+        in.ml[i] = __ldcg(a.ml_part + at);
+#pragma unroll
+        for (int v = 0; v < V; ++v) in.x[i][v] = __ldcg(a.o_part + at * (D / 4) + col + v * LPR);
+      }
+    }
+  }
+  __device__ __forceinline__ void scale(float f) {
+    l *= f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v].x *= f, o[v].y *= f, o[v].z *= f, o[v].w *= f;
+  }
+  // (a piece that saw nothing may have written no values)
+  __device__ __forceinline__ void add(const Loads& in, float scale_log2) {
+    float mm = m;
+#pragma unroll
+    for (int i = 0; i < P; ++i) mm = fmaxf(mm, in.ml[i].x);
+    if (m != -INFINITY) scale(ptx::ex2_ftz((m - mm) * scale_log2));
+    m = mm;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (in.ml[i].x == -INFINITY && in.ml[i].y == 0.0f) continue;
+      // a sum without a maximum is NaN, and stays so
+      const float f = in.ml[i].x == -INFINITY ? in.ml[i].y : ptx::ex2_ftz((in.ml[i].x - mm) * scale_log2);
+      l += in.ml[i].y * f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        o[v].x += in.x[i][v].x * f;
+        o[v].y += in.x[i][v].y * f;
+        o[v].z += in.x[i][v].z * f;
+        o[v].w += in.x[i][v].w * f;
+      }
+    }
+  }
+};
+
 template <int D, int BITS>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAttnArgs a, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(const ChunkAttnArgs a, int blocks) {
+  using J = Joined<D>;
   constexpr int QB = chunk_rows(D);
-  constexpr int LPR = D >= 128 ? 32 : D / 4;  // lanes of a row
-  constexpr int V = D / 4 / LPR;              // float4 of a lane
-  __shared__ int ends[kMaxBlocks];            // rows of the units that blocks 0 .. i began
-  __shared__ int sums[kJoinWarps];
-  __shared__ Seg heads[kMaxBlocks];           // ... and those units
-  __shared__ float part[kJoinWarps][D + 1];   // a block's row: O and l of each warp
+  constexpr int LPR = J::LPR, V = J::V;
+  constexpr int kGroups = kJoinThreads / LPR;  // rows of a block at a time
+  __shared__ int ends[kMaxBlocks];             // rows of the units that blocks 0 .. i began
+  __shared__ int sums[kJoinThreads / 32];
+  __shared__ Seg heads[kMaxBlocks];            // ... and those units
+  __shared__ float2 part_ml[kGroups];          // a block's row: the groups' parts of it
+  __shared__ float part[kGroups][D + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1345,108 +1411,103 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkAtt
     __syncthreads();
   }
   const int total = ends[kJoinThreads - 1];
-  const bool team = total <= (int)gridDim.x;  // a block to a row
-  const int step = team ? gridDim.x : gridDim.x * kJoinWarps;
-  for (int it = team ? blockIdx.x : blockIdx.x * kJoinWarps + warp; it < total; it += step) {
-    int head = 0;  // the first block with ends > it
+  // the unit of the line's row `it`: the first block with ends > it; rows before it
+  auto head_of = [&](int it, int& row) {
+    int head = 0;
 #pragma unroll
     for (int o = kMaxBlocks / 2; o > 0; o >>= 1)
       if (ends[head + o - 1] <= it) head += o;
-    const int row = it - (head > 0 ? ends[head - 1] : 0);
-    const Seg k = heads[head];
-    const int subs = (k.last_b - head + 1) << (k.alt ? 1 : 0);  // pieces, or both lanes' of each
-    // where piece s of the row is
-    auto piece = [&](int s) {
-      const int p = head + (k.alt ? s >> 1 : s);
-      return (2 * (int64_t)p + (p == head)) * QB + row + (k.alt ? (s & 1) * 128 : 0);
-    };
-    const float2 ml0 = lane < subs ? __ldcg(a.ml_part + piece(lane)) : make_float2(-INFINITY, 0.0f);
-    float m = ml0.x;
-    for (int s = lane + 32; s < subs; s += 32) m = fmaxf(m, __ldcg(a.ml_part + piece(s)).x);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.0f;
-    float4 o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s0 = 0; s0 < subs; s0 += 32) {
-      // the weight of the lane's piece; one that saw nothing may have written nothing
-      float f = 0.0f;
-      bool seen = false;
-      if (s0 + lane < subs) {
-        const float2 ml = s0 == 0 ? ml0 : __ldcg(a.ml_part + piece(s0 + lane));
-        seen = !(ml.x == -INFINITY && ml.y == 0.0f);
-        if (seen) {
-          f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
-          l += ml.y * f;
-        }
-      }
-      const uint32_t all = __ballot_sync(0xffffffffu, seen);
-      const int n = min(32, subs - s0);
-      constexpr int AT = 32 / LPR;  // pieces at a time
-      const int first = team ? warp * AT : 0, stride = team ? kJoinWarps * AT : AT;
-#pragma unroll 4
-      for (int i = first; i < n; i += stride) {
-        const int s = i + lane / LPR;
-        const float fs = __shfl_sync(0xffffffffu, f, s & 31);
-        if (s < n && ((all >> s) & 1u)) {
-          const float4* src = a.o_part + piece(s0 + s) * (D / 4) + lane % LPR;
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float4 x = __ldcg(src + v * LPR);
-            o[v].x += x.x * fs;
-            o[v].y += x.y * fs;
-            o[v].z += x.z * fs;
-            o[v].w += x.w * fs;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-#pragma unroll
-    for (int x = LPR; x < 32; x <<= 1) {
-      o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, x);
-      o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, x);
-      o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, x);
-      o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, x);
-    }
-    if (l == 0.0f && lane == 0 && (!team || warp == 0)) set_error(a.err_word, KVQ_ERRBIT_EMPTY);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    row = it - (head > 0 ? ends[head - 1] : 0);
+    return head;
+  };
+  auto subs_of = [&](int head) { return (heads[head].last_b - head + 1) << (heads[head].alt ? 1 : 0); };
+  auto place = [&](int head, int row) {
+    const Seg& k = heads[head];
     const int R = k.qb * QB + row;
     const int tok = token_of(a, R);
-    const int64_t at = ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
-    auto store = [&](int c, float y) {  // to the element that is stored at column c
-      const int c16 = c & 15;
-      const int el = (c & ~15) + (BITS == 2 ? (c16 & 1) * 8 + (c16 >> 3) * 4 + ((c16 & 7) >> 1)
-                                            : (c16 & 8) + ((c16 & 7) >> 1) + 4 * (c16 & 1));
-      if (a.out_f32)
-        static_cast<float*>(a.out)[at + el] = y * inv;
-      else
-        static_cast<__half*>(a.out)[at + el] = __float2half_rn(y * inv);
-    };
-    if (team) {  // (uniform over the block)
+    return ((int64_t)(k.c0 + tok) * a.Hq + k.h * a.gq + (R - tok * a.gq)) * D;
+  };
+  auto store = [&](int64_t at, int c, float y) {  // to the element that is stored at column c
+    const int c16 = c & 15;
+    const int el = (c & ~15) + (BITS == 2 ? (c16 & 1) * 8 + (c16 >> 3) * 4 + ((c16 & 7) >> 1)
+                                          : (c16 & 8) + ((c16 & 7) >> 1) + 4 * (c16 & 1));
+    if (a.out_f32)
+      static_cast<float*>(a.out)[at + el] = y;
+    else
+      static_cast<__half*>(a.out)[at + el] = __float2half_rn(y);
+  };
+  auto inverse = [&](float l, bool first) {
+    if (l == 0.0f && first) set_error(a.err_word, KVQ_ERRBIT_EMPTY);
+    return l == 0.0f ? 0.0f : 1.0f / l;
+  };
+
+  const int group = tid / LPR, col = tid % LPR;
+  if (total <= (int)gridDim.x) {  // a block to a row
+    const int it = blockIdx.x;
+    if (it >= total) return;
+    int row;
+    const int head = head_of(it, row), alt = heads[head].alt, subs = subs_of(head);
+    J j;
+    for (int s = group; s < subs; s += J::P * kGroups) {
+      typename J::Loads in;
+      J::load(a, in, head, alt, row, subs, s, kGroups);
+      j.add(in, a.scale_log2);
+    }
+    if (col == 0) part_ml[group] = make_float2(j.m, j.l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float* to = &part[group][4 * (col + v * LPR)];
+      to[0] = j.o[v].x, to[1] = j.o[v].y, to[2] = j.o[v].z, to[3] = j.o[v].w;
+    }
+    __syncthreads();
+    const int64_t at = place(head, row);
+    for (int c = tid; c < D; c += kJoinThreads) {
+      float m = -INFINITY, l = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) m = fmaxf(m, part_ml[g].x);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float2 ml = part_ml[g];
+        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+        const float f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
+        l += ml.y * f;
+        y += part[g][c] * f;
+      }
+      store(at, c, y * inverse(l, c == 0));
+    }
+    return;
+  }
+  constexpr int K = 2;  // rows in flight
+  const int step = gridDim.x * kGroups;
+  for (int it = blockIdx.x * kGroups + group; it < total; it += K * step) {
+    int row[K], head[K], alt[K], subs[K];
+    J j[K];
+    int most = 0;
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const bool there = it + u * step < total;
+      head[u] = head_of(there ? it + u * step : it, row[u]);
+      alt[u] = heads[head[u]].alt;
+      subs[u] = there ? subs_of(head[u]) : 0;
+      most = max(most, subs[u]);
+    }
+    for (int s = 0; s < most; s += J::P) {
+      typename J::Loads in[K];
+#pragma unroll
+      for (int u = 0; u < K; ++u) J::load(a, in[u], head[u], alt[u], row[u], subs[u], s, 1);
+#pragma unroll
+      for (int u = 0; u < K; ++u) j[u].add(in[u], a.scale_log2);
+    }
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      if (subs[u] == 0) continue;
+      const float inv = inverse(j[u].l, col == 0);
+      const int64_t at = place(head[u], row[u]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (lane < LPR) {
-          float* to = &part[warp][4 * (lane + v * LPR)];
-          to[0] = o[v].x, to[1] = o[v].y, to[2] = o[v].z, to[3] = o[v].w;
-        }
-      }
-      __syncthreads();
-      for (int c = tid; c < D; c += kJoinThreads) {
-        float y = 0.0f;
+        const float y[4] = {j[u].o[v].x, j[u].o[v].y, j[u].o[v].z, j[u].o[v].w};
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) y += part[w][c];
-        store(c, y);
-      }
-      __syncthreads();
-    } else if (lane < LPR) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float y[4] = {o[v].x, o[v].y, o[v].z, o[v].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) store(4 * (lane + v * LPR) + j, y[j]);
+        for (int i = 0; i < 4; ++i) store(at, 4 * (col + v * LPR) + i, y[i] * inv);
       }
     }
   }
@@ -1480,7 +1541,7 @@ cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(5 * grid);  // as many as an SM has registers for
+  cfg.gridDim = dim3(kJoinBlocks * grid);
   cfg.blockDim = kJoinThreads;
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join, a, grid);
