@@ -109,6 +109,8 @@ struct Cfg {
   static constexpr int UN = (TB + 15) / 16;         // 16-byte units of them in the ring
   static constexpr int PB = GPT * 4;                // param bytes of a thread
   static constexpr int RAWB = kDeqThreads * (UN * 16 + PB);
+  // rows that bulk copies can move (multiples of 16 bytes wherever they start)
+  static constexpr bool BULK = D >= 128;
   static constexpr int RAWN = D == 256 ? 2 : D == 128 ? 3 : 6;  // half tiles of the ring
   static constexpr int SMW = 8 * LANES;             // softmax warps
   // TMEM columns
@@ -143,9 +145,10 @@ struct alignas(16) Seg {
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
 enum { B_QFULL = 0, B_SFULL = 2, B_PREADY = 4, B_ODONE = 6, B_PAIR = 8, B_DRAIN = 9, B_KFULL = 10,
-       B_KEMPTY = 14, B_VFULL = 18, B_VEMPTY = 22, B_SEGFULL = 26, B_SEGEMPTY = 34, B_MAX = 42, B_COUNT = 50 };
-enum { W_TMEM = 100, W_ABORT = 101, W_PFLAG = 102, W_EPI = 103, W_STARTB = 105,
-       W_STARTQ = 106, W_BASE = 108 /* int64 */ };
+       B_KEMPTY = 14, B_VFULL = 18, B_VEMPTY = 22, B_SEGFULL = 26, B_SEGEMPTY = 34, B_MAX = 42, B_RAWFULL = 50,
+       B_RAWEMPTY = 53, B_COUNT = 56 };
+enum { W_TMEM = 112, W_ABORT = 113, W_PFLAG = 114, W_EPI = 115, W_STARTB = 116, W_STARTQ = 117,
+       W_BASE = 118 /* int64 */, W_PAGES = 120 /* a ring slot's pages that are there */ };
 
 __device__ __forceinline__ uint32_t lds(uint32_t addr) {
   uint32_t v;
@@ -517,36 +520,49 @@ struct Deq {
   }
   __device__ __forceinline__ int column(int g, int c) const { return ((dt % C::TPR) * C::GPT + g) * 32 + c * 8; }
 
-  // A fetched half tile as fp16 at `dst`.  first: logical place of the tile's first token.
-  __device__ __forceinline__ bool packed_tile(int first, int w, int slot, uint32_t dst) {
+  // A fetched half tile as fp16 at `dst`.  first: logical place of the tile's first token;
+  // there: the thread's row is one (BULK: others hold what the ring held).
+  __device__ __forceinline__ bool packed_tile(int first, int w, int slot, uint32_t dst, bool there) {
     constexpr uint32_t kQmax2 = BITS == 4 ? 0x4b804b80u : BITS == 3 ? 0x47004700u : 0x42004200u;  // 15, 7, 3
-    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * 16;
+    // With rows of codes as they are in memory, lanes take their groups in different
+    // orders (by pieces of 16 bytes), so that the banks are all in use.
+    const int rot = !C::BULK || BITS == 3 ? 0 : BITS == 4 ? (dt >> 1) & 3 : (dt >> 2) & 1;
+    auto group = [&](int g) {
+      return BITS == 4 ? (g + rot) & (C::GPT - 1) : BITS == 2 ? g ^ (rot << 1) : g;
+    };
+    const uint32_t dc = smem + C::OFF_RAW + slot * C::RAWB + dt * (C::BULK ? C::TB : 16);
     const uint32_t dp = smem + C::OFF_RAW + slot * C::RAWB + kDeqThreads * C::UN * 16 + dt * C::PB;
     uint32_t raw[C::UN * 4], prm[C::GPT];
 #pragma unroll
     for (int i = 0; i < C::UN; ++i) {
-      const uint4 v = ld_shared_v4(dc + i * (kDeqThreads * 16));
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (!C::BULK)
+        v = ld_shared_v4(dc + i * (kDeqThreads * 16));
+      else if (there)
+        v = ld_shared_v4(dc + (BITS == 4 ? group(i) : BITS == 2 ? i ^ rot : i) * 16);
       raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i)
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(prm[i]) : "r"(dp + 4 * i) : "memory");
+    for (int i = 0; i < C::GPT; ++i) prm[i] = there ? lds(dp + 4 * group(i)) : 0;
+    if (C::BULK) wt.arrive_warp(B_RAWEMPTY + slot);
     const uint32_t at = row_addr(dst);
+    auto piece = [&](int g, int c) { return (at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP; };
     uint32_t rare = 0;
 #pragma unroll
-    for (int g = 0; g < C::GPT; ++g) {
-      const uint32_t s2 = ptx::prmt(prm[g], prm[g], 0x1010), m2 = ptx::prmt(prm[g], prm[g], 0x3232);
+    for (int i = 0; i < C::GPT; ++i) {
+      const int g = group(i);
+      const uint32_t s2 = ptx::prmt(prm[i], prm[i], 0x1010), m2 = ptx::prmt(prm[i], prm[i], 0x3232);
       // the group's largest value; only where it is not finite can any value be so
-      if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) rare |= 1u << g;
+      if (f16_nonfinite(ptx::hfma2_u32(kQmax2, s2, m2))) rare |= 1u << i;
       uint32_t x[4];
-      code_words<BITS>(raw, g, x);
+      code_words<BITS>(raw, i, x);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t y[4];
         codes_f16<BITS>(x[c], y);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = ptx::hfma2_u32(y[j], s2, m2);
-        st_shared_v4((at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP, make_uint4(y[0], y[1], y[2], y[3]));
+        st_shared_v4(piece(g, c), make_uint4(y[0], y[1], y[2], y[3]));
       }
     }
     if (rare == 0) return true;
@@ -554,11 +570,13 @@ struct Deq {
     // scale's rounding, or meant (params that are not finite)
 #pragma unroll 1
     for (int e = 0; e < 32 * C::GPT; ++e) {
-      const int g = e >> 5;
-      if (!((rare >> g) & 1u)) continue;
-      uint32_t pg;
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(pg) : "r"(dp + 4 * g) : "memory");
-      const uint32_t ea = (at ^ (((g & 1) * 4 + ((e >> 3) & 3)) << 4)) + (g / 2) * C::KP + 2 * (e & 7);
+      if (!((rare >> (e >> 5)) & 1u)) continue;
+      const int g = group(e >> 5);
+      uint32_t pg = prm[0];
+#pragma unroll
+      for (int i = 1; i < C::GPT; ++i)
+        if ((e >> 5) == i) pg = prm[i];
+      const uint32_t ea = piece(g, (e >> 3) & 3) + 2 * (e & 7);
       unsigned short hv;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(ea) : "memory");
       if (!f16_nonfinite(hv)) continue;
@@ -644,27 +662,38 @@ struct Deq {
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint32_t kv = 0;  // tiles so far
+    uint32_t kv = 0;     // tiles so far
     int slot = 0;
+    uint32_t phase = 0;  // of the slot (BULK)
     // RAWN - 1 half tiles ahead: a free slot is filled before the oldest is taken
+    if constexpr (!C::BULK) {
 #pragma unroll 1
-    for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
+      for (int i = 0; i < C::RAWN - 1; ++i) fetch_next(i);
+    }
     for (; ok; ++k.i, ++seg) {
       ok = ok && __all_sync(0xffffffffu, k.wait(wt));
       if (!ok) break;
       const Seg& s = k.get(ring);
       if (s.b < 0) break;
-      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns;
+      const int lo = s.lo, hi = s.hi, npt = s.npt, ns = s.ns, npk = s.npk;
       for (int h = 2 * lo; h < 2 * hi; ++h) {
-        fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
+        if constexpr (!C::BULK) fetch_next(slot == 0 ? C::RAWN - 1 : slot - 1);
         const int t = h >> 1, w = h & 1;
         const int stage = kv % C::ST;
         const uint32_t dst = smem + (w ? C::OFF_V : C::OFF_K) + stage * C::KBYTES;
         ok = ok && wt.wait_warp((w ? B_VEMPTY : B_KEMPTY) + stage, ((kv / C::ST) & 1) ^ 1);
         if (!ok) break;
         if (t < npt) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
-          ok = packed_tile(ns + t * C::TN, w, slot, dst);
+          bool there = true;
+          if constexpr (C::BULK) {
+            ok = wt.wait_warp(B_RAWFULL + slot, phase);
+            if (!ok) break;
+            const int row = dt / C::TPR;
+            there = t * C::TN + row < npk && ((wt.word(W_PAGES + slot) >> (row / kPage)) & 1u);
+          } else {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWN - 1) : "memory");
+          }
+          ok = packed_tile(ns + t * C::TN, w, slot, dst, there);
         } else {
           ok = f16_tile(s, (t - npt) * C::TN, w, dst);
         }
@@ -672,7 +701,9 @@ struct Deq {
         if (!ok) break;
         ptx::fence_proxy_async_shared();
         wt.arrive_warp((w ? B_VFULL : B_KFULL) + stage);
-        if (++slot == C::RAWN) slot = 0;
+        if (!C::BULK || t < npt) {  // (BULK: slots are of packed half tiles alone)
+          if (++slot == C::RAWN) slot = 0, phase ^= 1;
+        }
         kv += w;
       }
       wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
@@ -680,6 +711,63 @@ struct Deq {
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
 };
+
+// The warp that copies packed rows into the ring (BULK): of each 32 rows of a half tile
+// (a page, where there are pages) one lane copies the codes and another the params.
+template <int D, int BITS>
+__device__ __forceinline__ void fetch_role(const ChunkAttnArgs& a, const Waits& wt, uint32_t smem, const Seg* ring) {
+  using C = Cfg<D, BITS>;
+  constexpr int NP = C::TN / kPage;
+  const int lane = threadIdx.x & 31, j = lane % NP;
+  const bool codes = lane < NP;
+  const uint32_t row_bytes = codes ? C::G * C::CB : C::G * 4;
+  const uint32_t to = smem + C::OFF_RAW + (codes ? 0 : kDeqThreads * C::UN * 16) + j * kPage * row_bytes;
+  SegReader k;
+  int slot = 0;
+  uint32_t n = 0;  // half tiles copied
+  bool ok = true;
+  for (; ok && (ok = __all_sync(0xffffffffu, k.wait(wt))); ++k.i) {
+    const Seg& s = k.get(ring);
+    if (s.b < 0) break;
+    const int hi = min(s.hi, s.npt), rows = s.npk - j * kPage;  // (of the sequence, from the lane's on)
+    const int64_t row0 = a.rm.paged ? (int64_t)s.h * kPage : ((int64_t)s.b * a.Hkv + s.h) * a.cap + j * kPage;
+    const int* table = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + j;
+    auto page_of = [&](int t) { return a.rm.paged && t < hi && t * C::TN < rows ? __ldg(table + t * NP) : 0; };
+    int next = page_of(s.lo);
+    for (int t = s.lo; ok && t < hi; ++t) {
+      const int page = next;
+      next = page_of(t + 1);
+      bool there = t * C::TN < rows;
+      if (there && (page < 0 || page >= a.rm.npages) && a.rm.paged) {
+        there = false;
+        set_error(a.err_word, KVQ_ERRBIT_BADPAGE);
+      }
+      const uint32_t pages = __ballot_sync(0xffffffffu, there);  // (lanes from NP on say the same again)
+      const uint32_t bytes = there && lane < 2 * NP ? min(kPage, rows - t * C::TN) * row_bytes : 0;
+      const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+      const int64_t row = row0 + (a.rm.paged ? (int64_t)page * a.Hkv * kPage : (int64_t)t * C::TN);
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w, ++n) {
+        ok = wt.wait_warp(B_RAWEMPTY + slot, ((n / C::RAWN) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          wt.set_word(W_PAGES + slot, pages);
+          ptx::mbar_arrive_expect_tx(wt.bar(B_RAWFULL + slot), all);
+        }
+        __syncwarp();
+        const char* src = codes ? reinterpret_cast<const char*>(a.codes[w]) : reinterpret_cast<const char*>(a.params[w]);
+        if (bytes) ptx::bulk_load(to + slot * C::RAWB, src + row * row_bytes, bytes, wt.bar(B_RAWFULL + slot));
+        if (++slot == C::RAWN) slot = 0;
+      }
+    }
+    wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
+  }
+  // copies still in flight when the block gives up land before its shared memory goes
+  const uint32_t t0 = timer_lo();
+  for (uint32_t i = n > C::RAWN ? n - C::RAWN : 0; i < n; ++i)
+    while (!ptx::mbar_try_wait(wt.bar(B_RAWFULL + i % C::RAWN), (i / C::RAWN) & 1))
+      if (timer_lo() - t0 > 1000000000u) return;
+}
 
 // ---------------------------------------------------------------------- MMA ---
 
@@ -1219,7 +1307,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       if (i == B_QFULL || i == B_QFULL + 1 || i == B_PREADY || i == B_PREADY + 1) n = 8;
       if (i == B_SFULL || i == B_SFULL + 1) n = 1 + (a.fault && blockIdx.x == 0 ? 1 : 0);
       if (i >= B_MAX && i < B_MAX + 8) n = 2;
-      if (i >= B_SEGEMPTY && i < B_SEGEMPTY + kSegs) n = C::SMW + 4 + 1;
+      if (i >= B_SEGEMPTY && i < B_SEGEMPTY + kSegs) n = C::SMW + 4 + 1 + C::BULK;
+      if (i >= B_RAWEMPTY && i < B_RAWEMPTY + 3) n = 4;
       if (i == B_PAIR) n = C::SMW;
       if ((i >= B_KFULL && i < B_KFULL + 4) || (i >= B_VFULL && i < B_VFULL + 4)) n = 4;
       ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n);
@@ -1293,6 +1382,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     tc5::regs_dec<40>();
     if (tid == 20 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
     if (tid == 21 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
+    if constexpr (C::BULK)
+      if (warp == 22) fetch_role<D, BITS>(a, wt, smem, ring);
     __syncwarp();
   }
   tc5::fence_before();
