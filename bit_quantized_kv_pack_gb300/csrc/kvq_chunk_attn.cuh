@@ -771,6 +771,8 @@ __device__ __forceinline__ void fetch_role(const ChunkAttnArgs& a, const Waits& 
 
 // ---------------------------------------------------------------------- MMA ---
 
+// The warp that issues the MMAs: all its lanes go the same way, so that descriptors and
+// addresses stay in the warp's uniform registers, and one of them issues.
 template <int D, int BITS>
 __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt, uint32_t smem, uint32_t tmem,
                                          const Seg* ring) {
@@ -781,14 +783,16 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
   uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
   uint32_t kv = 0;                          // tiles so far
   bool ok = true;
+  auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
   for (;; ++k.i) {
-    if (!k.wait(wt) || k.get(ring).b < 0) break;
-    const bool alt = k.get(ring).alt;
-    const int n = k.get(ring).hi - k.get(ring).lo;
-    ptx::mbar_arrive(wt.bar(B_SEGEMPTY + k.i % kSegs));
+    if (!all(k.wait(wt)) || uniform(k.get(ring).b) < 0) break;
+    const bool alt = uniform(k.get(ring).alt);
+    const int n = uniform(k.get(ring).hi - k.get(ring).lo);
+    wt.arrive_warp(B_SEGEMPTY + k.i % kSegs);
     const int U = C::LANES == 2 && !alt ? 2 * n : n;
-    ok = wt.wait(B_QFULL, qn[0]++ & 1);
-    if (ok && C::LANES == 2 && !alt) ok = wt.wait(B_QFULL + 1, qn[1]++ & 1);
+    ok = wt.wait_warp(B_QFULL, qn[0]++ & 1);
+    if (ok && C::LANES == 2 && !alt) ok = wt.wait_warp(B_QFULL + 1, qn[1]++ & 1);
     if (!ok) break;
     auto tile = [&](int u) { return C::LANES == 2 && !alt ? u >> 1 : u; };
     auto lane_of = [&](int u) { return C::LANES == 2 ? u & 1 : 0; };
@@ -797,50 +801,56 @@ __device__ __forceinline__ void mma_role(const ChunkAttnArgs& a, const Waits& wt
     auto qk = [&](int u) -> bool {
       const uint32_t t = kv + tile(u);
       const int stage = t % C::ST, lane = lane_of(u);
-      if ((C::LANES == 1 || alt || lane == 0) && !wt.wait(B_KFULL + stage, (t / C::ST) & 1)) return false;
+      if ((C::LANES == 1 || alt || lane == 0) && !wt.wait_warp(B_KFULL + stage, (t / C::ST) & 1)) return false;
       tc5::fence_after();
       const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (alt ? 0 : lane * C::QBYTES), 16, 8 * C::RB, C::SWZ);
       const uint64_t kd = tc5::smem_desc(smem + C::OFF_K + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+      if (tc5::elect()) {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        constexpr int PW = C::PW;
-        const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
-        tc5::mma_ss(tmem + C::S0 + lane * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
-                    kIdescQK, j > 0);
+        for (int j = 0; j < D / 16; ++j) {
+          constexpr int PW = C::PW;
+          const int panel = j * 16 / PW, in = (j * 16 % PW) * 2;
+          tc5::mma_ss(tmem + C::S0 + lane * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+                      kIdescQK, j > 0);
+        }
+        tc5::commit(wt.bar(B_SFULL + lane));
+        if (releases(u)) tc5::commit(wt.bar(B_KEMPTY + stage));
       }
-      tc5::commit(wt.bar(B_SFULL + lane));
-      if (releases(u)) tc5::commit(wt.bar(B_KEMPTY + stage));
+      __syncwarp();
       return true;
     };
     for (int u = 0; ok && u < C::LANES && u < U; ++u) ok = qk(u);
     for (int u = 0; ok && u < U; ++u) {
       const uint32_t t = kv + tile(u);
       const int stage = t % C::ST, lane = lane_of(u);
-      ok = wt.wait(B_PREADY + lane, pn[lane]++ & 1);
-      if (ok && (C::LANES == 1 || alt || lane == 0)) ok = wt.wait(B_VFULL + stage, (t / C::ST) & 1);
+      ok = wt.wait_warp(B_PREADY + lane, pn[lane]++ & 1);
+      if (ok && (C::LANES == 1 || alt || lane == 0)) ok = wt.wait_warp(B_VFULL + stage, (t / C::ST) & 1);
       if (!ok) break;
       tc5::fence_after();
       const uint64_t vd = tc5::smem_desc(smem + C::OFF_V + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
       const bool acc = u >= C::LANES;  // the lane's first tile of the segment starts O
+      if (tc5::elect()) {
 #pragma unroll
-      for (int j = 0; j < C::TN / 16; ++j) {
-        // P of each half of the tokens lies at the start of that half of S
-        const int col = j * 16 / C::HC * C::HC + (j * 16 % C::HC) / 2;
-        tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + col,
-                    vd + ((j * 16 * C::RB) >> 4), kIdescPV, acc || j > 0);
+        for (int j = 0; j < C::TN / 16; ++j) {
+          // P of each half of the tokens lies at the start of that half of S
+          const int col = j * 16 / C::HC * C::HC + (j * 16 % C::HC) / 2;
+          tc5::mma_ts(tmem + C::O0 + lane * C::OSTEP, tmem + C::S0 + lane * C::TN + col,
+                      vd + ((j * 16 * C::RB) >> 4), kIdescPV, acc || j > 0);
+        }
+        if (releases(u)) tc5::commit(wt.bar(B_VEMPTY + stage));
+        if (u + C::LANES >= U) tc5::commit(wt.bar(B_ODONE + lane));
       }
-      if (releases(u)) tc5::commit(wt.bar(B_VEMPTY + stage));
-      if (u + C::LANES < U)
-        ok = qk(u + C::LANES);  // after PV(u) in the tensor cores' order: S may take P's place
-      else
-        tc5::commit(wt.bar(B_ODONE + lane));
+      __syncwarp();
+      // after PV(u) in the tensor cores' order: S may take P's place
+      if (u + C::LANES < U) ok = qk(u + C::LANES);
     }
     if (!ok) break;
     kv += n;
   }
   // nothing of this thread's is in flight when TMEM is freed
-  tc5::commit(wt.bar(B_DRAIN));
-  wt.wait(B_DRAIN, 0);
+  if (tc5::elect()) tc5::commit(wt.bar(B_DRAIN));
+  __syncwarp();
+  wt.wait_warp(B_DRAIN, 0);
 }
 
 // ------------------------------------------------------------------ softmax ---
@@ -1265,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   }
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(base + C::OFF_BAR);
   volatile int64_t* wide = reinterpret_cast<volatile int64_t*>(base + C::OFF_BAR);
-  const int tid = threadIdx.x, warp = tid >> 5, lid = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lid = tid & 31;
   // nothing is read or written before the kernel before this one is done
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1361,7 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  const uint32_t tmem = words[W_TMEM];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[W_TMEM], 0);
   const Waits wt = {a, smem + C::OFF_BAR};
   Seg* ring = reinterpret_cast<Seg*>(base + C::OFF_SEG);
   const int sb = words[W_STARTB], sq = words[W_STARTQ];
@@ -1380,7 +1390,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     deq.run();
   } else {
     tc5::regs_dec<40>();
-    if (tid == 20 * 32) mma_role<D, BITS>(a, wt, smem, tmem, ring);
+    if (warp == 20) mma_role<D, BITS>(a, wt, smem, tmem, ring);
     if (tid == 21 * 32) walk_role<D, BITS>(a, wt, ring, sb, sq, sbase, x0, x1, W, G);
     if constexpr (C::BULK)
       if (warp == 22) fetch_role<D, BITS>(a, wt, smem, ring);

@@ -147,6 +147,15 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// One lane of the warp, which the compiler knows to be one.
+__device__ __forceinline__ bool elect() {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(x)::"memory");
+  return x != 0;
+}
+
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
