@@ -527,7 +527,7 @@ cudaError_t launch_append_chunk(const Dims& s, const kvq_cache_view& v, const kv
   const int64_t units = (len + tpw - 1) / tpw * a.groups;
   int blocks = 0, threads = 0;
   constexpr int kWarps = kRunThreads / 32;
-  if (units <= 16 * kWarps && s.B < (1 << 28)) {
+  if (units <= 16 * kWarps) {
     blocks = units <= kWarps ? 1 : units <= 2 * kWarps ? 2 : units <= 4 * kWarps ? 4 : 8;
     threads = 32 * (int)(units < 1 ? 1 : units < kWarps ? units : kWarps);
   }
@@ -576,17 +576,11 @@ cudaError_t launch_read_tokens(const Dims& s, const kvq_cache_view& v, const int
   auto blocks = [&](int rows) { return (pieces + kReadThreads * rows - 1) / (kReadThreads * rows); };
   a.rows = kReadRows;
   while (a.rows > 1 && blocks(a.rows) * s.B * s.Hkv * 2 < 4 * device_sm_count()) a.rows /= 2;
-  const dim3 grid((unsigned)blocks(a.rows), (unsigned)(s.B * s.Hkv), 2);
   const bool f32 = (flags & KVQ_OUT_F32) != 0;
-  if (s.bits == 4)
-    f32 ? read_tokens_kernel<4, true><<<grid, kReadThreads, 0, st>>>(a)
-        : read_tokens_kernel<4, false><<<grid, kReadThreads, 0, st>>>(a);
-  else if (s.bits == 3)
-    f32 ? read_tokens_kernel<3, true><<<grid, kReadThreads, 0, st>>>(a)
-        : read_tokens_kernel<3, false><<<grid, kReadThreads, 0, st>>>(a);
-  else
-    f32 ? read_tokens_kernel<2, true><<<grid, kReadThreads, 0, st>>>(a)
-        : read_tokens_kernel<2, false><<<grid, kReadThreads, 0, st>>>(a);
+  auto kernel = s.bits == 4   ? (f32 ? read_tokens_kernel<4, true> : read_tokens_kernel<4, false>)
+                : s.bits == 3 ? (f32 ? read_tokens_kernel<3, true> : read_tokens_kernel<3, false>)
+                              : (f32 ? read_tokens_kernel<2, true> : read_tokens_kernel<2, false>);
+  kernel<<<dim3((unsigned)blocks(a.rows), (unsigned)(s.B * s.Hkv), 2), kReadThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -14,13 +14,26 @@
 //   0-15   softmax: S from TMEM, P back to TMEM (it takes S's place and is the A operand
 //          of the second MMA), the epilogue.  Four groups of four warps: two for each of
 //          the block's two accumulators (lanes 0 and 1), each with half of the tile's
-//          tokens and half of O's columns, a thread per query row.  (One group per
-//          accumulator left the chain S -> P -> next S as the bound: 42 % of the issue
-//          slots used.)
-//   16-19  dequantize: a row of codes comes by cp.async into a ring that is private to
-//          its thread (no barrier), becomes fp16 in registers and goes to shared memory
+//          tokens and half of O's columns, a thread per query row.
+//   16-19  dequantize: raw rows in a ring become fp16 in registers and go to shared memory
 //          in the MMA's 128-byte swizzle, K as the K-major and V as the MN-major B operand.
-//   20     issues the MMAs; 21 works out the segments.
+//          Up to head_dim 64 each thread also copies its rows (cp.async, no barrier).
+//   20     issues the MMAs; 21 works out the segments; 22 copies the raw rows from head_dim
+//          128 on (bulk copies: the dequantizing warps spent a quarter of their time on the
+//          addresses, 2048 x 32768 tokens of INT2 1039 -> 1002 us, 1024 x 16384 of INT4
+//          593 -> 557 us without).
+// The MMA warp's lanes all go the same way and one is elected for each batch, so that the
+// descriptors are in uniform registers: a lone thread moved each of them there per MMA and
+// was the bound (1002 -> 819 us and 557 -> 457 us).  Eight dequantizing warps, keys and
+// values apart, made runs of few rows 3-6 % faster and the long ones 6-7 % slower (72
+// registers a thread at launch in place of 80).
+//
+// What bounds it now: the chain S -> softmax -> P -> PV -> next S of each accumulator, with
+// the other's MMAs under it, and the shared memory that the MMAs read Q and K from; 2048 x
+// 32768 tokens of INT2 (32 heads on 8, head_dim 128) take 819 us, 68 % of the bf16 rate
+// that a library product reaches.  Calls of few rows are bound by the warps that
+// dequantize, and the smallest by the way to the first tile (7 us) and the join (5 us).
+//
 // A unit of work is (sequence, block of query rows, KV head).  With more than 128 rows in
 // the block the two lanes are its two halves and share each tile; with fewer they take
 // alternate tiles of the same rows and are joined at the end, so that the softmax of one
@@ -65,7 +78,7 @@ struct ChunkAttnArgs {
   int B, Hkv, Hq, gq, cap, Nr, Ns, total, max_len, causal, out_f32;
   uint32_t gq_mul, gq_shift;  // row / gq = row * gq_mul >> gq_shift for rows below 2^31
   uint32_t wait_limit_us;
-  int fault;  // testing hook: one barrier of block 0 waits for an arrival that never comes
+  int fault;  // testing hook: 1 makes the scores' barriers wait for an arrival that never comes
   float scale_log2;
 };
 
@@ -82,8 +95,8 @@ namespace chunk {
 constexpr int kThreads = 768;
 constexpr int kDeqThreads = 128;
 // What the line of tiles is cut by, in quarters of a shared tile's time (128 tokens x 256
-// rows): a shared tile 2.0 us, a lane's own 1.5 us, a unit's begin and end about 5 us
-// (head_dim 128; measured).
+// rows): a shared tile 2 us, a lane's own 1.5 us, a unit's begin and end about 5 us
+// (head_dim 128, measured).
 constexpr int kCostShared = 4, kCostOwn = 3, kCostUnit = 10;
 
 template <int D, int BITS>
@@ -755,8 +768,10 @@ __device__ __forceinline__ void fetch_role(const ChunkAttnArgs& a, const Waits& 
           ptx::mbar_arrive_expect_tx(wt.bar(B_RAWFULL + slot), all);
         }
         __syncwarp();
-        const char* src = codes ? reinterpret_cast<const char*>(a.codes[w]) : reinterpret_cast<const char*>(a.params[w]);
-        if (bytes) ptx::bulk_load(to + slot * C::RAWB, src + row * row_bytes, bytes, wt.bar(B_RAWFULL + slot));
+        const void* of = codes ? static_cast<const void*>(a.codes[w]) : a.params[w];
+        if (bytes)
+          ptx::bulk_load(to + slot * C::RAWB, static_cast<const char*>(of) + row * row_bytes, bytes,
+                         wt.bar(B_RAWFULL + slot));
         if (++slot == C::RAWN) slot = 0;
       }
     }
@@ -1315,7 +1330,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     for (int i = lid; i < B_COUNT; i += 32) {
       int n = 1;  // arrivals of a phase
       if (i == B_QFULL || i == B_QFULL + 1 || i == B_PREADY || i == B_PREADY + 1) n = 8;
-      if (i == B_SFULL || i == B_SFULL + 1) n = 1 + (a.fault && blockIdx.x == 0 ? 1 : 0);
+      if (i == B_SFULL || i == B_SFULL + 1) n = 1 + a.fault;
       if (i >= B_MAX && i < B_MAX + 8) n = 2;
       if (i >= B_SEGEMPTY && i < B_SEGEMPTY + kSegs) n = C::SMW + 4 + 1 + C::BULK;
       if (i >= B_RAWEMPTY && i < B_RAWEMPTY + 3) n = 4;

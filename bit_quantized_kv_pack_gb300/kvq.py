@@ -520,12 +520,12 @@ def kvq_chunk_workspace_bytes(desc: CacheDesc, num_q_heads: int) -> int:
 
 
 def chunk_workspace_for(cache: KVCache, num_q_heads: int) -> torch.Tensor:
-    """A zeroed workspace for kvq_chunk_attention and kvq_cross_attention (zeroed
-    once; any run lengths)."""
+    """A workspace for kvq_chunk_attention and kvq_cross_attention (any run lengths; one
+    call at a time)."""
     n = kvq_chunk_workspace_bytes(cache.desc, num_q_heads)
     if n == 0:
         raise KvqError(KVQ_ERR_INVALID_ARG, "kvq_chunk_workspace_bytes")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspace, stream, flags):
@@ -605,7 +605,7 @@ def kvq_version() -> int:
 
 def kvq_testing_wait_fault(limit_us: int) -> None:
     """Testing hook (see kvq.h): limit_us > 0 makes one bounded wait of the next
-    tensor-core decode calls run out after limit_us microseconds; 0 turns it off."""
+    tensor-core decode calls, and of the next calls on runs, run out after limit_us microseconds; 0 turns it off."""
     load().kvq_testing_wait_fault(int(limit_us))
 
 

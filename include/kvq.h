@@ -421,8 +421,8 @@ typedef struct {
  *   R3  with q, q_out[t] is row t's queries rotated to the same position; rows of
  *       dropped tokens included.
  * A position outside [0, rope_rows) sets KVQ_ERRBIT_BADPOS and uses the nearest
- * row.  One launch for short runs (a block per sequence), two otherwise (the
- * counters move in the second).  Asynchronous; needs no workspace. */
+ * row.  One launch for short runs (a cluster of blocks per sequence), two otherwise
+ * (the counters move in the second).  Asynchronous; needs no workspace. */
 kvq_status kvq_append_chunk(const kvq_cache_desc* desc, const kvq_cache_view* view,
                             const kvq_append_args* args, void* stream);
 
@@ -437,14 +437,15 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* desc, int32_t num_q_heads
  * packed_len + res_len tokens, in the form in which the cache holds them.
  *   q          fp16 device [total][Hq][d], 16-byte aligned (rotated, where positions are).
  *   out        device [total][Hq][d], fp16 (fp32 with KVQ_OUT_F32 in flags), rounded
- *              once from the fp32 result.
+ *              once from the fp32 result; overlaps no input.
  *   workspace  device scratch of ws_bytes >= kvq_chunk_workspace_bytes(desc, Hq),
- *              16-byte aligned, zeroed before its first use; each completed call
- *              leaves it ready for the next, whatever its shapes.  Zero it again
- *              after a call that reported KVQ_ERR_TIMEOUT.  One workspace serves
- *              one call at a time.
+ *              16-byte aligned; whatever it holds, each call writes what it reads.
+ *              One workspace serves one call at a time.
  *   flags      0 or KVQ_OUT_F32; other bits return KVQ_ERR_INVALID_ARG.
  * A row with no token to attend over gets zeros and sets KVQ_ERRBIT_EMPTY.
+ * Keys, values and weights are rounded to fp16 once each (operands of the tensor
+ * cores), scores and sums are fp32; results do not depend on timing.  A value past
+ * fp16's range by the rounding of its scale counts as fp16's largest.
  * Tokens a row does not attend over have no part in its output, whatever they
  * hold.  Tokens in a page outside the pool are left out (KVQ_ERRBIT_BADPAGE).
  * With one token for every sequence kvq_decode_attention is the faster call.
@@ -499,6 +500,9 @@ int32_t kvq_version(void); /* 160: two-part weights in the tensor-core MMAs, MMA
  * complete, so nothing is in flight when that CTA gives up: it sets
  * KVQ_ERRBIT_TIMEOUT, contributes nothing to its head's output (which is then
  * wrong for that head) and returns; the call's other results are unaffected.
+ * kvq_chunk_attention and kvq_cross_attention give the barriers of their scores an
+ * arrival that never comes: every block gives up, with nothing in flight, and the
+ * output is wrong.
  * limit_us = 0 (the default) restores normal behaviour.  Process-wide; not for
  * production use. */
 void kvq_testing_wait_fault(uint32_t limit_us);
