@@ -548,15 +548,17 @@ struct Deq {
     uint32_t raw[C::UN * 4], prm[C::GPT];
 #pragma unroll
     for (int i = 0; i < C::UN; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (!C::BULK)
-        v = ld_shared_v4(dc + i * (kDeqThreads * 16));
-      else if (there)
-        v = ld_shared_v4(dc + (BITS == 4 ? group(i) : BITS == 2 ? i ^ rot : i) * 16);
+      const uint4 v = ld_shared_v4(dc + (!C::BULK    ? i * (kDeqThreads * 16)
+                                         : BITS == 4 ? group(i) * 16
+                                         : BITS == 2 ? (i ^ rot) * 16
+                                                     : i * 16));
       raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < C::GPT; ++i) prm[i] = there ? lds(dp + 4 * group(i)) : 0;
+    for (int i = 0; i < C::GPT; ++i) {
+      const uint32_t x = lds(dp + 4 * group(i));
+      prm[i] = there ? x : 0;  // whatever the codes, zeros
+    }
     if (C::BULK) wt.arrive_warp(B_RAWEMPTY + slot);
     const uint32_t at = row_addr(dst);
     auto piece = [&](int g, int c) { return (at ^ (((g & 1) * 4 + c) << 4)) + (g / 2) * C::KP; };
