@@ -2,7 +2,7 @@
 // Every entry point validates on the host and launches nothing on an error.
 #include <string.h>
 
-#include "kvq_internal.cuh"
+#include "kvq_runs.cuh"
 
 namespace {
 

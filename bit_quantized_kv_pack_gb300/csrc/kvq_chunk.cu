@@ -16,8 +16,8 @@
 // of a block share their tokens, so that cosines and sines come from L1 after the
 // first.  The rotation's partner values (rotary_dim / 2 away) are in a lane of the
 // same row and come by shuffles.
-#include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
+#include "kvq_runs.cuh"
 
 namespace kvq {
 namespace {

@@ -52,8 +52,8 @@
 
 #include <math.h>
 
-#include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
+#include "kvq_runs.cuh"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
