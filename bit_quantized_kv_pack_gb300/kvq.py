@@ -522,10 +522,12 @@ def kvq_chunk_workspace_bytes(desc: CacheDesc, num_q_heads: int) -> int:
 def chunk_workspace_for(cache: KVCache, num_q_heads: int) -> torch.Tensor:
     """A workspace for kvq_chunk_attention and kvq_cross_attention (any run lengths; one
     call at a time)."""
-    n = kvq_chunk_workspace_bytes(cache.desc, num_q_heads)
+    device = cache.counters.device
+    with torch.cuda.device(device):  # its size follows from the device
+        n = kvq_chunk_workspace_bytes(cache.desc, num_q_heads)
     if n == 0:
         raise KvqError(KVQ_ERR_INVALID_ARG, "kvq_chunk_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspace, stream, flags):
@@ -538,8 +540,10 @@ def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspa
     out, flags = _out(q, out, flags)
     if workspace is None:
         workspace = chunk_workspace_for(cache, heads)
-    if out.shape != q.shape or out.device != device or workspace.device != device:
-        raise ValueError("out must have q's shape; out and workspace must be on the cache's device")
+    if out.shape != q.shape or out.device != device:
+        raise ValueError("out must have q's shape, on the cache's device")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the cache's device")
     _run_call(name, cache, device, stream, qp, heads, cu, total, int(max_len), out.data_ptr(),
               workspace.data_ptr(), workspace.numel() * workspace.element_size(), flags)
     return out

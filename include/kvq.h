@@ -378,7 +378,7 @@ kvq_status kvq_decode_attention_noalloc(const kvq_cache_desc* desc, const kvq_ca
  *               sequence b is rows [cu_seqlens[b], cu_seqlens[b + 1]) of the
  *               token-major inputs and outputs.  A run may be empty.
  *   total       rows those arrays have (cu_seqlens[B] <= total).  Rows of no
- *               run are neither read nor written.
+ *               run are not written and have no part in any result.
  *   max_len     host upper bound of the run lengths, >= 0.
  * A sequence whose entries are not 0 <= cu[b] <= cu[b+1] <= total with at most
  * max_len tokens is skipped and sets KVQ_ERRBIT_BADLEN. */

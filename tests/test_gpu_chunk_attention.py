@@ -153,7 +153,8 @@ def test_large_scores_and_values(d):
         _check(_call(g, q, cu, causal, flags=kvq.KVQ_OUT_F32), want, bound, rel=None)
 
 
-@pytest.mark.parametrize("d,bits,Nr", [(128, 4, 40), (128, 4, 0), (64, 2, 0), (256, 3, 16), (32, 4, 8)])
+@pytest.mark.parametrize("d,bits,Nr", [(128, 4, 40), (128, 4, 0), (64, 2, 0), (256, 3, 16), (32, 4, 8),
+                                       (128, 2, 16), (128, 3, 0), (256, 2, 0), (256, 4, 16), (64, 3, 8)])
 def test_hidden_tokens_have_no_part(d, bits, Nr):
     """Infinities and NaN in tokens that a row does not see: the run's later tokens, and
     memory past the sequence's end (packed rows, ring slots).  The rows that see an
