@@ -976,14 +976,17 @@ struct Soft {
   // Hides what the row does not see of 32 tokens (a page: `bad` all of them); the largest
   // score that is left.
   static __device__ __forceinline__ float mask(float (&s)[32], int visible, uint32_t bad) {
-    const int v = bad ? 0 : visible;
-    float x = -INFINITY;
+    // a bit for each token (bits become predicates several at a time)
+    const uint32_t seen = bad || visible <= 0 ? 0u : visible >= 32 ? ~0u : (1u << visible) - 1u;
+    float x = -INFINITY, y = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      s[j] = j < v ? s[j] : -INFINITY;
+    for (int j = 0; j < 32; j += 2) {
+      s[j] = (seen >> j) & 1u ? s[j] : -INFINITY;
+      s[j + 1] = (seen >> (j + 1)) & 1u ? s[j + 1] : -INFINITY;
       x = fmaxf(x, s[j]);
+      y = fmaxf(y, s[j + 1]);
     }
-    return x;
+    return fmaxf(x, y);
   }
 
   // One tile: the weights of the group's half of S's row into TMEM, m (the same in both
