@@ -52,6 +52,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include "kvq_ptx.cuh"
 #include "kvq_runs.cuh"
 #include "kvq_tcgen05.cuh"
@@ -1634,21 +1636,34 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(c
   }
 }
 
+// The kernels' attributes, once per device.
 template <int D, int BITS>
-cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
-  static_assert(Cfg<D, BITS>::SMEM <= 227 * 1024, "shared memory of a block");
-  if (grid > kMaxBlocks) return cudaErrorInvalidConfiguration;
+cudaError_t ensure_attrs() {
   auto kernel = chunk_attn_kernel<D, BITS>;
   auto join = chunk_join_kernel<D, BITS>;
-  cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  static std::atomic<uint64_t> done{0};  // bit i: set on device i
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
   // the warps' shares (setmaxnreg) come out of what the block is launched with
   if (at.numRegs != 80) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, BITS>::SMEM);
   if (e != cudaSuccess) return e;
   // the same split of L1 and shared memory: an SM that changes it drains first
   e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
+template <int D, int BITS>
+cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
+  static_assert(Cfg<D, BITS>::SMEM <= 227 * 1024, "shared memory of a block");
+  if (grid > kMaxBlocks) return cudaErrorInvalidConfiguration;
+  cudaError_t e = ensure_attrs<D, BITS>();
   if (e != cudaSuccess) return e;
   // each may be launched while the kernel before it ends, and waits for it
   cudaLaunchAttribute attr[1];
@@ -1661,11 +1676,11 @@ cudaError_t launch(const ChunkAttnArgs& a, int grid, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D, BITS>, a)) != cudaSuccess) return e;
   cfg.gridDim = dim3(kJoinBlocks * grid);
   cfg.blockDim = kJoinThreads;
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join, a, grid);
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, BITS>, a, grid);
 }
 
 template <int D>
