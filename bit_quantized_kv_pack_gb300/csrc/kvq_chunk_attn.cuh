@@ -30,7 +30,7 @@
 //
 // What bounds it now: the chain S -> softmax -> P -> PV -> next S of each accumulator, with
 // the other's MMAs under it, and the shared memory that the MMAs read Q and K from; 2048 x
-// 32768 tokens of INT2 (32 heads on 8, head_dim 128) take 819 us, 68 % of the bf16 rate
+// 32768 tokens of INT2 (32 heads on 8, head_dim 128) take 805 us, 69 % of the bf16 rate
 // that a library product reaches.  Calls of few rows are bound by the warps that
 // dequantize, and the smallest by the way to the first tile (7 us) and the join (5 us).
 //
