@@ -421,8 +421,8 @@ typedef struct {
  *   R3  with q, q_out[t] is row t's queries rotated to the same position; rows of
  *       dropped tokens included.
  * A position outside [0, rope_rows) sets KVQ_ERRBIT_BADPOS and uses the nearest
- * row.  One launch for short runs (a cluster of blocks per sequence), two otherwise
- * (the counters move in the second).  Asynchronous; needs no workspace. */
+ * row.  One launch for the shortest runs (a block per sequence), two otherwise (the
+ * counters move in the second).  Asynchronous; needs no workspace. */
 kvq_status kvq_append_chunk(const kvq_cache_desc* desc, const kvq_cache_view* view,
                             const kvq_append_args* args, void* stream);
 
