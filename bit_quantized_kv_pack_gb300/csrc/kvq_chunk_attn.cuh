@@ -96,9 +96,11 @@ namespace chunk {
 
 constexpr int kThreads = 768;
 constexpr int kDeqThreads = 128;
-// What the line of tiles is cut by, in quarters of a shared tile's time (128 tokens x 256
-// rows): a shared tile 2 us, a lane's own 1.5 us, a unit's begin and end about 5 us
-// (head_dim 128, measured).
+// What the line of tiles is cut by, in half microseconds (head_dim 128): a tile of 128
+// tokens that the lanes share, one lane's own, a unit's begin and end.  Fitted to blocks'
+// times a shared tile takes 2.0 us, an own one 1.1 to 1.4, a unit 3 with few rows and 9
+// with many; dearer units (20, with 8 for a tile of fp16 tokens) made the 40-head case 6 %
+// faster and a batch of drafts 9 % slower.
 constexpr int kCostShared = 4, kCostOwn = 3, kCostUnit = 10;
 
 template <int D, int BITS>
