@@ -1189,11 +1189,13 @@ struct Soft {
       if (!wait_seg()) return false;
       const bool more = ref().b() >= 0;
       if (more && !pass) load_q();
-      // l of both groups
+      // l of both groups.  The next segment's Q may be there already, and its first maximum
+      // goes where l is: the partner says when it has read (waited for below).
       if (live) {
         stsf(xmax() + half() * 512 + r() * 4, l);
         if (!row_sync()) return false;
         l += ldsf(xmax() + (half() ^ 1) * 512 + r() * 4);
+        wt.arrive_warp(B_MAX + lane() * 4 + (r() >> 5));
       }
       const bool noted = wt.word(W_PFLAG) != 0;
       const int slot = 2 * block + (k.lo() == 0);
@@ -1270,6 +1272,7 @@ struct Soft {
         if (threadIdx.x == 0) wt.set_word(W_PFLAG, 0);
         if (!pair_sync()) return false;
       }
+      if (live && !wait(B_MAX + lane() * 4 + (r() >> 5), P_MAX)) return false;  // (as a rule long since)
       tc5::fence_before();
       __threadfence_block();
       __syncwarp();
