@@ -173,6 +173,26 @@ def _stream(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _made(stream, device, make, returned: bool = False) -> torch.Tensor:
+    """make(), a tensor of the call's own, on the call's stream.  The allocator hands memory
+    on in the order of the stream that it was taken on, so what a call drops when it returns
+    (a workspace) must come from the stream that its kernels run on, and so must what they
+    write.  What is returned is the caller's on the current stream, and recorded there."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _f16(t: torch.Tensor, name: str) -> torch.Tensor:
     if t.dtype != torch.float16 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float16 CUDA tensor")
@@ -182,12 +202,12 @@ def _f16(t: torch.Tensor, name: str) -> torch.Tensor:
 KVQ_OUT_F32 = 2
 
 
-def _out(q: torch.Tensor, out: torch.Tensor | None, flags: int):
+def _out(q: torch.Tensor, out: torch.Tensor | None, flags: int, stream=None):
     """The output tensor and the flags that match its dtype: float16, or float32
     (KVQ_OUT_F32).  Without `out`, the dtype follows KVQ_OUT_F32 in flags."""
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32 if flags & KVQ_OUT_F32 else torch.float16,
-                          device=q.device)
+        dtype = torch.float32 if flags & KVQ_OUT_F32 else torch.float16
+        out = _made(stream, q.device, lambda: torch.empty(q.shape, dtype=dtype, device=q.device), True)
     if out.dtype not in (torch.float16, torch.float32) or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous float16 or float32 CUDA tensor")
     if out.dtype == torch.float32:
@@ -335,9 +355,9 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor | No
     """O = softmax(q K^T / sqrt(d)) V; q fp16 [B][Hq][d] -> out [B][Hq][d], fp16
     or fp32 (an fp32 `out`, or flags=KVQ_OUT_F32)."""
     _f16(q, "q")
-    out, flags = _out(q, out, flags)
+    out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = workspace_for(cache, q.shape[1])
+        workspace = _made(stream, cache.device, lambda: workspace_for(cache, q.shape[1]))
     st = load().kvq_decode_attention(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
                                      int(q.shape[1]), _ptr(out), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), int(flags),
@@ -359,9 +379,9 @@ def kvq_decode_step(cache: KVCache, q: torch.Tensor, k_new: torch.Tensor, v_new:
     before does not write this cache (see kvq.h).  An fp32 `out` (or
     KVQ_OUT_F32 in flags) gives fp32 output."""
     _f16(q, "q"), _f16(k_new, "k_new"), _f16(v_new, "v_new")
-    out, flags = _out(q, out, flags)
+    out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = workspace_for(cache, q.shape[1])
+        workspace = _made(stream, cache.device, lambda: workspace_for(cache, q.shape[1]))
     st = load().kvq_decode_step(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
                                 int(q.shape[1]), _ptr(k_new), _ptr(v_new), _ptr(out),
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -414,7 +434,7 @@ def kvq_decode_attention_noalloc(cache: KVCache, q: torch.Tensor, out: torch.Ten
     library's own static device array holds the split partials.  Calls that
     overlap on the GPU share that array and race; keep them on one stream."""
     _f16(q, "q")
-    out, flags = _out(q, out, 0)
+    out, flags = _out(q, out, 0, stream)
     st = load().kvq_decode_attention_noalloc(ctypes.byref(cache.desc), ctypes.byref(cache.view),
                                              _ptr(q), int(q.shape[1]), _ptr(out), int(flags),
                                              _stream(stream, q.device))
@@ -500,7 +520,7 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         heads = q.shape[1]
         a.q = _run_tensor(q, heads, cache, device, "q", False)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=device)
+            q_out = _made(stream, device, lambda: torch.empty(q.shape, dtype=torch.float16, device=device), True)
         a.q_out = _run_tensor(q_out, heads, cache, device, "q_out", True)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
@@ -542,9 +562,9 @@ def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspa
     total, heads, _ = q.shape
     cu = _run_int(cu_seqlens, cache.desc.batch + 1, device, "cu_seqlens")
     qp = _run_tensor(q, heads, cache, device, "q", True)
-    out, flags = _out(q, out, flags)
+    out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = chunk_workspace_for(cache, heads)
+        workspace = _made(stream, device, lambda: chunk_workspace_for(cache, heads))
     if out.shape != q.shape or out.device != device:
         raise ValueError("out must have q's shape, on the cache's device")
     if workspace.device != device or not workspace.is_contiguous():
@@ -588,7 +608,8 @@ def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
         torch.float32 if flags & KVQ_OUT_F32 else torch.float16)
     if dtype not in (torch.float16, torch.float32):
         raise ValueError("k_out and v_out must be float16 or float32")
-    outs = [torch.empty(shape, dtype=dtype, device=device) if t is None else t for t in (k_out, v_out)]
+    outs = [_made(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device), True) if t is None
+            else t for t in (k_out, v_out)]
     for t in (k_out, v_out):
         if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_cuda or t.device != device
                               or not t.is_contiguous()):
