@@ -8,7 +8,10 @@
 // running maximum lazily: it moves (and O, l are rescaled) only when the maximum has
 // passed it by 2^8, so weights stay below 256 and the sums lose nothing in fp32.
 // Roundings: the dequantized keys and values min + code * scale are rounded to fp16 once
-// (operands of the MMA), the weights P to fp16 once; scores, m, l and O are fp32.
+// (operands of the MMA), the weights P to fp16 once; scores, m, l and O are fp32.  P and l
+// carry a factor 2^7, which O / l and every join of parts cancel: P reaches 2^15, near
+// the top of fp16's range, so that weights keep 11 bits down to 2^-21 of the reference
+// and lose at most 2^-32 of it below (a long tail under one dominant token).
 //
 // A block (one per SM, persistent) has 24 warps:
 //   0-15   softmax: S from TMEM, P back to TMEM (it takes S's place and is the A operand
@@ -95,6 +98,7 @@ __host__ __device__ constexpr int chunk_rows(int d) { return d == 256 ? 128 : 25
 namespace chunk {
 
 constexpr int kThreads = 768;
+constexpr float kWeightBits = 7.0f;  // log2 of the weights' factor
 constexpr int kDeqThreads = 128;
 // What the line of tiles is cut by, in half microseconds (head_dim 128): a tile of 128
 // tokens that the lanes share, one lane's own, a unit's begin and end.  Fitted to blocks'
@@ -1037,7 +1041,7 @@ struct Soft {
         }
       }
     }
-    const float off = m == -INFINITY ? 0.0f : -m * a.scale_log2;
+    const float off = m == -INFINITY ? 0.0f : fmaf(-m, a.scale_log2, kWeightBits);
     const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
     uint64_t sum2 = pack_f32x2(l, 0.0f);
 #pragma unroll

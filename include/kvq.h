@@ -444,7 +444,8 @@ size_t kvq_chunk_workspace_bytes(const kvq_cache_desc* desc, int32_t num_q_heads
  *   flags      0 or KVQ_OUT_F32; other bits return KVQ_ERR_INVALID_ARG.
  * A row with no token to attend over gets zeros and sets KVQ_ERRBIT_EMPTY.
  * Keys, values and weights are rounded to fp16 once each (operands of the tensor
- * cores), scores and sums are fp32; results do not depend on timing.  A value past
+ * cores; weights below 2^-21 of a row's largest by at most 2^-32 of that), scores and
+ * sums are fp32; results do not depend on timing.  A value past
  * fp16's range by the rounding of its scale counts as fp16's largest.
  * Tokens a row does not attend over have no part in its output, whatever they
  * hold.  Tokens in a page outside the pool are left out (KVQ_ERRBIT_BADPAGE).

@@ -1,0 +1,42 @@
+"""Values at the edges of attention of runs: weights far below the largest, infinities and
+NaN among seen tokens.  Against plain attention in 64 bits over the cache's own tokens."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_kv_pack_gb300 import kvq
+
+from _runs import attend, tokens_of
+from _util import gpu_cache, oracle_sequences, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("T", [4, 140])  # the accumulators take turns; they share the tiles
+@pytest.mark.parametrize("d,bits", [(64, 4), (128, 2), (256, 3)])
+def test_a_long_tail_under_one_dominant_token_keeps_its_mass(d, bits, T):
+    """Token 0 outweighs each of 32767 others by e^9 to e^18, values of one sign: the tail's
+    part of the output is n times a weight that fp16 alone would not hold.  The weights'
+    own rounding: half a step of fp16, or 2^-25 of a weight 2^7 times the row's reference."""
+    rng = np.random.default_rng(40 + d)
+    H, n = 160, 32768  # more heads than blocks: whole units
+    k = torch.zeros(1, H, n, d, dtype=torch.float16, device=DEV)
+    k[:, :, 0] = 1.0
+    gen = torch.Generator(DEV).manual_seed(d)
+    v = (torch.rand(1, H, n, d, generator=gen, device=DEV) + 0.5).half()
+    v[:, :, 0] = 0.0
+    g = gpu_cache(1, H, d, bits, n, 0)
+    kvq.kvq_quantize_pack(g, k, v, torch.tensor([n], dtype=torch.int32, device=DEV))
+    nats = np.linspace(9.0, 18.0, T)
+    q = np.broadcast_to((nats / np.sqrt(d))[:, None, None], (T, H, d)).astype(np.float16)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    got = to_np(kvq.kvq_cross_attention(g, torch.from_numpy(q).to(DEV), cu, T, flags=kvq.KVQ_OUT_F32))
+    assert kvq.kvq_read_error(g) == (kvq.KVQ_OK, 0)
+    for h in (0, 1, 77, H - 1):
+        r = oracle_sequences(*(to_np(x[:, h:h + 1]) for x in (k, v)), np.array([n], np.int32), bits, n, 0)[0]
+        want, bound = attend(tokens_of(r, "k", 0), tokens_of(r, "v", 0), q[:, h:h + 1].astype(np.float64), [n] * T)
+        bound += n * 2.0 ** -32 * 1.5
+        err = np.abs(got[:, h:h + 1] - want)
+        assert (err <= bound).all(), (h, float((err / bound).max()))
