@@ -1443,6 +1443,12 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinBlocks = 3;   // of an SM
 constexpr int kMaxBlocks = 256;  // of the kernel above
 
+// A part's weight against the row's maximum: never zero, so that an infinite value that a
+// part has from the notes stays one (0 x inf is NaN); finite parts of 2^-126 are nothing.
+__device__ __forceinline__ float part_weight(float below, float scale_log2) {
+  return fmaxf(ptx::ex2_ftz(below * scale_log2), 1.17549435e-38f);
+}
+
 template <int D>
 struct Joined {
   static constexpr int LPR = D >= 128 ? 32 : D / 4;  // lanes of a row
@@ -1488,13 +1494,13 @@ struct Joined {
     float mm = m;
 #pragma unroll
     for (int i = 0; i < P; ++i) mm = fmaxf(mm, in.ml[i].x);
-    if (m != -INFINITY) scale(ptx::ex2_ftz((m - mm) * scale_log2));
+    if (m != -INFINITY) scale(part_weight(m - mm, scale_log2));
     m = mm;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (in.ml[i].x == -INFINITY && in.ml[i].y == 0.0f) continue;
       // a sum without a maximum is NaN, and stays so
-      const float f = in.ml[i].x == -INFINITY ? in.ml[i].y : ptx::ex2_ftz((in.ml[i].x - mm) * scale_log2);
+      const float f = in.ml[i].x == -INFINITY ? in.ml[i].y : part_weight(in.ml[i].x - mm, scale_log2);
       l += in.ml[i].y * f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -1601,7 +1607,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) chunk_join_kernel(c
       for (int g = 0; g < kGroups; ++g) {
         const float2 ml = part_ml[g];
         if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-        const float f = ml.x == -INFINITY ? ml.y : ptx::ex2_ftz((ml.x - m) * a.scale_log2);
+        const float f = ml.x == -INFINITY ? ml.y : part_weight(ml.x - m, a.scale_log2);
         l += ml.y * f;
         y += part[g][c] * f;
       }

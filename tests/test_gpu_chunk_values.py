@@ -40,3 +40,40 @@ def test_a_long_tail_under_one_dominant_token_keeps_its_mass(d, bits, T):
         bound += n * 2.0 ** -32 * 1.5
         err = np.abs(got[:, h:h + 1] - want)
         assert (err <= bound).all(), (h, float((err / bound).max()))
+
+
+def _cache(rng, n, H, d, bits, cap, Nr, S, k, v):
+    g = gpu_cache(1, H, d, bits, cap, Nr, sink=S)
+    lens = np.array([n], np.int32)
+    kvq.kvq_quantize_pack(g, *(torch.from_numpy(x).to(DEV) for x in (k, v, lens)))
+    return g, oracle_sequences(k, v, lens, bits, cap, Nr, S)[0]
+
+
+@pytest.mark.parametrize("T", [3, 700])  # the join's two forms: a block for a row; rows in one line
+@pytest.mark.parametrize("d,bits", [(64, 4), (128, 3), (256, 2)])
+def test_an_infinite_value_outlasts_much_larger_scores_in_other_pieces(d, bits, T):
+    """Infinite values (a group whose min is infinite) at the start of a cache that several
+    blocks share, under scores hundreds of nats higher from its middle on: still infinite
+    in the rows that see them, NaN where both signs meet, the other columns as ever."""
+    rng = np.random.default_rng(50 + d)
+    H, gq, n, S = 1, 2, 24000, 4
+    k = rng.standard_normal((1, H, n, d)).astype(np.float16)
+    k[:, :, n // 2:] = 6.0
+    v = rng.standard_normal((1, H, n, d)).astype(np.float16)
+    g, r = _cache(rng, n, H, d, bits, n, 0, S, k, v)
+    up, down = 0x7C00 << 16, (0xFC00 << 16) - (1 << 32)  # scale 0, min +-inf
+    g.v_params[0, 0, 1, 0], g.v_params[0, 0, 2, 1] = up, down
+    g.v_sink[0, 0, 1, 33] = float("inf")
+    q = (rng.random((T, H * gq, d)) * 3 + 1).astype(np.float16)  # 6 sum(q) / sqrt(d): 100 nats and more
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    rows = np.unique(np.linspace(0, T - 1, 7).astype(int))
+    for causal in (True, False):
+        f = kvq.kvq_chunk_attention if causal else kvq.kvq_cross_attention
+        got = to_np(f(g, torch.from_numpy(q).to(DEV), cu, T, flags=kvq.KVQ_OUT_F32))
+        assert kvq.kvq_read_error(g) == (kvq.KVQ_OK, 0)
+        assert np.isposinf(got[..., :32]).all() and np.isnan(got[..., 33]).all()
+        assert np.isneginf(np.delete(got[..., 32:64], 1, -1)).all()
+        seen = [n - T + i + 1 if causal else n for i in rows]
+        want, bound = attend(tokens_of(r, "k", 0), tokens_of(r, "v", 0), q[rows].astype(np.float64), seen)
+        bound += n * 2.0 ** -32 * np.abs(v).max()
+        assert (np.abs(got[rows] - want) <= bound)[..., 64:].all()
