@@ -1069,15 +1069,16 @@ struct Soft {
   }
 
   // What the notes say of the group's columns of the row: it sees `lim` tokens; written over the
-  // thread's own earlier stores, to the output (whole) or to the piece's O in `slot`.
-  __device__ __forceinline__ void notes(int lim, bool whole, int64_t at, int slot, int row) const {
+  // thread's own earlier stores, to the output (whole) or to the piece's O in `slot`.  A row
+  // whose sum is NaN (inv; a seen key may be) stays NaN; the join sees to that for pieces.
+  __device__ __forceinline__ void notes(int lim, bool whole, float inv, int64_t at, int slot, int row) const {
     const uint32_t pn = smem + C::OFF_POISON;
 #pragma unroll 1
     for (int c = half() * C::HD; c < (half() + 1) * C::HD; ++c) {
       const bool up = (int)lds(pn + 4 * c) < lim, down = (int)lds(pn + 4 * (D + c)) < lim,
                  nan = (int)lds(pn + 4 * (2 * D + c)) < lim;
       if (!(up || down || nan)) continue;
-      const float v = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+      const float v = nan || (up && down) || inv != inv ? NAN : up ? INFINITY : -INFINITY;
       if (!whole) {
         __stcg(reinterpret_cast<float*>(a.o_part) + ((int64_t)slot * C::QB + row) * D + c, v);
         continue;
@@ -1268,7 +1269,7 @@ struct Soft {
       if (noted) {
         if (mine) {
           const int lim = seen_of(a, k.n(), k.ns() + k.npk() + k.nres(), token_of(a, k.qb() * C::QB + row));
-          notes(lim, whole, at, slot, prow);
+          notes(lim, whole, inv, at, slot, prow);
         }
         // the notes have been read: clean them
         if (!pair_sync()) return false;

@@ -77,3 +77,26 @@ def test_an_infinite_value_outlasts_much_larger_scores_in_other_pieces(d, bits, 
         want, bound = attend(tokens_of(r, "k", 0), tokens_of(r, "v", 0), q[rows].astype(np.float64), seen)
         bound += n * 2.0 ** -32 * np.abs(v).max()
         assert (np.abs(got[rows] - want) <= bound)[..., 64:].all()
+
+
+@pytest.mark.parametrize("n", [90, 24000])  # whole units; pieces
+@pytest.mark.parametrize("d,bits", [(32, 2), (64, 4), (128, 3), (256, 4)])
+def test_a_nan_score_is_not_hidden_by_an_infinite_value(d, bits, n):
+    """Rows that see a NaN key are NaN in every column, those of an infinite value too."""
+    rng = np.random.default_rng(60 + d)
+    H, gq, T = 2, 2, 20
+    k, v = (rng.standard_normal((1, H, n, d)).astype(np.float16) for _ in range(2))
+    g, r = _cache(rng, n, H, d, bits, n, 32, 0, k, v)
+    bad = n - T + 12  # token 12 of the run, in the window
+    g.k_res[0, 0, 32 - T + 12, 3] = float("nan")
+    g.v_res[0, :, 2, 5] = float("inf")  # seen by all rows
+    q = rng.standard_normal((T, H * gq, d)).astype(np.float16)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    got = to_np(kvq.kvq_chunk_attention(g, torch.from_numpy(q).to(DEV), cu, T, flags=kvq.KVQ_OUT_F32))
+    assert np.isnan(got[12:, :gq]).all()
+    assert np.isposinf(got[:12, :, 5]).all() and np.isposinf(got[:, gq:, 5]).all()
+    want, bound = attend(tokens_of(r, "k", 0), tokens_of(r, "v", 0), q.astype(np.float64),
+                         [n - T + i + 1 for i in range(T)])
+    ok = np.abs(got - want) <= bound + n * 2.0 ** -32 * np.abs(v).max()
+    ok[..., 5] = True
+    assert bad >= n - 32 and ok[:12].all() and ok[:, gq:].all()
