@@ -67,7 +67,7 @@ __device__ __forceinline__ SeqLens lens_of(const ChunkAppendArgs& a, int b) {
 }
 
 // The last sequence whose first row is <= t, by a 32-way search of the warp
-// (t is warp-uniform; with entries out of order it still ends, at some sequence).
+// (t is warp-uniform; with entries out of order it ends at some sequence).
 __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = B;
@@ -80,6 +80,15 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int t) {
     hi = min(hi, lo + step);
   }
   return lo;
+}
+
+// The sequence that append_rows_kernel gives row t to, t of the warp's rows from t0 on.
+// With entries in order it is the one that has the row.
+__device__ __forceinline__ int seq_of_row(const ChunkAppendArgs& a, int64_t t0, int64_t t, bool live) {
+  int b = find_seq(a.cu, a.B, (int)t0);
+  if (live)
+    while (b + 1 < a.B && __ldg(a.cu + b + 1) <= t) ++b;
+  return b;
 }
 
 // R1 for the 8 values of a lane at element e < rd; partner: the 8 values rd / 2 away.
@@ -292,17 +301,46 @@ __global__ void __launch_bounds__(kRowThreads, 6) append_rows_kernel(ChunkAppend
   const Group g = group_of(a, grp);
   uint4 own[kHeads];
   load_rows(a, g, (int)(live ? t : t0), live, own);
-  int b = find_seq(a.cu, a.B, (int)t0);
-  if (live)
-    while (b + 1 < a.B && __ldg(a.cu + b + 1) <= t) ++b;
+  const int b = seq_of_row(a, t0, t, live);
   append_unit<BITS, HYB>(a, g, (int)(live ? t : t0), b, live, own);
 }
 
-// (on its way while the rows are worked on, and waits for them)
-__global__ void append_finish_kernel(ChunkAppendArgs a) {
+// Where entries are out of order (a broken one spoils the two sequences beside it), a row
+// that sequence b has may have been given to another: those rows of b, before its counters
+// move.  Each has its own place in the line, so when they come makes no difference.
+template <int BITS, bool HYB>
+__device__ __noinline__ void append_late_rows(const ChunkAppendArgs& a, int b) {
+  const Run run = run_of(a.cu, b, a.total, a.max_len);
+  if (run.n <= 0) return;
+  const int lane = threadIdx.x & 31, tpw = 256 / a.d;
+  for (int64_t t0 = run.c0 / tpw * tpw; t0 < (int64_t)run.c0 + run.n; t0 += tpw) {
+    const int64_t t = t0 + lane / (a.d >> 3);
+    const bool there = t >= run.c0 && t < (int64_t)run.c0 + run.n;
+    const bool late = seq_of_row(a, t0, t, there) != b && there;
+    if (!__any_sync(0xffffffffu, late)) continue;
+    for (int grp = threadIdx.x >> 5; grp < a.groups; grp += blockDim.x >> 5) {
+      const Group g = group_of(a, grp);
+      uint4 own[kHeads];
+      load_rows(a, g, (int)(late ? t : t0), late, own);
+      append_unit<BITS, HYB>(a, g, (int)(late ? t : t0), b, late, own);
+    }
+  }
+}
+
+// (on its way while the rows are worked on: reads the entries, then waits for the rows)
+template <int BITS, bool HYB>
+__global__ void __launch_bounds__(kRowThreads) append_finish_kernel(const __grid_constant__ ChunkAppendArgs a) {
+  const int b0 = blockIdx.x * kRowThreads;
+  bool falls = false;
+  for (int i = threadIdx.x; i < a.B; i += kRowThreads) falls |= __ldg(a.cu + i) > __ldg(a.cu + i + 1);
+  falls = __syncthreads_or(falls);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (falls) {
+    for (int b = b0; b < min(a.B, b0 + kRowThreads); ++b) append_late_rows<BITS, HYB>(a, b);
+    __syncthreads();
+  }
+  const int b = b0 + threadIdx.x;
   if (b < a.B) finish_seq(a, b);
 }
 
@@ -464,15 +502,15 @@ cudaError_t launch_append_bits(const ChunkAppendArgs& a, int threads, cudaStream
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.B + 127) / 128));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)((a.B + kRowThreads - 1) / kRowThreads));
+  cfg.blockDim = dim3(kRowThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_finish_kernel, a);
+  return cudaLaunchKernelEx(&cfg, append_finish_kernel<BITS, HYB>, a);
 }
 
 }  // namespace

@@ -381,7 +381,9 @@ kvq_status kvq_decode_attention_noalloc(const kvq_cache_desc* desc, const kvq_ca
  *               run are not written and have no part in any result.
  *   max_len     host upper bound of the run lengths, >= 0.
  * A sequence whose entries are not 0 <= cu[b] <= cu[b+1] <= total with at most
- * max_len tokens is skipped and sets KVQ_ERRBIT_BADLEN. */
+ * max_len tokens is skipped and sets KVQ_ERRBIT_BADLEN; the others are served.  A row
+ * that two of them have (entries out of order) counts for both; its output is either's
+ * (queries rotated in place: undefined). */
 
 /* Arguments of kvq_append_chunk; zero-initialise the struct. */
 typedef struct {
