@@ -474,6 +474,14 @@ def _run_tensor(t: torch.Tensor, heads: int, cache: KVCache, device: torch.devic
     return t.data_ptr()
 
 
+def _strides(t: torch.Tensor) -> tuple[int, int]:
+    """Strides of rows and heads; of a dimension with one entry (or none) any will do, and
+    torch keeps whatever it was made with."""
+    rows, heads, d = t.shape
+    head = t.stride(1) if heads > 1 else d
+    return (t.stride(0) if rows > 1 else heads * head), head
+
+
 # The current stream's handle without a Stream object: 2-3 us of a call's 10.
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -511,9 +519,9 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     a = AppendArgs(k=_run_tensor(k, D.num_kv_heads, cache, device, "k", False),
                    v=_run_tensor(v, D.num_kv_heads, cache, device, "v", False),
                    cu_seqlens=cu, total=total, max_len=int(max_len), interleaved=int(interleaved))
-    a.kv_stride_token, a.kv_stride_head, _ = k.stride()
-    if k.shape != v.shape or k.stride() != v.stride():
+    if k.shape != v.shape or _strides(k) != _strides(v):
         raise ValueError("k and v must have the same shape and strides")
+    a.kv_stride_token, a.kv_stride_head = _strides(k)
     if q is not None:
         if q.dim() != 3 or q.shape[0] != total:
             raise ValueError("q must be [total][Hq][d] with k's rows")
@@ -527,7 +535,7 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         if a.q_out == a.q and not q.is_contiguous():
             raise ValueError("q must be contiguous to be rotated in place")
         a.num_q_heads = heads
-        a.q_stride_token, a.q_stride_head, _ = q.stride()
+        a.q_stride_token, a.q_stride_head = _strides(q)
     if rope is not None:
         if (rope.dtype != torch.float32 or not rope.is_cuda or rope.device != device
                 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous()):

@@ -1,0 +1,46 @@
+"""Arguments of the calls on runs that the documentation allows: views whose dimensions of
+one entry carry odd strides, bounds on the run lengths past 32 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_kv_pack_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _odd(t, *dims):
+    """t with another stride in its dimensions of one entry."""
+    stride = list(t.stride())
+    for i in dims:
+        assert t.shape[i] == 1
+        stride[i] = 3 + i
+    return t.as_strided(t.shape, stride)
+
+
+@pytest.mark.parametrize("total,H", [(1, 2), (5, 1), (1, 1)])
+def test_strides_of_dimensions_with_one_entry_do_not_matter(total, H):
+    rng = np.random.default_rng(80)
+    d = 64
+    dims = [i for i, n in enumerate((total, H)) if n == 1]
+    k, v, q = (torch.from_numpy(rng.standard_normal((total, H, d)).astype(np.float16)).to(DEV) for _ in range(3))
+    cu = torch.tensor([0, total], dtype=torch.int32, device=DEV)
+    table = kvq.rope_table(10, d)
+    caches = [kvq.KVCache(1, H, d, 4, 64, 2) for _ in range(3)]
+    want = kvq.kvq_append_chunk(caches[0], k, v, cu, total, q=q, rope=table)
+    # all three odd; then the keys alone, the values being columns of a wider tensor
+    got = kvq.kvq_append_chunk(caches[1], _odd(k, *dims), _odd(v, *dims), cu, total, q=_odd(q, *dims), rope=table)
+    assert torch.equal(got, want)
+    wide = torch.cat([v, v], 1)[:, :H] if total == 1 else v
+    q2 = _odd(q, *dims).clone(memory_format=torch.preserve_format)
+    got = kvq.kvq_append_chunk(caches[2], _odd(k, *dims), wide, cu, total, q=q2, q_out=q2, rope=table)
+    assert torch.equal(got, want)
+    for c in caches[1:]:
+        for name in ("k_codes", "v_codes", "k_params", "v_params", "k_res", "v_res", "counters"):
+            assert torch.equal(getattr(c, name), getattr(caches[0], name)), name
+    a = kvq.kvq_chunk_attention(caches[0], want, cu, total)
+    b = kvq.kvq_chunk_attention(caches[0], _odd(want, *dims), cu, total)
+    assert torch.equal(a, b)
+    assert kvq.kvq_read_error(caches[0]) == (kvq.KVQ_OK, 0)
