@@ -616,6 +616,8 @@ def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
         torch.float32 if flags & KVQ_OUT_F32 else torch.float16)
     if dtype not in (torch.float16, torch.float32):
         raise ValueError("k_out and v_out must be float16 or float32")
+    if device.type != "cuda":
+        raise ValueError("the cache must be in CUDA memory")
     outs = [_made(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device), True) if t is None
             else t for t in (k_out, v_out)]
     for t in (k_out, v_out):
