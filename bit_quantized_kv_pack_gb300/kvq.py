@@ -474,6 +474,11 @@ def _run_tensor(t: torch.Tensor, heads: int, cache: KVCache, device: torch.devic
     return t.data_ptr()
 
 
+def _max_len(n: int) -> int:
+    """An upper bound as the library's 32 bits hold it (a call has fewer rows than that)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 def _strides(t: torch.Tensor) -> tuple[int, int]:
     """Strides of rows and heads; of a dimension with one entry (or none) any will do, and
     torch keeps whatever it was made with."""
@@ -518,7 +523,7 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     cu = _run_int(cu_seqlens, D.batch + 1, device, "cu_seqlens")
     a = AppendArgs(k=_run_tensor(k, D.num_kv_heads, cache, device, "k", False),
                    v=_run_tensor(v, D.num_kv_heads, cache, device, "v", False),
-                   cu_seqlens=cu, total=total, max_len=int(max_len), interleaved=int(interleaved))
+                   cu_seqlens=cu, total=total, max_len=_max_len(max_len), interleaved=int(interleaved))
     if k.shape != v.shape or _strides(k) != _strides(v):
         raise ValueError("k and v must have the same shape and strides")
     a.kv_stride_token, a.kv_stride_head = _strides(k)
@@ -577,7 +582,7 @@ def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspa
         raise ValueError("out must have q's shape, on the cache's device")
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the cache's device")
-    _run_call(name, cache, device, stream, qp, heads, cu, total, int(max_len), out.data_ptr(),
+    _run_call(name, cache, device, stream, qp, heads, cu, total, _max_len(max_len), out.data_ptr(),
               workspace.data_ptr(), workspace.numel() * workspace.element_size(), flags)
     return out
 

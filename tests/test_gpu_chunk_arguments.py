@@ -44,3 +44,23 @@ def test_strides_of_dimensions_with_one_entry_do_not_matter(total, H):
     b = kvq.kvq_chunk_attention(caches[0], _odd(want, *dims), cu, total)
     assert torch.equal(a, b)
     assert kvq.kvq_read_error(caches[0]) == (kvq.KVQ_OK, 0)
+
+
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 40])
+def test_any_upper_bound_of_the_run_lengths_serves(bound):
+    rng = np.random.default_rng(81)
+    H, d, T = 2, 64, 9
+    k, v, q = (torch.from_numpy(rng.standard_normal((T, H, d)).astype(np.float16)).to(DEV) for _ in range(3))
+    cu = torch.tensor([0, 5, 9], dtype=torch.int32, device=DEV)
+    caches = [kvq.KVCache(2, H, d, 4, 64, 2) for _ in range(2)]
+    outs = []
+    for c, n in zip(caches, (5, bound)):
+        kvq.kvq_append_chunk(c, k, v, cu, n)
+        outs.append([kvq.kvq_chunk_attention(c, q, cu, n), kvq.kvq_cross_attention(c, q, cu, n)])
+        assert kvq.kvq_read_error(c) == (kvq.KVQ_OK, 0)
+        for bad in (-1, -2 ** 32, -2 ** 40):
+            for f in (lambda: kvq.kvq_append_chunk(c, k, v, cu, bad), lambda: kvq.kvq_cross_attention(c, q, cu, bad)):
+                with pytest.raises(kvq.KvqError, match="invalid argument"):
+                    f()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(caches[0].counters, caches[1].counters) and torch.equal(caches[0].k_codes, caches[1].k_codes)
