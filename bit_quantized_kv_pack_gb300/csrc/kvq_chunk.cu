@@ -168,12 +168,13 @@ __device__ __forceinline__ void append_unit(const ChunkAppendArgs& a, const Grou
   const int half = a.rd >> 1;
   const bool second = !a.interleaved && e >= half;
   if (rot) {
-    int pos = a.positions ? __ldg(a.positions + t) : s.ns + s.npk + s.nres + i;
+    // (what the sequence holds may pass 2^31 with its sink and window)
+    int64_t pos = a.positions ? __ldg(a.positions + t) : (int64_t)s.npk + (s.ns + s.nres) + i;
     if (pos < 0 || pos >= a.rope_rows) {
       set_error(a.err_word, KVQ_ERRBIT_BADPOS);
-      pos = min(max(pos, 0), a.rope_rows - 1);
+      pos = pos < 0 ? 0 : a.rope_rows - 1;
     }
-    const float2* src = a.rope + (int64_t)pos * half + (a.interleaved ? e / 2 : second ? e - half : e);
+    const float2* src = a.rope + pos * half + (a.interleaved ? e / 2 : second ? e - half : e);
     const float4* src4 = reinterpret_cast<const float4*>(src);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -64,3 +64,23 @@ def test_any_upper_bound_of_the_run_lengths_serves(bound):
                     f()
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     assert torch.equal(caches[0].counters, caches[1].counters) and torch.equal(caches[0].k_codes, caches[1].k_codes)
+
+
+@pytest.mark.parametrize("T", [1, 13, 40])  # a block per sequence (up to 12 warps of work); rows in one line
+def test_positions_past_31_bits_take_the_last_row_of_the_table(T):
+    """A paged cache of 2^31 - 32 packed tokens (its pages are the same two) and a sink."""
+    rng = np.random.default_rng(82)
+    d, cap, rows = 32, 2 ** 31 - 32, 50
+    c = kvq.KVCache(1, 1, d, 2, cap, 64, sink=64, page_size=32, num_pages=2)
+    c.counters.copy_(torch.tensor([[cap], [0], [0], [64]], dtype=torch.int32))
+    k, q = (torch.from_numpy(rng.standard_normal((T, 1, d)).astype(np.float16)).to(DEV) for _ in range(2))
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    table = kvq.rope_table(rows, d)
+    got = kvq.kvq_append_chunk(c, k, k, cu, T, q=q, rope=table)
+    assert kvq.kvq_read_error(c)[1] == kvq.KVQ_ERRBIT_BADPOS
+    from _runs import rotate
+    last = np.full(T, rows - 1)
+    assert np.array_equal(got.cpu().numpy(), rotate(q.cpu().numpy(), table.cpu().numpy(), last, d, False))
+    assert np.array_equal(c.k_res[0, :, :T].transpose(0, 1).cpu().numpy(),
+                          rotate(k.cpu().numpy(), table.cpu().numpy(), last, d, False))
+    assert c.counters[:, 0].tolist() == [cap, T, 0, 64]
