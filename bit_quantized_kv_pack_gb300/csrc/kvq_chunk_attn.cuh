@@ -1301,10 +1301,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw;
   const uint32_t smem = ptx::smem_u32(base);
-  if (smem & 1023u) {  // the swizzles count on it (a block without static shared memory has it)
-    set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
-    return;
-  }
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(base + C::OFF_BAR);
   volatile int64_t* wide = reinterpret_cast<volatile int64_t*>(base + C::OFF_BAR);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lid = tid & 31;
@@ -1312,6 +1308,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) a.heads[blockIdx.x * 4].x = -1;  // (a later head is this thread's store too)
+  if (smem & 1023u) {  // the swizzles count on it (a block without static shared memory has it)
+    if (tid == 0) set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
+    return;
+  }
 
   // The line of tiles: each thread sums up some sequences, then the block scans.
   const int per = (a.B + kThreads - 1) / kThreads;
