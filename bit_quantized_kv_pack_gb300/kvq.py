@@ -173,23 +173,38 @@ def _stream(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
-def _made(stream, device, make, returned: bool = False) -> torch.Tensor:
-    """make(), a tensor of the call's own, on the call's stream.  The allocator hands memory
-    on in the order of the stream that it was taken on, so what a call drops when it returns
-    (a workspace) must come from the stream that its kernels run on, and so must what they
-    write.  What is returned is the caller's on the current stream, and recorded there."""
-    if stream is None:
-        return make()
+def _other_stream(stream, device):
+    """The stream given to a call as torch's, or None where it is the current one."""
     current = torch.cuda.current_stream(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
-    if stream.cuda_stream == current.cuda_stream:
+    return None if stream.cuda_stream == current.cuda_stream else stream
+
+
+# A call's own tensors come from the stream that it runs on.  The allocator hands memory
+# on in the order of that stream, so what a call drops when it returns (a workspace) is
+# not another's before its kernels are done, and what they write was not in use before.
+
+
+def _scratch(make, device, stream):
+    """make(), a workspace that the call drops, on the call's stream."""
+    other = None if stream is None else _other_stream(stream, device)
+    if other is None:
         return make()
-    with torch.cuda.stream(stream):
-        t = make()
-    if returned:
-        t.record_stream(current)
+    with torch.cuda.stream(other):
+        return make()
+
+
+def _empty(shape, dtype, device, stream):
+    """An output, from the call's stream; it is the caller's on the current one, and
+    recorded there."""
+    other = None if stream is None else _other_stream(stream, device)
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -207,7 +222,7 @@ def _out(q: torch.Tensor, out: torch.Tensor | None, flags: int, stream=None):
     (KVQ_OUT_F32).  Without `out`, the dtype follows KVQ_OUT_F32 in flags."""
     if out is None:
         dtype = torch.float32 if flags & KVQ_OUT_F32 else torch.float16
-        out = _made(stream, q.device, lambda: torch.empty(q.shape, dtype=dtype, device=q.device), True)
+        out = _empty(q.shape, dtype, q.device, stream)
     if out.dtype not in (torch.float16, torch.float32) or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous float16 or float32 CUDA tensor")
     if out.dtype == torch.float32:
@@ -357,7 +372,7 @@ def kvq_decode_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor | No
     _f16(q, "q")
     out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = _made(stream, cache.device, lambda: workspace_for(cache, q.shape[1]))
+        workspace = _scratch(lambda: workspace_for(cache, q.shape[1]), cache.device, stream)
     st = load().kvq_decode_attention(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
                                      int(q.shape[1]), _ptr(out), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), int(flags),
@@ -381,7 +396,7 @@ def kvq_decode_step(cache: KVCache, q: torch.Tensor, k_new: torch.Tensor, v_new:
     _f16(q, "q"), _f16(k_new, "k_new"), _f16(v_new, "v_new")
     out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = _made(stream, cache.device, lambda: workspace_for(cache, q.shape[1]))
+        workspace = _scratch(lambda: workspace_for(cache, q.shape[1]), cache.device, stream)
     st = load().kvq_decode_step(ctypes.byref(cache.desc), ctypes.byref(cache.view), _ptr(q),
                                 int(q.shape[1]), _ptr(k_new), _ptr(v_new), _ptr(out),
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -479,12 +494,11 @@ def _max_len(n: int) -> int:
     return max(-1, min(int(n), 2 ** 31 - 1))
 
 
-def _strides(t: torch.Tensor) -> tuple[int, int]:
-    """Strides of rows and heads; of a dimension with one entry (or none) any will do, and
-    torch keeps whatever it was made with."""
-    rows, heads, d = t.shape
-    head = t.stride(1) if heads > 1 else d
-    return (t.stride(0) if rows > 1 else heads * head), head
+def _strides(t: torch.Tensor, rows: int, heads: int) -> tuple[int, int]:
+    """Strides of rows and heads; of a dimension with one entry (or none) any will do (0),
+    and torch keeps whatever it was made with."""
+    row, head, _ = t.stride()
+    return row if rows > 1 else 0, head if heads > 1 else 0
 
 
 # The current stream's handle without a Stream object: 2-3 us of a call's 10.
@@ -524,23 +538,24 @@ def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     a = AppendArgs(k=_run_tensor(k, D.num_kv_heads, cache, device, "k", False),
                    v=_run_tensor(v, D.num_kv_heads, cache, device, "v", False),
                    cu_seqlens=cu, total=total, max_len=_max_len(max_len), interleaved=int(interleaved))
-    if k.shape != v.shape or _strides(k) != _strides(v):
+    strides = _strides(k, total, D.num_kv_heads)
+    if k.shape != v.shape or strides != _strides(v, total, D.num_kv_heads):
         raise ValueError("k and v must have the same shape and strides")
-    a.kv_stride_token, a.kv_stride_head = _strides(k)
+    a.kv_stride_token, a.kv_stride_head = strides
     if q is not None:
         if q.dim() != 3 or q.shape[0] != total:
             raise ValueError("q must be [total][Hq][d] with k's rows")
         heads = q.shape[1]
         a.q = _run_tensor(q, heads, cache, device, "q", False)
         if q_out is None:
-            q_out = _made(stream, device, lambda: torch.empty(q.shape, dtype=torch.float16, device=device), True)
+            q_out = _empty(q.shape, torch.float16, device, stream)
         a.q_out = _run_tensor(q_out, heads, cache, device, "q_out", True)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         if a.q_out == a.q and not q.is_contiguous():
             raise ValueError("q must be contiguous to be rotated in place")
         a.num_q_heads = heads
-        a.q_stride_token, a.q_stride_head = _strides(q)
+        a.q_stride_token, a.q_stride_head = _strides(q, total, heads)
     if rope is not None:
         if (rope.dtype != torch.float32 or not rope.is_cuda or rope.device != device
                 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous()):
@@ -577,7 +592,7 @@ def _attend_runs(name: str, cache: KVCache, q, cu_seqlens, max_len, out, workspa
     qp = _run_tensor(q, heads, cache, device, "q", True)
     out, flags = _out(q, out, flags, stream)
     if workspace is None:
-        workspace = _made(stream, device, lambda: chunk_workspace_for(cache, heads))
+        workspace = _scratch(lambda: chunk_workspace_for(cache, heads), device, stream)
     if out.shape != q.shape or out.device != device:
         raise ValueError("out must have q's shape, on the cache's device")
     if workspace.device != device or not workspace.is_contiguous():
@@ -623,8 +638,7 @@ def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
         raise ValueError("k_out and v_out must be float16 or float32")
     if device.type != "cuda":
         raise ValueError("the cache must be in CUDA memory")
-    outs = [_made(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device), True) if t is None
-            else t for t in (k_out, v_out)]
+    outs = [_empty(shape, dtype, device, stream) if t is None else t for t in (k_out, v_out)]
     for t in (k_out, v_out):
         if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_cuda or t.device != device
                               or not t.is_contiguous()):
