@@ -15,9 +15,11 @@
 // rows are loaded together before anything about the sequence is known; the warps
 // of a block share their tokens, so that cosines and sines come from L1 after the
 // first.  The rotation's partner values (rotary_dim / 2 away) are in a lane of the
-// same row and come by shuffles.  Long runs are bound by instructions (69 % of the issue
-// slots: the quantizer's and the rotation's separate roundings): four prompts of 501 to
-// 4096 tokens, 32 / 8 heads, INT2, take 55 us for 211 MB read and written.
+// same row and come by shuffles.  Long runs are bound by instructions (70 % of the issue
+// slots at a third of the warps): four prompts of 501 to 4096 tokens, 32 / 8 heads, INT2,
+// take 55 us for 211 MB read and written.  The four lanes of a group each work out its
+// scale; the prefill's pack, with a lane to a group, does not and reaches 0.7 of the
+// copy rate.
 #include "kvq_ptx.cuh"
 #include "kvq_runs.cuh"
 

@@ -32,8 +32,10 @@
 // registers a thread at launch in place of 80).
 //
 // What bounds it now: the chain S -> softmax -> P -> PV -> next S of each accumulator, with
-// the other's MMAs under it, and the shared memory that the MMAs read Q and K from; 2048 x
-// 32768 tokens of INT2 (32 heads on 8, head_dim 128) take 805 us, 69 % of the bf16 rate
+// the other's MMAs under it, and shared memory: for a shared tile (128 tokens, 256 rows,
+// head_dim 128) the MMAs read 192 KB and the dequantizing warps write 64 KB, by count
+// about the 2048 cycles that the MMAs themselves take.  2048 x 32768 tokens of INT2 (32
+// heads on 8, head_dim 128) take 805 to 855 us by the box, 65 to 69 % of the bf16 rate
 // that a library product reaches.  Calls of few rows are bound by the warps that
 // dequantize, and the smallest by the way to the first tile (7 us) and the join (5 us).
 //
@@ -103,8 +105,9 @@ constexpr int kDeqThreads = 128;
 // What the line of tiles is cut by, in half microseconds (head_dim 128): a tile of 128
 // tokens that the lanes share, one lane's own, a unit's begin and end.  Fitted to blocks'
 // times a shared tile takes 2.0 us, an own one 1.1 to 1.4, a unit 3 with few rows and 9
-// with many; dearer units (20, with 8 for a tile of fp16 tokens) made the 40-head case 6 %
-// faster and a batch of drafts 9 % slower.
+// with many.  The unit's 5 us is between the two: dearer units (20, with 8 for a tile of
+// fp16 tokens) made the 40-head case 6 % faster and a batch of drafts 9 % slower.  A cost
+// for each kind of unit, and fits at other head_dims (where these serve too), are untried.
 constexpr int kCostShared = 4, kCostOwn = 3, kCostUnit = 10;
 
 template <int D, int BITS>
