@@ -177,7 +177,8 @@ def _other_stream(stream, device):
     """The stream given to a call as torch's, or None where it is the current one."""
     current = torch.cuda.current_stream(device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+        handle = stream.value or 0 if isinstance(stream, ctypes.c_void_p) else int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
                   else torch.cuda.default_stream(device))
     return None if stream.cuda_stream == current.cuda_stream else stream
 

@@ -2,7 +2,8 @@
 stream that it runs on: memory of the current stream could be handed on while the kernels
 still use it on the other one, or still be in use by work of the current stream."""
 
-import numpy as np
+import ctypes
+
 import pytest
 import torch
 
@@ -154,3 +155,17 @@ def test_a_returned_output_outlives_its_use_on_the_current_stream():
             torch.full_like(want, float("nan"))
     torch.cuda.synchronize()
     assert all(torch.equal(c, want) for c in copies)
+
+
+@pytest.mark.parametrize("name", ["chunk", "cross", "read"])
+def test_a_stream_may_be_given_as_a_pointer(name, monkeypatch):
+    g, calls = _calls()
+    want = [t.clone() for t in calls[name](None)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle, stream in ((side.cuda_stream, side.cuda_stream), (None, 0)):
+        got, made = _taken(calls[name], ctypes.c_void_p(handle), monkeypatch)
+        assert all(_stream_of(t) == stream for t in got + made)
+        torch.cuda.synchronize()
+        assert _same(name, got, want)
+    assert kvq.kvq_read_error(g) == (kvq.KVQ_OK, 0)
