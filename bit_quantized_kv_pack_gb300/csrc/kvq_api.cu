@@ -2,6 +2,7 @@
 // Every entry point validates on the host and launches nothing on an error.
 #include <string.h>
 
+#include "kvq_around.cuh"
 #include "kvq_runs.cuh"
 
 namespace {
@@ -326,6 +327,108 @@ kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* vie
                                            static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// One tensor of kvq_rotate: its heads, strides and places.
+kvq_status check_rows(const void* x, const void* y, int32_t heads, int64_t st, int64_t sh, int64_t yt,
+                      int64_t yh) {
+  if (!y || heads < 1 || st < 0 || sh < 0 || yt < 0 || yh < 0) return KVQ_ERR_INVALID_ARG;
+  if (x == y && (st != yt || sh != yh)) return KVQ_ERR_INVALID_ARG;  // in place: the same rows
+  // every 8-value piece a lane moves must start on a 16-byte boundary
+  if (!aligned(x, 16) || !aligned(y, 16) || st % 8 || sh % 8 || yt % 8 || yh % 8) return KVQ_ERR_MISALIGNED;
+  return heads > 65535 ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+}
+bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128 || d == 256; }
+}  // namespace
+
+kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
+  if (!args) return KVQ_ERR_INVALID_ARG;
+  const kvq_rotate_args& A = *args;
+  if (A.total < 0 || A.head_dim < 32 || A.head_dim % 32 || (!A.q && !A.k && A.total > 0)) return KVQ_ERR_INVALID_ARG;
+  if (!head_dim_ok(A.head_dim)) return KVQ_ERR_UNSUPPORTED;
+  if (A.rotary_dim < 1 || A.rotary_dim > A.head_dim || (A.interleaved != 0 && A.interleaved != 1))
+    return KVQ_ERR_INVALID_ARG;
+  if (A.rotary_dim % 16 || A.axes > 4) return KVQ_ERR_UNSUPPORTED;
+  if (A.axes < 1 || !A.rope || A.rope_rows < 1 || (A.total > 0 && !A.positions)) return KVQ_ERR_INVALID_ARG;
+  if (A.pair_axis)
+    for (int i = 0; i < A.rotary_dim / 2; ++i)
+      if (A.pair_axis[i] >= A.axes) return KVQ_ERR_INVALID_ARG;
+  kvq_status st;
+  if (A.q && (st = check_rows(A.q, A.q_out, A.num_q_heads, A.q_stride_token, A.q_stride_head,
+                              A.q_out_stride_token, A.q_out_stride_head)) != KVQ_OK)
+    return st;
+  if (A.k && (st = check_rows(A.k, A.k_out, A.num_kv_heads, A.k_stride_token, A.k_stride_head,
+                              A.k_out_stride_token, A.k_out_stride_head)) != KVQ_OK)
+    return st;
+  if (!aligned(A.rope, 16) || !aligned(A.positions, 4) || !aligned(A.err_word, 4)) return KVQ_ERR_MISALIGNED;
+  return from_cuda(kvq::launch_rotate(A, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+kvq_status check_beams(int32_t batch, int32_t beams, int32_t vocab, int32_t n) {
+  if (batch < 1 || beams < 1 || vocab < 1 || n < 1 || (int64_t)beams * vocab < n) return KVQ_ERR_INVALID_ARG;
+  // a selection is a lane each, a proposal's place has 32 bits
+  if (beams > 32 || n > 32 || (int64_t)batch * beams > 65535 || (int64_t)beams * vocab > 2147483646LL)
+    return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+}  // namespace
+
+size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t n) {
+  return check_beams(batch, beams, vocab, n) == KVQ_OK ? kvq::beam_workspace_bytes(batch, beams, vocab, n) : 0;
+}
+
+kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream) {
+  if (!args) return KVQ_ERR_INVALID_ARG;
+  const kvq_beam_args& A = *args;
+  const kvq_status st = check_beams(A.batch, A.beams, A.vocab, A.n);
+  if (st != KVQ_OK) return st;
+  if (!A.logits || !A.scores || !A.parent || !A.token || !A.score || !A.workspace ||
+      (A.flags & ~(uint32_t)KVQ_LOGITS_F32) || A.stride_row < A.vocab)
+    return KVQ_ERR_INVALID_ARG;
+  if (A.finished && (A.end_token < 0 || A.end_token >= A.vocab)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(A.logits, 16) || !aligned(A.workspace, 16) || !aligned(A.scores, 4) || !aligned(A.parent, 4) ||
+      !aligned(A.token, 4) || !aligned(A.score, 4) || !aligned(A.err_word, 4))
+    return KVQ_ERR_MISALIGNED;
+  if (A.ws_bytes < kvq::beam_workspace_bytes(A.batch, A.beams, A.vocab, A.n)) return KVQ_ERR_INVALID_ARG;
+  return from_cuda(kvq::launch_beam_select(A, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_reorder(const kvq_cache_desc* dst_desc, const kvq_cache_view* dst,
+                       const kvq_cache_desc* src_desc, const kvq_cache_view* src, const int32_t* index,
+                       uint32_t flags, void* stream) {
+  kvq_status st;
+  if ((st = check_desc(dst_desc)) != KVQ_OK || (st = check_desc(src_desc)) != KVQ_OK) return st;
+  if ((st = check_view(*dst_desc, dst)) != KVQ_OK || (st = check_view(*src_desc, src)) != KVQ_OK) return st;
+  const kvq_cache_desc &d = *dst_desc, &s = *src_desc;
+  if (!index || (flags & ~(uint32_t)KVQ_REORDER_SHARE_PAGES) || d.num_kv_heads != s.num_kv_heads ||
+      d.head_dim != s.head_dim || d.bits != s.bits || d.residual != s.residual || d.sink != s.sink ||
+      d.hybrid != s.hybrid || d.page_size != s.page_size)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned(index, 4)) return KVQ_ERR_MISALIGNED;
+  auto same = [](const void* a, const void* b) { return a && a == b; };
+  const bool share = flags & KVQ_REORDER_SHARE_PAGES, both = d.capacity > 0 && s.capacity > 0;
+  // one sequence's bytes would be another's before they are read
+  if (same(dst->packed_len, src->packed_len) || same(dst->res_len, src->res_len) ||
+      same(dst->res_head, src->res_head) ||
+      (d.sink && (same(dst->sink_len, src->sink_len) || same(dst->k_sink, src->k_sink) ||
+                  same(dst->v_sink, src->v_sink))) ||
+      (d.residual && (same(dst->k_res, src->k_res) || same(dst->v_res, src->v_res))) ||
+      (d.page_size && both && same(dst->block_table, src->block_table)))
+    return KVQ_ERR_INVALID_ARG;
+  if (!d.page_size && both &&
+      (same(dst->k_codes, src->k_codes) || same(dst->v_codes, src->v_codes) ||
+       same(dst->k_params, src->k_params) || same(dst->v_params, src->v_params) ||
+       (d.hybrid && (same(dst->k_mode, src->k_mode) || same(dst->v_mode, src->v_mode)))))
+    return KVQ_ERR_INVALID_ARG;
+  if (share && (!d.page_size || d.num_pages != s.num_pages || dst->k_codes != src->k_codes ||
+                dst->v_codes != src->v_codes || dst->k_params != src->k_params ||
+                dst->v_params != src->v_params ||
+                (d.hybrid && (dst->k_mode != src->k_mode || dst->v_mode != src->v_mode))))
+    return KVQ_ERR_INVALID_ARG;  // there is no one pool
+  return from_cuda(kvq::launch_reorder(kvq::dims_of(d), *dst, kvq::dims_of(s), *src, index, share,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
 kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* stream) {
   if (!view || !view->err_word) return KVQ_ERR_INVALID_ARG;
   if (!aligned(view->err_word, 4)) return KVQ_ERR_MISALIGNED;
@@ -340,7 +443,9 @@ kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* 
   if (w & KVQ_ERRBIT_CAPACITY) return KVQ_ERR_CAPACITY;
   if (w & KVQ_ERRBIT_EMPTY) return KVQ_ERR_EMPTY;
   if (w & KVQ_ERRBIT_TIMEOUT) return KVQ_ERR_TIMEOUT;
-  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE | KVQ_ERRBIT_BADPOS)) return KVQ_ERR_INVALID_ARG;
+  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE | KVQ_ERRBIT_BADPOS | KVQ_ERRBIT_BADINDEX |
+           KVQ_ERRBIT_BADSCORE))
+    return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
 

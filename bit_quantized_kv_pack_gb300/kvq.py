@@ -34,6 +34,8 @@ KVQ_ERRBIT_TIMEOUT = 0x4
 KVQ_ERRBIT_BADLEN = 0x8
 KVQ_ERRBIT_BADPAGE = 0x10
 KVQ_ERRBIT_BADPOS = 0x20
+KVQ_ERRBIT_BADINDEX = 0x40
+KVQ_ERRBIT_BADSCORE = 0x80
 
 KVQ_ARRAY_CODES = 0
 KVQ_ARRAY_PARAMS = 1
@@ -46,7 +48,8 @@ EXPORTS = ("kvq_cache_bytes", "kvq_decode_workspace_bytes", "kvq_quantize_pack",
            "kvq_quantize_pack_strided", "kvq_append",
            "kvq_decode_attention", "kvq_decode_step", "kvq_decode_step_host", "kvq_step_io_bytes",
            "kvq_decode_attention_noalloc", "kvq_append_chunk", "kvq_chunk_workspace_bytes",
-           "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens",
+           "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens", "kvq_rotate",
+           "kvq_beam_workspace_bytes", "kvq_beam_select", "kvq_reorder",
            "kvq_read_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
            "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding")
 
@@ -75,6 +78,26 @@ class AppendArgs(ctypes.Structure):
                 ("total", ctypes.c_int32), ("max_len", ctypes.c_int32), ("rope", ctypes.c_void_p),
                 ("rope_rows", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
+
+
+class RotateArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out")]
+                + [(n, ctypes.c_int64) for n in (
+                    "q_stride_token", "q_stride_head", "k_stride_token", "k_stride_head",
+                    "q_out_stride_token", "q_out_stride_head", "k_out_stride_token", "k_out_stride_head")]
+                + [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "total")]
+                + [("rope", ctypes.c_void_p)]
+                + [(n, ctypes.c_int32) for n in ("rope_rows", "rotary_dim", "interleaved", "axes")]
+                + [(n, ctypes.c_void_p) for n in ("positions", "pair_axis", "err_word")])
+
+
+class BeamArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("stride_row", ctypes.c_int64), ("scores", ctypes.c_void_p),
+                ("finished", ctypes.c_void_p), ("batch", ctypes.c_int32), ("beams", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("n", ctypes.c_int32), ("end_token", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("parent", ctypes.c_void_p), ("token", ctypes.c_void_p),
+                ("score", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+                ("err_word", ctypes.c_void_p)]
 
 
 class KvqError(RuntimeError):
@@ -132,6 +155,14 @@ def load(path: str | None = None):
                 fn.restype = ctypes.c_int
             lib.kvq_read_tokens.argtypes = [DP, VP, P, i32, P, P, ctypes.c_uint32, P]
             lib.kvq_read_tokens.restype = ctypes.c_int
+            lib.kvq_rotate.argtypes = [ctypes.POINTER(RotateArgs), P]
+            lib.kvq_rotate.restype = ctypes.c_int
+            lib.kvq_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            lib.kvq_beam_workspace_bytes.restype = sz
+            lib.kvq_beam_select.argtypes = [ctypes.POINTER(BeamArgs), P]
+            lib.kvq_beam_select.restype = ctypes.c_int
+            lib.kvq_reorder.argtypes = [DP, VP, DP, VP, P, ctypes.c_uint32, P]
+            lib.kvq_reorder.restype = ctypes.c_int
             lib.kvq_read_error.argtypes = [VP, ctypes.POINTER(ctypes.c_uint32), P]
             lib.kvq_read_error.restype = ctypes.c_int
             lib.kvq_status_string.argtypes = [ctypes.c_int]
@@ -282,6 +313,25 @@ class KVCache:
                          _ptr(self.counters[1]), _ptr(self.counters[2]), _ptr(self.err),
                          r(self.k_sink), r(self.v_sink), _ptr(self.counters[3]),
                          r(self.k_mode), r(self.v_mode), r(self.block_table))
+
+    def twin(self, batch=None, capacity=None, num_pages=None, share_pages=False) -> "KVCache":
+        """A cache of the same kind (for kvq_reorder), of this batch and capacity unless
+        others are given.  share_pages: its packed rows are in this cache's pool; its block
+        table is for the caller to fill, with pages that no other sequence has."""
+        D = self.desc
+        if share_pages and (not D.page_size or num_pages not in (None, D.num_pages)):
+            raise ValueError("only paged caches share a pool, whole")
+        pages = D.num_pages if num_pages is None else num_pages
+        t = KVCache(D.batch if batch is None else batch, D.num_kv_heads, D.head_dim, D.bits,
+                    D.capacity if capacity is None else capacity, D.residual, self.device, D.sink, D.hybrid,
+                    D.page_size, 0 if share_pages else pages)
+        if share_pages:
+            for name in ("k_codes", "v_codes", "k_params", "v_params", "k_mode", "v_mode"):
+                setattr(t, name, getattr(self, name))
+            t.desc.num_pages = pages
+            t.block_table.fill_(-1)
+            t.view = t._make_view()
+        return t
 
     @property
     def packed_len(self):
@@ -507,19 +557,24 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run_call(fn: str, cache: KVCache, device: torch.device, stream, *args) -> None:
-    """One library call on the cache's device, whichever is current."""
+def _call_on(fn: str, device: torch.device, stream, *args) -> None:
+    """One library call on a device, whichever is current."""
     f = getattr(_lib or load(), fn)
     if stream is None:
         stream = _current_raw(device.index)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        st = f(ctypes.byref(cache.desc), ctypes.byref(cache.view), *args, stream)
+        st = f(*args, stream)
     else:
         with torch.cuda.device(device):
-            st = f(ctypes.byref(cache.desc), ctypes.byref(cache.view), *args, stream)
+            st = f(*args, stream)
     _check(st, fn)
+
+
+def _run_call(fn: str, cache: KVCache, device: torch.device, stream, *args) -> None:
+    """One library call on the cache's device."""
+    _call_on(fn, device, stream, ctypes.byref(cache.desc), ctypes.byref(cache.view), *args)
 
 
 def kvq_append_chunk(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -649,6 +704,165 @@ def kvq_read_tokens(cache: KVCache, first: torch.Tensor | None, count: int,
     _run_call("kvq_read_tokens", cache, device, stream, first_ptr, int(count), outs[0].data_ptr(),
               outs[1].data_ptr(), flags)
     return outs[0], outs[1]
+
+
+# ------------------------------------------------------- around the cache ----
+
+
+def axes_of_pairs(sections, interleaved: bool = False) -> bytes:
+    """The axis of each pair of a head, for kvq_rotate: sections[a] pairs for axis a, one
+    axis after the other, or in turn (0, 1, 2, 0, 1, ...) while each has some left."""
+    if not interleaved:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    left, out = list(sections), []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return bytes(out)
+
+
+def _rows_tensor(t: torch.Tensor, device: torch.device, name: str) -> int:
+    if (t.dtype != torch.float16 or not t.is_cuda or t.device != device or t.dim() != 3
+            or (t.stride(2) != 1 and t.shape[2] > 1)):
+        raise ValueError(f"{name} must be a float16 CUDA tensor [total][heads][d] with d contiguous, all on one device")
+    return t.data_ptr()
+
+
+def _err_ptr(err: torch.Tensor | None, device: torch.device) -> int | None:
+    if err is None:
+        return None
+    if err.dtype != torch.int32 or not err.is_cuda or err.device != device or err.numel() < 1:
+        raise ValueError("err must be an int32 CUDA tensor (a cache's err) on the same device")
+    return err.data_ptr()
+
+
+def kvq_rotate(q: torch.Tensor | None, k: torch.Tensor | None, rope: torch.Tensor, positions: torch.Tensor,
+               pair_axis=None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+               k_out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+               stream=None) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """Rotate queries and keys (fp16 [total][heads][d] views with d contiguous; either may
+    be None) to ``positions``, int32 [axes][total] or [total], at ``rope`` (fp32
+    [rows][rotary_dim / 2][2], see rope_table).  ``pair_axis``: the axis of each pair
+    (axes_of_pairs; None: axis 0 for all).  The outputs are new tensors, or q_out and
+    k_out, which may be q and k themselves.  ``err``: a cache's err, for positions outside
+    the table."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k must be [total][heads][d]")
+    device = x.device
+    total, _, d = x.shape
+    if (rope.dtype != torch.float32 or not rope.is_cuda or rope.device != device or rope.dim() != 3
+            or rope.shape[2] != 2 or not rope.is_contiguous()):
+        raise ValueError("rope must be a contiguous float32 CUDA tensor [rows][rotary_dim / 2][2] on q's device")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if (positions.dtype != torch.int32 or not positions.is_cuda or positions.device != device
+            or positions.dim() not in (1, 2) or positions.shape[-1] != total or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 CUDA tensor [axes][total] on q's device")
+    a = RotateArgs(head_dim=d, total=total, rope=rope.data_ptr(), rope_rows=rope.shape[0],
+                   rotary_dim=2 * rope.shape[1], interleaved=int(interleaved), axes=axes,
+                   positions=positions.data_ptr(), err_word=_err_ptr(err, device))
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != rope.shape[1]:
+            raise ValueError("pair_axis must have an axis for each pair of rope")
+        a.pair_axis = ctypes.cast(ctypes.c_char_p(pair_axis), ctypes.c_void_p)
+    for t in (q, k):
+        if t is not None and (t.dim() != 3 or t.shape[0] != total or t.shape[2] != d):
+            raise ValueError("q and k must be [total][heads][d] of the same rows and d")
+    if q is not None:
+        a.q, a.num_q_heads = _rows_tensor(q, device, "q"), q.shape[1]
+        if q_out is None:
+            q_out = _empty(q.shape, torch.float16, device, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        a.q_out = _rows_tensor(q_out, device, "q_out")
+        a.q_stride_token, a.q_stride_head = _strides(q, total, q.shape[1])
+        a.q_out_stride_token, a.q_out_stride_head = _strides(q_out, total, q.shape[1])
+    if k is not None:
+        a.k, a.num_kv_heads = _rows_tensor(k, device, "k"), k.shape[1]
+        if k_out is None:
+            k_out = _empty(k.shape, torch.float16, device, stream)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        a.k_out = _rows_tensor(k_out, device, "k_out")
+        a.k_stride_token, a.k_stride_head = _strides(k, total, k.shape[1])
+        a.k_out_stride_token, a.k_out_stride_head = _strides(k_out, total, k.shape[1])
+    _call_on("kvq_rotate", device, stream, ctypes.byref(a))
+    return q_out, k_out
+
+
+def kvq_beam_workspace_bytes(batch: int, beams: int, vocab: int, n: int) -> int:
+    return int(load().kvq_beam_workspace_bytes(batch, beams, vocab, n))
+
+
+def beam_workspace_for(batch: int, beams: int, vocab: int, n: int, device="cuda") -> torch.Tensor:
+    """A workspace for kvq_beam_select (one call at a time)."""
+    b = kvq_beam_workspace_bytes(batch, beams, vocab, n)
+    if b == 0:
+        raise KvqError(KVQ_ERR_INVALID_ARG, "kvq_beam_workspace_bytes")
+    return torch.empty(b, dtype=torch.uint8, device=device)
+
+
+KVQ_LOGITS_F32 = 1
+
+
+def kvq_beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, finished: torch.Tensor | None = None,
+                    end_token: int = 0, out=None, workspace: torch.Tensor | None = None,
+                    err: torch.Tensor | None = None, stream=None):
+    """Beam search's selection: logits [B][W][V] (fp16 or fp32, V contiguous, equal strides
+    from row to row), scores fp32 [B][W]; the n best of scores + log_softmax(logits) over
+    beams and tokens for each batch entry, best first, equal ones in order.  ``finished``
+    (uint8 or bool [B][W]): complete beams, which go on with ``end_token`` at their score.
+    Returns (parent, token, score), each [B][n] (``out``: such a triple): parent is the row
+    b W + w, an index for kvq_reorder."""
+    if (logits.dim() != 3 or logits.dtype not in (torch.float16, torch.float32) or not logits.is_cuda
+            or (logits.stride(2) != 1 and logits.shape[2] > 1)):
+        raise ValueError("logits must be a float16 or float32 CUDA tensor [B][W][V] with V contiguous")
+    device = logits.device
+    B, W, V = logits.shape
+    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    if B > 1 and W > 1 and logits.stride(0) != W * row:
+        raise ValueError("logits' rows must have one stride")
+    for t, types, name in ((scores, (torch.float32,), "scores"), (finished, (torch.uint8, torch.bool), "finished")):
+        if t is not None and (t.dtype not in types or not t.is_cuda or t.device != device or t.shape != (B, W)
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [B][W] of {types[0]} on logits' device")
+    if out is None:
+        out = [_empty((B, int(n)), t, device, stream) for t in (torch.int32, torch.int32, torch.float32)]
+    parent, token, score = out
+    for t, dtype in ((parent, torch.int32), (token, torch.int32), (score, torch.float32)):
+        if t.dtype != dtype or not t.is_cuda or t.device != device or t.shape != (B, n) or not t.is_contiguous():
+            raise ValueError("out must be contiguous CUDA tensors [B][n], int32, int32 and float32, on logits' device")
+    if workspace is None:
+        workspace = _scratch(lambda: beam_workspace_for(B, W, V, n, device), device, stream)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on logits' device")
+    a = BeamArgs(logits=logits.data_ptr(), stride_row=row, scores=scores.data_ptr(),
+                 finished=None if finished is None else finished.data_ptr(), batch=B, beams=W, vocab=V, n=int(n),
+                 end_token=int(end_token), flags=KVQ_LOGITS_F32 if logits.dtype == torch.float32 else 0,
+                 parent=parent.data_ptr(), token=token.data_ptr(), score=score.data_ptr(),
+                 workspace=workspace.data_ptr(), ws_bytes=workspace.numel() * workspace.element_size(),
+                 err_word=_err_ptr(err, device))
+    _call_on("kvq_beam_select", device, stream, ctypes.byref(a))
+    return parent, token, score
+
+
+KVQ_REORDER_SHARE_PAGES = 1
+
+
+def kvq_reorder(dst: KVCache, src: KVCache, index: torch.Tensor, share_pages: bool = False, stream=None) -> None:
+    """Sequence i of ``dst`` becomes sequence index[i] of ``src`` (int32 [dst's batch], any
+    shape): packed rows, window, sink and counters, live bytes alone.  ``share_pages`` (two
+    paged caches over one pool, see KVCache.twin): full pages go to dst's block table, only
+    the page that is being filled is copied, to the page that dst's table has for it."""
+    device = dst.counters.device
+    if src.counters.device != device:
+        raise ValueError("both caches must be on one device")
+    at = _run_int(index, dst.desc.batch, device, "index")
+    _call_on("kvq_reorder", device, stream, ctypes.byref(dst.desc), ctypes.byref(dst.view), ctypes.byref(src.desc),
+             ctypes.byref(src.view), at, KVQ_REORDER_SHARE_PAGES if share_pages else 0)
 
 
 def kvq_read_error(cache: KVCache, stream=None) -> tuple[int, int]:

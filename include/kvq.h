@@ -27,7 +27,8 @@
  *   - TurboQuant 3-bit article, section 3.1: eight 3-bit codes in 24 bits; section
  *     6.1: a paged cache of 32-token blocks.
  * The calls on runs of several tokens (kvq_append_chunk, kvq_chunk_attention,
- * kvq_cross_attention, kvq_read_tokens) are this library's additions.
+ * kvq_cross_attention, kvq_read_tokens) and those around the cache (kvq_rotate,
+ * kvq_prompt_attention, kvq_beam_select, kvq_reorder) are this library's additions.
  *
  * ---------------------------------------------------------------------------
  * Notation
@@ -140,6 +141,9 @@ typedef enum {
 #define KVQ_ERRBIT_BADPAGE 0x10u /* a block-table page outside [0, NP): pack/append wrote nothing
                                    there; decode output of that sequence is undefined */
 #define KVQ_ERRBIT_BADPOS 0x20u  /* a position outside the rotation table; the nearest row was used */
+#define KVQ_ERRBIT_BADINDEX 0x40u /* kvq_reorder: an index outside the source; that sequence was skipped */
+#define KVQ_ERRBIT_BADSCORE 0x80u /* kvq_beam_select: NaN or +inf in a beam's logits or score; the beam
+                                    proposed nothing */
 
 /* Static description of one layer's cache.  group must be 32.  Every field is
  * significant: zero-initialise the struct (sink = 0 keeps no sink window). */
@@ -484,6 +488,120 @@ kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* vie
                            const int32_t* first, int32_t count, void* k_out, void* v_out,
                            uint32_t flags, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the cache: a generation from prompts of text and images, with beams.
+ *   prompt   kvq_rotate (queries and keys to their positions), kvq_prompt_attention (their
+ *            attention in full precision), kvq_quantize_pack_strided (keys and values into
+ *            the cache; all three read and write the columns of a fused projection's
+ *            output in place), kvq_reorder (one cached prompt to all its beams)
+ *   token    kvq_rotate, kvq_decode_step, kvq_beam_select, kvq_reorder
+ * Where a call takes an err_word (a cache's, or any zeroed device word) and it is NULL,
+ * errors that depend on data are not reported; the results are the same. */
+
+/* Arguments of kvq_rotate; zero-initialise the struct. */
+typedef struct {
+  const void* q;           /* fp16 device: element j of head h of row t at */
+  const void* k;           /*   t * stride_token + h * stride_head + j; q or k may be NULL */
+  void* q_out;             /* fp16 device, by strides of its own; may be q itself with the */
+  void* k_out;             /*   same strides, and overlaps no input otherwise */
+  int64_t q_stride_token;  /* in elements, non-negative multiples of 8 */
+  int64_t q_stride_head;
+  int64_t k_stride_token;
+  int64_t k_stride_head;
+  int64_t q_out_stride_token;
+  int64_t q_out_stride_head;
+  int64_t k_out_stride_token;
+  int64_t k_out_stride_head;
+  int32_t num_q_heads;     /* (read only with q) */
+  int32_t num_kv_heads;    /* (read only with k) */
+  int32_t head_dim;        /* 32, 64, 128 or 256 */
+  int32_t total;           /* rows */
+  const float* rope;       /* fp32 device [rope_rows][rotary_dim / 2][2]: cos, sin */
+  int32_t rope_rows;
+  int32_t rotary_dim;      /* leading elements that are rotated: a multiple of 16, 16..head_dim */
+  int32_t interleaved;     /* pairs: 0 (i, i + rotary_dim / 2), 1 (2i, 2i + 1) */
+  int32_t axes;            /* 1..4 */
+  const int32_t* positions; /* int32 device [axes][total] */
+  const uint8_t* pair_axis; /* HOST [rotary_dim / 2]: the axis of each pair (NULL: axis 0);
+                               read during the call */
+  uint32_t* err_word;      /* device, or NULL */
+} kvq_rotate_args;
+
+/* Rotate queries and keys to positions on several axes (time, height and width of the
+ * patches of images and video; text has the same position on each).  Pair i of row t is
+ * rotated by R1 (kvq_append_chunk's rule, with the same roundings) at
+ * rope[positions[pair_axis[i]][t]][i]; elements from rotary_dim on are copied.  With one
+ * axis the result is the append's, bit for bit: keys rotated here enter the cache by
+ * kvq_quantize_pack_strided, kvq_append or kvq_append_chunk without a table.
+ * A position outside [0, rope_rows) sets KVQ_ERRBIT_BADPOS and uses the nearest row.
+ * Asynchronous. */
+kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream);
+
+/* Arguments of kvq_beam_select; zero-initialise the struct. */
+typedef struct {
+  const void* logits;      /* device, 16-byte aligned: token t of row r at r * stride_row + t;
+                              fp16, or fp32 with KVQ_LOGITS_F32.  Row b * beams + w is beam w
+                              of batch entry b */
+  int64_t stride_row;      /* in elements, >= vocab */
+  const float* scores;     /* fp32 device [batch * beams]: the beams' sums of log-probabilities */
+  const uint8_t* finished; /* device [batch * beams], non-zero: the beam is complete; or NULL */
+  int32_t batch;
+  int32_t beams;           /* W, 1..32 */
+  int32_t vocab;           /* V */
+  int32_t n;               /* selected per batch entry: 1..32, at most W V */
+  int32_t end_token;       /* what a complete beam goes on with, 0..V-1 (read only with finished) */
+  uint32_t flags;          /* 0 or KVQ_LOGITS_F32 */
+  int32_t* parent;         /* device [batch][n]: row of the beam (an index for kvq_reorder) */
+  int32_t* token;          /* device [batch][n] */
+  float* score;            /* device [batch][n] */
+  void* workspace;         /* device, 16-byte aligned, ws_bytes >= kvq_beam_workspace_bytes;
+                              whatever it holds, each call writes what it reads; one call at a time */
+  size_t ws_bytes;
+  uint32_t* err_word;      /* device, or NULL */
+} kvq_beam_args;
+
+#define KVQ_LOGITS_F32 1u
+
+/* Bytes of scratch kvq_beam_select needs (0 for invalid arguments). */
+size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t n);
+
+/* Beam search's selection.  Beam w proposes token t with the score
+ *   scores[w] + x[t] - log sum_u exp(x[u]),   x its logits;
+ * a complete beam proposes end_token alone, at scores[w].  For each batch entry the n
+ * best proposals, best first; equal scores in the order of (w, t).  What is not proposed
+ * (logits of -inf, other tokens of complete beams, beams with a score of -inf) counts as a
+ * score of -inf, so n entries always come back.
+ * A beam with a NaN or +inf among its logits, or as its score, proposes nothing and sets
+ * KVQ_ERRBIT_BADSCORE (a complete beam's logits are not looked at).
+ * The sums of exponentials are fp32 (within 2^-20 of the whole), their logarithms and the
+ * scores that are compared 64-bit; scores are rounded to fp32 once.  Results do not depend
+ * on timing.  Asynchronous. */
+kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream);
+
+/* Copy sequences from one cache to another: sequence i of `dst` becomes sequence index[i]
+ * of `src` (beams after a selection, a prompt to its beams, a batch to a larger cache).
+ *   index      int32 device [dst_desc.batch]; entries may repeat.
+ * The caches have the same heads, head_dim, bits, residual, sink, hybrid and page_size;
+ * batch, capacity and pages may differ.  Only live bytes move: packed rows (codes, params,
+ * modes), the window's tokens (in the same ring slots), the sink's, the counters.
+ * Other bytes of dst stay as they are.  dst's arrays are not src's (the pools of two
+ * paged caches may be one, with pages of their own in each table); paged, dst's table
+ * has pages for the tokens that it gets.
+ *   flags      0, or KVQ_REORDER_SHARE_PAGES (paged caches over one pool): full pages do
+ *              not move; dst's table entries for them become the source's.  The page
+ *              that is being filled is copied to the page in dst's own table, so that
+ *              each sequence appends to a page of its own.  With two tables that take
+ *              turns, each with own pages for the tokens to come, a page is never
+ *              written again once it is full.
+ * An index outside src sets KVQ_ERRBIT_BADINDEX, more packed tokens than dst's capacity
+ * KVQ_ERRBIT_CAPACITY; such a sequence stays as it was.  A page outside the pool sets
+ * KVQ_ERRBIT_BADPAGE and its tokens are not copied.  (Bits go to dst's err_word.)
+ * Asynchronous; lengths and indices are read on the device. */
+#define KVQ_REORDER_SHARE_PAGES 1u
+kvq_status kvq_reorder(const kvq_cache_desc* dst_desc, const kvq_cache_view* dst,
+                       const kvq_cache_desc* src_desc, const kvq_cache_view* src,
+                       const int32_t* index, uint32_t flags, void* stream);
+
 /* Synchronize `stream`, copy *err_word to *word_out (may be NULL), clear it, and
  * return KVQ_OK if it was 0, else the status of its lowest set bit. */
 kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* stream);
@@ -493,7 +611,8 @@ const char* kvq_status_string(kvq_status status);
 
 /* Library version as 10000 * major + 100 * minor + patch. */
 int32_t kvq_version(void); /* 160: two-part weights in the tensor-core MMAs, MMA rounding hook
-                              (and, under the same number, the calls on runs and BADPOS);
+                              (and, under the same number, the calls on runs and BADPOS,
+                              then the calls around the cache, BADINDEX and BADSCORE);
                               150: timeout testing hook, cached tensor maps; 140: paged caches;
                               130: 3-bit; 120: hybrid; 110: sink, fp32 out */
 
