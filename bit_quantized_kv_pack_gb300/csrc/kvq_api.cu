@@ -363,6 +363,29 @@ kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
   return from_cuda(kvq::launch_rotate(A, static_cast<cudaStream_t>(stream)));
 }
 
+kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream) {
+  if (!args) return KVQ_ERR_INVALID_ARG;
+  const kvq_prompt_args& A = *args;
+  if (A.total < 0 || A.max_len < 0 || A.batch < 1 || !A.cu_seqlens || A.num_kv_heads < 1 || A.num_q_heads < 1 ||
+      A.num_q_heads % A.num_kv_heads || A.head_dim < 32 || A.head_dim % 32 || (A.flags & ~(uint32_t)KVQ_OUT_F32))
+    return KVQ_ERR_INVALID_ARG;
+  if (A.total > 0 && (!A.q || !A.k || !A.v || !A.out)) return KVQ_ERR_INVALID_ARG;
+  if (!head_dim_ok(A.head_dim) || A.num_q_heads / A.num_kv_heads > 128 || A.total > (1 << 30) || A.batch > (1 << 24))
+    return KVQ_ERR_UNSUPPORTED;
+  const int64_t strides[6] = {A.q_stride_token, A.k_stride_token, A.v_stride_token,
+                              A.q_stride_head,  A.k_stride_head,  A.v_stride_head};
+  for (int i = 0; i < 6; ++i) {
+    const int32_t entries = i < 3 ? A.total : i == 3 ? A.num_q_heads : A.num_kv_heads;
+    if (strides[i] < 0) return KVQ_ERR_INVALID_ARG;
+    if (strides[i] % 8) return KVQ_ERR_MISALIGNED;  // rows start on 16-byte boundaries
+    if (entries > 1 && (strides[i] == 0 || strides[i] >= (1LL << 39) / 128)) return KVQ_ERR_UNSUPPORTED;
+  }
+  if (!aligned(A.q, 16) || !aligned(A.k, 16) || !aligned(A.v, 16) || !aligned(A.out, 16) ||
+      !aligned(A.cu_seqlens, 4) || !aligned(A.err_word, 4))
+    return KVQ_ERR_MISALIGNED;
+  return from_cuda(kvq::launch_prompt_attention(A, static_cast<cudaStream_t>(stream)));
+}
+
 namespace {
 kvq_status check_beams(int32_t batch, int32_t beams, int32_t vocab, int32_t n) {
   if (batch < 1 || beams < 1 || vocab < 1 || n < 1 || (int64_t)beams * vocab < n) return KVQ_ERR_INVALID_ARG;

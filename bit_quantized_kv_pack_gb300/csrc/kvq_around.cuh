@@ -8,6 +8,8 @@ namespace kvq {
 
 cudaError_t launch_rotate(const kvq_rotate_args& args, cudaStream_t st);
 
+cudaError_t launch_prompt_attention(const kvq_prompt_args& args, cudaStream_t st);
+
 size_t beam_workspace_bytes(int batch, int beams, int vocab, int n);
 cudaError_t launch_beam_select(const kvq_beam_args& args, cudaStream_t st);
 

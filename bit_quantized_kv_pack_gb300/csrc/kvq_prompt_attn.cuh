@@ -1,0 +1,744 @@
+// kvq_prompt_attn.cuh -- causal attention over whole prompts in full precision, on the
+// fifth-generation tensor cores.
+//
+// The mathematics.  The query rows of a block are T = 128 / gq tokens times the gq heads
+// that share a KV head, row = token * gq + head, twice (two lanes): one pass over K and V
+// serves them all.  For a tile of TN tokens S = Q K^T, P = exp2(S c - m c) with the row's
+// reference maximum m, O += P V, l += sum P; c = log2(e) / sqrt(d).  m follows the running
+// maximum lazily: it moves (and O, l are rescaled) only when the maximum has passed it by
+// 2^8.  Roundings: the weights P to fp16 once (they and l carry a factor 2^7, which O / l
+// cancels, so that they keep 11 bits down to 2^-21 of the reference and lose at most 2^-32
+// of it below), the output once; scores, m, l and O are fp32.
+//
+// A block (one per SM, persistent) has 12 warps:
+//   0-7   softmax: a thread per query row, four warps for each of the two accumulators
+//         (lanes): S from TMEM, P back to TMEM in S's place as the A operand of the second
+//         MMA, the epilogue.
+//   8     issues the MMAs: the lanes' steps in turn, so that the softmax of one runs under
+//         the MMAs of the other.
+//   9     loads Q, K and V (TMA tiles, 128-byte swizzle; K and V through one ring).
+//   10    looks at values that some row of the block does not see (the tiles at the
+//         diagonal): a weight of zero would turn an infinite one into NaN.
+//   11    works out the units.
+// head_dim 256 has room for one lane and tiles of 64 tokens.
+//
+// A unit of work is (sequence, KV head, block of 2 T tokens).  Units lie in one line,
+// sequence after sequence, the longest first within each; blocks take them in turn, back and
+// forth, which evens out the lengths that fall along the line.
+#pragma once
+
+#include <cuda.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "kvq_around.cuh"
+#include "kvq_ptx.cuh"
+#include "kvq_runs.cuh"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+
+struct PromptAttnArgs {
+  CUtensorMap mq, mk, mv;  // {element, head of the group, token, KV head}; {element, token, KV head}
+  const int32_t* cu;
+  uint32_t* err_word;
+  void* out;  // [total][Hq][d]
+  int B, Hkv, gq, T, total, max_len, out_f32;
+  uint32_t wait_limit_us;
+  int fault;  // testing hook: 1 makes the scores' barriers wait for an arrival that never comes
+  float scale_log2;
+};
+
+cudaError_t launch_prompt_attn_d32(const PromptAttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_prompt_attn_d64(const PromptAttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_prompt_attn_d128(const PromptAttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_prompt_attn_d256(const PromptAttnArgs& a, int grid, cudaStream_t st);
+
+// The kernel's shapes: lanes of a block, tokens of a tile, elements of a tile's row in
+// shared memory (a panel; 128 bytes, or 64 at head_dim 32).
+__host__ __device__ constexpr int prompt_lanes(int d) { return d == 256 ? 1 : 2; }
+__host__ __device__ constexpr int prompt_tile(int d) { return d == 256 ? 64 : 128; }
+__host__ __device__ constexpr int prompt_panel(int d) { return d < 64 ? d : 64; }
+
+namespace prompt {
+
+constexpr int kThreads = 384;
+constexpr float kWeightBits = 7.0f;  // log2 of the weights' factor
+constexpr int kUnits = 4;            // ring of units
+constexpr int kMaxStages = 8;
+
+template <int D>
+struct Cfg {
+  static constexpr int LANES = prompt_lanes(D);
+  static constexpr int TN = prompt_tile(D);
+  static constexpr int PW = prompt_panel(D);
+  static constexpr int NP = D / PW;
+  static constexpr int RB = PW * 2;  // bytes of a panel's row
+  static constexpr int SWZ = RB == 128 ? 2 : 4;
+  static constexpr int QP = 128 * RB;  // bytes of a panel of Q
+  static constexpr int KP = TN * RB;   // of a panel of K or V
+  static constexpr int QBYTES = 128 * D * 2;
+  static constexpr int KBYTES = TN * D * 2;
+  static constexpr int ST = D == 256 ? 4 : D == 128 ? 5 : 8;  // stages of K and V
+  static constexpr int SMW = 4 * LANES;        // softmax warps
+  // TMEM columns
+  static constexpr int S0 = 0;
+  static constexpr int O0 = 256;
+  // shared memory
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = OFF_Q + LANES * QBYTES;
+  static constexpr int OFF_NOTES = OFF_KV + ST * KBYTES;  // int [3][D]
+  static constexpr int OFF_BAR = OFF_NOTES + 3 * D * 4;
+  static constexpr int OFF_UNIT = OFF_BAR + 512;
+  // (more than half an SM's, so that a block has the tensor memory to itself)
+  static constexpr int SMEM = OFF_UNIT + kUnits * 32 > 117 * 1024 ? OFF_UNIT + kUnits * 32 : 117 * 1024;
+};
+
+// Sequence rows [c0, c0 + n), KV head h, first token t0 of the block; tiles of each lane
+// (lane 1's are 0 or not fewer); no: 1, 2, .. in the block's order, 0: the end.
+struct alignas(16) Unit {
+  int c0, n, h, t0;
+  int tiles0, tiles1, no, pad;
+};
+
+// Barriers (8 bytes each from OFF_BAR) and words behind them.
+enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 6, B_ODONE = 8, B_DRAIN = 10, B_UFULL = 11,
+       B_UEMPTY = B_UFULL + kUnits, B_KVFULL = B_UEMPTY + kUnits, B_KVEMPTY = B_KVFULL + kMaxStages,
+       B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
+enum { W_TMEM = 96, W_ABORT = 97, W_NOTED = 98 /* the unit that the notes are of */, W_EPI = 99 };
+static_assert(B_COUNT * 2 <= W_TMEM, "words behind the barriers");
+
+__device__ __forceinline__ uint32_t lds(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t v) {
+  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t timer_lo() {  // nanoseconds, modulo 2^32
+  uint32_t t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// 3D and 4D tile loads, completion counted in bytes on `bar`.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Bounded waits (at most a second): all give up when one has.
+struct Waits {
+  uint32_t bars;  // shared address of the barriers and words
+  uint32_t limit_us;
+
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+  __device__ __forceinline__ uint32_t word(int i) const { return lds(bars + 4 * i); }
+  __device__ __forceinline__ void set_word(int i, uint32_t v) const { sts(bars + 4 * i, v); }
+  __device__ __forceinline__ bool late(uint32_t t0) const {
+    if (word(W_ABORT)) return true;
+    if (timer_lo() - t0 <= limit_us * 1000u) return false;
+    set_word(W_ABORT, 1);
+    return true;
+  }
+  __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+    const uint32_t b = bar(i);
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    const uint32_t t0 = timer_lo();
+#pragma unroll 1
+    for (uint32_t k = 1; !ptx::mbar_try_wait(b, parity); ++k)
+      if ((k & 63u) == 0 && late(t0)) return false;
+    return true;
+  }
+  // a whole warp waits; the same answer for all its lanes
+  __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait(i, parity));
+  }
+  __device__ __forceinline__ void arrive_warp(int i) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar(i));
+  }
+};
+
+// A role's place in the ring of units (all of a warp).
+struct UnitReader {
+  const Waits& wt;
+  const Unit* ring;
+  uint32_t i = 0;
+  // the next unit; no == 0 at the end of the line or when a wait gave up
+  __device__ __forceinline__ Unit next() {
+    Unit u;
+    u.no = 0;
+    if (wt.wait_warp(B_UFULL + i % kUnits, (i / kUnits) & 1)) u = ring[i % kUnits];
+    return u;
+  }
+  __device__ __forceinline__ void release() {
+    wt.arrive_warp(B_UEMPTY + i % kUnits);
+    ++i;
+  }
+};
+
+// -------------------------------------------------------------------- units ---
+
+// The warp that works out the units: a window of 32 sequences goes along the line.
+template <int D>
+__device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, Unit* ring) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  const int step = C::LANES * a.T;  // tokens of a unit
+  const int G = gridDim.x;
+  int b0 = 0;
+  int64_t base = 0, scan = 0;  // units before the window; of its sequences up to the lane's
+  Run run = {0, 0};
+  auto window = [&] {
+    run.n = 0;
+    if (b0 + lane < a.B) run = run_of(a.cu, b0 + lane, a.total, a.max_len);
+    if (run.n < 0 && blockIdx.x == 0) set_error(a.err_word, KVQ_ERRBIT_BADLEN);
+    scan = run.n > 0 ? (int64_t)((run.n + step - 1) / step) * a.Hkv : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+  };
+  window();
+  for (uint32_t i = 0;; ++i) {
+    const int64_t u = (int64_t)i * G + (i & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    while (b0 < a.B) {
+      const int64_t all = __shfl_sync(0xffffffffu, scan, 31);
+      if (u < base + all) break;
+      base += all;
+      b0 += 32;
+      window();
+    }
+    const bool more = b0 < a.B;
+    if (!wt.wait_warp(B_UEMPTY + i % kUnits, ((i / kUnits) & 1) ^ 1)) return;
+    // the sequence that has unit u; its last block first, heads within blocks
+    const uint32_t has = __ballot_sync(0xffffffffu, more && u < base + scan);
+    if (more ? lane == __ffs(has) - 1 : lane == 0) {
+      Unit s;
+      s.no = 0;
+      if (more) {
+        const int r = (int)(base + scan - 1 - u);  // units after it in the sequence
+        s.c0 = run.c0, s.n = run.n;
+        s.h = a.Hkv - 1 - r % a.Hkv;
+        s.t0 = r / a.Hkv * step;
+        auto tiles = [&](int l) {
+          const int first = s.t0 + l * a.T;
+          return first < run.n ? (min(first + a.T, run.n) + C::TN - 1) / C::TN : 0;
+        };
+        s.tiles0 = tiles(0);
+        s.tiles1 = C::LANES == 2 ? tiles(1) : 0;
+        s.no = i + 1;
+      }
+      ring[i % kUnits] = s;
+      ptx::mbar_arrive(wt.bar(B_UFULL + i % kUnits));
+    }
+    __syncwarp();
+    if (!more) return;
+  }
+}
+
+// -------------------------------------------------------------------- loads ---
+
+template <int D>
+__device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* ring) {
+  using C = Cfg<D>;
+  const bool one = (threadIdx.x & 31) == 0;
+  if (one) {
+    ptx::prefetch_tensormap(&a.mq);
+    ptx::prefetch_tensormap(&a.mk);
+    ptx::prefetch_tensormap(&a.mv);
+  }
+  UnitReader units = {wt, ring};
+  uint32_t item = 0, qn[2] = {0, 0};  // half tiles so far, units of each lane
+  bool ok = true;
+  while (ok) {
+    const Unit u = units.next();
+    units.release();
+    if (u.no == 0) break;
+    const int nt = max(u.tiles0, u.tiles1);
+    auto kv = [&](int t, int w) {
+      const int stage = item % C::ST;
+      ok = ok && wt.wait_warp(B_KVEMPTY + stage, ((item / C::ST) & 1) ^ 1);
+      if (!ok) return;
+      if (one) {
+        ptx::mbar_arrive_expect_tx(wt.bar(B_KVFULL + stage), C::KBYTES);
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p)
+          tma_load(smem + C::OFF_KV + stage * C::KBYTES + p * C::KP, w ? &a.mv : &a.mk, p * C::PW, u.c0 + t * C::TN, u.h,
+                   wt.bar(B_KVFULL + stage));
+      }
+      ++item;
+    };
+    kv(0, 0);
+#pragma unroll
+    for (int l = 0; l < C::LANES; ++l) {
+      if ((l ? u.tiles1 : u.tiles0) == 0) continue;
+      ok = ok && wt.wait_warp(B_QEMPTY + l, (qn[l] & 1) ^ 1);
+      if (!ok) break;
+      if (one) {
+        ptx::mbar_arrive_expect_tx(wt.bar(B_QFULL + l), a.T * a.gq * D * 2);
+#pragma unroll
+        for (int p = 0; p < C::NP; ++p)
+          tma_load(smem + C::OFF_Q + l * C::QBYTES + p * C::QP, &a.mq, p * C::PW, 0, u.c0 + u.t0 + l * a.T, u.h,
+                   wt.bar(B_QFULL + l));
+      }
+      ++qn[l];
+    }
+    kv(0, 1);
+    for (int t = 1; ok && t < nt; ++t) {
+      kv(t, 0);
+      kv(t, 1);
+    }
+  }
+  // copies still in flight when the block gives up land before its shared memory goes
+  const uint32_t t0 = timer_lo();
+  auto landed = [&](int bar, uint32_t parity) {
+    while (!ptx::mbar_try_wait(wt.bar(bar), parity))
+      if (timer_lo() - t0 > 1000000000u) return;
+  };
+  for (uint32_t i = item > C::ST ? item - C::ST : 0; i < item; ++i) landed(B_KVFULL + i % C::ST, (i / C::ST) & 1);
+  for (int l = 0; l < C::LANES; ++l)
+    if (qn[l] > 0) landed(B_QFULL + l, (qn[l] - 1) & 1);
+}
+
+// ------------------------------------------------------------- values' check ---
+
+// Values that are not finite, at tokens that some row of the block does not see (tokens of
+// the next sequence among them): zeros take their place in the tile, and the first
+// token with +inf, -inf or NaN in a column is noted; the epilogue gives the rows that see
+// it what the sum would be.  In tiles that all rows see whole the MMA does that itself.
+// The warp sees every fill of the ring (a parity alone does not tell a fill from the one
+// before the last), and a stage is free when it and the MMAs are done with it.
+template <int D>
+__device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* ring) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  UnitReader units = {wt, ring};
+  uint32_t item = 0, before = 0;  // half tiles of earlier units; those units' epilogues, a warp each
+  while (true) {
+    const Unit u = units.next();
+    units.release();
+    if (u.no == 0) return;
+    const int nt = max(u.tiles0, u.tiles1);
+    bool clean = false;  // the notes are this unit's
+    for (int half = 0; half < 2 * nt; ++half) {
+      const uint32_t it = item + half;
+      const int stage = it % C::ST, t = half >> 1;
+      if (!wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1)) return;
+      // the block's first row sees tokens up to t0
+      if (!(half & 1) || t < (u.t0 + 1) / C::TN) {
+        wt.arrive_warp(B_KVEMPTY + stage);
+        continue;
+      }
+      const uint32_t tile = smem + C::OFF_KV + stage * C::KBYTES;
+      const int r0 = max(0, u.t0 + 1 - t * C::TN);  // rows before it are seen by all
+      bool any = false;
+#pragma unroll 1
+      for (int p = 0; p < C::NP; ++p)
+#pragma unroll 4
+        for (int at = r0 * C::RB + lane * 16; at < C::KP; at += 512) {
+          const uint4 v = lds_v4(tile + p * C::KP + at);
+          // an exponent of ones carries into the bit above it
+          const uint32_t m = 0x7c007c00u, c = 0x04000400u;
+          any |= ((((v.x & m) + c) | ((v.y & m) + c) | ((v.z & m) + c) | ((v.w & m) + c)) & 0x80008000u) != 0;
+        }
+      if (__any_sync(0xffffffffu, any)) {
+        if (!clean) {  // earlier notes have been read
+          const uint32_t t0 = timer_lo();
+          while (wt.word(W_EPI) < before)
+            if (wt.late(t0)) break;
+          if (__any_sync(0xffffffffu, wt.word(W_ABORT) != 0)) return;
+          for (int i = lane; i < 3 * D; i += 32) sts(smem + C::OFF_NOTES + 4 * i, 0x7fffffffu);
+          __syncwarp();
+          wt.set_word(W_NOTED, u.no);
+          clean = true;
+        }
+#pragma unroll 1
+        for (int i = r0 * D + lane; i < C::TN * D; i += 32) {
+          const int r = i / D, col = i % D, in = (col % C::PW) * 2;
+          const uint32_t x = (uint32_t)(C::RB == 128 ? r & 7 : (r >> 1) & 3) << 4;
+          const uint32_t at = tile + (col / C::PW) * C::KP + r * C::RB + (in ^ x);
+          unsigned short hv;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(at) : "memory");
+          if ((hv & 0x7c00u) != 0x7c00u) continue;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+          const int token = t * C::TN + r, kind = (hv & 0x3ffu) ? 2 : (hv & 0x8000u) ? 1 : 0;
+          if (token < u.n)
+            asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(smem + C::OFF_NOTES + 4 * (kind * D + col)), "r"(token)
+                         : "memory");
+        }
+        __threadfence_block();
+        ptx::fence_proxy_async_shared();
+      }
+      wt.arrive_warp(B_VOK + stage);
+      wt.arrive_warp(B_KVEMPTY + stage);
+    }
+    item += 2 * nt;
+    before += (u.tiles0 > 0 ? 4 : 0) + (u.tiles1 > 0 ? 4 : 0);
+  }
+}
+
+// ---------------------------------------------------------------------- MMA ---
+
+// All lanes of the warp go the same way, so that descriptors and addresses stay in its
+// uniform registers, and one of them issues.
+template <int D>
+__device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
+  constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
+  UnitReader units = {wt, ring};
+  uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
+  uint32_t item = 0, vok = 0;               // half tiles of earlier units; a phase bit of each stage
+  bool ok = true;
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  while (ok) {
+    const Unit u = units.next();
+    units.release();
+    if (uniform(u.no) == 0) break;
+    const int n[2] = {uniform(u.tiles0), uniform(u.tiles1)};
+    const int nt = max(n[0], n[1]), checked = (uniform(u.t0) + 1) / C::TN;
+    auto last_user = [&](int l, int t) { return l == (t < n[1] ? 1 : 0); };
+    auto qk = [&](int l, int t) -> bool {
+      const uint32_t it = item + 2 * t;
+      const int stage = it % C::ST;
+      if (t == 0 && !wt.wait_warp(B_QFULL + l, qn[l]++ & 1)) return false;
+      if (!wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1)) return false;
+      tc5::fence_after();
+      const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + l * C::QBYTES, 16, 8 * C::RB, C::SWZ);
+      const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+      if (tc5::elect()) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
+          tc5::mma_ss(tmem + C::S0 + l * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+                      kIdescQK, j > 0);
+        }
+        tc5::commit(wt.bar(B_SFULL + l));
+        if (last_user(l, t)) tc5::commit(wt.bar(B_KVEMPTY + stage));
+        if (t + 1 == n[l]) tc5::commit(wt.bar(B_QEMPTY + l));
+      }
+      __syncwarp();
+      return true;
+    };
+#pragma unroll
+    for (int l = 0; l < C::LANES; ++l)
+      if (ok && n[l] > 0) ok = qk(l, 0);
+    for (int t = 0; ok && t < nt; ++t) {
+      const uint32_t it = item + 2 * t + 1;
+      const int stage = it % C::ST;
+      if (t >= checked) {
+        ok = wt.wait_warp(B_VOK + stage, (vok >> stage) & 1);
+        vok ^= 1u << stage;
+      }
+#pragma unroll
+      for (int l = 0; l < C::LANES; ++l) {
+        if (!ok || t >= n[l]) continue;
+        ok = wt.wait_warp(B_PREADY + l, pn[l]++ & 1) && wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1);
+        if (!ok) continue;
+        tc5::fence_after();
+        const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+        if (tc5::elect()) {
+#pragma unroll
+          for (int j = 0; j < C::TN / 16; ++j)
+            tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
+                        t > 0 || j > 0);
+          if (last_user(l, t)) tc5::commit(wt.bar(B_KVEMPTY + stage));
+          if (t + 1 == n[l]) tc5::commit(wt.bar(B_ODONE + l));
+        }
+        __syncwarp();
+        // after this step in the tensor cores' order: S may take P's place
+        if (t + 1 < n[l]) ok = qk(l, t + 1);
+      }
+    }
+    item += 2 * nt;
+  }
+  // nothing of this thread's is in flight when TMEM is freed
+  if (tc5::elect()) tc5::commit(wt.bar(B_DRAIN));
+  __syncwarp();
+  wt.wait_warp(B_DRAIN, 0);
+}
+
+// ------------------------------------------------------------------ softmax ---
+
+template <int D>
+struct Soft {
+  using C = Cfg<D>;
+  const PromptAttnArgs& a;
+  const Waits& wt;
+  const uint32_t smem, tmem;  // tmem: with the warp's lanes
+  uint32_t sn = 0, on = 0;    // phases of the scores and of the finished sums
+
+  static __device__ __forceinline__ int lane() { return threadIdx.x >> 7; }
+  static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
+
+  // Hides what the row does not see of 32 tokens; the largest score that is left.
+  static __device__ __forceinline__ float mask(float* s, int visible) {
+    const uint32_t seen = visible <= 0 ? 0u : visible >= 32 ? ~0u : (1u << visible) - 1u;
+    float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      s[j] = (seen >> j) & 1u ? s[j] : -INFINITY;
+      s[j + 1] = (seen >> (j + 1)) & 1u ? s[j + 1] : -INFINITY;
+      x = fmaxf(x, s[j]);
+      y = fmaxf(y, s[j + 1]);
+    }
+    return fmaxf(x, y);
+  }
+
+  // One tile: the row's weights into TMEM, m and l brought up to date.  visible: tokens of
+  // the tile that the row sees (a prefix).
+  __device__ __forceinline__ void tile(int visible, bool started, float& m, float& l) const {
+    const uint32_t sa = tmem + C::S0 + lane() * C::TN;
+    float s[C::TN], mx[C::TN / 32];
+#pragma unroll
+    for (int i = 0; i < C::TN / 32; ++i) tc5::ld32_max(sa + 32 * i, reinterpret_cast<uint32_t*>(s + 32 * i), mx[i]);
+    tc5::wait_ld();
+#pragma unroll
+    for (int i = 0; i < C::TN / 32; ++i) {
+      tc5::pin32(reinterpret_cast<uint32_t*>(s + 32 * i));
+      asm volatile("" : "+f"(mx[i]));
+    }
+    if (__any_sync(0xffffffffu, visible < C::TN)) {
+#pragma unroll
+      for (int i = 0; i < C::TN / 32; ++i) mx[i] = mask(s + 32 * i, visible - 32 * i);
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < C::TN / 32; ++i) mn = fmaxf(mn, mx[i]);
+    const bool moves = (mn - m) * a.scale_log2 > 8.0f;
+    if (__any_sync(0xffffffffu, moves)) {
+      const float f = moves ? ptx::ex2_ftz((m - mn) * a.scale_log2) : 1.0f;
+      if (moves) m = mn;
+      l *= f;
+      if (started) {
+        const uint32_t oa = tmem + C::O0 + lane() * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 16) {
+          uint32_t o[16];
+          tc5::ld16(oa + i, o);
+          tc5::wait_ld();
+          tc5::pin16(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tc5::st16(oa + i, o);
+        }
+      }
+    }
+    const float off = m == -INFINITY ? 0.0f : fmaf(-m, a.scale_log2, kWeightBits);
+    const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
+    uint64_t sum2 = pack_f32x2(l, 0.0f);
+#pragma unroll
+    for (int h = 0; h < C::TN; h += 32) {
+      uint32_t p[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t x = fma_f32x2(pack_f32x2(s[h + i], s[h + i + 1]), c2, off2);
+        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
+        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
+        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
+        p[i / 2] = ptx::pack_h2(e0, e1);
+      }
+      tc5::st16(sa + h / 2, p);
+    }
+    l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
+    tc5::wait_st();
+  }
+
+  __device__ __forceinline__ void store16(const float* o, float f, int64_t at) const {
+    if (a.out_f32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        dst[e] = make_uint4(ptx::pack_h2(o[8 * e] * f, o[8 * e + 1] * f), ptx::pack_h2(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                            ptx::pack_h2(o[8 * e + 4] * f, o[8 * e + 5] * f),
+                            ptx::pack_h2(o[8 * e + 6] * f, o[8 * e + 7] * f));
+    }
+  }
+
+  // What the notes say of the row's columns, over the thread's own stores.  A row whose sum
+  // is NaN stays NaN.
+  __device__ __forceinline__ void notes(int lim, float inv, int64_t at) const {
+    const uint32_t n = smem + C::OFF_NOTES;
+#pragma unroll 1
+    for (int c = 0; c < D; ++c) {
+      const bool up = (int)lds(n + 4 * c) < lim, down = (int)lds(n + 4 * (D + c)) < lim,
+                 nan = (int)lds(n + 4 * (2 * D + c)) < lim;
+      if (!(up || down || nan)) continue;
+      float v = nan || (up && down) || inv != inv ? NAN : up ? INFINITY : -INFINITY;
+      // (with an infinite value of the other sign in a tile that all rows see, or NaN there)
+      const float o = a.out_f32 ? static_cast<float*>(a.out)[at + c] : __half2float(static_cast<__half*>(a.out)[at + c]);
+      if (o != o || (isinf(o) && o != v)) v = NAN;
+      if (a.out_f32)
+        static_cast<float*>(a.out)[at + c] = v;
+      else
+        static_cast<__half*>(a.out)[at + c] = __float2half(v);
+    }
+  }
+
+  __device__ __forceinline__ void run(const Unit* ring) {
+    UnitReader units = {wt, ring};
+    while (true) {
+      const Unit u = units.next();
+      units.release();
+      if (u.no == 0) return;
+      const int n = lane() ? u.tiles1 : u.tiles0;
+      if (n == 0) continue;
+      const int in = r() / a.gq, tok = u.t0 + lane() * a.T + in;
+      const bool live = in < a.T && tok < u.n;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      int visible = live ? tok + 1 : 1 << 30;  // rows that are not there need no mask
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        if (!wt.wait_warp(B_SFULL + lane(), sn++ & 1)) return;
+        tc5::fence_after();
+        if (warp_live) tile(visible, t > 0, m, l);
+        tc5::fence_before();
+        wt.arrive_warp(B_PREADY + lane());
+        if (live) visible -= C::TN;
+      }
+      if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
+      tc5::fence_after();
+      if (warp_live) {
+        const float inv = 1.0f / l;  // (of scores that are all -inf: NaN, as of NaN ones)
+        const int64_t at = (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tc5::ld32(tmem + C::O0 + lane() * D + c, reinterpret_cast<uint32_t*>(o));
+          tc5::wait_ld();
+          tc5::pin32(reinterpret_cast<uint32_t*>(o));
+          if (live) {
+            store16(o, inv, at + c);
+            store16(o + 16, inv, at + c + 16);
+          }
+          __syncwarp();
+        }
+        if (wt.word(W_NOTED) == (uint32_t)u.no && live) notes(tok + 1, inv, at);
+      }
+      tc5::fence_before();
+      __threadfence_block();
+      __syncwarp();
+      if ((r() & 31) == 0) asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(wt.bars + 4 * W_EPI) : "memory");
+    }
+  }
+};
+
+// ------------------------------------------------------------------- kernel ---
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = ptx::smem_u32(smem_raw);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lid = tid & 31;
+  const Waits wt = {smem + C::OFF_BAR, a.wait_limit_us};
+  Unit* ring = reinterpret_cast<Unit*>(smem_raw + C::OFF_UNIT);
+  if (smem & 1023u) {  // the swizzles count on it (a block without static shared memory has it)
+    if (tid == 0) set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
+    return;
+  }
+  if (warp == 8) {
+    tc5::alloc(smem + C::OFF_BAR + 4 * W_TMEM, 512);
+  } else if (warp == 9) {
+    for (int i = lid; i < B_COUNT; i += 32) {
+      int n = 1;  // arrivals of a phase
+      if (i == B_PREADY || i == B_PREADY + 1) n = 4;
+      if (i == B_SFULL || i == B_SFULL + 1) n = 1 + a.fault;
+      if (i >= B_UEMPTY && i < B_UEMPTY + kUnits) n = C::SMW + 3;
+      if (i >= B_KVEMPTY && i < B_KVEMPTY + kMaxStages) n = 2;
+      ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n);
+    }
+    if (lid == 0) {
+      wt.set_word(W_ABORT, 0);
+      wt.set_word(W_NOTED, 0);
+      wt.set_word(W_EPI, 0);
+    }
+    ptx::fence_mbar_init();
+  }
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, wt.word(W_TMEM), 0);
+  wait_for_previous();
+
+  // Registers: 168 a thread at launch (64512 in all) = 256 x 208 + 128 x 88.
+  if (warp < 8) {
+    tc5::regs_inc<208>();
+    if (warp < C::SMW) {
+      Soft<D> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
+      soft.run(ring);
+    }
+  } else {
+    tc5::regs_dec<88>();
+    if (warp == 8) mma_role<D>(wt, smem, tmem, ring);
+    if (warp == 9) load_role<D>(a, wt, smem, ring);
+    if (warp == 10) check_role<D>(a, wt, smem, ring);
+    if (warp == 11) unit_role<D>(a, wt, ring);
+    __syncwarp();
+  }
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  if (tid == 0 && wt.word(W_ABORT)) set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
+  if (warp == 8) tc5::dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const PromptAttnArgs& a, int grid, cudaStream_t st) {
+  static_assert(Cfg<D>::SMEM <= 227 * 1024, "shared memory of a block");
+  auto kernel = prompt_attn_kernel<D>;
+  // the kernel's attributes, once per device
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
+    // the warps' shares (setmaxnreg) come out of what the block is launched with
+    if (at.numRegs != 168) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_overlapped(kernel, dim3(grid), kThreads, Cfg<D>::SMEM, st, a);
+}
+
+}  // namespace prompt
+}  // namespace kvq

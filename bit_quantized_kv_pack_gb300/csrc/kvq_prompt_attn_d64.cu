@@ -1,0 +1,10 @@
+// kvq_prompt_attn_d64.cu -- attention over prompts, head_dim 64 (kvq_prompt_attn.cuh).
+#include "kvq_prompt_attn.cuh"
+
+namespace kvq {
+
+cudaError_t launch_prompt_attn_d64(const PromptAttnArgs& a, int grid, cudaStream_t st) {
+  return prompt::launch<64>(a, grid, st);
+}
+
+}  // namespace kvq

@@ -48,7 +48,7 @@ EXPORTS = ("kvq_cache_bytes", "kvq_decode_workspace_bytes", "kvq_quantize_pack",
            "kvq_quantize_pack_strided", "kvq_append",
            "kvq_decode_attention", "kvq_decode_step", "kvq_decode_step_host", "kvq_step_io_bytes",
            "kvq_decode_attention_noalloc", "kvq_append_chunk", "kvq_chunk_workspace_bytes",
-           "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens", "kvq_rotate",
+           "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens", "kvq_rotate", "kvq_prompt_attention",
            "kvq_beam_workspace_bytes", "kvq_beam_select", "kvq_reorder",
            "kvq_read_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
            "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding")
@@ -89,6 +89,15 @@ class RotateArgs(ctypes.Structure):
                 + [("rope", ctypes.c_void_p)]
                 + [(n, ctypes.c_int32) for n in ("rope_rows", "rotary_dim", "interleaved", "axes")]
                 + [(n, ctypes.c_void_p) for n in ("positions", "pair_axis", "err_word")])
+
+
+class PromptArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_int64) for n in ("q_stride_token", "q_stride_head", "k_stride_token",
+                                                 "k_stride_head", "v_stride_token", "v_stride_head")]
+                + [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "batch")]
+                + [("cu_seqlens", ctypes.c_void_p), ("total", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                   ("out", ctypes.c_void_p), ("flags", ctypes.c_uint32), ("err_word", ctypes.c_void_p)])
 
 
 class BeamArgs(ctypes.Structure):
@@ -157,6 +166,8 @@ def load(path: str | None = None):
             lib.kvq_read_tokens.restype = ctypes.c_int
             lib.kvq_rotate.argtypes = [ctypes.POINTER(RotateArgs), P]
             lib.kvq_rotate.restype = ctypes.c_int
+            lib.kvq_prompt_attention.argtypes = [ctypes.POINTER(PromptArgs), P]
+            lib.kvq_prompt_attention.restype = ctypes.c_int
             lib.kvq_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
             lib.kvq_beam_workspace_bytes.restype = sz
             lib.kvq_beam_select.argtypes = [ctypes.POINTER(BeamArgs), P]
@@ -791,6 +802,36 @@ def kvq_rotate(q: torch.Tensor | None, k: torch.Tensor | None, rope: torch.Tenso
         a.k_out_stride_token, a.k_out_stride_head = _strides(k_out, total, k.shape[1])
     _call_on("kvq_rotate", device, stream, ctypes.byref(a))
     return q_out, k_out
+
+
+def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                         max_len: int, out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                         stream=None, flags: int = 0) -> torch.Tensor:
+    """Causal attention over whole prompts in full precision: q fp16 [total][Hq][d], k and v
+    [total][Hkv][d] (views with d contiguous: columns of a fused projection's output, say),
+    prompt b being rows cu_seqlens[b] .. cu_seqlens[b+1] (int32 [B + 1]).  out [total][Hq][d],
+    fp16, or fp32 as for kvq_decode_attention.  ``err``: a cache's err."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [total][Hq][d], k and v [total][Hkv][d]")
+    device = q.device
+    total, heads, d = q.shape
+    kv_heads = k.shape[1]
+    a = PromptArgs(q=_rows_tensor(q, device, "q"), k=_rows_tensor(k, device, "k"), v=_rows_tensor(v, device, "v"),
+                   num_q_heads=heads, num_kv_heads=kv_heads, head_dim=d, batch=cu_seqlens.numel() - 1, total=total,
+                   cu_seqlens=_run_int(cu_seqlens, cu_seqlens.numel(), device, "cu_seqlens"),
+                   max_len=_max_len(max_len), err_word=_err_ptr(err, device))
+    a.q_stride_token, a.q_stride_head = _strides(q, total, heads)
+    a.k_stride_token, a.k_stride_head = _strides(k, total, kv_heads)
+    a.v_stride_token, a.v_stride_head = _strides(v, total, kv_heads)
+    if out is None:
+        out = _empty(q.shape, torch.float32 if flags & KVQ_OUT_F32 else torch.float16, device, stream)
+    elif (out.dtype not in (torch.float16, torch.float32) or out.shape != q.shape or out.device != device
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous float16 or float32 tensor of q's shape, on its device")
+    a.flags = (flags & ~KVQ_OUT_F32) | (KVQ_OUT_F32 if out.dtype == torch.float32 else 0)
+    a.out = out.data_ptr()
+    _call_on("kvq_prompt_attention", device, stream, ctypes.byref(a))
+    return out
 
 
 def kvq_beam_workspace_bytes(batch: int, beams: int, vocab: int, n: int) -> int:

@@ -537,6 +537,40 @@ typedef struct {
  * Asynchronous. */
 kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream);
 
+/* Arguments of kvq_prompt_attention; zero-initialise the struct. */
+typedef struct {
+  const void* q;           /* fp16 device: element j of head h of row t at */
+  const void* k;           /*   t * stride_token + h * stride_head + j */
+  const void* v;
+  int64_t q_stride_token;  /* in elements, positive multiples of 8 (where there is more than */
+  int64_t q_stride_head;   /*   one row or head), below 2^32 */
+  int64_t k_stride_token;
+  int64_t k_stride_head;
+  int64_t v_stride_token;
+  int64_t v_stride_head;
+  int32_t num_q_heads;     /* Hq, at most 128 Hkv */
+  int32_t num_kv_heads;    /* Hkv */
+  int32_t head_dim;        /* 32, 64, 128 or 256 */
+  int32_t batch;           /* B */
+  const int32_t* cu_seqlens; /* as for the calls on runs: prompt b is rows */
+  int32_t total;           /*   [cu_seqlens[b], cu_seqlens[b + 1]) of q, k, v and out */
+  int32_t max_len;
+  void* out;               /* device [total][Hq][d], fp16 (fp32 with KVQ_OUT_F32); overlaps no input */
+  uint32_t flags;          /* 0 or KVQ_OUT_F32 */
+  uint32_t* err_word;      /* device, or NULL */
+} kvq_prompt_args;
+
+/* Causal attention over whole prompts in full precision (before the cache is packed):
+ * row i of a prompt attends over its rows 0..i, query head hq over KV head hq / (Hq / Hkv):
+ *   out[i] = sum_j softmax_j(q[i] . k[j] / sqrt(d)) v[j],  j <= i.
+ * Weights are rounded to fp16 once (operands of the tensor cores; weights below 2^-21 of a
+ * row's largest by at most 2^-32 of that), scores and sums are fp32, the output is rounded
+ * once; results do not depend on timing.  Tokens a row does not attend over, other
+ * prompts' among them, have no part in its output, whatever they hold.  Entries of
+ * cu_seqlens that break the rule set KVQ_ERRBIT_BADLEN.  Asynchronous; lengths are read
+ * on the device. */
+kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream);
+
 /* Arguments of kvq_beam_select; zero-initialise the struct. */
 typedef struct {
   const void* logits;      /* device, 16-byte aligned: token t of row r at r * stride_row + t;
@@ -626,7 +660,7 @@ int32_t kvq_version(void); /* 160: two-part weights in the tensor-core MMAs, MMA
  * complete, so nothing is in flight when that CTA gives up: it sets
  * KVQ_ERRBIT_TIMEOUT, contributes nothing to its head's output (which is then
  * wrong for that head) and returns; the call's other results are unaffected.
- * kvq_chunk_attention and kvq_cross_attention give the barriers of their scores an
+ * kvq_chunk_attention, kvq_cross_attention and kvq_prompt_attention give the barriers of their scores an
  * arrival that never comes: every block gives up, with nothing in flight, and the
  * output is wrong.
  * limit_us = 0 (the default) restores normal behaviour.  Process-wide; not for

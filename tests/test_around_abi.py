@@ -50,6 +50,30 @@ def test_rotate_refuses(lib, kw, expect):
     assert lib.kvq_rotate(None, None) == INVALID
 
 
+def _prompt(lib, **kw):
+    base = dict(q=0x100000, k=0x200000, v=0x300000, q_stride_token=4096, q_stride_head=128, k_stride_token=1024,
+                k_stride_head=128, v_stride_token=1024, v_stride_head=128, num_q_heads=32, num_kv_heads=8,
+                head_dim=128, batch=2, cu_seqlens=0x400000, total=10, max_len=5, out=0x500000, flags=0, err_word=0)
+    base.update(kw)
+    return lib.kvq_prompt_attention(ctypes.byref(kvq.PromptArgs(**base)), None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID), (dict(out=0), INVALID),
+    (dict(cu_seqlens=0), INVALID), (dict(batch=0), INVALID), (dict(total=-1), INVALID), (dict(max_len=-1), INVALID),
+    (dict(num_kv_heads=0), INVALID), (dict(num_q_heads=0), INVALID), (dict(num_q_heads=12), INVALID),
+    (dict(num_q_heads=129, num_kv_heads=1), UNSUPPORTED), (dict(head_dim=24), INVALID), (dict(head_dim=96), UNSUPPORTED),
+    (dict(total=(1 << 30) + 1), UNSUPPORTED), (dict(batch=(1 << 24) + 1), UNSUPPORTED), (dict(flags=1), INVALID),
+    (dict(q_stride_token=-8), INVALID), (dict(v_stride_head=-8), INVALID), (dict(k_stride_token=1028), MISALIGNED),
+    (dict(k_stride_head=0), UNSUPPORTED), (dict(v_stride_token=0), UNSUPPORTED), (dict(q_stride_token=1 << 32), UNSUPPORTED),
+    (dict(q=0x100008), MISALIGNED), (dict(v=0x300002), MISALIGNED), (dict(out=0x500008), MISALIGNED),
+    (dict(cu_seqlens=0x400002), MISALIGNED), (dict(err_word=0x600002), MISALIGNED),
+])
+def test_prompt_attention_refuses(lib, kw, expect):
+    assert _prompt(lib, **kw) == expect
+    assert lib.kvq_prompt_attention(None, None) == INVALID
+
+
 def _select(lib, **kw):
     base = dict(logits=0x100000, stride_row=1000, scores=0x200000, finished=0, batch=2, beams=4, vocab=1000, n=8,
                 end_token=0, flags=0, parent=0x300000, token=0x400000, score=0x500000, workspace=0x600000,
