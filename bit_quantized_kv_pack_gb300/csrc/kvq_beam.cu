@@ -4,27 +4,32 @@
 // ones in the order of (w, t).  Within a row the order is that of (x, t), so a row's n
 // largest logits are all that can be selected of it.
 //
-// Pass 1, a block for a piece of a row: the piece stays in registers (kNV 16-byte vectors
+// Pass 1, a block for a piece of a row: the piece stays in registers (NV 16-byte vectors
 // a thread, loaded at once), which gives its maximum M, sum exp(x - M), and its n
-// largest (x, t).  For these a bound comes first: each thread's largest, and the n-th
-// largest of those; all that can be in the result is at or above it, in n threads at
-// most.  With ordinary logits a few more than n values pass, and one warp sorts them.
+// largest (x, t).  For these a bound comes first: of each thread's largest value each warp
+// gives its four largest, and the n-th largest of those is at most the n-th largest of
+// the piece.  With ordinary logits a few dozen values pass; each counts those before it,
+// and that is its place in the result.  Where many pass (equal logits, rows that are
+// masked) the bound is made again with the tokens' order in it.
 // Keys are 64 bits: the logit in an order of whole numbers, then the token, inverted, so
 // that of equal logits the lower token is the larger key.
-// Pass 2, a block for a batch entry: the pieces' sums become the rows' log-normalisers (64
-// bits), a warp merges some pieces of a row, then the warps' lists are merged by the
-// scores in 64 bits.
+// Pass 2, a block for a batch entry: the pieces' sums become the rows' log-normalisers, a
+// warp merges some pieces of a row, the warps of a row theirs, and the rows' lists are merged
+// by the scores (64 bits, in the order of whole numbers too: the chip has few units for
+// doubles, and comparing them as such took 24 us where the merge takes 4).
 //
 // Bound: memory for large batches (the logits are read once), the two launches and the
 // chain of merges for a few rows.
 #include "kvq_around.cuh"
+#include "kvq_ptx.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kJoinThreads = 1024;
-constexpr int kMaxN = 32;  // a list is a lane each
+constexpr int kMaxN = 32;   // a list is a lane each
+constexpr int kFew = 256;   // values that are ranked by counting
 
 struct BeamArgs {
   const void* x;
@@ -179,14 +184,58 @@ __device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, int64_t 
   }
 }
 
+// The block's values with the n largest keys, largest first, in warp 0's lanes: the bound
+// is made of whole keys.  Each thread gives the key that no value of its largest's vector
+// is below; only the n threads that give the largest have values that pass.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads, 2) beam_piece_kernel(const __grid_constant__ BeamArgs a) {
+__device__ __noinline__ uint64_t select_many(const T* row, int64_t first, int V, int n, uint64_t (*lists)[32],
+                                             uint64_t* passed, int* count) {
+  constexpr int E = Vec<T>::E, WARPS = kThreads / 32, kMost = kMaxN * NV * E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint4 v[NV];  // (again: the caller's stay in its registers)
+  load_vecs(v, row, first, V);
+  uint64_t key = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t t0 = first + (int64_t)j * (kThreads * E);
+    if (t0 >= V) break;
+    float mx = Vec<T>::get(v[j], 0);
+#pragma unroll
+    for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[j], e));
+    if (key == 0 || ordered(mx) > (uint32_t)(key >> 32)) key = key_of(mx, (uint32_t)min(t0 + E, (int64_t)V) - 1);
+  }
+  key = merge_warps<WARPS>(sort_down(key), lists);
+  if (warp == 0 && lane == n - 1) lists[0][0] = key;
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  const uint64_t least = lists[0][0];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t t0 = first + (int64_t)j * (kThreads * E);
+    if (t0 >= V) break;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint64_t k = key_of(Vec<T>::get(v[j], e), (uint32_t)(t0 + e));
+      if (t0 + e < V && k >= least) {
+        const int at = atomicAdd(count, 1);
+        if (at < kMost) passed[at] = k;
+      }
+    }
+  }
+  __syncthreads();
+  const int c = min(*count, kMost);
+  uint64_t k = 0;
+  for (int i = warp * 32; i < c; i += kThreads) k = merge_lists(k, sort_down(i + lane < c ? passed[i + lane] : 0));
+  return merge_warps<WARPS>(k, lists);
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int E = Vec<T>::E;
   constexpr int WARPS = kThreads / 32;
-  constexpr int kMost = kMaxN * NV * E;  // values that can pass the bound
   __shared__ uint64_t lists[WARPS][32];
-  __shared__ uint64_t passed[kMost];
-  __shared__ uint64_t bound;
+  __shared__ __align__(16) uint64_t passed[kMaxN * NV * E];  // (at least kFew)
+  __shared__ __align__(16) uint32_t tops[32];
   __shared__ float part[WARPS];
   __shared__ int count;
   wait_for_previous();
@@ -195,57 +244,63 @@ __global__ void __launch_bounds__(kThreads, 2) beam_piece_kernel(const __grid_co
   if (a.finished && a.finished[r]) return;  // (the second pass does not look at such a row)
   const T* row = static_cast<const T*>(a.x) + (int64_t)r * a.stride;
   const int64_t first = (int64_t)piece * (kThreads * NV * E) + tid * E;
+  uint64_t* out = a.keys + ((int64_t)r * a.pieces + piece) * a.n;
 
   uint4 v[NV];
   load_vecs(v, row, first, a.V);
   if (tid == 0) count = 0;
 
-  // the thread's largest, and the key that no value of that vector with it is below
+  // the thread's largest, and the warp's four largest of those
   float best = -INFINITY;
-  uint64_t key = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t t0 = first + (int64_t)j * (kThreads * E);
-    if (t0 >= a.V) break;
-    float mx = Vec<T>::get(v[j], 0);
+    if (first + (int64_t)j * (kThreads * E) >= a.V) break;
 #pragma unroll
-    for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[j], e));
-    if (key == 0 || mx > best) {
-      best = fmaxf(mx, best);
-      key = key_of(best, (uint32_t)min(t0 + E, (int64_t)a.V) - 1);
-    }
+    for (int e = 0; e < E; ++e) best = fmaxf(best, Vec<T>::get(v[j], e));
   }
-  float m = best;
+  uint32_t left = first < a.V ? ordered(best) : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) part[warp] = m;
-  key = merge_warps<WARPS>(sort_down(key), lists);  // (its barriers are part's and count's too)
+  for (int i = 0; i < 32 / WARPS; ++i) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, left);
+    if (lane == 0) tops[warp * (32 / WARPS) + i] = top;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, left == top)) - 1) left = 0;
+  }
+  __syncthreads();
+  // the n-th largest of the 32 (0: there are not so many values), and the largest
+  const uint32_t mine = tops[lane];
+  int above = 0;
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) m = fmaxf(m, part[i]);
-  if (warp == 0 && lane == a.n - 1) bound = key;
+  for (int i = 0; i < 32; i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(tops + i);
+    above += (o.x > mine || (o.x == mine && i < lane)) + (o.y > mine || (o.y == mine && i + 1 < lane)) +
+             (o.z > mine || (o.z == mine && i + 2 < lane)) + (o.w > mine || (o.w == mine && i + 3 < lane));
+  }
+  const uint32_t least = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == a.n - 1)) - 1);
+  const float m = unordered(__reduce_max_sync(0xffffffffu, mine));
 
   // sum exp(x - M): differences first, so that the largest terms' exponents are exact
-  float sum = 0.0f, sum2 = 0.0f;
   const float off = m == -INFINITY ? 0.0f : m;
+  const uint64_t off2 = pack_f32x2(off, off), log2e2 = pack_f32x2(1.4426950408889634f, 1.4426950408889634f);
+  uint64_t sum2 = 0;  // (two zeros)
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (first + (int64_t)j * (kThreads * E) >= a.V) break;
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      sum += exp2f((Vec<T>::get(v[j], e) - off) * 1.4426950408889634f);
-      sum2 += exp2f((Vec<T>::get(v[j], e + 1) - off) * 1.4426950408889634f);
+      const uint64_t x =
+          mul_f32x2(sub_f32x2(pack_f32x2(Vec<T>::get(v[j], e), Vec<T>::get(v[j], e + 1)), off2), log2e2);
+      sum2 = add_f32x2(sum2, pack_f32x2(ptx::ex2_ftz(__uint_as_float(lo_bits(x))),
+                                        ptx::ex2_ftz(__uint_as_float(hi_bits(x)))));
     }
   }
-  sum += sum2;
+  float sum = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncthreads();  // part has been read, bound is there
   if (lane == 0) part[warp] = sum;
 
   // what passes the bound
-  const uint64_t least = bound;
-  const float least_v = unordered((uint32_t)(least >> 32));
-  if (least == 0 || best >= least_v) {
+  const float least_v = least == 0 ? -INFINITY : unordered(least);
+  if (best >= least_v && first < a.V) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t t0 = first + (int64_t)j * (kThreads * E);
@@ -253,40 +308,47 @@ __global__ void __launch_bounds__(kThreads, 2) beam_piece_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float x = Vec<T>::get(v[j], e);
-        if (least != 0 && !(x >= least_v)) continue;
-        const int64_t t = t0 + e;
-        const uint64_t k = key_of(x, (uint32_t)t);
-        if (t < a.V && k >= least) {
+        if (x >= least_v && t0 + e < a.V) {
           const int at = atomicAdd(&count, 1);
-          if (at < kMost) passed[at] = k;
+          if (at < kFew) passed[at] = key_of(x, (uint32_t)(t0 + e));
         }
       }
     }
   }
   __syncthreads();
-  const int c = min(count, kMost);
-  uint64_t k = 0;
-  if (c <= 32) {
-    if (warp == 0) k = sort_down(lane < c ? passed[lane] : 0);
+  const int c = count;
+  if (c <= kFew) {
+    if (tid < max(c, a.n)) {
+      const uint64_t k = tid < c ? passed[tid] : 0;
+      int place = 0;
+      for (int i = 0; i < c; ++i) place += passed[i] > k;
+      if (tid >= c) place = tid;  // (a piece of fewer than n tokens: no token)
+      if (place < a.n) out[place] = k;
+    }
   } else {
-    for (int i = warp * 32; i < c; i += kThreads) k = merge_lists(k, sort_down(i + lane < c ? passed[i + lane] : 0));
-    k = merge_warps<WARPS>(k, lists);
+    const uint64_t k = select_many<T, NV>(row, first, a.V, a.n, lists, passed, &count);
+    if (warp == 0 && lane < a.n) out[lane] = k;
   }
-  const int64_t at = (int64_t)r * a.pieces + piece;
-  if (warp == 0 && lane < a.n) a.keys[at * a.n + lane] = k;
   if (tid == 0) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) s += part[i];
-    a.ms[at] = make_float2(m, s);
+    a.ms[(int64_t)r * a.pieces + piece] = make_float2(m, s);
   }
 }
 
-// A proposal: its score and its place w * V + t, larger in the order of the result.
+// A proposal: its score in an order of whole numbers and its place w * V + t.
 struct Prop {
-  double s;
+  uint64_t s;
   int at;
 };
+__device__ __forceinline__ uint64_t ordered64(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double unordered64(uint64_t o) {
+  return __longlong_as_double((long long)((o >> 63) ? o ^ (1ull << 63) : ~o));
+}
 __device__ __forceinline__ bool before(const Prop& a, const Prop& b) {
   return a.s > b.s || (a.s == b.s && a.at < b.at);
 }
@@ -307,7 +369,8 @@ __device__ __forceinline__ Prop merge_props(const Prop& a, const Prop& b) {
 
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int WARPS = kJoinThreads / 32;
-  __shared__ double list_s[WARPS][32];
+  constexpr int AHEAD = 4;  // lists in flight
+  __shared__ uint64_t lists[WARPS][32];
   __shared__ int list_at[WARPS][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // warp i has row i % W and, of its pieces, every (WARPS / W)-th
@@ -315,62 +378,85 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   const int w = warp % a.W, part = warp / a.W;
   const int64_t r = (int64_t)blockIdx.x * a.W + w;
   wait_for_previous();
-  Prop p = {-INFINITY, 0x7fffffff};
-  if (part < per) {
-    const float base = __ldg(a.scores + r);
-    const bool done = a.finished && __ldg(a.finished + r);
-    // the row's normaliser
+  const float base = __ldg(a.scores + r);
+  const bool done = a.finished && __ldg(a.finished + r);
+  const float2 none = make_float2(-INFINITY, 0.0f);
+  const float2 sums = part == 0 && !done && lane < a.pieces ? __ldcg(a.ms + r * a.pieces + lane) : none;
+
+  uint64_t k = 0;
+  if (part < per && !done && base > -INFINITY && base < INFINITY) {
+    const uint64_t* src = a.keys + r * a.pieces * a.n + lane;
+    for (int i = part; i < a.pieces; i += per * AHEAD) {
+      uint64_t x[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int at = i + u * per;
+        x[u] = at < a.pieces && lane < a.n ? __ldcg(src + (int64_t)at * a.n) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (__shfl_sync(0xffffffffu, x[u], 0) > __shfl_sync(0xffffffffu, k, a.n - 1)) k = merge_lists(k, x[u]);
+    }
+  }
+  // the row's pieces: of all its warps
+  for (int o = 16; o > 0; o >>= 1) {
+    if (part >= o && part < min(2 * o, per)) lists[warp][lane] = k;
+    if (o < per) __syncthreads();
+    if (part + o < per && part < o) k = merge_lists(k, lists[warp + o * a.W][lane]);
+  }
+
+  Prop p = {0, 0x7fffffff};  // (before nothing)
+  if (part == 0) {
     double norm = 0.0;
     bool bad = !(base < INFINITY);  // +inf or NaN
     if (!done) {
-      float m = -INFINITY;
-      for (int i = lane; i < a.pieces; i += 32) m = fmaxf(m, __ldcg(a.ms + r * a.pieces + i).x);
+      float m = sums.x;
+      for (int i = lane + 32; i < a.pieces; i += 32) m = fmaxf(m, __ldcg(a.ms + r * a.pieces + i).x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double s = 0.0;
+      float s = 0.0f;
       for (int i = lane; i < a.pieces; i += 32) {
-        const float2 x = __ldcg(a.ms + r * a.pieces + i);
+        const float2 x = i == lane ? sums : __ldcg(a.ms + r * a.pieces + i);
         // a piece without a maximum has a sum of 0, or NaN
-        s += x.x == -INFINITY ? (double)x.y : (double)x.y * exp((double)x.x - (double)m);
+        s += x.x == -INFINITY ? x.y : x.y * ptx::ex2_ftz((x.x - m) * 1.4426950408889634f);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       bad = bad || !(m < INFINITY) || s != s;
-      norm = (double)m + log(s);
+      // log s: the exponent apart, so that the rest is rounded near zero
+      int e = 0;
+      const float f = frexpf(s, &e);
+      norm = s > 0.0f ? (double)m + ((double)e * 0.69314718055994530942 + (double)logf(f)) : -INFINITY;
     }
-    if (bad && part == 0 && lane == 0) set_error(a.err_word, KVQ_ERRBIT_BADSCORE);
+    if (bad && lane == 0) set_error(a.err_word, KVQ_ERRBIT_BADSCORE);
+    double score = -INFINITY;
     if (bad || done || base == -INFINITY || norm == -INFINITY) {
       // proposes its end alone, or nothing: the row's first tokens follow at -inf
-      if (part == 0 && lane < min(a.n, a.V)) {
+      if (lane < min(a.n, a.V)) {
         const bool ends = done && !bad;
         const int t = !ends ? lane : lane == 0 ? a.end : lane - (lane <= a.end);
-        p.s = ends && lane == 0 ? (double)base : -INFINITY;
+        if (ends && lane == 0) score = (double)base;
         p.at = w * a.V + t;
       }
-    } else {
-      uint64_t k = 0;
-      for (int i = part; i < a.pieces; i += per) {
-        const uint64_t x = lane < a.n ? __ldcg(a.keys + (r * a.pieces + i) * a.n + lane) : 0;
-        if (__shfl_sync(0xffffffffu, x, 0) > __shfl_sync(0xffffffffu, k, a.n - 1)) k = merge_lists(k, x);
-      }
-      if (k != 0) {
-        p.s = (double)base + ((double)unordered((uint32_t)(k >> 32)) - norm);
-        p.at = w * a.V + (int)~(uint32_t)k;
-      }
+    } else if (k != 0) {
+      score = (double)base + ((double)unordered((uint32_t)(k >> 32)) - norm);
+      p.at = w * a.V + (int)~(uint32_t)k;
     }
+    if (p.at != 0x7fffffff) p.s = ordered64(score);
   }
-#pragma unroll
-  for (int o = WARPS / 2; o > 0; o >>= 1) {
-    if (warp >= o && warp < 2 * o) list_s[warp][lane] = p.s, list_at[warp][lane] = p.at;
+  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= a.W) continue;
+    if (part == 0 && w >= o && w < 2 * o) lists[w][lane] = p.s, list_at[w][lane] = p.at;
     __syncthreads();
-    if (warp < o) p = merge_props(p, {list_s[warp + o][lane], list_at[warp + o][lane]});
+    if (part == 0 && w < o && w + o < a.W) p = merge_props(p, {lists[w + o][lane], list_at[w + o][lane]});
   }
   if (warp == 0 && lane < a.n) {
     const int64_t at = (int64_t)blockIdx.x * a.n + lane;
     const int beam = p.at / a.V;
     a.parent[at] = blockIdx.x * a.W + beam;
     a.token[at] = p.at - beam * a.V;
-    a.score[at] = (float)p.s;
+    a.score[at] = (float)unordered64(p.s);
   }
 }
 
