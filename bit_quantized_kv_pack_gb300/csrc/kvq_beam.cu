@@ -14,9 +14,9 @@
 // Keys are 64 bits: the logit in an order of whole numbers, then the token, inverted, so
 // that of equal logits the lower token is the larger key.
 // Pass 2, a block for a batch entry: the pieces' sums become the rows' log-normalisers, a
-// warp merges some pieces of a row, the warps of a row theirs, and the rows' lists are merged
-// by the scores (64 bits, in the order of whole numbers too: the chip has few units for
-// doubles, and comparing them as such took 24 us where the merge takes 4).
+// warp merges some pieces of a row, and each lane works out its entry's score.  A bound that
+// n scores and not many more are at or above is found bit by bit (a barrier that counts for
+// each), and those count what is before them.
 //
 // Bound: memory for large batches (the logits are read once), the two launches and the
 // chain of merges for a few rows.
@@ -122,7 +122,7 @@ struct Vec<float> {
 
 // Tokens t0 .. of a row as a vector; places outside the row hold -inf.
 template <typename T>
-__device__ __forceinline__ uint4 load_edge(const T* row, int64_t t0, int V) {
+__device__ __forceinline__ uint4 load_edge(const T* row, uint32_t t0, uint32_t V) {
   constexpr int E = Vec<T>::E;
   uint32_t b[E];
 #pragma unroll
@@ -150,17 +150,17 @@ __device__ __forceinline__ uint4 from_two(const uint4& a, const uint4& b, int by
 // the last bit, and their tokens stay equal.  Rows that do not start on 16 bytes (odd
 // vocabularies) read two neighbouring vectors for each, four at a time.
 template <typename T, int NV>
-__device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, int64_t t0, int V) {
-  constexpr int E = Vec<T>::E, STEP = kThreads * E;
+__device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, uint32_t t0, uint32_t V) {
+  constexpr uint32_t E = Vec<T>::E, STEP = kThreads * E;
   const int skip = (int)((uintptr_t)row & 15);
   if (skip == 0) {
+    const uint4* src = reinterpret_cast<const uint4*>(row + t0);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t t = t0 + j * STEP;
-      v[j] = make_uint4(0, 0, 0, 0);
+      const uint32_t t = t0 + j * STEP;
       if (t + E <= V)
-        v[j] = __ldg(reinterpret_cast<const uint4*>(row + t));
-      else if (t < V)
+        v[j] = __ldg(src + j * kThreads);
+      else
         v[j] = load_edge(row, t, V);
     }
     return;
@@ -171,15 +171,15 @@ __device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, int64_t 
     uint4 a[4], b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const bool in = t0 + (g + u) * STEP + 2 * E <= V;  // both vectors end in the row
+      const bool in = t0 + (uint32_t)(g + u) * STEP + 2 * E <= V;  // both vectors end in the row
       a[u] = b[u] = make_uint4(0, 0, 0, 0);
       if (in) a[u] = __ldg(src + (g + u) * kThreads), b[u] = __ldg(src + (g + u) * kThreads + 1);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t t = t0 + (g + u) * STEP;
+      const uint32_t t = t0 + (uint32_t)(g + u) * STEP;
       v[g + u] = from_two(a[u], b[u], skip);
-      if (t + 2 * E > V && t < V) v[g + u] = load_edge(row, t, V);
+      if (t + 2 * E > V) v[g + u] = load_edge(row, t, V);
     }
   }
 }
@@ -188,21 +188,21 @@ __device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, int64_t 
 // is made of whole keys.  Each thread gives the key that no value of its largest's vector
 // is below; only the n threads that give the largest have values that pass.
 template <typename T, int NV>
-__device__ __noinline__ uint64_t select_many(const T* row, int64_t first, int V, int n, uint64_t (*lists)[32],
+__device__ __noinline__ uint64_t select_many(const T* row, uint32_t first, uint32_t V, int n, uint64_t (*lists)[32],
                                              uint64_t* passed, int* count) {
-  constexpr int E = Vec<T>::E, WARPS = kThreads / 32, kMost = kMaxN * NV * E;
+  constexpr uint32_t E = Vec<T>::E, WARPS = kThreads / 32, kMost = kMaxN * NV * E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint4 v[NV];  // (again: the caller's stay in its registers)
   load_vecs(v, row, first, V);
   uint64_t key = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t t0 = first + (int64_t)j * (kThreads * E);
+    const uint32_t t0 = first + j * (kThreads * E);
     if (t0 >= V) break;
     float mx = Vec<T>::get(v[j], 0);
 #pragma unroll
     for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[j], e));
-    if (key == 0 || ordered(mx) > (uint32_t)(key >> 32)) key = key_of(mx, (uint32_t)min(t0 + E, (int64_t)V) - 1);
+    if (key == 0 || ordered(mx) > (uint32_t)(key >> 32)) key = key_of(mx, min(t0 + E, V) - 1);
   }
   key = merge_warps<WARPS>(sort_down(key), lists);
   if (warp == 0 && lane == n - 1) lists[0][0] = key;
@@ -211,19 +211,19 @@ __device__ __noinline__ uint64_t select_many(const T* row, int64_t first, int V,
   const uint64_t least = lists[0][0];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t t0 = first + (int64_t)j * (kThreads * E);
+    const uint32_t t0 = first + j * (kThreads * E);
     if (t0 >= V) break;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint64_t k = key_of(Vec<T>::get(v[j], e), (uint32_t)(t0 + e));
+      const uint64_t k = key_of(Vec<T>::get(v[j], e), t0 + e);
       if (t0 + e < V && k >= least) {
-        const int at = atomicAdd(count, 1);
+        const uint32_t at = atomicAdd(count, 1);
         if (at < kMost) passed[at] = k;
       }
     }
   }
   __syncthreads();
-  const int c = min(*count, kMost);
+  const int c = min(*count, (int)kMost);
   uint64_t k = 0;
   for (int i = warp * 32; i < c; i += kThreads) k = merge_lists(k, sort_down(i + lane < c ? passed[i + lane] : 0));
   return merge_warps<WARPS>(k, lists);
@@ -231,11 +231,12 @@ __device__ __noinline__ uint64_t select_many(const T* row, int64_t first, int V,
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_constant__ BeamArgs a) {
-  constexpr int E = Vec<T>::E;
-  constexpr int WARPS = kThreads / 32;
+  constexpr uint32_t E = Vec<T>::E;
+  constexpr int WARPS = kThreads / 32, TOPS = 32 / WARPS;
   __shared__ uint64_t lists[WARPS][32];
   __shared__ __align__(16) uint64_t passed[kMaxN * NV * E];  // (at least kFew)
   __shared__ __align__(16) uint32_t tops[32];
+  __shared__ uint32_t top[WARPS];
   __shared__ float part[WARPS];
   __shared__ int count;
   wait_for_previous();
@@ -243,27 +244,29 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
   const int piece = blockIdx.x, r = blockIdx.y;
   if (a.finished && a.finished[r]) return;  // (the second pass does not look at such a row)
   const T* row = static_cast<const T*>(a.x) + (int64_t)r * a.stride;
-  const int64_t first = (int64_t)piece * (kThreads * NV * E) + tid * E;
+  const uint32_t first = (uint32_t)piece * (kThreads * NV * E) + tid * E, V = a.V;
   uint64_t* out = a.keys + ((int64_t)r * a.pieces + piece) * a.n;
 
-  uint4 v[NV];
-  load_vecs(v, row, first, a.V);
+  uint4 v[NV];  // (places outside the row hold -inf)
+  load_vecs(v, row, first, V);
   if (tid == 0) count = 0;
 
-  // the thread's largest, and the warp's four largest of those
+  // the thread's largest, and the warp's four largest of those.  Their last five bits are a
+  // number of their own, so that no two are equal: the bound is made of the others
   float best = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (first + (int64_t)j * (kThreads * E) >= a.V) break;
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) best = fmaxf(best, Vec<T>::get(v[j], e));
-  }
-  uint32_t left = first < a.V ? ordered(best) : 0;
+  uint32_t left = first < V ? ordered(best) : 0;
 #pragma unroll
-  for (int i = 0; i < 32 / WARPS; ++i) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, left);
-    if (lane == 0) tops[warp * (32 / WARPS) + i] = top;
-    if (lane == __ffs(__ballot_sync(0xffffffffu, left == top)) - 1) left = 0;
+  for (int i = 0; i < TOPS; ++i) {
+    const uint32_t x = __reduce_max_sync(0xffffffffu, left);
+    if (lane == 0) {
+      tops[warp * TOPS + i] = (x & ~31u) | (warp * TOPS + i);
+      if (i == 0) top[warp] = x;
+    }
+    if (lane == __ffs(__ballot_sync(0xffffffffu, left == x)) - 1) left = 0;
   }
   __syncthreads();
   // the n-th largest of the 32 (0: there are not so many values), and the largest
@@ -272,19 +275,18 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const uint4 o = *reinterpret_cast<const uint4*>(tops + i);
-    above += (o.x > mine || (o.x == mine && i < lane)) + (o.y > mine || (o.y == mine && i + 1 < lane)) +
-             (o.z > mine || (o.z == mine && i + 2 < lane)) + (o.w > mine || (o.w == mine && i + 3 < lane));
+    above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
   }
-  const uint32_t least = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == a.n - 1)) - 1);
-  const float m = unordered(__reduce_max_sync(0xffffffffu, mine));
+  const uint32_t least =
+      __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == a.n - 1)) - 1) & ~31u;
+  const float m = unordered(__reduce_max_sync(0xffffffffu, top[lane % WARPS]));
 
   // sum exp(x - M): differences first, so that the largest terms' exponents are exact
   const float off = m == -INFINITY ? 0.0f : m;
   const uint64_t off2 = pack_f32x2(off, off), log2e2 = pack_f32x2(1.4426950408889634f, 1.4426950408889634f);
   uint64_t sum2 = 0;  // (two zeros)
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (first + (int64_t)j * (kThreads * E) >= a.V) break;
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const uint64_t x =
@@ -292,26 +294,30 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
       sum2 = add_f32x2(sum2, pack_f32x2(ptx::ex2_ftz(__uint_as_float(lo_bits(x))),
                                         ptx::ex2_ftz(__uint_as_float(hi_bits(x)))));
     }
-  }
   float sum = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) part[warp] = sum;
 
-  // what passes the bound
-  const float least_v = least == 0 ? -INFINITY : unordered(least);
-  if (best >= least_v && first < a.V) {
+  // what passes the bound: vectors first, whose values are then read again
+  const float least_v = least < 0x00800000u ? -INFINITY : unordered(least);  // (below the lowest finite one)
+  uint32_t vecs = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t t0 = first + (int64_t)j * (kThreads * E);
-      if (t0 >= a.V) break;
+  for (int j = 0; j < NV; ++j) {
+    float mx = Vec<T>::get(v[j], 0);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float x = Vec<T>::get(v[j], e);
-        if (x >= least_v && t0 + e < a.V) {
-          const int at = atomicAdd(&count, 1);
-          if (at < kFew) passed[at] = key_of(x, (uint32_t)(t0 + e));
-        }
+    for (int e = 1; e < E; ++e) mx = fmaxf(mx, Vec<T>::get(v[j], e));
+    vecs |= mx >= least_v ? 1u << j : 0u;
+  }
+  while (vecs) {
+    const uint32_t t0 = first + (__ffs(vecs) - 1) * (kThreads * E);
+    vecs &= vecs - 1;
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const float x = t0 + e < V ? (float)row[t0 + e] : -INFINITY;
+      if (x >= least_v && t0 + e < V) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kFew) passed[at] = key_of(x, t0 + e);
       }
     }
   }
@@ -321,12 +327,13 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
     if (tid < max(c, a.n)) {
       const uint64_t k = tid < c ? passed[tid] : 0;
       int place = 0;
+#pragma unroll 4
       for (int i = 0; i < c; ++i) place += passed[i] > k;
       if (tid >= c) place = tid;  // (a piece of fewer than n tokens: no token)
       if (place < a.n) out[place] = k;
     }
   } else {
-    const uint64_t k = select_many<T, NV>(row, first, a.V, a.n, lists, passed, &count);
+    const uint64_t k = select_many<T, NV>(row, first, V, a.n, lists, passed, &count);
     if (warp == 0 && lane < a.n) out[lane] = k;
   }
   if (tid == 0) {
@@ -337,54 +344,59 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
   }
 }
 
-// A proposal: its score in an order of whole numbers and its place w * V + t.
-struct Prop {
-  uint64_t s;
-  int at;
+// Scores are two fp32 parts, hi + lo with |lo| at most half a step of hi (the chip has few
+// units for doubles).  The sum of two numbers so:
+struct Two {
+  float hi, lo;
 };
-__device__ __forceinline__ uint64_t ordered64(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double unordered64(uint64_t o) {
-  return __longlong_as_double((long long)((o >> 63) ? o ^ (1ull << 63) : ~o));
-}
-__device__ __forceinline__ bool before(const Prop& a, const Prop& b) {
-  return a.s > b.s || (a.s == b.s && a.at < b.at);
-}
-__device__ __forceinline__ Prop shfl(const Prop& p, int src) {
-  return {__shfl_sync(0xffffffffu, p.s, src), __shfl_sync(0xffffffffu, p.at, src)};
-}
-__device__ __forceinline__ Prop merge_props(const Prop& a, const Prop& b) {
-  const int lane = threadIdx.x & 31;
-  const Prop r = shfl(b, 31 - lane);
-  Prop p = before(a, r) ? a : r;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Prop q = shfl(p, lane ^ o);
-    if (before(p, q) == ((lane & o) != 0)) p = q;
+// ... of 53 bits, as a double has: what lies below is not told apart (tokens masked by the
+// type's lowest value come in order, whatever their beams' scores)
+__device__ __forceinline__ Two of_53_bits(Two v) {
+  const int e = (int)(__float_as_uint(v.hi) & 0x7f800000u) - (29 << 23);
+  if (e > 0) {
+    const float c = 1.5f * __int_as_float(e);
+    v.lo = __fsub_rn(__fadd_rn(v.lo, c), c);
   }
-  return p;
+  return v;
+}
+__device__ __forceinline__ uint64_t ordered(const Two& v) { return (uint64_t)ordered(v.hi) << 32 | ordered(v.lo); }
+
+// m + log s, 0 < s.  The exponent of s apart, so that the logarithm is rounded near zero.
+__device__ __forceinline__ Two log_norm(float m, float s) {
+  int e = 0;
+  const float f = frexpf(s, &e);
+  // log 2 as a part of few bits, whose product with e is exact, and the rest (Cody, Waite)
+  const float hi = 0.693359375f, lo = -2.12194440e-4f;
+  const Two a = two_sum(m, __fmul_rn((float)e, hi));
+  const Two b = two_sum(a.hi, __fadd_rn(logf(f), __fmul_rn((float)e, lo)));
+  return two_sum(b.hi, __fadd_rn(a.lo, b.lo));
 }
 
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ BeamArgs a) {
   constexpr int WARPS = kJoinThreads / 32;
-  constexpr int AHEAD = 4;  // lists in flight
-  __shared__ uint64_t lists[WARPS][32];
-  __shared__ int list_at[WARPS][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int AHEAD = 4;     // lists in flight
+  constexpr int kEnough = 64;  // entries that are ranked by counting
+  __shared__ __align__(16) uint64_t passed[kJoinThreads];
+  __shared__ __align__(16) int passed_at[kJoinThreads];
+  __shared__ int count;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // warp i has row i % W and, of its pieces, every (WARPS / W)-th
   const int per = WARPS / a.W;
   const int w = warp % a.W, part = warp / a.W;
   const int64_t r = (int64_t)blockIdx.x * a.W + w;
+  if (tid == 0) count = 0;
   wait_for_previous();
   const float base = __ldg(a.scores + r);
   const bool done = a.finished && __ldg(a.finished + r);
-  const float2 none = make_float2(-INFINITY, 0.0f);
-  const float2 sums = part == 0 && !done && lane < a.pieces ? __ldcg(a.ms + r * a.pieces + lane) : none;
+  const bool read = part < per && !done;
+  const float2 sums = read && lane < a.pieces ? __ldcg(a.ms + r * a.pieces + lane) : make_float2(-INFINITY, 0.0f);
 
   uint64_t k = 0;
-  if (part < per && !done && base > -INFINITY && base < INFINITY) {
+  if (read && base > -INFINITY && base < INFINITY) {
     const uint64_t* src = a.keys + r * a.pieces * a.n + lane;
     for (int i = part; i < a.pieces; i += per * AHEAD) {
       uint64_t x[AHEAD];
@@ -393,70 +405,85 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
         const int at = i + u * per;
         x[u] = at < a.pieces && lane < a.n ? __ldcg(src + (int64_t)at * a.n) : 0;
       }
+      if (i == part) k = x[0];
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
-        if (__shfl_sync(0xffffffffu, x[u], 0) > __shfl_sync(0xffffffffu, k, a.n - 1)) k = merge_lists(k, x[u]);
+        if ((u > 0 || i > part) && __shfl_sync(0xffffffffu, x[u], 0) > __shfl_sync(0xffffffffu, k, a.n - 1))
+          k = merge_lists(k, x[u]);
     }
-  }
-  // the row's pieces: of all its warps
-  for (int o = 16; o > 0; o >>= 1) {
-    if (part >= o && part < min(2 * o, per)) lists[warp][lane] = k;
-    if (o < per) __syncthreads();
-    if (part + o < per && part < o) k = merge_lists(k, lists[warp + o * a.W][lane]);
   }
 
-  Prop p = {0, 0x7fffffff};  // (before nothing)
-  if (part == 0) {
-    double norm = 0.0;
-    bool bad = !(base < INFINITY);  // +inf or NaN
-    if (!done) {
-      float m = sums.x;
-      for (int i = lane + 32; i < a.pieces; i += 32) m = fmaxf(m, __ldcg(a.ms + r * a.pieces + i).x);
+  // the row's normaliser
+  Two norm = {0.0f, 0.0f};
+  bool bad = !(base < INFINITY);  // +inf or NaN
+  if (read) {
+    float m = sums.x;
+    for (int i = lane + 32; i < a.pieces; i += 32) m = fmaxf(m, __ldcg(a.ms + r * a.pieces + i).x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float s = 0.0f;
-      for (int i = lane; i < a.pieces; i += 32) {
-        const float2 x = i == lane ? sums : __ldcg(a.ms + r * a.pieces + i);
-        // a piece without a maximum has a sum of 0, or NaN
-        s += x.x == -INFINITY ? x.y : x.y * ptx::ex2_ftz((x.x - m) * 1.4426950408889634f);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      bad = bad || !(m < INFINITY) || s != s;
-      // log s: the exponent apart, so that the rest is rounded near zero
-      int e = 0;
-      const float f = frexpf(s, &e);
-      norm = s > 0.0f ? (double)m + ((double)e * 0.69314718055994530942 + (double)logf(f)) : -INFINITY;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = 0.0f;
+    for (int i = lane; i < a.pieces; i += 32) {
+      const float2 x = i == lane ? sums : __ldcg(a.ms + r * a.pieces + i);
+      // a piece without a maximum has a sum of 0, or NaN
+      s += x.x == -INFINITY ? x.y : x.y * ptx::ex2_ftz((x.x - m) * 1.4426950408889634f);
     }
-    if (bad && lane == 0) set_error(a.err_word, KVQ_ERRBIT_BADSCORE);
-    double score = -INFINITY;
-    if (bad || done || base == -INFINITY || norm == -INFINITY) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    bad = bad || !(m < INFINITY) || s != s;
+    norm.hi = -INFINITY;
+    if (s > 0.0f) norm = log_norm(m, s);
+  }
+  if (bad && part == 0 && lane == 0) set_error(a.err_word, KVQ_ERRBIT_BADSCORE);
+
+  // the lane's proposal
+  const uint64_t silent = ordered(Two{-INFINITY, 0.0f});
+  uint64_t score = 0;  // none, behind all others
+  int at = 0x7fffffff;
+  if (part < per) {
+    if (bad || done || base == -INFINITY || norm.hi == -INFINITY) {
       // proposes its end alone, or nothing: the row's first tokens follow at -inf
-      if (lane < min(a.n, a.V)) {
+      if (part == 0 && lane < min(a.n, a.V)) {
         const bool ends = done && !bad;
-        const int t = !ends ? lane : lane == 0 ? a.end : lane - (lane <= a.end);
-        if (ends && lane == 0) score = (double)base;
-        p.at = w * a.V + t;
+        score = ends && lane == 0 && base > -INFINITY ? ordered(Two{base, 0.0f}) : silent;
+        at = w * a.V + (!ends ? lane : lane == 0 ? a.end : lane - (lane <= a.end));
       }
     } else if (k != 0) {
-      score = (double)base + ((double)unordered((uint32_t)(k >> 32)) - norm);
-      p.at = w * a.V + (int)~(uint32_t)k;
+      const float x = unordered((uint32_t)(k >> 32));
+      const Two d = two_sum(x, -norm.hi);
+      const Two b = two_sum(base, d.hi);
+      // (below fp32's range: -inf)
+      score = x == -INFINITY || !(b.hi > -INFINITY) ? silent : ordered(of_53_bits(two_sum(b.hi, b.lo + (d.lo - norm.lo))));
+      at = w * a.V + (int)~(uint32_t)k;
     }
-    if (p.at != 0x7fffffff) p.s = ordered64(score);
+  }
+  // the scores' upper half that n entries, and few more, are not below, bit by bit
+  const uint32_t top = (uint32_t)(score >> 32);
+  uint32_t least = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const int c = __syncthreads_count(top >= (least | 1u << bit));
+    if (c >= a.n) least |= 1u << bit;
+    if (c >= a.n && c <= kEnough) break;
+  }
+  if (top >= least && score != 0) {
+    const int i = atomicAdd(&count, 1);
+    passed[i] = score;
+    passed_at[i] = at;
   }
   __syncthreads();
-  for (int o = 16; o > 0; o >>= 1) {
-    if (o >= a.W) continue;
-    if (part == 0 && w >= o && w < 2 * o) lists[w][lane] = p.s, list_at[w][lane] = p.at;
-    __syncthreads();
-    if (part == 0 && w < o && w + o < a.W) p = merge_props(p, {lists[w + o][lane], list_at[w + o][lane]});
-  }
-  if (warp == 0 && lane < a.n) {
-    const int64_t at = (int64_t)blockIdx.x * a.n + lane;
-    const int beam = p.at / a.V;
-    a.parent[at] = blockIdx.x * a.W + beam;
-    a.token[at] = p.at - beam * a.V;
-    a.score[at] = (float)unordered64(p.s);
+  const int c = count;
+  if (tid < c) {
+    const uint64_t s = passed[tid];
+    const int mine = passed_at[tid];
+    int place = 0;
+#pragma unroll 4
+    for (int i = 0; i < c; ++i) place += passed[i] > s || (passed[i] == s && passed_at[i] < mine);
+    if (place < a.n) {
+      const int64_t to = (int64_t)blockIdx.x * a.n + place;
+      const int beam = mine / a.V;
+      a.parent[to] = blockIdx.x * a.W + beam;
+      a.token[to] = mine - beam * a.V;
+      a.score[to] = unordered((uint32_t)(s >> 32));
+    }
   }
 }
 

@@ -608,8 +608,9 @@ size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int
  * A beam with a NaN or +inf among its logits, or as its score, proposes nothing and sets
  * KVQ_ERRBIT_BADSCORE (a complete beam's logits are not looked at).
  * The sums of exponentials are fp32 (within 2^-20 of the whole), their logarithms and the
- * scores that are compared 64-bit; scores are rounded to fp32 once.  Results do not depend
- * on timing.  Asynchronous. */
+ * scores that are compared have 53 bits; scores are rounded to fp32 once, and one
+ * below fp32's range is -inf.  Beams of equal logits and scores have equal scores to the
+ * last bit; results do not depend on timing.  Asynchronous. */
 kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream);
 
 /* Copy sequences from one cache to another: sequence i of `dst` becomes sequence index[i]
