@@ -73,11 +73,11 @@ cudaError_t launch_prompt_attention(const kvq_prompt_args& A, cudaStream_t st) {
   a.wait_limit_us = fault_us ? fault_us : 1000000u;
   a.fault = fault_us ? 1 : 0;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d));
-  // one block per SM, and no more than there can be units
+  // as many blocks as there can be units
   const int64_t tokens = (int64_t)prompt_lanes(d) * a.T;
-  const int64_t units = (A.total / tokens + A.batch) * heads;
-  const int sms = device_sm_count();
-  const int grid = (int)(units < sms ? units : sms);
+  const int64_t units = (A.total / tokens + A.batch) * (int64_t)heads;
+  if (units > 2147483647) return cudaErrorInvalidValue;
+  const int grid = (int)units;
   if (d == 32) return launch_prompt_attn_d32(a, grid, st);
   if (d == 64) return launch_prompt_attn_d64(a, grid, st);
   if (d == 128) return launch_prompt_attn_d128(a, grid, st);

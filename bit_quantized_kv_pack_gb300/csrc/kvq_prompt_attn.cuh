@@ -23,8 +23,11 @@
 // head_dim 256 has room for one lane and tiles of 64 tokens.
 //
 // A unit of work is (sequence, KV head, block of 2 T tokens).  Units lie in one line,
-// sequence after sequence, the longest first within each; blocks take them in turn, back and
-// forth, which evens out the lengths that fall along the line.
+// sequence after sequence, the longest first within each.  The grid has a block for each;
+// those that run take over the next of those that do not yet (cluster launch control), when
+// they load the last tiles of the unit before, so that the loads go on from unit to unit
+// and SMs are done at about the same time (units dealt out in turn made 16 prompts of
+// 17 to 2048 tokens 10 % slower and 8 of 100 to 1500 at head_dim 64 26 %).
 #pragma once
 
 #include <cuda.h>
@@ -65,7 +68,6 @@ namespace prompt {
 
 constexpr int kThreads = 384;
 constexpr float kWeightBits = 7.0f;  // log2 of the weights' factor
-constexpr int kUnits = 4;            // ring of units
 constexpr int kMaxStages = 8;
 
 template <int D>
@@ -90,9 +92,9 @@ struct Cfg {
   static constexpr int OFF_KV = OFF_Q + LANES * QBYTES;
   static constexpr int OFF_NOTES = OFF_KV + ST * KBYTES;  // int [3][D]
   static constexpr int OFF_BAR = OFF_NOTES + 3 * D * 4;
-  static constexpr int OFF_UNIT = OFF_BAR + 512;
+  static constexpr int OFF_UNIT = OFF_BAR + 512;  // Unit, and the answer of the launch control
   // (more than half an SM's, so that a block has the tensor memory to itself)
-  static constexpr int SMEM = OFF_UNIT + kUnits * 32 > 117 * 1024 ? OFF_UNIT + kUnits * 32 : 117 * 1024;
+  static constexpr int SMEM = OFF_UNIT + 48 > 117 * 1024 ? OFF_UNIT + 48 : 117 * 1024;
 };
 
 // Sequence rows [c0, c0 + n), KV head h, first token t0 of the block; tiles of each lane
@@ -103,9 +105,8 @@ struct alignas(16) Unit {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 6, B_ODONE = 8, B_DRAIN = 10, B_UFULL = 11,
-       B_UEMPTY = B_UFULL + kUnits, B_KVFULL = B_UEMPTY + kUnits, B_KVEMPTY = B_KVFULL + kMaxStages,
-       B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
+enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 6, B_ODONE = 8, B_DRAIN = 10, B_UFULL = 11, B_UEMPTY = 12,
+       B_NEXT = 13, B_KVFULL = 14, B_KVEMPTY = B_KVFULL + kMaxStages, B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
 enum { W_TMEM = 96, W_ABORT = 97, W_NOTED = 98 /* the unit that the notes are of */, W_EPI = 99 };
 static_assert(B_COUNT * 2 <= W_TMEM, "words behind the barriers");
 
@@ -186,40 +187,61 @@ struct Waits {
   }
 };
 
-// A role's place in the ring of units (all of a warp).
+// A role's place in the line of units (all of a warp).
 struct UnitReader {
   const Waits& wt;
-  const Unit* ring;
+  const Unit* unit;
   uint32_t i = 0;
   // the next unit; no == 0 at the end of the line or when a wait gave up
   __device__ __forceinline__ Unit next() {
     Unit u;
     u.no = 0;
-    if (wt.wait_warp(B_UFULL + i % kUnits, (i / kUnits) & 1)) u = ring[i % kUnits];
+    if (wt.wait_warp(B_UFULL, i & 1)) u = *unit;
+    ++i;
     return u;
   }
-  __device__ __forceinline__ void release() {
-    wt.arrive_warp(B_UEMPTY + i % kUnits);
-    ++i;
-  }
+  __device__ __forceinline__ void release() { wt.arrive_warp(B_UEMPTY); }
 };
 
 // -------------------------------------------------------------------- units ---
 
-// The warp that works out the units: a window of 32 sequences goes along the line.
+// Asks for a block of the grid that has not begun; the answer goes to `to` (16 bytes),
+// which counts on `bar`.  One thread.
+__device__ __forceinline__ void ask_next(uint32_t to, uint32_t bar) {
+  ptx::mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+      "r"(bar)
+      : "memory");
+}
+// The answer: that block's index, which is the asker's now, or -1 (all have begun).
+__device__ __forceinline__ int next_block(uint32_t at) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+      : "=r"(ok), "=r"(x)
+      : "r"(at)
+      : "memory");
+  // (read before the next answer is written)
+  ptx::fence_proxy_async_shared();
+  return ok ? (int)x : -1;
+}
+
+// The warp that works out the units: a window of 32 sequences goes along the line (the
+// blocks that it gets come in rising order).
 template <int D>
-__device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, Unit* ring) {
+__device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, Unit* unit) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   const int step = C::LANES * a.T;  // tokens of a unit
-  const int G = gridDim.x;
   int b0 = 0;
   int64_t base = 0, scan = 0;  // units before the window; of its sequences up to the lane's
   Run run = {0, 0};
   auto window = [&] {
     run.n = 0;
     if (b0 + lane < a.B) run = run_of(a.cu, b0 + lane, a.total, a.max_len);
-    if (run.n < 0 && blockIdx.x == 0) set_error(a.err_word, KVQ_ERRBIT_BADLEN);
     scan = run.n > 0 ? (int64_t)((run.n + step - 1) / step) * a.Hkv : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -228,17 +250,38 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
     }
   };
   window();
+  const uint32_t answer = smem + C::OFF_UNIT + sizeof(Unit);
+  int u = blockIdx.x;
+  bool own = true;
+  uint32_t asked = 0;
   for (uint32_t i = 0;; ++i) {
-    const int64_t u = (int64_t)i * G + (i & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    while (b0 < a.B) {
-      const int64_t all = __shfl_sync(0xffffffffu, scan, 31);
-      if (u < base + all) break;
-      base += all;
-      b0 += 32;
-      window();
+    // the roles have the last unit, and the loads of it are on their way
+    if (i > 0 && !wt.wait_warp(B_UEMPTY, (i - 1) & 1)) return;
+    while (true) {
+      if (!own) {
+        if (lane == 0) ask_next(answer, wt.bar(B_NEXT));
+        __syncwarp();
+        if (!wt.wait_warp(B_NEXT, asked & 1)) return;
+        ++asked;
+        u = next_block(answer);
+        __syncwarp();
+      }
+      own = false;
+      if (u < 0) break;
+      // each block of the grid, and each that is taken over, looks at one sequence's entries
+      if (lane == 0 && u < a.B && run_of(a.cu, u, a.total, a.max_len).n < 0)
+        set_error(a.err_word, KVQ_ERRBIT_BADLEN);
+      while (b0 < a.B) {
+        const int64_t all = __shfl_sync(0xffffffffu, scan, 31);
+        if (u < base + all) break;
+        base += all;
+        b0 += 32;
+        window();
+      }
+      if (b0 < a.B) break;
+      // the grid may have more blocks than there are units: the rest are taken over here
     }
-    const bool more = b0 < a.B;
-    if (!wt.wait_warp(B_UEMPTY + i % kUnits, ((i / kUnits) & 1) ^ 1)) return;
+    const bool more = u >= 0;
     // the sequence that has unit u; its last block first, heads within blocks
     const uint32_t has = __ballot_sync(0xffffffffu, more && u < base + scan);
     if (more ? lane == __ffs(has) - 1 : lane == 0) {
@@ -257,8 +300,8 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
         s.tiles1 = C::LANES == 2 ? tiles(1) : 0;
         s.no = i + 1;
       }
-      ring[i % kUnits] = s;
-      ptx::mbar_arrive(wt.bar(B_UFULL + i % kUnits));
+      *unit = s;
+      ptx::mbar_arrive(wt.bar(B_UFULL));
     }
     __syncwarp();
     if (!more) return;
@@ -268,7 +311,7 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
 // -------------------------------------------------------------------- loads ---
 
 template <int D>
-__device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* ring) {
+__device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* unit) {
   using C = Cfg<D>;
   const bool one = (threadIdx.x & 31) == 0;
   if (one) {
@@ -276,12 +319,11 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
     ptx::prefetch_tensormap(&a.mk);
     ptx::prefetch_tensormap(&a.mv);
   }
-  UnitReader units = {wt, ring};
+  UnitReader units = {wt, unit};
   uint32_t item = 0, qn[2] = {0, 0};  // half tiles so far, units of each lane
   bool ok = true;
   while (ok) {
     const Unit u = units.next();
-    units.release();
     if (u.no == 0) break;
     const int nt = max(u.tiles0, u.tiles1);
     auto kv = [&](int t, int w) {
@@ -317,6 +359,7 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
       kv(t, 0);
       kv(t, 1);
     }
+    units.release();
   }
   // copies still in flight when the block gives up land before its shared memory goes
   const uint32_t t0 = timer_lo();
@@ -338,10 +381,10 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
 // The warp sees every fill of the ring (a parity alone does not tell a fill from the one
 // before the last), and a stage is free when it and the MMAs are done with it.
 template <int D>
-__device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* ring) {
+__device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* unit) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
-  UnitReader units = {wt, ring};
+  UnitReader units = {wt, unit};
   uint32_t item = 0, before = 0;  // half tiles of earlier units; those units' epilogues, a warp each
   while (true) {
     const Unit u = units.next();
@@ -411,11 +454,11 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
 // All lanes of the warp go the same way, so that descriptors and addresses stay in its
 // uniform registers, and one of them issues.
 template <int D>
-__device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
+__device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* unit) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
-  UnitReader units = {wt, ring};
+  UnitReader units = {wt, unit};
   uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
   uint32_t item = 0, vok = 0;               // half tiles of earlier units; a phase bit of each stage
   bool ok = true;
@@ -609,8 +652,8 @@ struct Soft {
     }
   }
 
-  __device__ __forceinline__ void run(const Unit* ring) {
-    UnitReader units = {wt, ring};
+  __device__ __forceinline__ void run(const Unit* unit) {
+    UnitReader units = {wt, unit};
     while (true) {
       const Unit u = units.next();
       units.release();
@@ -667,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   const uint32_t smem = ptx::smem_u32(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lid = tid & 31;
   const Waits wt = {smem + C::OFF_BAR, a.wait_limit_us};
-  Unit* ring = reinterpret_cast<Unit*>(smem_raw + C::OFF_UNIT);
+  Unit* unit = reinterpret_cast<Unit*>(smem_raw + C::OFF_UNIT);
   if (smem & 1023u) {  // the swizzles count on it (a block without static shared memory has it)
     if (tid == 0) set_error(a.err_word, KVQ_ERRBIT_TIMEOUT);
     return;
@@ -679,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       int n = 1;  // arrivals of a phase
       if (i == B_PREADY || i == B_PREADY + 1) n = 4;
       if (i == B_SFULL || i == B_SFULL + 1) n = 1 + a.fault;
-      if (i >= B_UEMPTY && i < B_UEMPTY + kUnits) n = C::SMW + 3;
+      if (i == B_UEMPTY) n = C::SMW + 3;
       if (i >= B_KVEMPTY && i < B_KVEMPTY + kMaxStages) n = 2;
       ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n);
     }
@@ -701,14 +744,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     tc5::regs_inc<208>();
     if (warp < C::SMW) {
       Soft<D> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
-      soft.run(ring);
+      soft.run(unit);
     }
   } else {
     tc5::regs_dec<88>();
-    if (warp == 8) mma_role<D>(wt, smem, tmem, ring);
-    if (warp == 9) load_role<D>(a, wt, smem, ring);
-    if (warp == 10) check_role<D>(a, wt, smem, ring);
-    if (warp == 11) unit_role<D>(a, wt, ring);
+    if (warp == 8) mma_role<D>(wt, smem, tmem, unit);
+    if (warp == 9) load_role<D>(a, wt, smem, unit);
+    if (warp == 10) check_role<D>(a, wt, smem, unit);
+    if (warp == 11) unit_role<D>(a, wt, smem, unit);
     __syncwarp();
   }
   tc5::fence_before();
