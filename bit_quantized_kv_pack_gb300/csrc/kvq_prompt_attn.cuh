@@ -261,7 +261,12 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
       if (!own) {
         if (lane == 0) ask_next(answer, wt.bar(B_NEXT));
         __syncwarp();
-        if (!wt.wait_warp(B_NEXT, asked & 1)) return;
+        if (!wt.wait_warp(B_NEXT, asked & 1)) {
+          // (the block gives up: the answer lands before its shared memory goes)
+          for (const uint32_t t0 = timer_lo(); !ptx::mbar_try_wait(wt.bar(B_NEXT), asked & 1);)
+            if (timer_lo() - t0 > 1000000000u) break;
+          return;
+        }
         ++asked;
         u = next_block(answer);
         __syncwarp();
@@ -452,77 +457,99 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
 // ---------------------------------------------------------------------- MMA ---
 
 // All lanes of the warp go the same way, so that descriptors and addresses stay in its
-// uniform registers, and one of them issues.
+// uniform registers, and one of them issues.  An MMA is taken up when the one before it is
+// nearly done, so what the warp does between two batches is added to the time: the waits
+// stand together before a lane's batch (its values, then its next scores), and the second
+// lane's are known to be over.
 template <int D>
-__device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* unit) {
+__device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
-  UnitReader units = {wt, unit};
-  uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of the lanes' barriers
-  uint32_t item = 0, vok = 0;               // half tiles of earlier units; a phase bit of each stage
-  bool ok = true;
+  UnitReader units = {wt, ring};
+  uint32_t qn = 0, pn = 0;     // phase bits of the lanes' barriers
+  uint32_t vok = 0;            // and of the stages'
+  // the places of a unit's first keys in the ring
+  int stage = 0;
+  uint32_t phase = 0;
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  auto next = [](int& st, uint32_t& ph) {
+    if (++st == C::ST) st = 0, ph ^= 1;
+  };
+  auto qk = [&](int l, int st) {  // by one thread
+    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + l * C::QBYTES, 16, 8 * C::RB, C::SWZ);
+    const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + st * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
+      tc5::mma_ss(tmem + C::S0 + l * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
+                  kIdescQK, j > 0);
+    }
+    tc5::commit(wt.bar(B_SFULL + l));
+  };
+  bool ok = true;
   while (ok) {
     const Unit u = units.next();
     units.release();
     if (uniform(u.no) == 0) break;
-    const int n[2] = {uniform(u.tiles0), uniform(u.tiles1)};
-    const int nt = max(n[0], n[1]), checked = (uniform(u.t0) + 1) / C::TN;
-    auto last_user = [&](int l, int t) { return l == (t < n[1] ? 1 : 0); };
-    auto qk = [&](int l, int t) -> bool {
-      const uint32_t it = item + 2 * t;
-      const int stage = it % C::ST;
-      if (t == 0 && !wt.wait_warp(B_QFULL + l, qn[l]++ & 1)) return false;
-      if (!wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1)) return false;
-      tc5::fence_after();
-      const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + l * C::QBYTES, 16, 8 * C::RB, C::SWZ);
-      const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + stage * C::KBYTES, 16, 8 * C::RB, C::SWZ);
-      if (tc5::elect()) {
+    const int n0 = uniform(u.tiles0), n1 = C::LANES == 2 ? uniform(u.tiles1) : 0;
+    const int nt = max(n0, n1), checked = (uniform(u.t0) + 1) / C::TN;
+    auto tiles = [&](int l) { return l ? n1 : n0; };
+    // the unit's first scores
+    ok = wt.wait_warp(B_KVFULL + stage, phase);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
-          tc5::mma_ss(tmem + C::S0 + l * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
-                      kIdescQK, j > 0);
-        }
-        tc5::commit(wt.bar(B_SFULL + l));
-        if (last_user(l, t)) tc5::commit(wt.bar(B_KVEMPTY + stage));
-        if (t + 1 == n[l]) tc5::commit(wt.bar(B_QEMPTY + l));
+    for (int l = 0; l < C::LANES; ++l) {
+      if (!ok || tiles(l) == 0) continue;
+      ok = wt.wait_warp(B_QFULL + l, (qn >> l) & 1);
+      qn ^= 1u << l;
+      tc5::fence_after();
+      if (ok && tc5::elect()) {
+        qk(l, stage);
+        if (l == (n1 > 0)) tc5::commit(wt.bar(B_KVEMPTY + stage));
+        if (tiles(l) == 1) tc5::commit(wt.bar(B_QEMPTY + l));
       }
       __syncwarp();
-      return true;
-    };
-#pragma unroll
-    for (int l = 0; l < C::LANES; ++l)
-      if (ok && n[l] > 0) ok = qk(l, 0);
+    }
+    next(stage, phase);
     for (int t = 0; ok && t < nt; ++t) {
-      const uint32_t it = item + 2 * t + 1;
-      const int stage = it % C::ST;
-      if (t >= checked) {
+      const int vst = stage;  // tile t's values, then the next tile's keys
+      ok = wt.wait_warp(B_KVFULL + stage, phase);
+      if (ok && t >= checked) {
         ok = wt.wait_warp(B_VOK + stage, (vok >> stage) & 1);
         vok ^= 1u << stage;
       }
+      next(stage, phase);
+      const int kst = stage;
+      if (t + 1 < nt) {
+        ok = ok && wt.wait_warp(B_KVFULL + stage, phase);
+        next(stage, phase);
+      }
+      const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + vst * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
 #pragma unroll
       for (int l = 0; l < C::LANES; ++l) {
-        if (!ok || t >= n[l]) continue;
-        ok = wt.wait_warp(B_PREADY + l, pn[l]++ & 1) && wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1);
+        if (!ok || t >= tiles(l)) continue;
+        ok = wt.wait_warp(B_PREADY + l, (pn >> l) & 1);
+        pn ^= 1u << l;
         if (!ok) continue;
         tc5::fence_after();
-        const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + stage * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
         if (tc5::elect()) {
 #pragma unroll
           for (int j = 0; j < C::TN / 16; ++j)
             tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
                         t > 0 || j > 0);
-          if (last_user(l, t)) tc5::commit(wt.bar(B_KVEMPTY + stage));
-          if (t + 1 == n[l]) tc5::commit(wt.bar(B_ODONE + l));
+          if (l == (t < n1)) tc5::commit(wt.bar(B_KVEMPTY + vst));
+          if (t + 1 == tiles(l)) {
+            tc5::commit(wt.bar(B_ODONE + l));
+          } else {
+            // after this step in the tensor cores' order: S may take P's place
+            qk(l, kst);
+            if (l == (t + 1 < n1)) tc5::commit(wt.bar(B_KVEMPTY + kst));
+            if (t + 2 == tiles(l)) tc5::commit(wt.bar(B_QEMPTY + l));
+          }
         }
         __syncwarp();
-        // after this step in the tensor cores' order: S may take P's place
-        if (t + 1 < n[l]) ok = qk(l, t + 1);
       }
     }
-    item += 2 * nt;
   }
   // nothing of this thread's is in flight when TMEM is freed
   if (tc5::elect()) tc5::commit(wt.bar(B_DRAIN));
