@@ -52,6 +52,7 @@ cudaError_t launch_prompt_attention(const kvq_prompt_args& A, cudaStream_t st) {
   const int d = A.head_dim;
   a.gq = A.num_q_heads / A.num_kv_heads;
   a.T = 128 / a.gq;
+  a.gq_mul = (uint32_t)(65536 / a.gq + (65536 % a.gq != 0));
   const uint64_t rows = (uint64_t)A.total, heads = (uint64_t)A.num_kv_heads;
   const uint32_t panel = prompt_panel(d), tile = prompt_tile(d);
   const uint64_t qe[4] = {(uint64_t)d, (uint64_t)a.gq, rows, heads}, ke[3] = {(uint64_t)d, rows, heads};

@@ -48,6 +48,7 @@ struct PromptAttnArgs {
   uint32_t* err_word;
   void* out;  // [total][Hq][d]
   int B, Hkv, gq, T, total, max_len, out_f32;
+  uint32_t gq_mul;  // row / gq = row * gq_mul >> 16 for rows below 128
   uint32_t wait_limit_us;
   int fault;  // testing hook: 1 makes the scores' barriers wait for an arrival that never comes
   float scale_log2;
@@ -82,7 +83,7 @@ struct Cfg {
   static constexpr int KP = TN * RB;   // of a panel of K or V
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int KBYTES = TN * D * 2;
-  static constexpr int ST = D == 256 ? 4 : D == 128 ? 5 : 8;  // stages of K and V
+  static constexpr int ST = D >= 128 ? 4 : 8;  // stages of K and V
   static constexpr int SMW = 4 * LANES;        // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
@@ -90,7 +91,8 @@ struct Cfg {
   // shared memory
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = OFF_Q + LANES * QBYTES;
-  static constexpr int OFF_NOTES = OFF_KV + ST * KBYTES;  // int [3][D]
+  static constexpr int OFF_OUT = OFF_KV + ST * KBYTES;  // 4 KiB of each softmax warp
+  static constexpr int OFF_NOTES = OFF_OUT + SMW * 4096;  // int [3][D]
   static constexpr int OFF_BAR = OFF_NOTES + 3 * D * 4;
   static constexpr int OFF_UNIT = OFF_BAR + 512;  // Unit, and the answer of the launch control
   // (more than half an SM's, so that a block has the tensor memory to itself)
@@ -125,6 +127,10 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t timer_lo() {  // nanoseconds, modulo 2^32
   uint32_t t;
@@ -643,23 +649,55 @@ struct Soft {
     tc5::wait_st();
   }
 
-  __device__ __forceinline__ void store16(const float* o, float f, int64_t at) const {
-    if (a.out_f32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+  // The warp's rows of O, times f, to the output.  A thread has a row: its 16-byte pieces go
+  // through shared memory (swizzled: no two of a row's or a column's share a bank), so that
+  // the warp's stores are whole 128-byte lines.  (A row to a thread, 32 lines a store, took
+  // 2.9 us a unit at head_dim 128, as long as two tiles.)
+  template <bool F32>
+  __device__ __forceinline__ void store_rows(const Unit& u, float f) const {
+    constexpr int BYTES = F32 ? 4 : 2;
+    constexpr int COLS = D * BYTES < 128 ? D : 128 / BYTES;  // of a round
+    constexpr int PPR = COLS * BYTES / 16;                   // pieces of a row
+    const int lid = threadIdx.x & 31, heads = a.Hkv * a.gq;
+    const uint32_t st = smem + C::OFF_OUT + (threadIdx.x >> 5) * 4096;
+    auto at = [&](int row, int piece) { return st + row * (PPR * 16) + ((piece ^ (row & (PPR - 1))) << 4); };
+    // the lane's first token, and how many it has
+    const int t0 = u.t0 + lane() * a.T, tokens = min(a.T, u.n - t0);
+    char* const base = static_cast<char*>(a.out) + (((int64_t)u.c0 + t0) * heads + u.h * a.gq) * (D * BYTES);
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += COLS) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at);
+      for (int c = 0; c < COLS; c += 32) {
+        float o[32];
+        tc5::ld32(tmem + C::O0 + lane() * D + c0 + c, reinterpret_cast<uint32_t*>(o));
+        tc5::wait_ld();
+        tc5::pin32(reinterpret_cast<uint32_t*>(o));
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        dst[e] = make_uint4(ptx::pack_h2(o[8 * e] * f, o[8 * e + 1] * f), ptx::pack_h2(o[8 * e + 2] * f, o[8 * e + 3] * f),
-                            ptx::pack_h2(o[8 * e + 4] * f, o[8 * e + 5] * f),
-                            ptx::pack_h2(o[8 * e + 6] * f, o[8 * e + 7] * f));
+        for (int i = 0; i < 32 * BYTES / 16; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = F32 ? __float_as_uint(o[(4 * i + k) & 31] * f)
+                       : ptx::pack_h2(o[(8 * i + 2 * k) & 31] * f, o[(8 * i + 2 * k + 1) & 31] * f);
+          sts_v4(at(lid, c * BYTES / 16 + i), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+      __syncwarp();
+      uint4 v[PPR];
+#pragma unroll
+      for (int i = 0; i < PPR; ++i) v[i] = lds_v4(at(i * (32 / PPR) + lid / PPR, lid % PPR));
+#pragma unroll
+      for (int i = 0; i < PPR; ++i) {
+        const uint32_t row = (r() & ~31) + i * (32 / PPR) + lid / PPR, in = (row * a.gq_mul) >> 16;
+        if ((int)in < tokens)
+          *reinterpret_cast<uint4*>(base + (uint64_t)(in * heads + (row - in * a.gq)) * (D * BYTES) + c0 * BYTES +
+                                    lid % PPR * 16) = v[i];
+      }
+      __syncwarp();
     }
   }
 
-  // What the notes say of the row's columns, over the thread's own stores.  A row whose sum
+  // What the notes say of the row's columns, over what the warp has stored.  A row whose sum
   // is NaN stays NaN.
   __device__ __forceinline__ void notes(int lim, float inv, int64_t at) const {
     const uint32_t n = smem + C::OFF_NOTES;
@@ -687,7 +725,7 @@ struct Soft {
       if (u.no == 0) return;
       const int n = lane() ? u.tiles1 : u.tiles0;
       if (n == 0) continue;
-      const int in = r() / a.gq, tok = u.t0 + lane() * a.T + in;
+      const int in = (int)(((uint32_t)r() * a.gq_mul) >> 16), tok = u.t0 + lane() * a.T + in;
       const bool live = in < a.T && tok < u.n;
       const bool warp_live = __any_sync(0xffffffffu, live);
       int visible = live ? tok + 1 : 1 << 30;  // rows that are not there need no mask
@@ -705,20 +743,12 @@ struct Soft {
       tc5::fence_after();
       if (warp_live) {
         const float inv = 1.0f / l;  // (of scores that are all -inf: NaN, as of NaN ones)
-        const int64_t at = (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tc5::ld32(tmem + C::O0 + lane() * D + c, reinterpret_cast<uint32_t*>(o));
-          tc5::wait_ld();
-          tc5::pin32(reinterpret_cast<uint32_t*>(o));
-          if (live) {
-            store16(o, inv, at + c);
-            store16(o + 16, inv, at + c + 16);
-          }
-          __syncwarp();
-        }
-        if (wt.word(W_NOTED) == (uint32_t)u.no && live) notes(tok + 1, inv, at);
+        if (a.out_f32)
+          store_rows<true>(u, inv);
+        else
+          store_rows<false>(u, inv);
+        if (wt.word(W_NOTED) == (uint32_t)u.no && live)
+          notes(tok + 1, inv, (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D);
       }
       tc5::fence_before();
       __threadfence_block();

@@ -47,7 +47,7 @@ __device__ __forceinline__ void load(uint4 (&v)[N], const uint8_t* src, int byte
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
-    if ((i * 32 + lane) * 16 < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
+    if ((i * 32 + lane) * 16 < bytes) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
   }
 }
 template <int N>
@@ -55,7 +55,7 @@ __device__ __forceinline__ void store(const uint4 (&v)[N], uint8_t* dst, int byt
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if ((i * 32 + lane) * 16 < bytes) reinterpret_cast<uint4*>(dst)[i * 32 + lane] = v[i];
+    if ((i * 32 + lane) * 16 < bytes) __stcs(reinterpret_cast<uint4*>(dst) + i * 32 + lane, v[i]);
 }
 // Rows that start anywhere (heads of 32 or 64 with odd capacities), and mode bytes: words
 // where both sides and the length allow, else bytes.
@@ -64,7 +64,7 @@ __device__ __forceinline__ void copy_any(uint8_t* dst, const uint8_t* src, int b
   if ((((uint32_t)(uintptr_t)dst | (uint32_t)(uintptr_t)src | (uint32_t)bytes) & 3) == 0) {
 #pragma unroll 4
     for (int i = lane; i < bytes / 4; i += 32)
-      reinterpret_cast<uint32_t*>(dst)[i] = __ldcs(reinterpret_cast<const uint32_t*>(src) + i);
+      reinterpret_cast<uint32_t*>(dst)[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
   } else {
 #pragma unroll 1
     for (int i = lane; i < bytes; i += 32) dst[i] = src[i];
@@ -183,12 +183,12 @@ __device__ __forceinline__ void copy_run(const ReorderArgs& g, const Plan& p, in
   for (int j = 0; j < kCodeBytes / 512; ++j) {
     const int at = j * 32 + lane;
     v[j] = make_uint4(0, 0, 0, 0);
-    if (live(at)) v[j] = __ldcs(reinterpret_cast<const uint4*>(src) + at);
+    if (live(at)) v[j] = __ldg(reinterpret_cast<const uint4*>(src) + at);
   }
 #pragma unroll
   for (int j = 0; j < kCodeBytes / 512; ++j) {
     const int at = j * 32 + lane;
-    if (live(at)) reinterpret_cast<uint4*>(dst)[at] = v[j];
+    if (live(at)) __stcs(reinterpret_cast<uint4*>(dst) + at, v[j]);
   }
 }
 
