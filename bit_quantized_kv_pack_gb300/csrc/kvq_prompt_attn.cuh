@@ -8,7 +8,10 @@
 // maximum lazily: it moves (and O, l are rescaled) only when the maximum has passed it by
 // 2^8.  Roundings: the weights P to fp16 once (they and l carry a factor 2^7, which O / l
 // cancels, so that they keep 11 bits down to 2^-21 of the reference and lose at most 2^-32
-// of it below), the output once; scores, m, l and O are fp32.
+// of it below), the output once; scores, m, l and O are fp32.  For fp32 output the weights
+// are two fp16 parts, P and what its rounding left, each times V; and as the tensor cores'
+// sums are cut off, not rounded (2^-25 of O a step, all towards zero: 6e-5 over 16384 tokens
+// of values of one sign), every kSegment tiles O goes to the output's fp32 sums.
 //
 // A block (one per SM, persistent) has 12 warps:
 //   0-7   softmax: a thread per query row, four warps for each of the two accumulators
@@ -70,6 +73,7 @@ namespace prompt {
 constexpr int kThreads = 384;
 constexpr float kWeightBits = 7.0f;  // log2 of the weights' factor
 constexpr int kMaxStages = 8;
+constexpr int kSegment = 16;         // tiles whose values the tensor cores add up for fp32 output (a power of two)
 
 template <int D>
 struct Cfg {
@@ -467,12 +471,13 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
 // nearly done, so what the warp does between two batches is added to the time: the waits
 // stand together before a lane's batch (its values, then its next scores), and the second
 // lane's are known to be over.
-template <int D>
+template <int D, bool TWO>
 __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
   UnitReader units = {wt, ring};
+  constexpr int seg = TWO ? kSegment - 1 : 0x7fffffff;  // (t & seg) == 0: O begins
   uint32_t qn = 0, pn = 0;     // phase bits of the lanes' barriers
   uint32_t vok = 0;            // and of the stages'
   // the places of a unit's first keys in the ring
@@ -542,11 +547,16 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
 #pragma unroll
           for (int j = 0; j < C::TN / 16; ++j)
             tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
-                        t > 0 || j > 0);
+                        (t & seg) > 0 || j > 0);
+          if (TWO) {  // the weights' second parts
+#pragma unroll
+            for (int j = 0; j < C::TN / 16; ++j)
+              tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + C::TN / 2 + j * 8,
+                          vd + ((j * 16 * C::RB) >> 4), kIdescPV, true);
+          }
           if (l == (t < n1)) tc5::commit(wt.bar(B_KVEMPTY + vst));
-          if (t + 1 == tiles(l)) {
-            tc5::commit(wt.bar(B_ODONE + l));
-          } else {
+          if (t + 1 == tiles(l) || ((t + 1) & seg) == 0) tc5::commit(wt.bar(B_ODONE + l));
+          if (t + 1 < tiles(l)) {
             // after this step in the tensor cores' order: S may take P's place
             qk(l, kst);
             if (l == (t + 1 < n1)) tc5::commit(wt.bar(B_KVEMPTY + kst));
@@ -565,7 +575,7 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
 
 // ------------------------------------------------------------------ softmax ---
 
-template <int D>
+template <int D, bool F32>
 struct Soft {
   using C = Cfg<D>;
   const PromptAttnArgs& a;
@@ -588,6 +598,30 @@ struct Soft {
       y = fmaxf(y, s[j + 1]);
     }
     return fmaxf(x, y);
+  }
+
+  // The row's weights of a tile into TMEM, and their sum.  F32: what the rounding to fp16
+  // leaves goes beside them.
+  static __device__ __forceinline__ void weights(uint32_t sa, const float* s, uint64_t c2, uint64_t off2,
+                                                 uint64_t& sum2) {
+#pragma unroll
+    for (int h = 0; h < C::TN; h += 32) {
+      uint32_t p[16], q[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t x = fma_f32x2(pack_f32x2(s[h + i], s[h + i + 1]), c2, off2);
+        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
+        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
+        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
+        p[i / 2] = ptx::pack_h2(e0, e1);
+        if (F32) {
+          const float2 f = __half22float2(ptx::u32_as_h2(p[i / 2]));
+          q[i / 2] = ptx::pack_h2(e0 - f.x, e1 - f.y);
+        }
+      }
+      tc5::st16(sa + h / 2, p);
+      if (F32) tc5::st16(sa + C::TN / 2 + h / 2, q);
+    }
   }
 
   // One tile: the row's weights into TMEM, m and l brought up to date.  visible: tokens of
@@ -632,19 +666,7 @@ struct Soft {
     const float off = m == -INFINITY ? 0.0f : fmaf(-m, a.scale_log2, kWeightBits);
     const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), off2 = pack_f32x2(off, off);
     uint64_t sum2 = pack_f32x2(l, 0.0f);
-#pragma unroll
-    for (int h = 0; h < C::TN; h += 32) {
-      uint32_t p[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const uint64_t x = fma_f32x2(pack_f32x2(s[h + i], s[h + i + 1]), c2, off2);
-        const float e0 = ptx::ex2_ftz(__uint_as_float(lo_bits(x)));
-        const float e1 = ptx::ex2_ftz(__uint_as_float(hi_bits(x)));
-        sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
-        p[i / 2] = ptx::pack_h2(e0, e1);
-      }
-      tc5::st16(sa + h / 2, p);
-    }
+    weights(sa, s, c2, off2, sum2);
     l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
     tc5::wait_st();
   }
@@ -652,9 +674,9 @@ struct Soft {
   // The warp's rows of O, times f, to the output.  A thread has a row: its 16-byte pieces go
   // through shared memory (swizzled: no two of a row's or a column's share a bank), so that
   // the warp's stores are whole 128-byte lines.  (A row to a thread, 32 lines a store, took
-  // 2.9 us a unit at head_dim 128, as long as two tiles.)
-  template <bool F32>
-  __device__ __forceinline__ void store_rows(const Unit& u, float f) const {
+  // 2.9 us a unit at head_dim 128, as long as two tiles.)  F32, g > 0: added to g times what
+  // is there (of the row, by the same thread).
+  __device__ __forceinline__ void store_rows(const Unit& u, float f, float g) const {
     constexpr int BYTES = F32 ? 4 : 2;
     constexpr int COLS = D * BYTES < 128 ? D : 128 / BYTES;  // of a round
     constexpr int PPR = COLS * BYTES / 16;                   // pieces of a row
@@ -689,9 +711,19 @@ struct Soft {
 #pragma unroll
       for (int i = 0; i < PPR; ++i) {
         const uint32_t row = (r() & ~31) + i * (32 / PPR) + lid / PPR, in = (row * a.gq_mul) >> 16;
-        if ((int)in < tokens)
-          *reinterpret_cast<uint4*>(base + (uint64_t)(in * heads + (row - in * a.gq)) * (D * BYTES) + c0 * BYTES +
-                                    lid % PPR * 16) = v[i];
+        uint4* to = reinterpret_cast<uint4*>(base + (uint64_t)(in * heads + (row - in * a.gq)) * (D * BYTES) +
+                                             c0 * BYTES + lid % PPR * 16);
+        if (F32) {
+          const float gr = __shfl_sync(0xffffffffu, g, i * (32 / PPR) + lid / PPR);
+          if ((int)in < tokens && gr > 0.0f) {
+            const uint4 was = *to;
+            v[i].x = __float_as_uint(fmaf(__uint_as_float(was.x), gr, __uint_as_float(v[i].x)));
+            v[i].y = __float_as_uint(fmaf(__uint_as_float(was.y), gr, __uint_as_float(v[i].y)));
+            v[i].z = __float_as_uint(fmaf(__uint_as_float(was.z), gr, __uint_as_float(v[i].z)));
+            v[i].w = __float_as_uint(fmaf(__uint_as_float(was.w), gr, __uint_as_float(v[i].w)));
+          }
+        }
+        if ((int)in < tokens) *to = v[i];
       }
       __syncwarp();
     }
@@ -708,9 +740,9 @@ struct Soft {
       if (!(up || down || nan)) continue;
       float v = nan || (up && down) || inv != inv ? NAN : up ? INFINITY : -INFINITY;
       // (with an infinite value of the other sign in a tile that all rows see, or NaN there)
-      const float o = a.out_f32 ? static_cast<float*>(a.out)[at + c] : __half2float(static_cast<__half*>(a.out)[at + c]);
+      const float o = F32 ? static_cast<float*>(a.out)[at + c] : __half2float(static_cast<__half*>(a.out)[at + c]);
       if (o != o || (isinf(o) && o != v)) v = NAN;
-      if (a.out_f32)
+      if (F32)
         static_cast<float*>(a.out)[at + c] = v;
       else
         static_cast<__half*>(a.out)[at + c] = __float2half(v);
@@ -729,24 +761,33 @@ struct Soft {
       const bool live = in < a.T && tok < u.n;
       const bool warp_live = __any_sync(0xffffffffu, live);
       int visible = live ? tok + 1 : 1 << 30;  // rows that are not there need no mask
-      float m = -INFINITY, l = 0.0f;
+      constexpr int seg = F32 ? kSegment - 1 : 0x7fffffff;
+      float m = -INFINITY, l = 0.0f, m_out = 0.0f;
+      bool begun = false;  // the output has sums, at the reference m_out
+      // what those weigh at the reference now: never zero, so that an infinite one stays so
+      auto weight = [&] { return !begun ? 0.0f : m == m_out ? 1.0f : fmaxf(ptx::ex2_ftz((m_out - m) * a.scale_log2), 1.17549435e-38f); };
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {
         if (!wt.wait_warp(B_SFULL + lane(), sn++ & 1)) return;
         tc5::fence_after();
-        if (warp_live) tile(visible, t > 0, m, l);
+        if (warp_live) tile(visible, (t & seg) > 0, m, l);
         tc5::fence_before();
         wt.arrive_warp(B_PREADY + lane());
         if (live) visible -= C::TN;
+        if (((t + 1) & seg) == 0 && t + 1 < n) {
+          if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
+          tc5::fence_after();
+          if (warp_live) store_rows(u, 1.0f, weight());
+          m_out = m;
+          begun = true;
+          tc5::fence_before();
+        }
       }
       if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
       tc5::fence_after();
       if (warp_live) {
         const float inv = 1.0f / l;  // (of scores that are all -inf: NaN, as of NaN ones)
-        if (a.out_f32)
-          store_rows<true>(u, inv);
-        else
-          store_rows<false>(u, inv);
+        store_rows(u, inv, weight() * inv);
         if (wt.word(W_NOTED) == (uint32_t)u.no && live)
           notes(tok + 1, inv, (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D);
       }
@@ -760,7 +801,7 @@ struct Soft {
 
 // ------------------------------------------------------------------- kernel ---
 
-template <int D>
+template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -800,12 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp < 8) {
     tc5::regs_inc<208>();
     if (warp < C::SMW) {
-      Soft<D> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
+      Soft<D, F32> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
       soft.run(unit);
     }
   } else {
     tc5::regs_dec<88>();
-    if (warp == 8) mma_role<D>(wt, smem, tmem, unit);
+    if (warp == 8) mma_role<D, F32>(wt, smem, tmem, unit);
     if (warp == 9) load_role<D>(a, wt, smem, unit);
     if (warp == 10) check_role<D>(a, wt, smem, unit);
     if (warp == 11) unit_role<D>(a, wt, smem, unit);
@@ -818,10 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp == 8) tc5::dealloc(tmem, 512);
 }
 
-template <int D>
-cudaError_t launch(const PromptAttnArgs& a, int grid, cudaStream_t st) {
+template <int D, bool F32>
+cudaError_t launch_as(const PromptAttnArgs& a, int grid, cudaStream_t st) {
   static_assert(Cfg<D>::SMEM <= 227 * 1024, "shared memory of a block");
-  auto kernel = prompt_attn_kernel<D>;
+  auto kernel = prompt_attn_kernel<D, F32>;
   // the kernel's attributes, once per device
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -838,6 +879,11 @@ cudaError_t launch(const PromptAttnArgs& a, int grid, cudaStream_t st) {
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
   return launch_overlapped(kernel, dim3(grid), kThreads, Cfg<D>::SMEM, st, a);
+}
+
+template <int D>
+cudaError_t launch(const PromptAttnArgs& a, int grid, cudaStream_t st) {
+  return a.out_f32 ? launch_as<D, true>(a, grid, st) : launch_as<D, false>(a, grid, st);
 }
 
 }  // namespace prompt

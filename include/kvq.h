@@ -564,11 +564,13 @@ typedef struct {
  * row i of a prompt attends over its rows 0..i, query head hq over KV head hq / (Hq / Hkv):
  *   out[i] = sum_j softmax_j(q[i] . k[j] / sqrt(d)) v[j],  j <= i.
  * Weights are rounded to fp16 once (operands of the tensor cores; weights below 2^-21 of a
- * row's largest by at most 2^-32 of that), scores and sums are fp32, the output is rounded
- * once; results do not depend on timing.  Tokens a row does not attend over, other
- * prompts' among them, have no part in its output, whatever they hold.  Entries of
- * cu_seqlens that break the rule set KVQ_ERRBIT_BADLEN.  Asynchronous; lengths are read
- * on the device. */
+ * row's largest by at most 2^-32 of that), with KVQ_OUT_F32 they are two fp16 parts (22 bits);
+ * scores and sums are fp32, the output is rounded once.  The tensor cores cut their sums off
+ * (2^-25 a step of 16 tokens, towards zero): fp32 output is within 1e-5 of the sums of
+ * values of one sign and about 1e-6 of others, whatever the length.  Results do not depend
+ * on timing.  Tokens a row does not attend over, other prompts' among them, have no part in
+ * its output, whatever they hold.  Entries of cu_seqlens that break the rule set
+ * KVQ_ERRBIT_BADLEN.  Asynchronous; lengths are read on the device. */
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream);
 
 /* Arguments of kvq_beam_select; zero-initialise the struct. */
