@@ -232,7 +232,7 @@ __device__ __noinline__ uint64_t select_many(const T* row, uint32_t first, uint3
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_constant__ BeamArgs a) {
   constexpr uint32_t E = Vec<T>::E;
-  constexpr int WARPS = kThreads / 32, TOPS = 32 / WARPS;
+  constexpr int WARPS = kThreads / 32;
   __shared__ uint64_t lists[WARPS][32];
   __shared__ __align__(16) uint64_t passed[kMaxN * NV * E];  // (at least kFew)
   __shared__ __align__(16) uint32_t tops[32];
@@ -251,21 +251,24 @@ __global__ void __launch_bounds__(kThreads, 3) beam_piece_kernel(const __grid_co
   load_vecs(v, row, first, V);
   if (tid == 0) count = 0;
 
-  // the thread's largest, and the warp's four largest of those.  Their last five bits are a
-  // number of their own, so that no two are equal: the bound is made of the others
+  // the thread's largest, and of those the warp's four largest (more, where the row's end
+  // leaves warps without tokens: 32 in all).  Their last five bits are a number of their
+  // own, so that no two are equal: the bound is made of the others
   float best = -INFINITY;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) best = fmaxf(best, Vec<T>::get(v[j], e));
   uint32_t left = first < V ? ordered(best) : 0;
-#pragma unroll
-  for (int i = 0; i < TOPS; ++i) {
+  const uint32_t behind = V - (first - tid * E);  // tokens from the piece's first on
+  const int share = behind >= kThreads * E ? 0 : __ffs(WARPS) - 1 - (31 - __clz((behind + 32 * E - 1) / (32 * E)));
+  const int mine_tops = (32 / WARPS) << share;
+  if (lane == 0) top[warp] = 0;
+#pragma unroll 4
+  for (int i = 0; i < mine_tops; ++i) {
     const uint32_t x = __reduce_max_sync(0xffffffffu, left);
-    if (lane == 0) {
-      tops[warp * TOPS + i] = (x & ~31u) | (warp * TOPS + i);
-      if (i == 0) top[warp] = x;
-    }
+    if (lane == 0 && warp * mine_tops + i < 32) tops[warp * mine_tops + i] = (x & ~31u) | (warp * mine_tops + i);
+    if (lane == 0 && i == 0) top[warp] = x;
     if (lane == __ffs(__ballot_sync(0xffffffffu, left == x)) - 1) left = 0;
   }
   __syncthreads();

@@ -734,19 +734,39 @@ def axes_of_pairs(sections, interleaved: bool = False) -> bytes:
     return bytes(out)
 
 
-def _rows_tensor(t: torch.Tensor, device: torch.device, name: str) -> int:
-    if (t.dtype != torch.float16 or not t.is_cuda or t.device != device or t.dim() != 3
-            or (t.stride(2) != 1 and t.shape[2] > 1)):
+# (dtypes compared by identity, devices by index, arguments in the structs' order: these
+# calls take as long on the host as the smallest of them on the GPU)
+
+
+def _rows_tensor(t: torch.Tensor, index: int, name: str) -> tuple[int, int, int, int]:
+    """Address, heads and strides of rows and heads of [total][heads][d] views."""
+    total, heads, d = t.shape
+    row, head, one = t.stride()
+    if t.dtype is not torch.float16 or index < 0 or t.get_device() != index or (one != 1 and d > 1):
         raise ValueError(f"{name} must be a float16 CUDA tensor [total][heads][d] with d contiguous, all on one device")
-    return t.data_ptr()
+    return t.data_ptr(), heads, row if total > 1 else 0, head if heads > 1 else 0
 
 
-def _err_ptr(err: torch.Tensor | None, device: torch.device) -> int | None:
+def _err_ptr(err: torch.Tensor | None, index: int) -> int | None:
     if err is None:
         return None
-    if err.dtype != torch.int32 or not err.is_cuda or err.device != device or err.numel() < 1:
+    if err.dtype is not torch.int32 or err.get_device() != index or err.numel() < 1:
         raise ValueError("err must be an int32 CUDA tensor (a cache's err) on the same device")
     return err.data_ptr()
+
+
+def _rotated_tensor(t, out, total, d, index, device, stream, name):
+    """The output of a tensor's rotation, and both's places."""
+    if t is None:
+        return None, (None, 0, 0, 0), (None, 0, 0, 0)
+    if t.dim() != 3 or t.shape[0] != total or t.shape[2] != d:
+        raise ValueError("q and k must be [total][heads][d] of the same rows and d")
+    at = _rows_tensor(t, index, name)
+    if out is None:
+        out = _empty(t.shape, torch.float16, device, stream)
+    elif out is not t and out.shape != t.shape:
+        raise ValueError(f"{name}_out must have {name}'s shape")
+    return out, at, at if out is t else _rows_tensor(out, index, name + "_out")
 
 
 def kvq_rotate(q: torch.Tensor | None, k: torch.Tensor | None, rope: torch.Tensor, positions: torch.Tensor,
@@ -762,44 +782,27 @@ def kvq_rotate(q: torch.Tensor | None, k: torch.Tensor | None, rope: torch.Tenso
     x = q if q is not None else k
     if x is None or x.dim() != 3:
         raise ValueError("q or k must be [total][heads][d]")
-    device = x.device
+    device, index = x.device, x.get_device()
     total, _, d = x.shape
-    if (rope.dtype != torch.float32 or not rope.is_cuda or rope.device != device or rope.dim() != 3
+    if (rope.dtype is not torch.float32 or rope.get_device() != index or index < 0 or rope.dim() != 3
             or rope.shape[2] != 2 or not rope.is_contiguous()):
         raise ValueError("rope must be a contiguous float32 CUDA tensor [rows][rotary_dim / 2][2] on q's device")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if (positions.dtype != torch.int32 or not positions.is_cuda or positions.device != device
-            or positions.dim() not in (1, 2) or positions.shape[-1] != total or not positions.is_contiguous()):
+    shape = positions.shape
+    if (positions.dtype is not torch.int32 or positions.get_device() != index or len(shape) not in (1, 2)
+            or shape[-1] != total or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int32 CUDA tensor [axes][total] on q's device")
-    a = RotateArgs(head_dim=d, total=total, rope=rope.data_ptr(), rope_rows=rope.shape[0],
-                   rotary_dim=2 * rope.shape[1], interleaved=int(interleaved), axes=axes,
-                   positions=positions.data_ptr(), err_word=_err_ptr(err, device))
+    rows, pairs, _ = rope.shape
     if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
-        if len(pair_axis) != rope.shape[1]:
+        if type(pair_axis) is not bytes:
+            pair_axis = bytes(pair_axis)
+        if len(pair_axis) != pairs:
             raise ValueError("pair_axis must have an axis for each pair of rope")
-        a.pair_axis = ctypes.cast(ctypes.c_char_p(pair_axis), ctypes.c_void_p)
-    for t in (q, k):
-        if t is not None and (t.dim() != 3 or t.shape[0] != total or t.shape[2] != d):
-            raise ValueError("q and k must be [total][heads][d] of the same rows and d")
-    if q is not None:
-        a.q, a.num_q_heads = _rows_tensor(q, device, "q"), q.shape[1]
-        if q_out is None:
-            q_out = _empty(q.shape, torch.float16, device, stream)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        a.q_out = _rows_tensor(q_out, device, "q_out")
-        a.q_stride_token, a.q_stride_head = _strides(q, total, q.shape[1])
-        a.q_out_stride_token, a.q_out_stride_head = _strides(q_out, total, q.shape[1])
-    if k is not None:
-        a.k, a.num_kv_heads = _rows_tensor(k, device, "k"), k.shape[1]
-        if k_out is None:
-            k_out = _empty(k.shape, torch.float16, device, stream)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        a.k_out = _rows_tensor(k_out, device, "k_out")
-        a.k_stride_token, a.k_stride_head = _strides(k, total, k.shape[1])
-        a.k_out_stride_token, a.k_out_stride_head = _strides(k_out, total, k.shape[1])
+    q_out, qa, qo = _rotated_tensor(q, q_out, total, d, index, device, stream, "q")
+    k_out, ka, ko = _rotated_tensor(k, k_out, total, d, index, device, stream, "k")
+    a = RotateArgs(qa[0], ka[0], qo[0], ko[0], qa[2], qa[3], ka[2], ka[3], qo[2], qo[3], ko[2], ko[3], qa[1], ka[1],
+                   d, total, rope.data_ptr(), rows, 2 * pairs, 1 if interleaved else 0,
+                   shape[0] if len(shape) == 2 else 1, positions.data_ptr(),
+                   None if pair_axis is None else ctypes.cast(pair_axis, ctypes.c_void_p), _err_ptr(err, index))
     _call_on("kvq_rotate", device, stream, ctypes.byref(a))
     return q_out, k_out
 
@@ -811,25 +814,23 @@ def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
     [total][Hkv][d] (views with d contiguous: columns of a fused projection's output, say),
     prompt b being rows cu_seqlens[b] .. cu_seqlens[b+1] (int32 [B + 1]).  out [total][Hq][d],
     fp16, or fp32 as for kvq_decode_attention.  ``err``: a cache's err."""
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    shape, kv = q.shape, k.shape
+    if len(shape) != 3 or len(kv) != 3 or kv != v.shape or kv[0] != shape[0] or kv[2] != shape[2]:
         raise ValueError("q must be [total][Hq][d], k and v [total][Hkv][d]")
-    device = q.device
-    total, heads, d = q.shape
-    kv_heads = k.shape[1]
-    a = PromptArgs(q=_rows_tensor(q, device, "q"), k=_rows_tensor(k, device, "k"), v=_rows_tensor(v, device, "v"),
-                   num_q_heads=heads, num_kv_heads=kv_heads, head_dim=d, batch=cu_seqlens.numel() - 1, total=total,
-                   cu_seqlens=_run_int(cu_seqlens, cu_seqlens.numel(), device, "cu_seqlens"),
-                   max_len=_max_len(max_len), err_word=_err_ptr(err, device))
-    a.q_stride_token, a.q_stride_head = _strides(q, total, heads)
-    a.k_stride_token, a.k_stride_head = _strides(k, total, kv_heads)
-    a.v_stride_token, a.v_stride_head = _strides(v, total, kv_heads)
+    device, index = q.device, q.get_device()
+    total, heads, d = shape
+    qa, ka, va = _rows_tensor(q, index, "q"), _rows_tensor(k, index, "k"), _rows_tensor(v, index, "v")
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.get_device() != index or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor of B + 1 entries on q's device")
     if out is None:
-        out = _empty(q.shape, torch.float32 if flags & KVQ_OUT_F32 else torch.float16, device, stream)
-    elif (out.dtype not in (torch.float16, torch.float32) or out.shape != q.shape or out.device != device
+        out = _empty(shape, torch.float32 if flags & KVQ_OUT_F32 else torch.float16, device, stream)
+    elif (out.dtype not in (torch.float16, torch.float32) or out.shape != shape or out.get_device() != index
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous float16 or float32 tensor of q's shape, on its device")
-    a.flags = (flags & ~KVQ_OUT_F32) | (KVQ_OUT_F32 if out.dtype == torch.float32 else 0)
-    a.out = out.data_ptr()
+    flags = flags | KVQ_OUT_F32 if out.dtype is torch.float32 else flags & ~KVQ_OUT_F32
+    a = PromptArgs(qa[0], ka[0], va[0], qa[2], qa[3], ka[2], ka[3], va[2], va[3], heads, ka[1], d,
+                   cu_seqlens.numel() - 1, cu_seqlens.data_ptr(), total, _max_len(max_len), out.data_ptr(), flags,
+                   _err_ptr(err, index))
     _call_on("kvq_prompt_attention", device, stream, ctypes.byref(a))
     return out
 
@@ -858,34 +859,38 @@ def kvq_beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, finished
     (uint8 or bool [B][W]): complete beams, which go on with ``end_token`` at their score.
     Returns (parent, token, score), each [B][n] (``out``: such a triple): parent is the row
     b W + w, an index for kvq_reorder."""
-    if (logits.dim() != 3 or logits.dtype not in (torch.float16, torch.float32) or not logits.is_cuda
-            or (logits.stride(2) != 1 and logits.shape[2] > 1)):
+    dtype, shape, index = logits.dtype, logits.shape, logits.get_device()
+    if (len(shape) != 3 or dtype not in (torch.float16, torch.float32) or index < 0
+            or (logits.stride(2) != 1 and shape[2] > 1)):
         raise ValueError("logits must be a float16 or float32 CUDA tensor [B][W][V] with V contiguous")
     device = logits.device
-    B, W, V = logits.shape
-    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
-    if B > 1 and W > 1 and logits.stride(0) != W * row:
+    B, W, V = shape
+    rows = shape[:2]
+    batch_stride, row, _ = logits.stride()
+    if W == 1:
+        row = batch_stride if B > 1 else V
+    elif B > 1 and batch_stride != W * row:
         raise ValueError("logits' rows must have one stride")
-    for t, types, name in ((scores, (torch.float32,), "scores"), (finished, (torch.uint8, torch.bool), "finished")):
-        if t is not None and (t.dtype not in types or not t.is_cuda or t.device != device or t.shape != (B, W)
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [B][W] of {types[0]} on logits' device")
+    if (scores.dtype is not torch.float32 or scores.get_device() != index or scores.shape != rows
+            or not scores.is_contiguous()):
+        raise ValueError("scores must be a contiguous float32 CUDA tensor [B][W] on logits' device")
+    if finished is not None and (finished.dtype not in (torch.uint8, torch.bool) or finished.get_device() != index
+                                 or finished.shape != rows or not finished.is_contiguous()):
+        raise ValueError("finished must be a contiguous uint8 or bool CUDA tensor [B][W] on logits' device")
+    n = int(n)
     if out is None:
-        out = [_empty((B, int(n)), t, device, stream) for t in (torch.int32, torch.int32, torch.float32)]
+        out = [_empty((B, n), t, device, stream) for t in (torch.int32, torch.int32, torch.float32)]
     parent, token, score = out
-    for t, dtype in ((parent, torch.int32), (token, torch.int32), (score, torch.float32)):
-        if t.dtype != dtype or not t.is_cuda or t.device != device or t.shape != (B, n) or not t.is_contiguous():
+    for t, of in ((parent, torch.int32), (token, torch.int32), (score, torch.float32)):
+        if t.dtype is not of or t.get_device() != index or t.shape != (B, n) or not t.is_contiguous():
             raise ValueError("out must be contiguous CUDA tensors [B][n], int32, int32 and float32, on logits' device")
     if workspace is None:
         workspace = _scratch(lambda: beam_workspace_for(B, W, V, n, device), device, stream)
-    if workspace.device != device or not workspace.is_contiguous():
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on logits' device")
-    a = BeamArgs(logits=logits.data_ptr(), stride_row=row, scores=scores.data_ptr(),
-                 finished=None if finished is None else finished.data_ptr(), batch=B, beams=W, vocab=V, n=int(n),
-                 end_token=int(end_token), flags=KVQ_LOGITS_F32 if logits.dtype == torch.float32 else 0,
-                 parent=parent.data_ptr(), token=token.data_ptr(), score=score.data_ptr(),
-                 workspace=workspace.data_ptr(), ws_bytes=workspace.numel() * workspace.element_size(),
-                 err_word=_err_ptr(err, device))
+    a = BeamArgs(logits.data_ptr(), row, scores.data_ptr(), None if finished is None else finished.data_ptr(), B, W, V,
+                 n, int(end_token), KVQ_LOGITS_F32 if dtype is torch.float32 else 0, parent.data_ptr(),
+                 token.data_ptr(), score.data_ptr(), workspace.data_ptr(), workspace.nbytes, _err_ptr(err, index))
     _call_on("kvq_beam_select", device, stream, ctypes.byref(a))
     return parent, token, score
 

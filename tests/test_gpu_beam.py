@@ -66,6 +66,16 @@ def test_selection(B, W, V, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("V", [8, 31, 127, 255, 257, 511, 769, 1002, 1025, 1793, 2047, 2049, 8193])
+def test_short_rows_and_many_proposals(V, dtype):
+    rng = np.random.default_rng(V)
+    x = (rng.standard_normal((20, 16, V)) * 3).astype(dtype)
+    x[0] = -np.sort(-x[0], axis=-1)                   # the largest side by side
+    x[1, :, :V // 2] = -np.inf
+    check(x, (-10 * rng.random((20, 16))).astype(np.float32), 32)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
 @pytest.mark.parametrize("V", [40, 3001, 60001])
 def test_equal_scores_come_in_order(V, dtype):
     rng = np.random.default_rng(V)
