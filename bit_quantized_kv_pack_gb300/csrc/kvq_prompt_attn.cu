@@ -76,7 +76,9 @@ cudaError_t launch_prompt_attention(const kvq_prompt_args& A, cudaStream_t st) {
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d));
   // as many blocks as there can be units
   const int64_t tokens = (int64_t)prompt_lanes(d) * a.T;
-  const int64_t units = (A.total / tokens + A.batch) * (int64_t)heads;
+  int64_t units = (A.total / tokens + A.batch) * (int64_t)heads;
+  a.shared = prompt_lanes(d) == 2 && units <= device_sm_count();
+  if (a.shared) units = (A.total / a.T + A.batch) * (int64_t)heads;
   if (units > 2147483647) return cudaErrorInvalidValue;
   const int grid = (int)units;
   if (d == 32) return launch_prompt_attn_d32(a, grid, st);

@@ -10,7 +10,7 @@
 // cancels, so that they keep 11 bits down to 2^-21 of the reference and lose at most 2^-32
 // of it below), the output once; scores, m, l and O are fp32.  For fp32 output the weights
 // are two fp16 parts, P and what its rounding left, each times V; and as the tensor cores'
-// sums are cut off, not rounded (2^-25 of O a step, all towards zero: 6e-5 over 16384 tokens
+// sums are cut off, not rounded (2^-23 of O a step, all towards zero: 6e-5 over 16384 tokens
 // of values of one sign), every kSegment tiles O goes to the output's fp32 sums.
 //
 // A block (one per SM, persistent) has 12 warps:
@@ -24,6 +24,13 @@
 //         diagonal): a weight of zero would turn an infinite one into NaN.
 //   11    works out the units.
 // head_dim 256 has room for one lane and tiles of 64 tokens.
+//
+// Where there cannot be more units than SMs, a unit is T tokens, and its two lanes have the
+// same rows: every second tile is lane 1's, and the lanes' sums meet in the epilogue, each
+// lane's warps storing half of the columns.  That halves the longest unit, which is what
+// such a call takes (4096 tokens of 8 heads on 2, head_dim 128: 49 -> 30 us; 10836 tokens
+// of 3 heads on 1: 120 -> 70); with more units K and V are loaded twice for nothing (4096
+// tokens of 16 heads on 4: 50 -> 58 us).
 //
 // A unit of work is (sequence, KV head, block of 2 T tokens).  Units lie in one line,
 // sequence after sequence, the longest first within each.  The grid has a block for each;
@@ -51,6 +58,7 @@ struct PromptAttnArgs {
   uint32_t* err_word;
   void* out;  // [total][Hq][d]
   int B, Hkv, gq, T, total, max_len, out_f32;
+  int shared;       // 1: the lanes have the same rows
   uint32_t gq_mul;  // row / gq = row * gq_mul >> 16 for rows below 128
   uint32_t wait_limit_us;
   int fault;  // testing hook: 1 makes the scores' barriers wait for an arrival that never comes
@@ -104,15 +112,16 @@ struct Cfg {
 };
 
 // Sequence rows [c0, c0 + n), KV head h, first token t0 of the block; tiles of each lane
-// (lane 1's are 0 or not fewer); no: 1, 2, .. in the block's order, 0: the end.
+// (lane 1's are 0 or not fewer; shared rows: every second one, lane 0 begins), and all that
+// are loaded; no: 1, 2, .. in the block's order, 0: the end.
 struct alignas(16) Unit {
   int c0, n, h, t0;
-  int tiles0, tiles1, no, pad;
+  int tiles0, tiles1, no, tiles;
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
 enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 6, B_ODONE = 8, B_DRAIN = 10, B_UFULL = 11, B_UEMPTY = 12,
-       B_NEXT = 13, B_KVFULL = 14, B_KVEMPTY = B_KVFULL + kMaxStages, B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
+       B_NEXT = 13, B_JOIN = 14, B_KVFULL = 15, B_KVEMPTY = B_KVFULL + kMaxStages, B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
 enum { W_TMEM = 96, W_ABORT = 97, W_NOTED = 98 /* the unit that the notes are of */, W_EPI = 99 };
 static_assert(B_COUNT * 2 <= W_TMEM, "words behind the barriers");
 
@@ -241,11 +250,11 @@ __device__ __forceinline__ int next_block(uint32_t at) {
 
 // The warp that works out the units: a window of 32 sequences goes along the line (the
 // blocks that it gets come in rising order).
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, Unit* unit) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
-  const int step = C::LANES * a.T;  // tokens of a unit
+  const int step = (SHARED ? 1 : C::LANES) * a.T;  // tokens of a unit
   int b0 = 0;
   int64_t base = 0, scan = 0;  // units before the window; of its sequences up to the lane's
   Run run = {0, 0};
@@ -312,7 +321,9 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
           return first < run.n ? (min(first + a.T, run.n) + C::TN - 1) / C::TN : 0;
         };
         s.tiles0 = tiles(0);
-        s.tiles1 = C::LANES == 2 ? tiles(1) : 0;
+        s.tiles1 = C::LANES == 2 && !SHARED ? tiles(1) : 0;
+        s.tiles = max(s.tiles0, s.tiles1);
+        if (SHARED) s.tiles1 = s.tiles / 2, s.tiles0 = s.tiles - s.tiles1;
         s.no = i + 1;
       }
       *unit = s;
@@ -325,7 +336,7 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
 
 // -------------------------------------------------------------------- loads ---
 
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* unit) {
   using C = Cfg<D>;
   const bool one = (threadIdx.x & 31) == 0;
@@ -340,7 +351,6 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
   while (ok) {
     const Unit u = units.next();
     if (u.no == 0) break;
-    const int nt = max(u.tiles0, u.tiles1);
     auto kv = [&](int t, int w) {
       const int stage = item % C::ST;
       ok = ok && wt.wait_warp(B_KVEMPTY + stage, ((item / C::ST) & 1) ^ 1);
@@ -357,7 +367,7 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
     kv(0, 0);
 #pragma unroll
     for (int l = 0; l < C::LANES; ++l) {
-      if ((l ? u.tiles1 : u.tiles0) == 0) continue;
+      if ((l ? u.tiles1 : u.tiles0) == 0 || (l && SHARED)) continue;
       ok = ok && wt.wait_warp(B_QEMPTY + l, (qn[l] & 1) ^ 1);
       if (!ok) break;
       if (one) {
@@ -369,10 +379,12 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
       }
       ++qn[l];
     }
-    kv(0, 1);
-    for (int t = 1; ok && t < nt; ++t) {
-      kv(t, 0);
+    // (in the order in which the MMAs take them)
+    const int ahead = SHARED ? 2 : 1;
+    if (SHARED && u.tiles > 1) kv(1, 0);
+    for (int t = 0; ok && t < u.tiles; ++t) {
       kv(t, 1);
+      if (t + ahead < u.tiles) kv(t + ahead, 0);
     }
     units.release();
   }
@@ -395,7 +407,7 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
 // it what the sum would be.  In tiles that all rows see whole the MMA does that itself.
 // The warp sees every fill of the ring (a parity alone does not tell a fill from the one
 // before the last), and a stage is free when it and the MMAs are done with it.
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* unit) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
@@ -405,14 +417,16 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
     const Unit u = units.next();
     units.release();
     if (u.no == 0) return;
-    const int nt = max(u.tiles0, u.tiles1);
+    const int nt = u.tiles, ahead = SHARED && nt > 1 ? 2 : 1;
     bool clean = false;  // the notes are this unit's
     for (int half = 0; half < 2 * nt; ++half) {
       const uint32_t it = item + half;
-      const int stage = it % C::ST, t = half >> 1;
+      // first `ahead` tiles' keys, then values and keys in turn, then the last values
+      const int stage = it % C::ST, past = half - 2 * nt + ahead, t = past >= 0 ? nt - ahead + past : (half - ahead) >> 1;
+      const bool values = past >= 0 || (half >= ahead && !((half - ahead) & 1));
       if (!wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1)) return;
       // the block's first row sees tokens up to t0
-      if (!(half & 1) || t < (u.t0 + 1) / C::TN) {
+      if (!values || t < (u.t0 + 1) / C::TN) {
         wt.arrive_warp(B_KVEMPTY + stage);
         continue;
       }
@@ -471,7 +485,7 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
 // nearly done, so what the warp does between two batches is added to the time: the waits
 // stand together before a lane's batch (its values, then its next scores), and the second
 // lane's are known to be over.
-template <int D, bool TWO>
+template <int D, bool TWO, bool SHARED>
 __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
@@ -487,8 +501,8 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
   auto next = [](int& st, uint32_t& ph) {
     if (++st == C::ST) st = 0, ph ^= 1;
   };
-  auto qk = [&](int l, int st) {  // by one thread
-    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + l * C::QBYTES, 16, 8 * C::RB, C::SWZ);
+  auto qk = [&](int l, int rows, int st) {  // by one thread; rows: the lane whose Q it is
+    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + rows * C::QBYTES, 16, 8 * C::RB, C::SWZ);
     const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + st * C::KBYTES, 16, 8 * C::RB, C::SWZ);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
@@ -498,13 +512,79 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
     }
     tc5::commit(wt.bar(B_SFULL + l));
   };
+  auto pv = [&](int l, uint64_t vd, bool begun) {
+#pragma unroll
+    for (int j = 0; j < C::TN / 16; ++j)
+      tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
+                  begun || j > 0);
+    if (TWO) {  // the weights' second parts
+#pragma unroll
+      for (int j = 0; j < C::TN / 16; ++j)
+        tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + C::TN / 2 + j * 8, vd + ((j * 16 * C::RB) >> 4),
+                    kIdescPV, true);
+    }
+  };
   bool ok = true;
   while (ok) {
     const Unit u = units.next();
     units.release();
     if (uniform(u.no) == 0) break;
     const int n0 = uniform(u.tiles0), n1 = C::LANES == 2 ? uniform(u.tiles1) : 0;
-    const int nt = max(n0, n1), checked = (uniform(u.t0) + 1) / C::TN;
+    const int nt = uniform(u.tiles), checked = (uniform(u.t0) + 1) / C::TN;
+    if constexpr (SHARED) {  // tile t is lane t % 2's, one Q is both's
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        if (!ok || l >= nt) continue;
+        ok = wt.wait_warp(B_KVFULL + stage, phase);
+        if (l == 0) {
+          ok = ok && wt.wait_warp(B_QFULL, qn & 1);
+          qn ^= 1;
+        }
+        tc5::fence_after();
+        if (ok && tc5::elect()) {
+          qk(l, 0, stage);
+          tc5::commit(wt.bar(B_KVEMPTY + stage));
+          if (l + 1 == nt) tc5::commit(wt.bar(B_QEMPTY));
+        }
+        __syncwarp();
+        next(stage, phase);
+      }
+      for (int t2 = 0; ok && t2 < nt; t2 += 2) {
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+          const int t = t2 + l, vst = stage;
+          if (!ok || t >= nt) continue;
+          ok = wt.wait_warp(B_KVFULL + stage, phase);
+          if (ok && t >= checked) {
+            ok = wt.wait_warp(B_VOK + stage, (vok >> stage) & 1);
+            vok ^= 1u << stage;
+          }
+          next(stage, phase);
+          const int kst = stage;
+          if (t + 2 < nt) {
+            ok = ok && wt.wait_warp(B_KVFULL + stage, phase);
+            next(stage, phase);
+          }
+          const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + vst * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+          ok = ok && wt.wait_warp(B_PREADY + l, (pn >> l) & 1);
+          pn ^= 1u << l;
+          if (!ok) continue;
+          tc5::fence_after();
+          if (tc5::elect()) {
+            pv(l, vd, ((t >> 1) & seg) > 0);
+            tc5::commit(wt.bar(B_KVEMPTY + vst));
+            if (t + 2 >= nt || (((t >> 1) + 1) & seg) == 0) tc5::commit(wt.bar(B_ODONE + l));
+            if (t + 2 < nt) {
+              qk(l, 0, kst);
+              tc5::commit(wt.bar(B_KVEMPTY + kst));
+              if (t + 3 == nt) tc5::commit(wt.bar(B_QEMPTY));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      continue;
+    }
     auto tiles = [&](int l) { return l ? n1 : n0; };
     // the unit's first scores
     ok = wt.wait_warp(B_KVFULL + stage, phase);
@@ -515,7 +595,7 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
       qn ^= 1u << l;
       tc5::fence_after();
       if (ok && tc5::elect()) {
-        qk(l, stage);
+        qk(l, l, stage);
         if (l == (n1 > 0)) tc5::commit(wt.bar(B_KVEMPTY + stage));
         if (tiles(l) == 1) tc5::commit(wt.bar(B_QEMPTY + l));
       }
@@ -544,21 +624,12 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
         if (!ok) continue;
         tc5::fence_after();
         if (tc5::elect()) {
-#pragma unroll
-          for (int j = 0; j < C::TN / 16; ++j)
-            tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
-                        (t & seg) > 0 || j > 0);
-          if (TWO) {  // the weights' second parts
-#pragma unroll
-            for (int j = 0; j < C::TN / 16; ++j)
-              tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + C::TN / 2 + j * 8,
-                          vd + ((j * 16 * C::RB) >> 4), kIdescPV, true);
-          }
+          pv(l, vd, (t & seg) > 0);
           if (l == (t < n1)) tc5::commit(wt.bar(B_KVEMPTY + vst));
           if (t + 1 == tiles(l) || ((t + 1) & seg) == 0) tc5::commit(wt.bar(B_ODONE + l));
           if (t + 1 < tiles(l)) {
             // after this step in the tensor cores' order: S may take P's place
-            qk(l, kst);
+            qk(l, l, kst);
             if (l == (t + 1 < n1)) tc5::commit(wt.bar(B_KVEMPTY + kst));
             if (t + 2 == tiles(l)) tc5::commit(wt.bar(B_QEMPTY + l));
           }
@@ -575,13 +646,13 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
 
 // ------------------------------------------------------------------ softmax ---
 
-template <int D, bool F32>
+template <int D, bool F32, bool SHARED>
 struct Soft {
   using C = Cfg<D>;
   const PromptAttnArgs& a;
   const Waits& wt;
   const uint32_t smem, tmem;  // tmem: with the warp's lanes
-  uint32_t sn = 0, on = 0;    // phases of the scores and of the finished sums
+  uint32_t sn = 0, on = 0, jn = 0;  // phases of the scores, of the finished sums and of the join
 
   static __device__ __forceinline__ int lane() { return threadIdx.x >> 7; }
   static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
@@ -675,8 +746,9 @@ struct Soft {
   // through shared memory (swizzled: no two of a row's or a column's share a bank), so that
   // the warp's stores are whole 128-byte lines.  (A row to a thread, 32 lines a store, took
   // 2.9 us a unit at head_dim 128, as long as two tiles.)  F32, g > 0: added to g times what
-  // is there (of the row, by the same thread).
-  __device__ __forceinline__ void store_rows(const Unit& u, float f, float g) const {
+  // is there (of the row, by the same thread).  joint: f times lane 0's O, and f1 times lane
+  // 1's unless that is 0; the lanes' warps do the rounds in turn.
+  __device__ __forceinline__ void store_rows(const Unit& u, float f, float g, bool joint, float f1, bool both) const {
     constexpr int BYTES = F32 ? 4 : 2;
     constexpr int COLS = D * BYTES < 128 ? D : 128 / BYTES;  // of a round
     constexpr int PPR = COLS * BYTES / 16;                   // pieces of a row
@@ -684,23 +756,34 @@ struct Soft {
     const uint32_t st = smem + C::OFF_OUT + (threadIdx.x >> 5) * 4096;
     auto at = [&](int row, int piece) { return st + row * (PPR * 16) + ((piece ^ (row & (PPR - 1))) << 4); };
     // the lane's first token, and how many it has
-    const int t0 = u.t0 + lane() * a.T, tokens = min(a.T, u.n - t0);
+    const int t0 = u.t0 + (joint ? 0 : lane() * a.T), tokens = min(a.T, u.n - t0);
     char* const base = static_cast<char*>(a.out) + (((int64_t)u.c0 + t0) * heads + u.h * a.gq) * (D * BYTES);
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += COLS) {
+      if (SHARED && joint && (c0 / COLS & 1) != lane()) continue;
 #pragma unroll
       for (int c = 0; c < COLS; c += 32) {
         float o[32];
-        tc5::ld32(tmem + C::O0 + lane() * D + c0 + c, reinterpret_cast<uint32_t*>(o));
+        tc5::ld32(tmem + C::O0 + (joint ? 0 : lane() * D) + c0 + c, reinterpret_cast<uint32_t*>(o));
         tc5::wait_ld();
         tc5::pin32(reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= f;
+        if (SHARED && both) {
+          float p[32];
+          tc5::ld32(tmem + C::O0 + D + c0 + c, reinterpret_cast<uint32_t*>(p));
+          tc5::wait_ld();
+          tc5::pin32(reinterpret_cast<uint32_t*>(p));
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(p[i], f1, o[i]);
+        }
 #pragma unroll
         for (int i = 0; i < 32 * BYTES / 16; ++i) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = F32 ? __float_as_uint(o[(4 * i + k) & 31] * f)
-                       : ptx::pack_h2(o[(8 * i + 2 * k) & 31] * f, o[(8 * i + 2 * k + 1) & 31] * f);
+            w[k] = F32 ? __float_as_uint(o[(4 * i + k) & 31])
+                       : ptx::pack_h2(o[(8 * i + 2 * k) & 31], o[(8 * i + 2 * k + 1) & 31]);
           sts_v4(at(lid, c * BYTES / 16 + i), make_uint4(w[0], w[1], w[2], w[3]));
         }
       }
@@ -749,6 +832,15 @@ struct Soft {
     }
   }
 
+  // All the softmax warps of the block, for lanes that share their rows.
+  __device__ __forceinline__ bool together() {
+    tc5::fence_before();
+    wt.arrive_warp(B_JOIN);
+    const bool ok = wt.wait_warp(B_JOIN, jn++ & 1);
+    tc5::fence_after();
+    return ok;
+  }
+
   __device__ __forceinline__ void run(const Unit* unit) {
     UnitReader units = {wt, unit};
     while (true) {
@@ -757,15 +849,46 @@ struct Soft {
       if (u.no == 0) return;
       const int n = lane() ? u.tiles1 : u.tiles0;
       if (n == 0) continue;
-      const int in = (int)(((uint32_t)r() * a.gq_mul) >> 16), tok = u.t0 + lane() * a.T + in;
+      const bool joint = SHARED && u.tiles1 > 0;  // both lanes have sums of the rows
+      const int in = (int)(((uint32_t)r() * a.gq_mul) >> 16), tok = u.t0 + (SHARED ? 0 : lane() * a.T) + in;
       const bool live = in < a.T && tok < u.n;
       const bool warp_live = __any_sync(0xffffffffu, live);
-      int visible = live ? tok + 1 : 1 << 30;  // rows that are not there need no mask
+      // (rows that are not there need no mask)
+      int visible = live ? tok + 1 - (SHARED ? lane() * C::TN : 0) : 1 << 30;
       constexpr int seg = F32 ? kSegment - 1 : 0x7fffffff;
       float m = -INFINITY, l = 0.0f, m_out = 0.0f;
       bool begun = false;  // the output has sums, at the reference m_out
-      // what those weigh at the reference now: never zero, so that an infinite one stays so
-      auto weight = [&] { return !begun ? 0.0f : m == m_out ? 1.0f : fmaxf(ptx::ex2_ftz((m_out - m) * a.scale_log2), 1.17549435e-38f); };
+      // what sums at a reference weigh at one that is not below it: never zero, so that an
+      // infinite one stays so
+      auto weight = [&](float from, float to) {
+        return from == to ? 1.0f : fmaxf(ptx::ex2_ftz((from - to) * a.scale_log2), 1.17549435e-38f);
+      };
+      // the sums so far to the output; both: lane 1's are not there already
+      auto store = [&](bool last, bool both) {
+        float top = m, f0 = 1.0f, f1 = 0.0f, sum = l;
+        if (joint) {
+          const uint32_t at = smem + C::OFF_OUT + (threadIdx.x & 31) * 8;
+          sts(at + (threadIdx.x >> 5) * 4096, __float_as_uint(m));
+          sts(at + (threadIdx.x >> 5) * 4096 + 4, __float_as_uint(l));
+          if (!together()) return false;
+          const uint32_t of = at + ((threadIdx.x >> 5) ^ 4) * 4096;
+          const float om = __uint_as_float(lds(of)), ol = __uint_as_float(lds(of + 4));
+          if (!together()) return false;  // (rows go where these were)
+          top = fmaxf(m, om);
+          f0 = weight(lane() ? om : m, top), f1 = weight(lane() ? m : om, top);
+          sum = fmaf(lane() ? ol : l, f0, (lane() ? l : ol) * f1);
+        }
+        const float inv = last ? 1.0f / sum : 1.0f;  // (of scores that are all -inf: NaN, as of NaN ones)
+        if (warp_live)
+          store_rows(u, f0 * inv, F32 && begun ? weight(m_out, top) * inv : 0.0f, joint, f1 * inv, joint && both);
+        if (joint && !together()) return false;
+        m_out = top;
+        begun = true;
+        if (last && warp_live && wt.word(W_NOTED) == (uint32_t)u.no && live && !(joint && lane()))
+          notes(tok + 1, inv, (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D);
+        return true;
+      };
+      const int end = joint ? u.tiles0 : n;
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {
         if (!wt.wait_warp(B_SFULL + lane(), sn++ & 1)) return;
@@ -773,24 +896,21 @@ struct Soft {
         if (warp_live) tile(visible, (t & seg) > 0, m, l);
         tc5::fence_before();
         wt.arrive_warp(B_PREADY + lane());
-        if (live) visible -= C::TN;
-        if (((t + 1) & seg) == 0 && t + 1 < n) {
+        if (live) visible -= SHARED ? 2 * C::TN : C::TN;
+        if (((t + 1) & seg) == 0 && t + 1 < end) {
           if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
           tc5::fence_after();
-          if (warp_live) store_rows(u, 1.0f, weight());
-          m_out = m;
-          begun = true;
+          if (!store(false, true)) return;
           tc5::fence_before();
         }
       }
-      if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
-      tc5::fence_after();
-      if (warp_live) {
-        const float inv = 1.0f / l;  // (of scores that are all -inf: NaN, as of NaN ones)
-        store_rows(u, inv, weight() * inv);
-        if (wt.word(W_NOTED) == (uint32_t)u.no && live)
-          notes(tok + 1, inv, (((int64_t)u.c0 + tok) * a.Hkv * a.gq + u.h * a.gq + (r() - in * a.gq)) * D);
+      // lane 1's sums may have gone with a segment of lane 0's
+      const bool rest = (u.tiles1 & seg) != 0 || u.tiles1 == u.tiles0;
+      if (!(joint && lane()) || rest) {
+        if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
+        tc5::fence_after();
       }
+      if (!store(true, rest)) return;
       tc5::fence_before();
       __threadfence_block();
       __syncwarp();
@@ -801,7 +921,7 @@ struct Soft {
 
 // ------------------------------------------------------------------- kernel ---
 
-template <int D, bool F32>
+template <int D, bool F32, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -821,6 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       if (i == B_PREADY || i == B_PREADY + 1) n = 4;
       if (i == B_SFULL || i == B_SFULL + 1) n = 1 + a.fault;
       if (i == B_UEMPTY) n = C::SMW + 3;
+      if (i == B_JOIN) n = C::SMW;
       if (i >= B_KVEMPTY && i < B_KVEMPTY + kMaxStages) n = 2;
       ptx::mbar_init(smem + C::OFF_BAR + 8 * i, n);
     }
@@ -841,15 +962,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp < 8) {
     tc5::regs_inc<208>();
     if (warp < C::SMW) {
-      Soft<D, F32> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
+      Soft<D, F32, SHARED> soft = {a, wt, smem, tmem + ((uint32_t)(warp & 3) << 21)};
       soft.run(unit);
     }
   } else {
     tc5::regs_dec<88>();
-    if (warp == 8) mma_role<D, F32>(wt, smem, tmem, unit);
-    if (warp == 9) load_role<D>(a, wt, smem, unit);
-    if (warp == 10) check_role<D>(a, wt, smem, unit);
-    if (warp == 11) unit_role<D>(a, wt, smem, unit);
+    if (warp == 8) mma_role<D, F32, SHARED>(wt, smem, tmem, unit);
+    if (warp == 9) load_role<D, SHARED>(a, wt, smem, unit);
+    if (warp == 10) check_role<D, SHARED>(a, wt, smem, unit);
+    if (warp == 11) unit_role<D, SHARED>(a, wt, smem, unit);
     __syncwarp();
   }
   tc5::fence_before();
@@ -859,10 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp == 8) tc5::dealloc(tmem, 512);
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool SHARED>
 cudaError_t launch_as(const PromptAttnArgs& a, int grid, cudaStream_t st) {
   static_assert(Cfg<D>::SMEM <= 227 * 1024, "shared memory of a block");
-  auto kernel = prompt_attn_kernel<D, F32>;
+  auto kernel = prompt_attn_kernel<D, F32, SHARED>;
   // the kernel's attributes, once per device
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -883,7 +1004,9 @@ cudaError_t launch_as(const PromptAttnArgs& a, int grid, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch(const PromptAttnArgs& a, int grid, cudaStream_t st) {
-  return a.out_f32 ? launch_as<D, true>(a, grid, st) : launch_as<D, false>(a, grid, st);
+  if constexpr (Cfg<D>::LANES == 2)
+    if (a.shared) return a.out_f32 ? launch_as<D, true, true>(a, grid, st) : launch_as<D, false, true>(a, grid, st);
+  return a.out_f32 ? launch_as<D, true, false>(a, grid, st) : launch_as<D, false, false>(a, grid, st);
 }
 
 }  // namespace prompt

@@ -53,6 +53,15 @@ def ints(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
 
+# Prompts without tokens behind the others: there could be more blocks of rows than SMs, and
+# a block's two lanes have rows of their own; with few, both have the same ones.
+EMPTY = pytest.mark.parametrize("empty", [0, 200])
+
+
+def ends(lens, empty=0):
+    return ints(np.concatenate([[0], np.cumsum(list(lens) + [0] * empty)]))
+
+
 def check(got, q, k, v, lens, first=0):
     at = first
     for n in lens:
@@ -67,10 +76,11 @@ def check(got, q, k, v, lens, first=0):
 @pytest.mark.parametrize("lens", [[1], [2, 1, 3], [77], [128], [129, 64, 127, 0, 300], [513], [1025, 1]])
 @pytest.mark.parametrize("hq,hkv,d", [(1, 1, 32), (4, 1, 64), (6, 2, 128), (8, 2, 128), (5, 1, 64), (3, 3, 128),
                                       (2, 2, 256), (8, 1, 256), (16, 2, 32), (71, 1, 64), (128, 1, 128)])
-def test_prompts(lens, hq, hkv, d):
+@EMPTY
+def test_prompts(lens, hq, hkv, d, empty):
     total = sum(lens)
     q, k, v = inputs(total + d, total, hq, hkv, d)
-    cu = ints(np.concatenate([[0], np.cumsum(lens)]))
+    cu = ends(lens, empty)
     out = kvq.kvq_prompt_attention(q, k, v, cu, max(lens))
     assert out.dtype == torch.float16
     check(out, q, k, v, lens)
@@ -88,17 +98,36 @@ def test_many_ragged_prompts(hq, hkv, d):
     check(kvq.kvq_prompt_attention(q, k, v, cu, max(lens)), q, k, v, lens)
 
 
-@pytest.mark.parametrize("n,hq,hkv,d", [(9001, 8, 2, 128), (20000, 2, 1, 64), (6000, 2, 2, 128), (5000, 2, 1, 256)])
-def test_long_prompts(n, hq, hkv, d):
+@pytest.mark.parametrize("n,hq,hkv,d", [(9001, 8, 2, 128), (20000, 2, 1, 64), (6000, 2, 2, 128), (5000, 2, 1, 256),
+                                      (4353, 1, 1, 64), (6200, 1, 1, 32)])
+@EMPTY
+def test_long_prompts(n, hq, hkv, d, empty):
     q, k, v = inputs(n, n, hq, hkv, d, scale=2.0)
-    out = kvq.kvq_prompt_attention(q, k, v, ints([0, n]), n, flags=kvq.KVQ_OUT_F32)
+    out = kvq.kvq_prompt_attention(q, k, v, ends([n], empty), n, flags=kvq.KVQ_OUT_F32)
     rows = torch.cat([torch.arange(300), torch.randint(300, n - 300, (400,), generator=torch.Generator().manual_seed(1)),
                       torch.arange(n - 300, n)]).to(DEV)
     want, bound = plain(q, k, v, rows, f32=True)
     err = (out[rows].double() - want).abs()
     assert (err <= bound).all(), float((err / bound).max())
-    again = kvq.kvq_prompt_attention(q, k, v, ints([0, n]), n, flags=kvq.KVQ_OUT_F32)
+    again = kvq.kvq_prompt_attention(q, k, v, ends([n], empty), n, flags=kvq.KVQ_OUT_F32)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@EMPTY
+def test_values_of_one_sign_add_up(d, empty):
+    """Sums that are cut off fall short of these, more with each tile; rows of all numbers of
+    tiles about a segment's and two segments' for each lane."""
+    n = 4500
+    q, k, v = inputs(d, n, 1, 1, d, scale=0.1)
+    v = v.abs()
+    out = kvq.kvq_prompt_attention(q, k, v, ends([n], empty), n, flags=kvq.KVQ_OUT_F32)
+    want, _ = plain(q, k, v, f32=True)
+    # a sum that is cut off to 24 bits is off by up to a whole step, 2^-23 (not half of one, which
+    # 2^-16 in all stood for), of what it is then, half of the segment's on average, in 16 tiles
+    # of 8 steps for each of the weights' parts: 2^-16; the exponentials 2^-19, scores
+    # (d + 2) 2^-23 of products of at most 1 / 4: 2^-18; the rest 2^-20: under 2^-16 + 2^-17
+    assert float(((out.double() - want).abs() / want).max()) < 1.5 * 2.0 ** -16
 
 
 def test_layouts_and_rows_of_no_prompt():
@@ -142,12 +171,13 @@ def test_broken_entries_cost_no_other_prompt():
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (2, 2, 64), (2, 1, 256), (1, 1, 32)])
-def test_what_a_row_does_not_see_has_no_part(hq, hkv, d):
+@EMPTY
+def test_what_a_row_does_not_see_has_no_part(hq, hkv, d, empty):
     """NaN and infinities in later tokens and in other prompts, keys and values alike."""
     lens = [70, 200, 1, 333]
     total = sum(lens)
     q, k, v = inputs(d, total, hq, hkv, d)
-    cu = ints(np.concatenate([[0], np.cumsum(lens)]))
+    cu = ends(lens, empty)
     want = kvq.kvq_prompt_attention(q, k, v, cu, 333)
     for value in (float("nan"), float("inf"), -float("inf")):
         for at in (0, 69, 70, 130, 199, 269, 270, 271, 400, 603):
@@ -162,14 +192,15 @@ def test_what_a_row_does_not_see_has_no_part(hq, hkv, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_infinite_values_that_are_seen(d):
+@EMPTY
+def test_infinite_values_that_are_seen(d, empty):
     """Single columns: the sign of the infinity where one sign is seen, NaN where both are or
     where NaN is, from the token on; other columns as ever.  Scores near each other, so that
     no weight vanishes."""
     hq, hkv, n = 4, 2, 300
     q, k, v = inputs(d, n, hq, hkv, d)
     q, k = q * 0.25, k * 0.25
-    cu = ints([0, n])
+    cu = ends([n], empty)
     want = kvq.kvq_prompt_attention(q, k, v, cu, n)
     v2 = v.clone()
     v2[20, 0, 3], v2[150, 0, 7], v2[160, 1, 9] = math.inf, -math.inf, math.nan
@@ -182,11 +213,12 @@ def test_infinite_values_that_are_seen(d):
     assert np.array_equal(to_np(got), to_np(expect), equal_nan=True)
 
 
-def test_scores_that_are_not_finite():
+@EMPTY
+def test_scores_that_are_not_finite(empty):
     n, d = 200, 64
     q, k, v = inputs(5, n, 2, 1, d)
     q, k, v = q.clone(), k.clone(), v
-    cu = ints([0, n])
+    cu = ends([n], empty)
     want = kvq.kvq_prompt_attention(q, k, v, cu, n)
     q[50, 1] = math.nan                                   # a query
     got = kvq.kvq_prompt_attention(q, k, v, cu, n)
@@ -244,9 +276,10 @@ def test_streams_and_graphs():
     check(out, q2, k2, v2, lens)
 
 
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_whole():
+@EMPTY
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_whole(empty):
     q, k, v = inputs(6, 500, 8, 2, 128)
-    cu, g = ints([0, 500]), gpu_cache(1, 1, 32, 4, 32, 0)
+    cu, g = ends([500], empty), gpu_cache(1, 1, 32, 4, 32, 0)
     want = kvq.kvq_prompt_attention(q, k, v, cu, 500)
     kvq.kvq_testing_wait_fault(2000)
     try:
