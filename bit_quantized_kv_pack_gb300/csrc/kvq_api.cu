@@ -329,9 +329,10 @@ kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* vie
 
 namespace {
 // One tensor of kvq_rotate: its heads, strides and places.
-kvq_status check_rows(const void* x, const void* y, int32_t heads, int64_t st, int64_t sh, int64_t yt,
-                      int64_t yh) {
+kvq_status check_rows(const void* x, const void* y, int32_t total, int32_t heads, int64_t st, int64_t sh,
+                      int64_t yt, int64_t yh) {
   if (!y || heads < 1 || st < 0 || sh < 0 || yt < 0 || yh < 0) return KVQ_ERR_INVALID_ARG;
+  if ((total > 1 && yt == 0) || (heads > 1 && yh == 0)) return KVQ_ERR_INVALID_ARG;  // one place for many rows
   if (x == y && (st != yt || sh != yh)) return KVQ_ERR_INVALID_ARG;  // in place: the same rows
   // every 8-value piece a lane moves must start on a 16-byte boundary
   if (!aligned(x, 16) || !aligned(y, 16) || st % 8 || sh % 8 || yt % 8 || yh % 8) return KVQ_ERR_MISALIGNED;
@@ -353,10 +354,10 @@ kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
     for (int i = 0; i < A.rotary_dim / 2; ++i)
       if (A.pair_axis[i] >= A.axes) return KVQ_ERR_INVALID_ARG;
   kvq_status st;
-  if (A.q && (st = check_rows(A.q, A.q_out, A.num_q_heads, A.q_stride_token, A.q_stride_head,
+  if (A.q && (st = check_rows(A.q, A.q_out, A.total, A.num_q_heads, A.q_stride_token, A.q_stride_head,
                               A.q_out_stride_token, A.q_out_stride_head)) != KVQ_OK)
     return st;
-  if (A.k && (st = check_rows(A.k, A.k_out, A.num_kv_heads, A.k_stride_token, A.k_stride_head,
+  if (A.k && (st = check_rows(A.k, A.k_out, A.total, A.num_kv_heads, A.k_stride_token, A.k_stride_head,
                               A.k_out_stride_token, A.k_out_stride_head)) != KVQ_OK)
     return st;
   if (!aligned(A.rope, 16) || !aligned(A.positions, 4) || !aligned(A.err_word, 4)) return KVQ_ERR_MISALIGNED;
@@ -370,7 +371,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream) {
       A.num_q_heads % A.num_kv_heads || A.head_dim < 32 || A.head_dim % 32 || (A.flags & ~(uint32_t)KVQ_OUT_F32))
     return KVQ_ERR_INVALID_ARG;
   if (A.total > 0 && (!A.q || !A.k || !A.v || !A.out)) return KVQ_ERR_INVALID_ARG;
-  if (!head_dim_ok(A.head_dim) || A.num_q_heads / A.num_kv_heads > 128 || A.total > (1 << 30) || A.batch > (1 << 24))
+  if (!head_dim_ok(A.head_dim) || A.num_q_heads / A.num_kv_heads > 128 || A.total > (1 << 30) || A.batch > (1 << 20))
     return KVQ_ERR_UNSUPPORTED;
   const int64_t strides[6] = {A.q_stride_token, A.k_stride_token, A.v_stride_token,
                               A.q_stride_head,  A.k_stride_head,  A.v_stride_head};
@@ -409,7 +410,7 @@ kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream) {
       (A.flags & ~(uint32_t)KVQ_LOGITS_F32) || A.stride_row < A.vocab)
     return KVQ_ERR_INVALID_ARG;
   if (A.finished && (A.end_token < 0 || A.end_token >= A.vocab)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(A.logits, 16) || !aligned(A.workspace, 16) || !aligned(A.scores, 4) || !aligned(A.parent, 4) ||
+  if (!aligned(A.logits, A.flags & KVQ_LOGITS_F32 ? 4 : 2) || !aligned(A.workspace, 16) || !aligned(A.scores, 4) || !aligned(A.parent, 4) ||
       !aligned(A.token, 4) || !aligned(A.score, 4) || !aligned(A.err_word, 4))
     return KVQ_ERR_MISALIGNED;
   if (A.ws_bytes < kvq::beam_workspace_bytes(A.batch, A.beams, A.vocab, A.n)) return KVQ_ERR_INVALID_ARG;

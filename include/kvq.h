@@ -508,7 +508,7 @@ typedef struct {
   int64_t q_stride_head;
   int64_t k_stride_token;
   int64_t k_stride_head;
-  int64_t q_out_stride_token;
+  int64_t q_out_stride_token; /* (positive where there is more than one row or head) */
   int64_t q_out_stride_head;
   int64_t k_out_stride_token;
   int64_t k_out_stride_head;
@@ -551,9 +551,9 @@ typedef struct {
   int32_t num_q_heads;     /* Hq, at most 128 Hkv */
   int32_t num_kv_heads;    /* Hkv */
   int32_t head_dim;        /* 32, 64, 128 or 256 */
-  int32_t batch;           /* B */
+  int32_t batch;           /* B, at most 2^20 */
   const int32_t* cu_seqlens; /* as for the calls on runs: prompt b is rows */
-  int32_t total;           /*   [cu_seqlens[b], cu_seqlens[b + 1]) of q, k, v and out */
+  int32_t total;           /*   [cu_seqlens[b], cu_seqlens[b + 1]) of q, k, v and out (at most 2^30) */
   int32_t max_len;
   void* out;               /* device [total][Hq][d], fp16 (fp32 with KVQ_OUT_F32); overlaps no input */
   uint32_t flags;          /* 0 or KVQ_OUT_F32 */
@@ -566,24 +566,27 @@ typedef struct {
  * Weights are rounded to fp16 once (operands of the tensor cores; weights below 2^-21 of a
  * row's largest by at most 2^-32 of that), with KVQ_OUT_F32 they are two fp16 parts (22 bits);
  * scores and sums are fp32, the output is rounded once.  The tensor cores cut their sums off
- * (2^-25 a step of 16 tokens, towards zero): fp32 output is within 1e-5 of the sums of
+ * (2^-23 a step of 16 tokens, towards zero): fp32 output is within 2e-5 of the sums of
  * values of one sign and about 1e-6 of others, whatever the length.  Results do not depend
- * on timing.  Tokens a row does not attend over, other prompts' among them, have no part in
+ * on timing; the order of a row's sums goes by how many blocks of rows there can be (total,
+ * batch and heads), so that a prompt may differ in its last bits from the same one in
+ * another batch.  Tokens a row does not attend over, other prompts' among them, have no part in
  * its output, whatever they hold.  Entries of cu_seqlens that break the rule set
- * KVQ_ERRBIT_BADLEN.  Asynchronous; lengths are read on the device. */
+ * KVQ_ERRBIT_BADLEN (where they let prompts overlap, some may stay unwritten).
+ * Asynchronous; lengths are read on the device. */
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream);
 
 /* Arguments of kvq_beam_select; zero-initialise the struct. */
 typedef struct {
-  const void* logits;      /* device, 16-byte aligned: token t of row r at r * stride_row + t;
+  const void* logits;      /* device: token t of row r at r * stride_row + t, rows at any place;
                               fp16, or fp32 with KVQ_LOGITS_F32.  Row b * beams + w is beam w
                               of batch entry b */
   int64_t stride_row;      /* in elements, >= vocab */
   const float* scores;     /* fp32 device [batch * beams]: the beams' sums of log-probabilities */
   const uint8_t* finished; /* device [batch * beams], non-zero: the beam is complete; or NULL */
-  int32_t batch;
+  int32_t batch;           /* at most 65535 rows in all */
   int32_t beams;           /* W, 1..32 */
-  int32_t vocab;           /* V */
+  int32_t vocab;           /* V, W V < 2^31 - 1 */
   int32_t n;               /* selected per batch entry: 1..32, at most W V */
   int32_t end_token;       /* what a complete beam goes on with, 0..V-1 (read only with finished) */
   uint32_t flags;          /* 0 or KVQ_LOGITS_F32 */

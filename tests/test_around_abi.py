@@ -42,6 +42,7 @@ def _rotate(lib, **kw):
     (dict(q_stride_token=-8), INVALID), (dict(k_out_stride_head=-8), INVALID),
     (dict(q_stride_head=12), MISALIGNED), (dict(k_stride_token=1028), MISALIGNED),
     (dict(q_out_stride_token=4), MISALIGNED), (dict(q=0x100008), MISALIGNED), (dict(k_out=0x400002), MISALIGNED),
+    (dict(q_out_stride_token=0), INVALID), (dict(k_out_stride_head=0), INVALID),
     (dict(rope=0x500008), MISALIGNED), (dict(positions=0x600002), MISALIGNED), (dict(err_word=0x700001), MISALIGNED),
     (dict(q_out=0x100000, q_out_stride_head=256), INVALID),  # in place, other rows
 ])
@@ -63,7 +64,7 @@ def _prompt(lib, **kw):
     (dict(cu_seqlens=0), INVALID), (dict(batch=0), INVALID), (dict(total=-1), INVALID), (dict(max_len=-1), INVALID),
     (dict(num_kv_heads=0), INVALID), (dict(num_q_heads=0), INVALID), (dict(num_q_heads=12), INVALID),
     (dict(num_q_heads=129, num_kv_heads=1), UNSUPPORTED), (dict(head_dim=24), INVALID), (dict(head_dim=96), UNSUPPORTED),
-    (dict(total=(1 << 30) + 1), UNSUPPORTED), (dict(batch=(1 << 24) + 1), UNSUPPORTED), (dict(flags=1), INVALID),
+    (dict(total=(1 << 30) + 1), UNSUPPORTED), (dict(batch=(1 << 20) + 1), UNSUPPORTED), (dict(flags=1), INVALID),
     (dict(q_stride_token=-8), INVALID), (dict(v_stride_head=-8), INVALID), (dict(k_stride_token=1028), MISALIGNED),
     (dict(k_stride_head=0), UNSUPPORTED), (dict(v_stride_token=0), UNSUPPORTED), (dict(q_stride_token=1 << 32), UNSUPPORTED),
     (dict(q=0x100008), MISALIGNED), (dict(v=0x300002), MISALIGNED), (dict(out=0x500008), MISALIGNED),
@@ -89,7 +90,8 @@ def _select(lib, **kw):
     (dict(beams=1, vocab=7, n=8), INVALID), (dict(batch=16384, beams=4), UNSUPPORTED),
     (dict(beams=32, vocab=1 << 26, stride_row=1 << 26), UNSUPPORTED), (dict(stride_row=999), INVALID),
     (dict(flags=2), INVALID), (dict(ws_bytes=100), INVALID), (dict(finished=0x700000, end_token=1000), INVALID),
-    (dict(finished=0x700000, end_token=-1), INVALID), (dict(logits=0x100002), MISALIGNED),
+    (dict(finished=0x700000, end_token=-1), INVALID), (dict(logits=0x100001), MISALIGNED),
+    (dict(logits=0x100002, flags=1), MISALIGNED),
     (dict(scores=0x200002), MISALIGNED), (dict(workspace=0x600008), MISALIGNED), (dict(score=0x500001), MISALIGNED),
     (dict(err_word=0x700002), MISALIGNED),
 ])

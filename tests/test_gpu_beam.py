@@ -164,6 +164,12 @@ def test_rows_apart_and_rows_of_any_alignment():
         wide = torch.full((2, 3, width), float("nan"), dtype=dtype, device=DEV)  # what lies between has no part
         wide[..., :V] = torch.from_numpy(rng.standard_normal((2, 3, V))).to(DEV)
         check(wide[..., :V], scores, 6)
+    for dtype in (torch.float16, torch.float32):  # the last token's logits of each row, an odd vocabulary
+        steps = torch.from_numpy(rng.standard_normal((4, 3, 1, 2503))).to(DEV).to(dtype)
+        for at in (1, 2):
+            x = steps[:, at]
+            assert x.data_ptr() % 16
+            check(x, scores.reshape(6, 1)[:4].copy(), 7)
     with pytest.raises(ValueError, match="one stride"):
         kvq.kvq_beam_select(torch.zeros(2, 4, 8, 50, dtype=torch.float16, device=DEV)[:, :, 1][:, :3],
                             torch.zeros(2, 3, device=DEV), 2)
