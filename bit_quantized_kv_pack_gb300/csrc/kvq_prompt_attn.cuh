@@ -11,7 +11,7 @@
 // of it below), the output once; scores, m, l and O are fp32.  For fp32 output the weights
 // are two fp16 parts, P and what its rounding left, each times V; and as the tensor cores'
 // sums are cut off, not rounded (2^-23 of O a step, all towards zero: 6e-5 over 16384 tokens
-// of values of one sign), every kSegment tiles O goes to the output's fp32 sums.
+// of values of one sign), every kSegment tokens O goes to the output's fp32 sums.
 //
 // A block (one per SM, persistent) has 12 warps:
 //   0-7   softmax: a thread per query row, four warps for each of the two accumulators
@@ -19,11 +19,22 @@
 //         MMA, the epilogue.
 //   8     issues the MMAs: the lanes' steps in turn, so that the softmax of one runs under
 //         the MMAs of the other.
-//   9     loads Q, K and V (TMA tiles, 128-byte swizzle; K and V through one ring).
+//   9     loads Q, K and V (TMA tiles, 128-byte swizzle).  A slot of the ring has what a batch
+//         of MMAs takes, a tile's values and a later tile's keys, under one barrier.
 //   10    looks at values that some row of the block does not see (the tiles at the
 //         diagonal): a weight of zero would turn an infinite one into NaN.
 //   11    works out the units.
-// head_dim 256 has room for one lane and tiles of 64 tokens.
+// head_dim 256 has room for one lane, tiles of 64 tokens, and the scores of two: the next
+// tile's are there when a tile's weights are done (8192 tokens' worth of 32 heads on 8,
+// 4096 each: 265 -> 220 us).  Two smaller tiles of scores in place of one made head_dim 128
+// 33 % slower (Q is read from shared memory for each) and 64 up to 70 %.
+//
+// Bound: at head_dim 128 the tensor cores take 2048 cycles for a tile of both lanes, and a
+// lane's own chain about 2600: softmax 1120 (loads from TMEM to the first exponential 280,
+// exponentials and weights 750), the MMA warp's waits, two batches of MMAs.  The MMA warp
+// itself is busy for about 1050 cycles a batch, which is what bounds head_dim 64.
+// 16384 tokens of 32 heads on 8: 1360 us (1.62 PFLOP/s, 1270 between others of its kind);
+// 16 prompts of 115 to 2048 tokens: 176 us.
 //
 // Where there cannot be more units than SMs, a unit is T tokens, and its two lanes have the
 // same rows: every second tile is lane 1's, and the lanes' sums meet in the epilogue, each
@@ -80,13 +91,14 @@ namespace prompt {
 
 constexpr int kThreads = 384;
 constexpr float kWeightBits = 7.0f;  // log2 of the weights' factor
-constexpr int kMaxStages = 8;
-constexpr int kSegment = 16;         // tiles whose values the tensor cores add up for fp32 output (a power of two)
+constexpr int kMaxStages = 4;
+constexpr int kSegment = 2048;       // tokens whose values the tensor cores add up for fp32 output (a power of two)
 
 template <int D>
 struct Cfg {
   static constexpr int LANES = prompt_lanes(D);
   static constexpr int TN = prompt_tile(D);
+  static constexpr int NB = D == 256 ? 2 : 1;  // tiles of scores that a lane has room for
   static constexpr int PW = prompt_panel(D);
   static constexpr int NP = D / PW;
   static constexpr int RB = PW * 2;  // bytes of a panel's row
@@ -95,7 +107,7 @@ struct Cfg {
   static constexpr int KP = TN * RB;   // of a panel of K or V
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int KBYTES = TN * D * 2;
-  static constexpr int ST = D >= 128 ? 4 : 8;  // stages of K and V
+  static constexpr int ST = D >= 128 ? 2 : 4;  // slots of the ring, values and keys each
   static constexpr int SMW = 4 * LANES;        // softmax warps
   // TMEM columns
   static constexpr int S0 = 0;
@@ -103,7 +115,7 @@ struct Cfg {
   // shared memory
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = OFF_Q + LANES * QBYTES;
-  static constexpr int OFF_OUT = OFF_KV + ST * KBYTES;  // 4 KiB of each softmax warp
+  static constexpr int OFF_OUT = OFF_KV + ST * 2 * KBYTES;  // 4 KiB of each softmax warp
   static constexpr int OFF_NOTES = OFF_OUT + SMW * 4096;  // int [3][D]
   static constexpr int OFF_BAR = OFF_NOTES + 3 * D * 4;
   static constexpr int OFF_UNIT = OFF_BAR + 512;  // Unit, and the answer of the launch control
@@ -120,8 +132,8 @@ struct alignas(16) Unit {
 };
 
 // Barriers (8 bytes each from OFF_BAR) and words behind them.
-enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 6, B_ODONE = 8, B_DRAIN = 10, B_UFULL = 11, B_UEMPTY = 12,
-       B_NEXT = 13, B_JOIN = 14, B_KVFULL = 15, B_KVEMPTY = B_KVFULL + kMaxStages, B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
+enum { B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PREADY = 8, B_ODONE = 12, B_DRAIN = 16, B_UFULL = 17,
+       B_UEMPTY = 18, B_NEXT = 19, B_JOIN = 20, B_KVFULL = 21, B_KVEMPTY = B_KVFULL + kMaxStages, B_VOK = B_KVEMPTY + kMaxStages, B_COUNT = B_VOK + kMaxStages };
 enum { W_TMEM = 96, W_ABORT = 97, W_NOTED = 98 /* the unit that the notes are of */, W_EPI = 99 };
 static_assert(B_COUNT * 2 <= W_TMEM, "words behind the barriers");
 
@@ -195,6 +207,14 @@ struct Waits {
     for (uint32_t k = 1; !ptx::mbar_try_wait(b, parity); ++k)
       if ((k & 63u) == 0 && late(t0)) return false;
     return true;
+  }
+  __device__ __forceinline__ bool test(int i, uint32_t parity) const {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar(i)), "r"(parity)
+                 : "memory");
+    return ok != 0;
   }
   // a whole warp waits; the same answer for all its lanes
   __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -346,25 +366,33 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
     ptx::prefetch_tensormap(&a.mv);
   }
   UnitReader units = {wt, unit};
-  uint32_t item = 0, qn[2] = {0, 0};  // half tiles so far, units of each lane
+  uint32_t item = 0, qn[2] = {0, 0};  // slots so far, units of each lane
   bool ok = true;
   while (ok) {
     const Unit u = units.next();
     if (u.no == 0) break;
-    auto kv = [&](int t, int w) {
-      const int stage = item % C::ST;
-      ok = ok && wt.wait_warp(B_KVEMPTY + stage, ((item / C::ST) & 1) ^ 1);
+    // values of tile tv (keys: its keys) and keys of tile tk into the next slot (none: -1)
+    auto fill = [&](int tv, int tk, bool keys) {
+      const int slot = item % C::ST;
+      ok = ok && wt.wait_warp(B_KVEMPTY + slot, ((item / C::ST) & 1) ^ 1);
       if (!ok) return;
       if (one) {
-        ptx::mbar_arrive_expect_tx(wt.bar(B_KVFULL + stage), C::KBYTES);
+        ptx::mbar_arrive_expect_tx(wt.bar(B_KVFULL + slot), ((tv >= 0) + (tk >= 0)) * C::KBYTES);
 #pragma unroll
-        for (int p = 0; p < C::NP; ++p)
-          tma_load(smem + C::OFF_KV + stage * C::KBYTES + p * C::KP, w ? &a.mv : &a.mk, p * C::PW, u.c0 + t * C::TN, u.h,
-                   wt.bar(B_KVFULL + stage));
+        for (int w = 0; w < 2; ++w) {
+          const int t = w ? tk : tv;
+          if (t < 0) continue;
+#pragma unroll
+          for (int p = 0; p < C::NP; ++p)
+            tma_load(smem + C::OFF_KV + (2 * slot + w) * C::KBYTES + p * C::KP, w || keys ? &a.mk : &a.mv, p * C::PW,
+                     u.c0 + t * C::TN, u.h, wt.bar(B_KVFULL + slot));
+        }
       }
       ++item;
     };
-    kv(0, 0);
+    constexpr int ahead = C::NB * (SHARED ? 2 : 1);  // (in the order in which the MMAs take them)
+    static_assert(ahead <= 2, "a unit's first keys have one slot");
+    fill(ahead == 2 && u.tiles > 1 ? 1 : -1, 0, true);
 #pragma unroll
     for (int l = 0; l < C::LANES; ++l) {
       if ((l ? u.tiles1 : u.tiles0) == 0 || (l && SHARED)) continue;
@@ -379,13 +407,7 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
       }
       ++qn[l];
     }
-    // (in the order in which the MMAs take them)
-    const int ahead = SHARED ? 2 : 1;
-    if (SHARED && u.tiles > 1) kv(1, 0);
-    for (int t = 0; ok && t < u.tiles; ++t) {
-      kv(t, 1);
-      if (t + ahead < u.tiles) kv(t + ahead, 0);
-    }
+    for (int t = 0; ok && t < u.tiles; ++t) fill(t, t + ahead < u.tiles ? t + ahead : -1, false);
     units.release();
   }
   // copies still in flight when the block gives up land before its shared memory goes
@@ -412,25 +434,21 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   UnitReader units = {wt, unit};
-  uint32_t item = 0, before = 0;  // half tiles of earlier units; those units' epilogues, a warp each
+  uint32_t item = 0, before = 0;  // slots so far; earlier units' epilogues, a warp each
   while (true) {
     const Unit u = units.next();
     units.release();
     if (u.no == 0) return;
-    const int nt = u.tiles, ahead = SHARED && nt > 1 ? 2 : 1;
     bool clean = false;  // the notes are this unit's
-    for (int half = 0; half < 2 * nt; ++half) {
-      const uint32_t it = item + half;
-      // first `ahead` tiles' keys, then values and keys in turn, then the last values
-      const int stage = it % C::ST, past = half - 2 * nt + ahead, t = past >= 0 ? nt - ahead + past : (half - ahead) >> 1;
-      const bool values = past >= 0 || (half >= ahead && !((half - ahead) & 1));
-      if (!wt.wait_warp(B_KVFULL + stage, (it / C::ST) & 1)) return;
+    for (int t = -1; t < u.tiles; ++t, ++item) {  // (keys alone first)
+      const int stage = item % C::ST;
+      if (!wt.wait_warp(B_KVFULL + stage, (item / C::ST) & 1)) return;
       // the block's first row sees tokens up to t0
-      if (!values || t < (u.t0 + 1) / C::TN) {
+      if (t < (u.t0 + 1) / C::TN) {
         wt.arrive_warp(B_KVEMPTY + stage);
         continue;
       }
-      const uint32_t tile = smem + C::OFF_KV + stage * C::KBYTES;
+      const uint32_t tile = smem + C::OFF_KV + 2 * stage * C::KBYTES;
       const int r0 = max(0, u.t0 + 1 - t * C::TN);  // rows before it are seen by all
       bool any = false;
 #pragma unroll 1
@@ -473,7 +491,6 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
       wt.arrive_warp(B_VOK + stage);
       wt.arrive_warp(B_KVEMPTY + stage);
     }
-    item += 2 * nt;
     before += (u.tiles0 > 0 ? 4 : 0) + (u.tiles1 > 0 ? 4 : 0);
   }
 }
@@ -482,46 +499,52 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
 
 // All lanes of the warp go the same way, so that descriptors and addresses stay in its
 // uniform registers, and one of them issues.  An MMA is taken up when the one before it is
-// nearly done, so what the warp does between two batches is added to the time: the waits
-// stand together before a lane's batch (its values, then its next scores), and the second
-// lane's are known to be over.
+// nearly done, so what the warp does between two batches is added to the time (a wait is
+// 120 cycles of it even when it is over): there is one for a slot, looked at while the
+// MMAs before it run, and one for a lane's weights (16 prompts 182 -> 176 us, 16384 tokens
+// 1395 -> 1355).
+//
+// A batch is tile k's values and tile k + NB's scores, which go where tile k's were.  Its end
+// is a phase of SFULL's barrier k % NB: those scores are there, and values up to tile k's are
+// in O.  Where the lane has no tile k + NB in the unit it is one of ODONE's instead, which
+// nothing comes after before the softmax has seen it.
 template <int D, bool TWO, bool SHARED>
 __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_t tmem, const Unit* ring) {
   using C = Cfg<D>;
+  constexpr int NB = C::NB;
   constexpr uint32_t kIdescQK = tc5::instr_desc(128, C::TN, false);
   constexpr uint32_t kIdescPV = tc5::instr_desc(128, D, true);
   UnitReader units = {wt, ring};
-  constexpr int seg = TWO ? kSegment - 1 : 0x7fffffff;  // (t & seg) == 0: O begins
+  constexpr int seg = TWO ? kSegment / C::TN - 1 : 0x7fffffff;  // (k & seg) == 0: O begins
   uint32_t qn = 0, pn = 0;     // phase bits of the lanes' barriers
   uint32_t vok = 0;            // and of the stages'
-  // the places of a unit's first keys in the ring
-  int stage = 0;
+  // the place in the ring
+  int slot = 0;
   uint32_t phase = 0;
+  constexpr int ahead = NB * (SHARED ? 2 : 1);
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-  auto next = [](int& st, uint32_t& ph) {
-    if (++st == C::ST) st = 0, ph ^= 1;
+  auto next = [&] {
+    if (++slot == C::ST) slot = 0, phase ^= 1;
   };
-  auto qk = [&](int l, int rows, int st) {  // by one thread; rows: the lane whose Q it is
-    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + rows * C::QBYTES, 16, 8 * C::RB, C::SWZ);
-    const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + st * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+  auto qk = [&](int l, int b, int half) {  // by one thread
+    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (SHARED ? 0 : l) * C::QBYTES, 16, 8 * C::RB, C::SWZ);
+    const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + (2 * slot + half) * C::KBYTES, 16, 8 * C::RB, C::SWZ);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
-      tc5::mma_ss(tmem + C::S0 + l * C::TN, qd + ((panel * C::QP + in) >> 4), kd + ((panel * C::KP + in) >> 4),
-                  kIdescQK, j > 0);
+      tc5::mma_ss(tmem + C::S0 + (l * NB + b) * C::TN, qd + ((panel * C::QP + in) >> 4),
+                  kd + ((panel * C::KP + in) >> 4), kIdescQK, j > 0);
     }
-    tc5::commit(wt.bar(B_SFULL + l));
   };
-  auto pv = [&](int l, uint64_t vd, bool begun) {
+  auto pv = [&](int l, int b, uint64_t vd, bool begun) {
+    const uint32_t p = tmem + C::S0 + (l * NB + b) * C::TN;
 #pragma unroll
     for (int j = 0; j < C::TN / 16; ++j)
-      tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV,
-                  begun || j > 0);
+      tc5::mma_ts(tmem + C::O0 + l * D, p + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, begun || j > 0);
     if (TWO) {  // the weights' second parts
 #pragma unroll
       for (int j = 0; j < C::TN / 16; ++j)
-        tc5::mma_ts(tmem + C::O0 + l * D, tmem + C::S0 + l * C::TN + C::TN / 2 + j * 8, vd + ((j * 16 * C::RB) >> 4),
-                    kIdescPV, true);
+        tc5::mma_ts(tmem + C::O0 + l * D, p + C::TN / 2 + j * 8, vd + ((j * 16 * C::RB) >> 4), kIdescPV, true);
     }
   };
   bool ok = true;
@@ -531,111 +554,67 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
     if (uniform(u.no) == 0) break;
     const int n0 = uniform(u.tiles0), n1 = C::LANES == 2 ? uniform(u.tiles1) : 0;
     const int nt = uniform(u.tiles), checked = (uniform(u.t0) + 1) / C::TN;
-    if constexpr (SHARED) {  // tile t is lane t % 2's, one Q is both's
+    auto tiles = [&](int l) { return l ? n1 : n0; };
+    // a lane's scores k, of keys in a half of the slot; its Q is free when they are the last
+    auto scores = [&](int l, int k, int half) {
+      qk(l, k % NB, half);
+      tc5::commit(wt.bar(B_SFULL + l * NB + k % NB));
+      if (SHARED ? 2 * k + l + 1 == nt : k + 1 == tiles(l)) tc5::commit(wt.bar(B_QEMPTY + (SHARED ? 0 : l)));
+    };
+    // the unit's first scores
+    ok = wt.wait_warp(B_KVFULL + slot, phase);
+    const int first = min(ahead, nt);
+    for (int t = 0; ok && t < first; ++t) {
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        if (!ok || l >= nt) continue;
-        ok = wt.wait_warp(B_KVFULL + stage, phase);
-        if (l == 0) {
-          ok = ok && wt.wait_warp(B_QFULL, qn & 1);
-          qn ^= 1;
+      for (int l = 0; l < C::LANES; ++l) {
+        if (!ok || (SHARED ? (t & 1) != l : t >= tiles(l))) continue;
+        const int k = SHARED ? t >> 1 : t;
+        if (SHARED ? t == 0 : k == 0) {
+          ok = wt.wait_warp(B_QFULL + l, (qn >> l) & 1);
+          qn ^= 1u << l;
         }
         tc5::fence_after();
         if (ok && tc5::elect()) {
-          qk(l, 0, stage);
-          tc5::commit(wt.bar(B_KVEMPTY + stage));
-          if (l + 1 == nt) tc5::commit(wt.bar(B_QEMPTY));
+          scores(l, k, 1 - t);
+          if (t + 1 == first && (SHARED || l == (t < n1))) tc5::commit(wt.bar(B_KVEMPTY + slot));
         }
         __syncwarp();
-        next(stage, phase);
       }
-      for (int t2 = 0; ok && t2 < nt; t2 += 2) {
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          const int t = t2 + l, vst = stage;
-          if (!ok || t >= nt) continue;
-          ok = wt.wait_warp(B_KVFULL + stage, phase);
-          if (ok && t >= checked) {
-            ok = wt.wait_warp(B_VOK + stage, (vok >> stage) & 1);
-            vok ^= 1u << stage;
-          }
-          next(stage, phase);
-          const int kst = stage;
-          if (t + 2 < nt) {
-            ok = ok && wt.wait_warp(B_KVFULL + stage, phase);
-            next(stage, phase);
-          }
-          const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + vst * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
-          ok = ok && wt.wait_warp(B_PREADY + l, (pn >> l) & 1);
-          pn ^= 1u << l;
-          if (!ok) continue;
-          tc5::fence_after();
-          if (tc5::elect()) {
-            pv(l, vd, ((t >> 1) & seg) > 0);
-            tc5::commit(wt.bar(B_KVEMPTY + vst));
-            if (t + 2 >= nt || (((t >> 1) + 1) & seg) == 0) tc5::commit(wt.bar(B_ODONE + l));
-            if (t + 2 < nt) {
-              qk(l, 0, kst);
-              tc5::commit(wt.bar(B_KVEMPTY + kst));
-              if (t + 3 == nt) tc5::commit(wt.bar(B_QEMPTY));
-            }
-          }
-          __syncwarp();
-        }
-      }
-      continue;
     }
-    auto tiles = [&](int l) { return l ? n1 : n0; };
-    // the unit's first scores
-    ok = wt.wait_warp(B_KVFULL + stage, phase);
-#pragma unroll
-    for (int l = 0; l < C::LANES; ++l) {
-      if (!ok || tiles(l) == 0) continue;
-      ok = wt.wait_warp(B_QFULL + l, (qn >> l) & 1);
-      qn ^= 1u << l;
-      tc5::fence_after();
-      if (ok && tc5::elect()) {
-        qk(l, l, stage);
-        if (l == (n1 > 0)) tc5::commit(wt.bar(B_KVEMPTY + stage));
-        if (tiles(l) == 1) tc5::commit(wt.bar(B_QEMPTY + l));
-      }
-      __syncwarp();
-    }
-    next(stage, phase);
+    next();
+    bool filled = false;  // the slot is known to be
     for (int t = 0; ok && t < nt; ++t) {
-      const int vst = stage;  // tile t's values, then the next tile's keys
-      ok = wt.wait_warp(B_KVFULL + stage, phase);
+      ok = filled || wt.wait_warp(B_KVFULL + slot, phase);
+      filled = false;
       if (ok && t >= checked) {
-        ok = wt.wait_warp(B_VOK + stage, (vok >> stage) & 1);
-        vok ^= 1u << stage;
+        ok = wt.wait_warp(B_VOK + slot, (vok >> slot) & 1);
+        vok ^= 1u << slot;
       }
-      next(stage, phase);
-      const int kst = stage;
-      if (t + 1 < nt) {
-        ok = ok && wt.wait_warp(B_KVFULL + stage, phase);
-        next(stage, phase);
-      }
-      const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + vst * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+      const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + 2 * slot * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+      const int slot1 = slot + 1 == C::ST ? 0 : slot + 1;
 #pragma unroll
       for (int l = 0; l < C::LANES; ++l) {
-        if (!ok || t >= tiles(l)) continue;
-        ok = wt.wait_warp(B_PREADY + l, (pn >> l) & 1);
-        pn ^= 1u << l;
+        if (!ok || (SHARED ? (t & 1) != l : t >= tiles(l))) continue;
+        const int k = SHARED ? t >> 1 : t, b = k % NB, i = l * NB + b;
+        ok = wt.wait_warp(B_PREADY + i, (pn >> i) & 1);
+        pn ^= 1u << i;
         if (!ok) continue;
         tc5::fence_after();
+        if (tc5::elect()) pv(l, b, vd, (k & seg) > 0);
+        __syncwarp();
+        // (while those run)
+        const bool last = SHARED || l == (t < n1);  // of the slot
+        if (last) filled = __all_sync(0xffffffffu, wt.test(B_KVFULL + slot1, phase ^ (slot1 == 0)));
         if (tc5::elect()) {
-          pv(l, vd, (t & seg) > 0);
-          if (l == (t < n1)) tc5::commit(wt.bar(B_KVEMPTY + vst));
-          if (t + 1 == tiles(l) || ((t + 1) & seg) == 0) tc5::commit(wt.bar(B_ODONE + l));
-          if (t + 1 < tiles(l)) {
-            // after this step in the tensor cores' order: S may take P's place
-            qk(l, l, kst);
-            if (l == (t + 1 < n1)) tc5::commit(wt.bar(B_KVEMPTY + kst));
-            if (t + 2 == tiles(l)) tc5::commit(wt.bar(B_QEMPTY + l));
-          }
+          if (k + NB < tiles(l))
+            scores(l, k + NB, 1);  // after this step in the tensor cores' order: S may take P's place
+          else
+            tc5::commit(wt.bar(B_ODONE + i));
+          if (last) tc5::commit(wt.bar(B_KVEMPTY + slot));
         }
         __syncwarp();
       }
+      next();
     }
   }
   // nothing of this thread's is in flight when TMEM is freed
@@ -652,7 +631,7 @@ struct Soft {
   const PromptAttnArgs& a;
   const Waits& wt;
   const uint32_t smem, tmem;  // tmem: with the warp's lanes
-  uint32_t sn = 0, on = 0, jn = 0;  // phases of the scores, of the finished sums and of the join
+  uint32_t sn = 0, on = 0, jn = 0;  // phase bits of the scores, of the finished sums and of the join
 
   static __device__ __forceinline__ int lane() { return threadIdx.x >> 7; }
   static __device__ __forceinline__ int r() { return threadIdx.x & 127; }
@@ -695,10 +674,25 @@ struct Soft {
     }
   }
 
+  // Waits for the scores at b.
+  __device__ __forceinline__ bool scored(int b) {
+    const bool ok = wt.wait_warp(B_SFULL + lane() * C::NB + b, (sn >> b) & 1);
+    sn ^= 1u << b;
+    tc5::fence_after();
+    return ok;
+  }
+  // Waits until the tile whose weights were at b is in O; more: scores take their place.
+  __device__ __forceinline__ bool summed(int b, bool more) const {
+    const bool ok = more ? wt.wait_warp(B_SFULL + lane() * C::NB + b, (sn >> b) & 1)
+                         : wt.wait_warp(B_ODONE + lane() * C::NB + b, (on >> b) & 1);
+    tc5::fence_after();
+    return ok;
+  }
+
   // One tile: the row's weights into TMEM, m and l brought up to date.  visible: tokens of
-  // the tile that the row sees (a prefix).
-  __device__ __forceinline__ void tile(int visible, bool started, float& m, float& l) const {
-    const uint32_t sa = tmem + C::S0 + lane() * C::TN;
+  // the tile that the row sees (a prefix).  b: its place; more: the unit has a tile after it.
+  __device__ __forceinline__ bool tile(int b, bool more, int visible, bool started, float& m, float& l) const {
+    const uint32_t sa = tmem + C::S0 + (lane() * C::NB + b) * C::TN;
     float s[C::TN], mx[C::TN / 32];
 #pragma unroll
     for (int i = 0; i < C::TN / 32; ++i) tc5::ld32_max(sa + 32 * i, reinterpret_cast<uint32_t*>(s + 32 * i), mx[i]);
@@ -721,6 +715,7 @@ struct Soft {
       if (moves) m = mn;
       l *= f;
       if (started) {
+        if (C::NB > 1 && !summed(b ^ 1, more)) return false;
         const uint32_t oa = tmem + C::O0 + lane() * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 16) {
@@ -740,6 +735,7 @@ struct Soft {
     weights(sa, s, c2, off2, sum2);
     l = __uint_as_float(lo_bits(sum2)) + __uint_as_float(hi_bits(sum2));
     tc5::wait_st();
+    return true;
   }
 
   // The warp's rows of O, times f, to the output.  A thread has a row: its 16-byte pieces go
@@ -855,7 +851,7 @@ struct Soft {
       const bool warp_live = __any_sync(0xffffffffu, live);
       // (rows that are not there need no mask)
       int visible = live ? tok + 1 - (SHARED ? lane() * C::TN : 0) : 1 << 30;
-      constexpr int seg = F32 ? kSegment - 1 : 0x7fffffff;
+      constexpr int seg = F32 ? kSegment / C::TN - 1 : 0x7fffffff;
       float m = -INFINITY, l = 0.0f, m_out = 0.0f;
       bool begun = false;  // the output has sums, at the reference m_out
       // what sums at a reference weigh at one that is not below it: never zero, so that an
@@ -891,25 +887,23 @@ struct Soft {
       const int end = joint ? u.tiles0 : n;
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {
-        if (!wt.wait_warp(B_SFULL + lane(), sn++ & 1)) return;
-        tc5::fence_after();
-        if (warp_live) tile(visible, (t & seg) > 0, m, l);
+        const int b = t % C::NB;
+        if (!scored(b)) return;
+        if (warp_live && !tile(b, t + 1 < n, visible, (t & seg) > 0, m, l)) return;
         tc5::fence_before();
-        wt.arrive_warp(B_PREADY + lane());
+        wt.arrive_warp(B_PREADY + lane() * C::NB + b);
         if (live) visible -= SHARED ? 2 * C::TN : C::TN;
         if (((t + 1) & seg) == 0 && t + 1 < end) {
-          if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
-          tc5::fence_after();
-          if (!store(false, true)) return;
+          if (!summed(b, t + C::NB < n) || !store(false, true)) return;
           tc5::fence_before();
         }
       }
+      for (int t = max(0, n - C::NB); t < n; ++t) {
+        if (!summed(t % C::NB, false)) return;
+        on ^= 1u << t % C::NB;
+      }
       // lane 1's sums may have gone with a segment of lane 0's
       const bool rest = (u.tiles1 & seg) != 0 || u.tiles1 == u.tiles0;
-      if (!(joint && lane()) || rest) {
-        if (!wt.wait_warp(B_ODONE + lane(), on++ & 1)) return;
-        tc5::fence_after();
-      }
       if (!store(true, rest)) return;
       tc5::fence_before();
       __threadfence_block();
@@ -938,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   } else if (warp == 9) {
     for (int i = lid; i < B_COUNT; i += 32) {
       int n = 1;  // arrivals of a phase
-      if (i == B_PREADY || i == B_PREADY + 1) n = 4;
-      if (i == B_SFULL || i == B_SFULL + 1) n = 1 + a.fault;
+      if (i >= B_PREADY && i < B_PREADY + 4) n = 4;
+      if (i >= B_SFULL && i < B_SFULL + 4) n = 1 + a.fault;
       if (i == B_UEMPTY) n = C::SMW + 3;
       if (i == B_JOIN) n = C::SMW;
       if (i >= B_KVEMPTY && i < B_KVEMPTY + kMaxStages) n = 2;
