@@ -25,8 +25,8 @@
 //         diagonal): a weight of zero would turn an infinite one into NaN.
 //   11    works out the units.
 // head_dim 256 has room for one lane, tiles of 64 tokens, and the scores of two: the next
-// tile's are there when a tile's weights are done (8192 tokens' worth of 32 heads on 8,
-// 4096 each: 265 -> 220 us).  Two smaller tiles of scores in place of one made head_dim 128
+// tile's are there when a tile's weights are done (4096 tokens of 32 heads on 8: 265 -> 220
+// us).  Two smaller tiles of scores in place of one made head_dim 128
 // 33 % slower (Q is read from shared memory for each) and 64 up to 70 %.
 //
 // Bound: at head_dim 128 the tensor cores take 2048 cycles for a tile of both lanes, and a

