@@ -526,9 +526,13 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
   auto next = [&] {
     if (++slot == C::ST) slot = 0, phase ^= 1;
   };
+  // (an address has 14 bits of a descriptor, and no sum passes them)
+  const uint64_t qd0 = tc5::smem_desc(smem + C::OFF_Q, 16, 8 * C::RB, C::SWZ);
+  const uint64_t kd0 = tc5::smem_desc(smem + C::OFF_KV, 16, 8 * C::RB, C::SWZ);
+  const uint64_t vd0 = tc5::smem_desc(smem + C::OFF_KV, C::KP, 8 * C::RB, C::SWZ);
   auto qk = [&](int l, int b, int half) {  // by one thread
-    const uint64_t qd = tc5::smem_desc(smem + C::OFF_Q + (SHARED ? 0 : l) * C::QBYTES, 16, 8 * C::RB, C::SWZ);
-    const uint64_t kd = tc5::smem_desc(smem + C::OFF_KV + (2 * slot + half) * C::KBYTES, 16, 8 * C::RB, C::SWZ);
+    const uint64_t qd = qd0 + (SHARED ? 0 : l) * (C::QBYTES >> 4);
+    const uint64_t kd = kd0 + (uint32_t)((2 * slot + half) * (C::KBYTES >> 4));
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       const int panel = j * 16 / C::PW, in = (j * 16 % C::PW) * 2;
@@ -590,7 +594,7 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
         ok = wt.wait_warp(B_VOK + slot, (vok >> slot) & 1);
         vok ^= 1u << slot;
       }
-      const uint64_t vd = tc5::smem_desc(smem + C::OFF_KV + 2 * slot * C::KBYTES, C::KP, 8 * C::RB, C::SWZ);
+      const uint64_t vd = vd0 + (uint32_t)(2 * slot * (C::KBYTES >> 4));
       const int slot1 = slot + 1 == C::ST ? 0 : slot + 1;
 #pragma unroll
       for (int l = 0; l < C::LANES; ++l) {
