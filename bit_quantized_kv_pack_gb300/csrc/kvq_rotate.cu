@@ -5,20 +5,22 @@
 //
 // Mapping.  A lane holds 8 values (16 bytes) of a head, a head is d / 8 neighbouring lanes,
 // a warp takes 256 / d rows.  Its cosines and sines stay in registers while it goes through
-// heads (queries, then keys), eight of them loaded at a time; few rows share the heads out
+// heads (queries, then keys), four of them loaded at a time; few rows share the heads out
 // over several warps instead.  The partner values (rotary_dim / 2 away) come by shuffles.
 // The axis of each pair (2 bits) comes with the launch, and a lane whose pairs have one axis
 // reads its row of the table in 16-byte pieces.
 //
-// Bound by memory: 34169 tokens (6 prompts) of 32 + 8 heads of 128 take 108 us, 96 % of the
-// measured copy rate.  16 tokens take 3.2 us, which is the launch and two dependent loads.
+// Bound by memory: 34169 tokens (6 prompts) of 32 + 8 heads of 128 take 107 us, 96 % of the
+// measured copy rate; 14314 of 16 + 16 heads of 64 18.9, 92 % (eight heads in flight and 16
+// warps an SM 21.2; two heads 21.1, and 116 for the first).  16 tokens take 2.4 us, which
+// is the launch and two dependent loads (eight heads 3.2).
 #include "kvq_around.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHeads = 8;  // heads in flight
+constexpr int kHeads = 4;  // heads in flight
 
 struct RotateArgs {
   const __half* x[2];  // queries, keys
@@ -152,8 +154,10 @@ cudaError_t launch_rotate(const kvq_rotate_args& args, cudaStream_t st) {
   if (a.total == 0 || a.heads == 0) return cudaSuccess;
   const int rows = 256 / a.d * (kThreads / 32);  // of a block
   const int64_t blocks = ((int64_t)a.total + rows - 1) / rows;
-  // a warp goes through all heads where there are blocks enough for 16 warps on each SM
-  const int64_t want = (4 * (int64_t)device_sm_count() + blocks - 1) / blocks;
+  // a warp goes through all heads where there are blocks enough for 128 warps on each SM
+  // (14314 tokens of 16 + 16 heads of 64: for 16 warps 24.7 us, 32 20.6, 64 18.3, 128 18.9;
+  // 34169 of 32 + 8 heads of 128: 108.4 for any fewer, 107.2)
+  const int64_t want = (32 * (int64_t)device_sm_count() + blocks - 1) / blocks;
   const int batches = (a.heads + kHeads - 1) / kHeads;
   const int ny = (int)(want < batches ? want : batches);
   a.per = (batches + ny - 1) / ny * kHeads;
