@@ -22,7 +22,8 @@
 //   9     loads Q, K and V (TMA tiles, 128-byte swizzle).  A slot of the ring has what a batch
 //         of MMAs takes, a tile's values and a later tile's keys, under one barrier.
 //   10    looks at values that some row of the block does not see (the tiles at the
-//         diagonal): a weight of zero would turn an infinite one into NaN.
+//         diagonal): a weight of zero would turn an infinite one into NaN.  With fp32 output
+//         at those of all tiles: of the weights' second parts about half are negative.
 //   11    works out the units.
 // head_dim 256 has room for one lane, tiles of 64 tokens, and the scores of two: the next
 // tile's are there when a tile's weights are done (4096 tokens of 32 heads on 8: 265 -> 220
@@ -423,13 +424,27 @@ __device__ __forceinline__ void load_role(const PromptAttnArgs& a, const Waits& 
 
 // ------------------------------------------------------------- values' check ---
 
+// The first tile that the MMAs of its values wait for the check of: all before it are seen
+// whole by every row of the block.  TWO: the notes of those have to be complete when either
+// lane's sums are, so the last tile of each lane is waited for in any case (a block of one
+// row, at a tile's end, sees all of it).
+template <int D, bool TWO, bool SHARED>
+__device__ __forceinline__ int checked_from(int t0, int tiles0, int tiles) {
+  const int first = (t0 + 1) / Cfg<D>::TN;  // the block's first row sees tokens up to t0
+  return TWO ? min(first, (SHARED ? tiles : tiles0) - 1) : first;
+}
+
 // Values that are not finite, at tokens that some row of the block does not see (tokens of
 // the next sequence among them): zeros take their place in the tile, and the first
 // token with +inf, -inf or NaN in a column is noted; the epilogue gives the rows that see
-// it what the sum would be.  In tiles that all rows see whole the MMA does that itself.
+// it what the sum would be.  In tiles that all rows see whole the MMA does that itself,
+// unless the weights have two parts (TWO): the second, what the first's rounding left, is
+// negative or zero as often as not, and either makes NaN of an infinite value.  So those of
+// all tiles are noted then, and what is in O does not count (8 prompts of 245 to 1500 tokens,
+// 16 heads of 64: 53.7 -> 54.8 us).
 // The warp sees every fill of the ring (a parity alone does not tell a fill from the one
 // before the last), and a stage is free when it and the MMAs are done with it.
-template <int D, bool SHARED>
+template <int D, bool TWO, bool SHARED>
 __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, const Unit* unit) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
@@ -440,16 +455,17 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
     units.release();
     if (u.no == 0) return;
     bool clean = false;  // the notes are this unit's
+    const int checked = checked_from<D, TWO, SHARED>(u.t0, u.tiles0, u.tiles);
     for (int t = -1; t < u.tiles; ++t, ++item) {  // (keys alone first)
       const int stage = item % C::ST;
       if (!wt.wait_warp(B_KVFULL + stage, (item / C::ST) & 1)) return;
-      // the block's first row sees tokens up to t0
-      if (t < (u.t0 + 1) / C::TN) {
+      const bool waited = t >= checked;  // by the MMAs, which may read the others by now
+      if (t < 0 || (!TWO && !waited)) {
         wt.arrive_warp(B_KVEMPTY + stage);
         continue;
       }
       const uint32_t tile = smem + C::OFF_KV + 2 * stage * C::KBYTES;
-      const int r0 = max(0, u.t0 + 1 - t * C::TN);  // rows before it are seen by all
+      const int r0 = TWO ? 0 : max(0, u.t0 + 1 - t * C::TN);  // rows before it are seen by all
       bool any = false;
 #pragma unroll 1
       for (int p = 0; p < C::NP; ++p)
@@ -479,7 +495,7 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
           unsigned short hv;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hv) : "r"(at) : "memory");
           if ((hv & 0x7c00u) != 0x7c00u) continue;
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+          if (waited) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
           const int token = t * C::TN + r, kind = (hv & 0x3ffu) ? 2 : (hv & 0x8000u) ? 1 : 0;
           if (token < u.n)
             asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(smem + C::OFF_NOTES + 4 * (kind * D + col)), "r"(token)
@@ -488,7 +504,7 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
         __threadfence_block();
         ptx::fence_proxy_async_shared();
       }
-      wt.arrive_warp(B_VOK + stage);
+      if (waited) wt.arrive_warp(B_VOK + stage);
       wt.arrive_warp(B_KVEMPTY + stage);
     }
     before += (u.tiles0 > 0 ? 4 : 0) + (u.tiles1 > 0 ? 4 : 0);
@@ -557,7 +573,7 @@ __device__ __forceinline__ void mma_role(const Waits& wt, uint32_t smem, uint32_
     units.release();
     if (uniform(u.no) == 0) break;
     const int n0 = uniform(u.tiles0), n1 = C::LANES == 2 ? uniform(u.tiles1) : 0;
-    const int nt = uniform(u.tiles), checked = (uniform(u.t0) + 1) / C::TN;
+    const int nt = uniform(u.tiles), checked = checked_from<D, TWO, SHARED>(uniform(u.t0), n0, nt);
     auto tiles = [&](int l) { return l ? n1 : n0; };
     // a lane's scores k, of keys in a half of the slot; its Q is free when they are the last
     auto scores = [&](int l, int k, int half) {
@@ -822,9 +838,11 @@ struct Soft {
                  nan = (int)lds(n + 4 * (2 * D + c)) < lim;
       if (!(up || down || nan)) continue;
       float v = nan || (up && down) || inv != inv ? NAN : up ? INFINITY : -INFINITY;
-      // (with an infinite value of the other sign in a tile that all rows see, or NaN there)
-      const float o = F32 ? static_cast<float*>(a.out)[at + c] : __half2float(static_cast<__half*>(a.out)[at + c]);
-      if (o != o || (isinf(o) && o != v)) v = NAN;
+      if (!F32) {
+        // (with an infinite value of the other sign in a tile that all rows see, or NaN there)
+        const float o = __half2float(static_cast<__half*>(a.out)[at + c]);
+        if (o != o || (isinf(o) && o != v)) v = NAN;
+      }
       if (F32)
         static_cast<float*>(a.out)[at + c] = v;
       else
@@ -967,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     tc5::regs_dec<88>();
     if (warp == 8) mma_role<D, F32, SHARED>(wt, smem, tmem, unit);
     if (warp == 9) load_role<D, SHARED>(a, wt, smem, unit);
-    if (warp == 10) check_role<D, SHARED>(a, wt, smem, unit);
+    if (warp == 10) check_role<D, F32, SHARED>(a, wt, smem, unit);
     if (warp == 11) unit_role<D, SHARED>(a, wt, smem, unit);
     __syncwarp();
   }

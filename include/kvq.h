@@ -571,7 +571,9 @@ typedef struct {
  * on timing; the order of a row's sums goes by how many blocks of rows there can be (total,
  * batch and heads), so that a prompt may differ in its last bits from the same one in
  * another batch.  Tokens a row does not attend over, other prompts' among them, have no part in
- * its output, whatever they hold.  Entries of cu_seqlens that break the rule set
+ * its output, whatever they hold.  An infinite value that it attends over makes its element of the
+ * output infinite, or NaN beside one of the other sign or NaN (with fp16 output also where the
+ * value's weight rounds to zero, below 2^-32 of the largest).  Entries of cu_seqlens that break the rule set
  * KVQ_ERRBIT_BADLEN (where they let prompts overlap, some may stay unwritten).
  * Asynchronous; lengths are read on the device. */
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream);

@@ -289,3 +289,47 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_whole(empty):
         kvq.kvq_testing_wait_fault(0)
     assert torch.equal(kvq.kvq_prompt_attention(q, k, v, cu, 500, err=g.err), want)
     assert kvq.kvq_read_error(g) == (kvq.KVQ_OK, 0)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 32), (4, 2, 64), (3, 1, 128), (4, 2, 256)])
+@pytest.mark.parametrize("n", [300, 4500])
+@EMPTY
+def test_infinite_values_that_are_seen_with_fp32_output(hq, hkv, d, n, empty):
+    """As with fp16 output, in tiles that every row of a block sees too, and over more than a
+    segment of 2048 tokens for either lane."""
+    q, k, v = inputs(d + n, n, hq, hkv, d)
+    q, k = q * 0.25, k * 0.25
+    cu, f32 = ends([n], empty), kvq.KVQ_OUT_F32
+    want = kvq.kvq_prompt_attention(q, k, v, cu, n, flags=f32)
+    v2, expect = v.clone(), want.clone()
+    gq, last = hq // hkv, n - 10
+    for tokens, head, column in (([(0, math.inf)], 0, 0), ([(20, math.inf)], 0, 3), ([(150, -math.inf)], 0, 7),
+                                 ([(160, math.nan)], hkv - 1, 9), ([(40, math.inf), (last, -math.inf)], hkv - 1, 11),
+                                 ([(n // 2, -math.inf), (n // 2 + 1, -math.inf)], 0, d - 1),
+                                 ([(last, math.inf), (last + 1, math.nan)], hkv - 1, d - 2)):
+        seen = None
+        for at, value in tokens:
+            v2[at, head, column] = value
+            seen = value if seen is None or seen == value else math.nan
+            expect[at:, head * gq:(head + 1) * gq, column] = seen
+    got = kvq.kvq_prompt_attention(q, k, v2, cu, n, flags=f32)
+    assert np.array_equal(to_np(got), to_np(expect), equal_nan=True)
+
+
+@pytest.mark.parametrize("d", [32, 64])
+def test_a_block_of_one_row_at_a_tile_s_end(d):
+    """128 query heads on one: a block's lanes have a token each, and the last token of a whole
+    number of tiles sees all of each tile."""
+    for lens in ([256], [128, 256, 257], [255, 256, 129] * 60):
+        q, k, v = inputs(d, sum(lens), 128, 1, d)
+        q, k = q * 0.25, k * 0.25
+        cu = ends(lens)
+        want = kvq.kvq_prompt_attention(q, k, v, cu, max(lens), flags=kvq.KVQ_OUT_F32)
+        v2, expect, at = v.clone(), want.clone(), 0
+        for n in lens:
+            for token, column, value in ((0, 1, math.inf), (127, 2, -math.inf), (n - 1, 3, math.nan)):
+                v2[at + token, 0, column] = value
+                expect[at + token:at + n, :, column] = value
+            at += n
+        got = kvq.kvq_prompt_attention(q, k, v2, cu, max(lens), flags=kvq.KVQ_OUT_F32)
+        assert np.array_equal(to_np(got), to_np(expect), equal_nan=True)
