@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     if (bad || done || base == -INFINITY || norm.hi == -INFINITY) {
       // proposes its end alone, or nothing: the row's first tokens follow at -inf
       if (part == 0 && lane < min(a.n, a.V)) {
-        const bool ends = done && !bad;
-        score = ends && lane == 0 && base > -INFINITY ? ordered(Two{base, 0.0f}) : silent;
+        const bool ends = done && !bad && base > -INFINITY;
+        score = ends && lane == 0 ? ordered(Two{base, 0.0f}) : silent;
         at = w * a.V + (!ends ? lane : lane == 0 ? a.end : lane - (lane <= a.end));
       }
     } else if (k != 0) {

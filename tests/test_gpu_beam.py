@@ -210,3 +210,16 @@ def test_workspace_streams_and_graphs():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+@pytest.mark.parametrize("end", [0, 1, 5, 9])
+def test_complete_beams_without_a_score(end):
+    """Nothing of an entry is live: what comes back is the first tokens, at -inf."""
+    x = np.random.default_rng(16).standard_normal((3, 2, 10)).astype(np.float32)
+    none = np.full((3, 2), -np.inf, np.float32)
+    for n in (1, 2, 5, 10, 15):
+        check(x, none, n, np.ones((3, 2), bool), end)
+        mixed = none.copy()
+        mixed[0, 1], mixed[1, 0] = -1.0, -2.0
+        check(x, mixed, n, np.ones((3, 2), bool), end)
+        check(x[:, :1].copy(), none[:, :1].copy(), min(n, 10), np.ones((3, 1), bool), end)
