@@ -1,7 +1,7 @@
 // kvq_beam.cu -- beam search's selection over beams and vocabulary.
 //
 // score(w, t) = s_w + x_wt - log sum_u exp(x_wu); the n best of each batch entry, equal
-// ones in the order of (w, t).  Within a row the order is that of (x, t), so a row's n
+// ones in the order of beams.  Within a row the order is that of (x, t), so a row's n
 // largest logits are all that can be selected of it.
 //
 // Pass 1, a block for a piece of a row: the piece stays in registers (NV 16-byte vectors
@@ -14,7 +14,8 @@
 // Keys are 64 bits: the logit in an order of whole numbers, then the token, inverted, so
 // that of equal logits the lower token is the larger key.
 // Pass 2, a block for a batch entry: the pieces' sums become the rows' log-normalisers, a
-// warp merges some pieces of a row, and each lane works out its entry's score.  A bound that
+// warp merges some pieces of a row, and each lane works out its entry's score (equal ones of a
+// beam keep the order of their logits: a score far from zero has no bits for them).  A bound that
 // n scores and not many more are at or above is found bit by bit (a barrier that counts for
 // each), and those count what is before them.
 //
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   constexpr int AHEAD = 4;     // lists in flight
   constexpr int kEnough = 64;  // entries that are ranked by counting
   __shared__ __align__(16) uint64_t passed[kJoinThreads];
-  __shared__ __align__(16) int passed_at[kJoinThreads];
+  __shared__ __align__(16) int2 passed_at[kJoinThreads];  // place (beam * V + token), logit in order
   __shared__ int count;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // warp i has row i % W and, of its pieces, every (WARPS / W)-th
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   const uint64_t silent = ordered(Two{-INFINITY, 0.0f});
   uint64_t score = 0;  // none, behind all others
   int at = 0x7fffffff;
+  uint32_t logit = 0;  // in order; tokens that are not proposed have none
   if (part < per) {
     if (bad || done || base == -INFINITY || norm.hi == -INFINITY) {
       // proposes its end alone, or nothing: the row's first tokens follow at -inf
@@ -454,7 +456,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
         at = w * a.V + (!ends ? lane : lane == 0 ? a.end : lane - (lane <= a.end));
       }
     } else if (k != 0) {
-      const float x = unordered((uint32_t)(k >> 32));
+      logit = (uint32_t)(k >> 32);
+      const float x = unordered(logit);
       const Two d = two_sum(x, -norm.hi);
       const Two b = two_sum(base, d.hi);
       // (below fp32's range: -inf)
@@ -473,19 +476,26 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   if (top >= least && score != 0) {
     const int i = atomicAdd(&count, 1);
     passed[i] = score;
-    passed_at[i] = at;
+    passed_at[i] = make_int2(at, (int)logit);
   }
   __syncthreads();
   const int c = count;
   if (tid < c) {
     const uint64_t s = passed[tid];
-    const int mine = passed_at[tid];
+    const int mine = passed_at[tid].x, beam = mine / a.V;
+    const uint32_t own = (uint32_t)passed_at[tid].y;
+    // of equal scores the first beam's, of a beam's the largest logit's, then the first token's
     int place = 0;
 #pragma unroll 4
-    for (int i = 0; i < c; ++i) place += passed[i] > s || (passed[i] == s && passed_at[i] < mine);
+    for (int i = 0; i < c; ++i) {
+      const int2 o = passed_at[i];
+      const bool larger = (uint32_t)(o.x - beam * a.V) < (uint32_t)a.V && (uint32_t)o.y != own
+                              ? (uint32_t)o.y > own
+                              : o.x < mine;
+      place += passed[i] > s || (passed[i] == s && larger);
+    }
     if (place < a.n) {
       const int64_t to = (int64_t)blockIdx.x * a.n + place;
-      const int beam = mine / a.V;
       a.parent[to] = blockIdx.x * a.W + beam;
       a.token[to] = mine - beam * a.V;
       a.score[to] = unordered((uint32_t)(s >> 32));

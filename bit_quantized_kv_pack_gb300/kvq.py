@@ -855,7 +855,7 @@ def kvq_beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, finished
                     err: torch.Tensor | None = None, stream=None):
     """Beam search's selection: logits [B][W][V] (fp16 or fp32, V contiguous, equal strides
     from row to row), scores fp32 [B][W]; the n best of scores + log_softmax(logits) over
-    beams and tokens for each batch entry, best first, equal ones in order.  ``finished``
+    beams and tokens for each batch entry, best first (a beam's in the order of its logits).  ``finished``
     (uint8 or bool [B][W]): complete beams, which go on with ``end_token`` at their score.
     Returns (parent, token, score), each [B][n] (``out``: such a triple): parent is the row
     b W + w, an index for kvq_reorder."""

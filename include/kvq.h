@@ -609,7 +609,10 @@ size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int
 /* Beam search's selection.  Beam w proposes token t with the score
  *   scores[w] + x[t] - log sum_u exp(x[u]),   x its logits;
  * a complete beam proposes end_token alone, at scores[w].  For each batch entry the n
- * best proposals, best first; equal scores in the order of (w, t).  What is not proposed
+ * best proposals, best first; those of one beam in the order of their logits, equal logits in
+ * that of their tokens, and equal scores of two beams in the order of the beams.  (Where a score
+ * is so far from zero that its last bit is more than the logits differ by, as at the type's
+ * lowest value, the logits still decide within a beam.)  What is not proposed
  * (logits of -inf, other tokens of complete beams, beams with a score of -inf) counts as a
  * score of -inf, so n entries always come back.
  * A beam with a NaN or +inf among its logits, or as its score, proposes nothing and sets

@@ -223,3 +223,27 @@ def test_complete_beams_without_a_score(end):
         mixed[0, 1], mixed[1, 0] = -1.0, -2.0
         check(x, mixed, n, np.ones((3, 2), bool), end)
         check(x[:, :1].copy(), none[:, :1].copy(), min(n, 10), np.ones((3, 1), bool), end)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("V", [50, 5003, 70001])
+def test_scores_whose_differences_are_below_their_last_bit(V, dtype):
+    """Beams at the type's lowest score: all their proposals are equal in 53 bits.  A beam's
+    come in the order of its logits, equal logits in that of their tokens."""
+    rng = np.random.default_rng(V)
+    B, W, n = 2, 3, 12
+    x = np.round(rng.standard_normal((B, W, V)) * 8).astype(dtype) / 8  # with equal ones among the largest
+    low = np.finfo(np.float32).min
+    scores = np.full((B, W), low, np.float32)
+    scores[:, 0] = -1.0
+    fin = np.zeros((B, W), bool)
+    fin[:, 0] = True
+    g = gpu_cache(1, 1, 32, 4, 32, 0)
+    parent, token, score = kvq.kvq_beam_select(torch.from_numpy(x).to(DEV), torch.from_numpy(scores).to(DEV), n,
+                                               finished=torch.from_numpy(fin).to(DEV), end_token=3, err=g.err)
+    assert kvq.kvq_read_error(g) == (kvq.KVQ_OK, 0)
+    for b in range(B):
+        order = np.argsort(-x[b, 1].astype(np.float64), kind="stable")[:n - 1]
+        assert to_np(token)[b].tolist() == [3] + order.tolist()
+        assert to_np(parent)[b].tolist() == [b * W] + [b * W + 1] * (n - 1)
+        assert to_np(score)[b].tolist() == [-1.0] + [float(low)] * (n - 1)
