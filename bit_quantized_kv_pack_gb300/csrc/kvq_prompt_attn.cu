@@ -44,6 +44,21 @@ bool encode(CUtensorMap* map, const void* base, int rank, const uint64_t* extent
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Units order[0 .. n) of the line to `units` (kvq_testing_prompt_units), by one warp.
+__global__ void units_kernel(prompt::UnitLine line, const int32_t* order, int n, int4* units) {
+  line.begin();
+  for (int i = 0; i < n; ++i) {
+    const bool found = line.find(order[i]), has = line.has(order[i]);
+    if (!found) {
+      if (threadIdx.x == 0) units[i] = make_int4(-1, 0, 0, 0);
+    } else if (has) {
+      int h, t0;
+      line.place(order[i], h, t0);
+      units[i] = make_int4(line.run.c0, line.run.n, h, t0);
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_prompt_attention(const kvq_prompt_args& A, cudaStream_t st) {
@@ -88,3 +103,18 @@ cudaError_t launch_prompt_attention(const kvq_prompt_args& A, cudaStream_t st) {
 }
 
 }  // namespace kvq
+
+extern "C" kvq_status kvq_testing_prompt_units(const int32_t* cu_seqlens, int32_t batch, int32_t total, int32_t max_len,
+                                               int32_t heads, int32_t tokens, const int32_t* order, int32_t n,
+                                               int32_t* units) {
+  if (!cu_seqlens || batch < 1 || total < 0 || max_len < 0 || heads < 1 || tokens < 1 || !order || n < 1 || !units ||
+      reinterpret_cast<uintptr_t>(units) % 16)
+    return KVQ_ERR_INVALID_ARG;
+  kvq::prompt::UnitLine line = {};
+  line.cu = cu_seqlens;
+  line.B = batch, line.total = total, line.max_len = max_len, line.Hkv = heads, line.step = tokens;
+  kvq::units_kernel<<<1, 32>>>(line, order, n, reinterpret_cast<int4*>(units));
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}

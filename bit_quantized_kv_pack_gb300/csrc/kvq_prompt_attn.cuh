@@ -269,27 +269,66 @@ __device__ __forceinline__ int next_block(uint32_t at) {
   return ok ? (int)x : -1;
 }
 
-// The warp that works out the units: a window of 32 sequences goes along the line (the
-// blocks that it gets come in rising order).
-template <int D, bool SHARED>
-__device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, Unit* unit) {
-  using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
-  const int step = (SHARED ? 1 : C::LANES) * a.T;  // tokens of a unit
-  int b0 = 0;
-  int64_t base = 0, scan = 0;  // units before the window; of its sequences up to the lane's
-  Run run = {0, 0};
-  auto window = [&] {
-    run.n = 0;
-    if (b0 + lane < a.B) run = run_of(a.cu, b0 + lane, a.total, a.max_len);
-    scan = run.n > 0 ? (int64_t)((run.n + step - 1) / step) * a.Hkv : 0;
+// The line of units as a warp sees it: a window of 32 sequences goes along it.
+struct UnitLine {
+  const int32_t* cu;
+  int B, total, max_len, Hkv, step;  // step: tokens of a unit
+  int b0;                            // the window's first sequence
+  int64_t base, scan;                // units before the window; of its sequences up to the lane's
+  Run run;
+
+  __device__ __forceinline__ void begin() {
+    b0 = 0;
+    base = 0;
+    window();
+  }
+  __device__ __forceinline__ void window() {
+    const int lane = threadIdx.x & 31;
+    run = {0, 0};
+    if (b0 + lane < B) run = run_of(cu, b0 + lane, total, max_len);
+    scan = run.n > 0 ? (int64_t)((run.n + step - 1) / step) * Hkv : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += v;
     }
-  };
-  window();
+  }
+  // The window goes to the one that has unit u; false: there are not so many.  Units mostly
+  // come in rising order, but nothing says that the blocks a block takes over do.
+  __device__ __forceinline__ bool find(int u) {
+    if (u < base) begin();
+    while (b0 < B) {
+      const int64_t all = __shfl_sync(0xffffffffu, scan, 31);
+      if (u < base + all) return true;
+      base += all;
+      b0 += 32;
+      window();
+    }
+    return false;
+  }
+  // Whether the lane's sequence is the one that has unit u of the window (all lanes ask).
+  __device__ __forceinline__ bool has(int u) const {
+    const uint32_t at = __ballot_sync(0xffffffffu, u < base + scan);
+    return (int)(threadIdx.x & 31) == __ffs(at) - 1;
+  }
+  // Its head and first token, by that lane: the sequence's last block first, heads within blocks.
+  __device__ __forceinline__ void place(int u, int& h, int& t0) const {
+    const int r = (int)(base + scan - 1 - u);  // units after it in the sequence
+    h = Hkv - 1 - r % Hkv;
+    t0 = r / Hkv * step;
+  }
+};
+
+// The warp that works out the units.
+template <int D, bool SHARED>
+__device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& wt, uint32_t smem, Unit* unit) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  UnitLine line;
+  line.cu = a.cu;
+  line.B = a.B, line.total = a.total, line.max_len = a.max_len, line.Hkv = a.Hkv;
+  line.step = (SHARED ? 1 : C::LANES) * a.T;
+  line.begin();
   const uint32_t answer = smem + C::OFF_UNIT + sizeof(Unit);
   int u = blockIdx.x;
   bool own = true;
@@ -316,30 +355,21 @@ __device__ __forceinline__ void unit_role(const PromptAttnArgs& a, const Waits& 
       // each block of the grid, and each that is taken over, looks at one sequence's entries
       if (lane == 0 && u < a.B && run_of(a.cu, u, a.total, a.max_len).n < 0)
         set_error(a.err_word, KVQ_ERRBIT_BADLEN);
-      while (b0 < a.B) {
-        const int64_t all = __shfl_sync(0xffffffffu, scan, 31);
-        if (u < base + all) break;
-        base += all;
-        b0 += 32;
-        window();
-      }
-      if (b0 < a.B) break;
+      if (line.find(u)) break;
       // the grid may have more blocks than there are units: the rest are taken over here
     }
     const bool more = u >= 0;
-    // the sequence that has unit u; its last block first, heads within blocks
-    const uint32_t has = __ballot_sync(0xffffffffu, more && u < base + scan);
-    if (more ? lane == __ffs(has) - 1 : lane == 0) {
+    // the lane of the sequence that has unit u
+    const bool has = line.has(u);
+    if (more ? has : lane == 0) {
       Unit s;
       s.no = 0;
       if (more) {
-        const int r = (int)(base + scan - 1 - u);  // units after it in the sequence
-        s.c0 = run.c0, s.n = run.n;
-        s.h = a.Hkv - 1 - r % a.Hkv;
-        s.t0 = r / a.Hkv * step;
+        s.c0 = line.run.c0, s.n = line.run.n;
+        line.place(u, s.h, s.t0);
         auto tiles = [&](int l) {
           const int first = s.t0 + l * a.T;
-          return first < run.n ? (min(first + a.T, run.n) + C::TN - 1) / C::TN : 0;
+          return first < s.n ? (min(first + a.T, s.n) + C::TN - 1) / C::TN : 0;
         };
         s.tiles0 = tiles(0);
         s.tiles1 = C::LANES == 2 && !SHARED ? tiles(1) : 0;

@@ -51,7 +51,7 @@ EXPORTS = ("kvq_cache_bytes", "kvq_decode_workspace_bytes", "kvq_quantize_pack",
            "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens", "kvq_rotate", "kvq_prompt_attention",
            "kvq_beam_workspace_bytes", "kvq_beam_select", "kvq_reorder",
            "kvq_read_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
-           "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding")
+           "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding", "kvq_testing_prompt_units")
 
 
 class CacheDesc(ctypes.Structure):
@@ -174,6 +174,8 @@ def load(path: str | None = None):
             lib.kvq_beam_select.restype = ctypes.c_int
             lib.kvq_reorder.argtypes = [DP, VP, DP, VP, P, ctypes.c_uint32, P]
             lib.kvq_reorder.restype = ctypes.c_int
+            lib.kvq_testing_prompt_units.argtypes = [P, i32, i32, i32, i32, i32, P, i32, P]
+            lib.kvq_testing_prompt_units.restype = ctypes.c_int
             lib.kvq_read_error.argtypes = [VP, ctypes.POINTER(ctypes.c_uint32), P]
             lib.kvq_read_error.restype = ctypes.c_int
             lib.kvq_status_string.argtypes = [ctypes.c_int]
@@ -944,3 +946,14 @@ def kvq_testing_mma_rounding(n: int = 8):
     out = (ctypes.c_float * 8)()
     _check(load().kvq_testing_mma_rounding(out, int(n)), "kvq_testing_mma_rounding")
     return [float(out[i]) for i in range(n)]
+
+
+def kvq_testing_prompt_units(cu_seqlens: torch.Tensor, max_len: int, total: int, heads: int, tokens: int,
+                             order: torch.Tensor) -> torch.Tensor:
+    """Testing hook (see kvq.h): units order[i] of kvq_prompt_attention's line, int32 [n][4], on
+    the current device."""
+    units = torch.empty(order.numel(), 4, dtype=torch.int32, device=order.device)
+    _check(load().kvq_testing_prompt_units(_ptr(cu_seqlens), cu_seqlens.numel() - 1, int(total), int(max_len),
+                                           int(heads), int(tokens), _ptr(order), order.numel(), _ptr(units)),
+           "kvq_testing_prompt_units")
+    return units

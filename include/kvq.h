@@ -698,6 +698,17 @@ kvq_status kvq_testing_check_arithmetic(uint64_t* div_mismatches, double* rcp_wo
  * default stream).  KVQ_ERR_INVALID_ARG for a null out or n outside 0..8. */
 kvq_status kvq_testing_mma_rounding(float* out, int32_t n);
 
+/* Testing hook (no passage of the pages corresponds to it): where kvq_prompt_attention
+ * finds its units of work, on the current device.  A unit is a KV head of `tokens` tokens
+ * of a prompt; they lie in one line, prompt after prompt (cu_seqlens, batch, total and
+ * max_len as there), the last tokens first, heads within them.  For unit order[i] >= 0,
+ * in any order, units[4 i ..] gets the prompt's first row and length, the head and the
+ * first token, or -1, 0, 0, 0 where there are fewer.  cu_seqlens, order [n] and units (16-byte
+ * aligned) are device arrays.  Synchronous (legacy default stream). */
+kvq_status kvq_testing_prompt_units(const int32_t* cu_seqlens, int32_t batch, int32_t total, int32_t max_len,
+                                    int32_t heads, int32_t tokens, const int32_t* order, int32_t n,
+                                    int32_t* units);
+
 #ifdef __cplusplus
 }
 #endif

@@ -187,3 +187,9 @@ def test_twins_have_the_shape_and_share_pools_only_when_asked():
 def test_axes_of_pairs():
     assert list(kvq.axes_of_pairs((2, 3, 1))) == [0, 0, 1, 1, 1, 2]
     assert list(kvq.axes_of_pairs((2, 3, 1), interleaved=True)) == [0, 1, 2, 0, 1, 1]
+
+
+def test_prompt_units_refuses(lib):
+    good = [0x100000, 2, 10, 5, 4, 64, 0x200000, 3, 0x300000]
+    for i, bad in ((0, 0), (1, 0), (2, -1), (3, -1), (4, 0), (5, 0), (6, 0), (7, 0), (8, 0), (8, 0x300008)):
+        assert lib.kvq_testing_prompt_units(*[bad if i == j else x for j, x in enumerate(good)]) == INVALID

@@ -333,3 +333,22 @@ def test_a_block_of_one_row_at_a_tile_s_end(d):
             at += n
         got = kvq.kvq_prompt_attention(q, k, v2, cu, max(lens), flags=kvq.KVQ_OUT_F32)
         assert np.array_equal(to_np(got), to_np(expect), equal_nan=True)
+
+
+@pytest.mark.parametrize("heads,tokens", [(1, 1), (8, 64), (3, 84), (2, 256)])
+def test_units_are_found_in_any_order(heads, tokens):
+    """Blocks take over units from others; that they come in rising order is not promised."""
+    rng = np.random.default_rng(heads * tokens)
+    lens = rng.integers(0, 5 * tokens, 200)
+    lens[rng.random(200) < 0.3] = 0
+    lens[:40] = 0                                     # the first window has none
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    line = [(cu[b], n, h, t * tokens) for b, n in enumerate(lens) for t in reversed(range(-(-n // tokens)))
+            for h in range(heads)]
+    most = len(line)
+    rising = np.arange(most)
+    orders = [rising, rising[::-1], rng.permutation(most + 50), [most + 7, 0, most, most - 1, 0, 0, most // 2, 1]]
+    for order in orders:
+        got = kvq.kvq_testing_prompt_units(ints(cu), int(lens.max()), int(cu[-1]), heads, tokens, ints(list(order)))
+        want = [line[u] if u < most else (-1, 0, 0, 0) for u in order]
+        assert np.array_equal(to_np(got), np.array(want))
