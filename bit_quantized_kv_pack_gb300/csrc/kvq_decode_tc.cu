@@ -603,11 +603,6 @@ __global__ void __launch_bounds__(NTHREADS, CPS)
       ptx::prefetch_tensormap(&tm_vc);
     }
   }
-  // A launch that depends on this one programmatically (the next step) may
-  // start filling the SMs this grid frees; it waits for this grid before it
-  // touches anything this grid writes.
-  asm volatile("griddepcontrol.launch_dependents;");
-
   int i0 = 0, i1 = 0, ntiles = 0, row0 = 0;
   uint32_t err_bits = 0;
   // packed rows in the codes / params arrays (bulk copies must stay inside)
@@ -744,6 +739,13 @@ __global__ void __launch_bounds__(NTHREADS, CPS)
     }
   }
   grid_dependency_wait();
+  // A launch that depends on this one programmatically (the next step) may
+  // start filling the SMs this grid frees; it waits for this grid before it
+  // touches anything this grid writes.  Not sooner: what it reads before its wait
+  // (KVQ_STEP_EARLY_CACHE_READ) may have been written by the kernel before
+  // this one, which is done now.  (The same for every kernel here that may itself
+  // begin early: its wait comes before this instruction.)
+  asm volatile("griddepcontrol.launch_dependents;");
 
   // The small loads go first -- q by every thread, the lengths by thread 0 --
   // so they are not queued behind the bulk tile copies.  QB * D / 128 = 4 halves

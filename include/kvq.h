@@ -297,7 +297,9 @@ kvq_status kvq_decode_attention(const kvq_cache_desc* desc, const kvq_cache_view
  *              kernel enqueued on `stream` just before this call does not write
  *              this cache (any array of its view, counters included) -- in a serving loop
  *              it computes q, k_new and v_new, and the cache was last written by
- *              this layer's previous step.  The step (launched as a programmatic
+ *              this layer's previous step.  What earlier kernels wrote is seen (a
+ *              kvq_reorder into this cache two kernels before, say; one just before
+ *              rules the flag out).  The step (launched as a programmatic
  *              dependent of that kernel) then reads the counters and cuts its
  *              ranges before it waits for that kernel, and starts its copies the
  *              moment the wait returns; q, k_new and v_new are read, and anything

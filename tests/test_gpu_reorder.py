@@ -11,6 +11,12 @@ from _util import to_np
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
 ROWS = ("k_codes", "v_codes", "k_params", "v_params", "k_mode", "v_mode")
 STATE = ("k_res", "v_res", "k_sink", "v_sink", "counters")
 
@@ -180,3 +186,52 @@ def test_many_sequences_streams_and_graphs():
     torch.cuda.synchronize()
     for n, x in want.items():
         assert np.array_equal(to_np(getattr(dst, n)).view(x.dtype), x), n
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("writer", ["reorder", "append"])
+def test_a_step_that_reads_early_sees_what_was_written_two_kernels_before(writer, paged):
+    """A reorder into (or an append to) one cache, a step of another, then a step of the first
+    with KVQ_STEP_EARLY_CACHE_READ: grids of a few blocks, so that all of them could run at once.
+    The same calls without the flag, one after the other, give every byte of the caches, and the
+    same outputs but for roundings: a step's splits add up in any order (red.add), up to 64 sums in
+    fp32, 2^-23 of values below 8 each: 2^-14; and each side is rounded to fp16, 2^-11 of the value."""
+    rng = np.random.default_rng(41 + paged)
+    H, d, gq, cap, Nr, rounds = 1, 128, 4, 1024, 16, 24
+    kw = dict(page_size=32, num_pages=200) if paged else {}
+    src = kvq.KVCache(4, H, d, 4, cap, Nr, **kw)
+    k, v = (torch.from_numpy(rng.standard_normal((4, H, 900, d)).astype(np.float16)).to(DEV) for _ in range(2))
+    if paged:
+        src.block_table.copy_(torch.arange(128, dtype=torch.int32).view(4, 32))
+    kvq.kvq_quantize_pack(src, k, v, ints([40, 900, 300, 610]))
+    order = [ints([int(i)]) for i in rng.integers(0, 4, rounds)]
+    q, kn, vn = (torch.from_numpy(rng.standard_normal((rounds, 3, 1, n, d)).astype(np.float16)).to(DEV)
+                 for n in (H * gq, H, H))
+    results = []
+    for flags in (kvq.KVQ_STEP_EARLY_CACHE_READ, 0):
+        a, b = (src.twin(batch=1) for _ in range(2))
+        for i, c in enumerate((a, b)):
+            if paged:
+                c.block_table.copy_(torch.arange(32 * i, 32 * i + 32, dtype=torch.int32).view(1, 32))
+            kvq.kvq_reorder(c, src, ints([i]))
+        ws = kvq.workspace_for(a, H * gq)
+        out = torch.zeros(rounds, 2, 1, H * gq, d, dtype=torch.float16, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(rounds):
+            if writer == "reorder":
+                kvq.kvq_reorder(a, src, order[i])
+            else:
+                kvq.kvq_append(a, kn[i, 2], vn[i, 2])
+            if not flags:
+                torch.cuda.synchronize()
+            for j, c in enumerate((b, a)):
+                kvq.kvq_decode_step(c, q[i, j], kn[i, j], vn[i, j], out[i, j], ws, flags=flags)
+                if not flags:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert kvq.kvq_read_error(a) == kvq.kvq_read_error(b) == (kvq.KVQ_OK, 0)
+        results.append([out] + [getattr(c, n) for c in (a, b) for n in (*ROWS, *STATE)])
+    x, y = (r.pop(0).double() for r in results)
+    assert ((x - y).abs() <= 2.0 ** -14 + 2.0 ** -10 * y.abs()).all()
+    for x, y in zip(*results):
+        assert to_np(x).tobytes() == to_np(y).tobytes()
