@@ -33,7 +33,9 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Nothing is read or written before the kernel before this one is done.
+// Nothing is read or written before the kernel before this one is done.  What is read then
+// changed while this kernel ran, so it is no read-only data (__ldg), which may be loaded at
+// any time.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");

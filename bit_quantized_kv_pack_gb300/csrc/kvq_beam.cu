@@ -163,7 +163,7 @@ __device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, uint32_t
     for (int j = 0; j < NV; ++j) {
       const uint32_t t = t0 + j * STEP;
       if (t + E <= V)
-        v[j] = __ldg(src + j * kThreads);
+        v[j] = src[j * kThreads];
       else
         v[j] = load_edge(row, t, V);
     }
@@ -177,7 +177,7 @@ __device__ __forceinline__ void load_vecs(uint4 (&v)[NV], const T* row, uint32_t
     for (int u = 0; u < 4; ++u) {
       const bool in = t0 + (uint32_t)(g + u) * STEP + 2 * E <= V;  // both vectors end in the row
       a[u] = b[u] = make_uint4(0, 0, 0, 0);
-      if (in) a[u] = __ldg(src + (g + u) * kThreads), b[u] = __ldg(src + (g + u) * kThreads + 1);
+      if (in) a[u] = src[(g + u) * kThreads], b[u] = src[(g + u) * kThreads + 1];
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   const int64_t r = (int64_t)blockIdx.x * a.W + w;
   if (tid == 0) count = 0;
   wait_for_previous();
-  const float base = __ldg(a.scores + r);
-  const bool done = a.finished && __ldg(a.finished + r);
+  const float base = a.scores[r];
+  const bool done = a.finished && a.finished[r];
   const bool read = part < per && !done;
   const float2 sums = read && lane < a.pieces ? __ldcg(a.ms + r * a.pieces + lane) : make_float2(-INFINITY, 0.0f);
 

@@ -758,7 +758,7 @@ __device__ __forceinline__ void fetch_role(const ChunkAttnArgs& a, const Waits& 
     const int hi = min(s.hi, s.npt), rows = s.npk - j * kPage;  // (of the sequence, from the lane's on)
     const int64_t row0 = a.rm.paged ? (int64_t)s.h * kPage : ((int64_t)s.b * a.Hkv + s.h) * a.cap + j * kPage;
     const int* table = a.rm.block_table + (int64_t)s.b * (a.cap / kPage) + j;
-    auto page_of = [&](int t) { return a.rm.paged && t < hi && t * C::TN < rows ? __ldg(table + t * NP) : 0; };
+    auto page_of = [&](int t) { return a.rm.paged && t < hi && t * C::TN < rows ? table[t * NP] : 0; };
     int next = page_of(s.lo);
     for (int t = s.lo; ok && t < hi; ++t) {
       const int page = next;
@@ -971,8 +971,8 @@ struct Soft {
       uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
       if (row < rows) {
         const uint4* src = reinterpret_cast<const uint4*>(a.q + row_at(k, lane() * 128 + row)) + c;
-        u0 = __ldg(src);
-        u1 = __ldg(src + 1);
+        u0 = src[0];
+        u1 = src[1];
       }
       to_storage<BITS>(u0, u1);
       const uint32_t at = base + (c * 8 / C::PW) * C::QP;

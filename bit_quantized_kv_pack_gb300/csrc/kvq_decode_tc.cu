@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(NTHREADS, CPS)
     const bool active = lane < D / 8;
     uint4 nv = make_uint4(0, 0, 0, 0);
     if (active)
-      nv = __ldg(reinterpret_cast<const uint4*>((which ? a.v_new : a.k_new) + bh * D) + lane);
+      nv = reinterpret_cast<const uint4*>((which ? a.v_new : a.k_new) + bh * D)[lane];
     float* xb = xbuf + which * 2 * D;
     if (xflags & 2) {
       // the oldest window token (or, with no window, the new one) -> slot Lp

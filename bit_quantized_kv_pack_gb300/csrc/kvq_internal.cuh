@@ -51,8 +51,10 @@ struct RowMap {
   const int32_t* block_table;  // [B][cap / 32] (paged)
   int Hkv, cap, paged, npages;
 
+  // (a plain load: kvq_reorder writes tables, and a kernel that may begin before the one
+  // that writes has no read-only data of it)
   __device__ __forceinline__ int page_of(int b, int j) const {  // j = t / 32
-    return __ldg(block_table + (int64_t)b * (cap / kPage) + j);
+    return block_table[(int64_t)b * (cap / kPage) + j];
   }
   __device__ __forceinline__ int64_t row(int b, int h, int t) const {
     if (!paged) return ((int64_t)b * Hkv + h) * cap + t;

@@ -8,8 +8,9 @@
 // bytes are read or written.
 //
 // Bound by memory: every live byte is read once and written once.  4 sequences of 32768
-// tokens, 8 heads, INT4: 55 us, 90 % of the measured copy rate (loads through the cache and
-// streaming stores; plain ones 59).  32 sequences with shared pages: 8.1 us, of which the
+// tokens, 8 heads, INT4: 56 us, 89 % of the measured copy rate (loads through the cache and
+// streaming stores; plain stores 59, loads past the first cache 57; read-only loads 55.5, but
+// the kernel before may be writing).  32 sequences with shared pages: 8.1 us, of which the
 // lengths' dependent loads and the launch are 4.
 #include "kvq_runs.cuh"
 
@@ -50,7 +51,7 @@ __device__ __forceinline__ void load(uint4 (&v)[N], const uint8_t* src, int byte
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
-    if ((i * 32 + lane) * 16 < bytes) v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
+    if ((i * 32 + lane) * 16 < bytes) v[i] = reinterpret_cast<const uint4*>(src)[i * 32 + lane];
   }
 }
 template <int N>
@@ -61,13 +62,19 @@ __device__ __forceinline__ void store(const uint4 (&v)[N], uint8_t* dst, int byt
     if ((i * 32 + lane) * 16 < bytes) __stcs(reinterpret_cast<uint4*>(dst) + i * 32 + lane, v[i]);
 }
 // Rows that start anywhere (heads of 32 or 64 with odd capacities), and mode bytes: words
-// where both sides and the length allow, else bytes.
+// where both sides and the length allow (four loads in flight), else bytes.
 __device__ __forceinline__ void copy_any(uint8_t* dst, const uint8_t* src, int bytes) {
   const int lane = threadIdx.x & 31;
   if ((((uint32_t)(uintptr_t)dst | (uint32_t)(uintptr_t)src | (uint32_t)bytes) & 3) == 0) {
-#pragma unroll 4
-    for (int i = lane; i < bytes / 4; i += 32)
-      reinterpret_cast<uint32_t*>(dst)[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
+    const int n = bytes / 4;
+    for (int i = lane; i < n; i += 128) {
+      uint32_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = i + 32 * u < n ? reinterpret_cast<const uint32_t*>(src)[i + 32 * u] : 0u;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + 32 * u < n) reinterpret_cast<uint32_t*>(dst)[i + 32 * u] = v[u];
+    }
   } else {
 #pragma unroll 1
     for (int i = lane; i < bytes; i += 32) dst[i] = src[i];
@@ -85,7 +92,7 @@ struct Plan {
 __device__ __forceinline__ Plan plan_of(const ReorderArgs& g, int i, bool report) {
   Plan p;
   p.runs = 0;
-  p.a = __ldg(g.index + i);
+  p.a = g.index[i];
   if (p.a < 0 || p.a >= g.s.B) {
     if (report) set_error(g.err_word, KVQ_ERRBIT_BADINDEX);
     p.a = -1;
@@ -110,7 +117,7 @@ __device__ __forceinline__ void packed_run(const ReorderArgs& g, const Plan& p, 
   const int t = p.t0 + c * g.chunk, rows = min(g.chunk, p.len.npk - t);
   int64_t from, to;
   if (g.paged) {  // a run is a page of one head
-    const int ps = __ldg(g.s.table + (int64_t)p.a * (g.s.cap / kPage) + t / kPage);
+    const int ps = g.s.table[(int64_t)p.a * (g.s.cap / kPage) + t / kPage];
     const int pd = g.d.table[(int64_t)i * (g.d.cap / kPage) + t / kPage];
     if (ps < 0 || ps >= g.s.npages || pd < 0 || pd >= g.d.npages) {
       if (lane == 0) set_error(g.err_word, KVQ_ERRBIT_BADPAGE);
@@ -153,7 +160,7 @@ __device__ __forceinline__ void copy_run(const ReorderArgs& g, const Plan& p, in
     }
     if (g.share)
       for (int j = lane; j < p.t0 / kPage; j += 32)
-        g.d.table[(int64_t)i * (g.d.cap / kPage) + j] = __ldg(g.s.table + (int64_t)p.a * (g.s.cap / kPage) + j);
+        g.d.table[(int64_t)i * (g.d.cap / kPage) + j] = g.s.table[(int64_t)p.a * (g.s.cap / kPage) + j];
     return;
   }
   x -= 1;
@@ -186,7 +193,7 @@ __device__ __forceinline__ void copy_run(const ReorderArgs& g, const Plan& p, in
   for (int j = 0; j < kCodeBytes / 512; ++j) {
     const int at = j * 32 + lane;
     v[j] = make_uint4(0, 0, 0, 0);
-    if (live(at)) v[j] = __ldg(reinterpret_cast<const uint4*>(src) + at);
+    if (live(at)) v[j] = reinterpret_cast<const uint4*>(src)[at];
   }
 #pragma unroll
   for (int j = 0; j < kCodeBytes / 512; ++j) {

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     const int n = a.interleaved ? 4 : 8;
     const uint32_t axes = (uint32_t)(a.axis[p0 >> 5] >> (2 * (p0 & 31))) & (a.interleaved ? 0xffu : 0xffffu);
     auto row = [&](int axis) -> const float2* {
-      int pos = __ldg(a.positions + (int64_t)axis * a.total + t);
+      int pos = a.positions[(int64_t)axis * a.total + t];
       if (pos < 0 || pos >= a.rows) {
         set_error(a.err_word, KVQ_ERRBIT_BADPOS);
         pos = pos < 0 ? 0 : a.rows - 1;
@@ -86,14 +86,14 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (2 * i >= n) break;
-        const float4 f = __ldg(src + i);
+        const float4 f = src[i];
         cs[2 * i] = make_float2(f.x, f.y);
         cs[2 * i + 1] = make_float2(f.z, f.w);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) cs[i] = __ldg(row((axes >> (2 * i)) & 3u) + i);
+        if (i < n) cs[i] = row((axes >> (2 * i)) & 3u)[i];
     }
   }
   const int partner = lane + (second ? -(half >> 3) : half >> 3);

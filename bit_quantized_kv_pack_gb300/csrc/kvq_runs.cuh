@@ -23,7 +23,7 @@ struct Run {
   int c0, n;
 };
 __device__ __forceinline__ Run run_of(const int32_t* cu, int b, int total, int max_len) {
-  const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+  const int c0 = cu[b], c1 = cu[b + 1];
   Run r;
   r.c0 = c0;
   r.n = (c0 >= 0 && c1 >= c0 && c1 <= total && c1 - c0 <= max_len) ? c1 - c0 : -1;

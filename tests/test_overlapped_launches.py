@@ -36,3 +36,12 @@ def test_a_kernel_that_waits_lets_the_next_begin_after_its_wait():
                 assert waits.start() < body.index(trigger), (os.path.basename(path), name)
                 seen += 1
     assert seen >= 4  # the step, both kernels of the attention of runs, the end of their append
+
+
+def test_kernels_that_begin_early_have_no_read_only_loads():
+    """Read-only loads are for data that nothing writes while the kernel runs, and these run
+    before the kernel that writes it is done: a compiler may move such a load over the wait."""
+    for name in ("kvq_internal.cuh", "kvq_runs.cuh", "kvq_around.cuh", "kvq_rotate.cu", "kvq_beam.cu", "kvq_reorder.cu",
+                 "kvq_prompt_attn.cuh", "kvq_chunk_attn.cuh", "kvq_decode_tc.cu"):
+        text = code(os.path.join(CSRC, name))
+        assert not re.search(r"__ldg\(|ld\.global\.nc|__restrict__", text), name
