@@ -2,12 +2,49 @@
 // Every entry point validates on the host and launches nothing on an error.
 #include <string.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "kvq_around.cuh"
 #include "kvq_runs.cuh"
 
 namespace {
 
 using kvq::Dims;
+
+// A device's word for the errors of calls that are given none, and where it is read through.
+__device__ uint32_t g_err_word;
+__device__ uint32_t g_err_taken;
+
+__global__ void take_errors_kernel() { g_err_taken = atomicExch(&g_err_word, 0u); }
+
+// The word of the current device (a symbol's address, looked up once for each).
+kvq_status device_err_word(uint32_t** word) {
+  static std::atomic<uint32_t*> words[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  uint32_t* w = dev < 64 ? words[dev].load(std::memory_order_acquire) : nullptr;
+  if (!w) {
+    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&w), g_err_word) != cudaSuccess) {
+      cudaGetLastError();
+      return KVQ_ERR_CUDA;
+    }
+    if (dev < 64) words[dev].store(w, std::memory_order_release);
+  }
+  *word = w;
+  return KVQ_OK;
+}
+
+// An error word's status: that of its lowest set bit.
+kvq_status status_of(uint32_t w) {
+  if (w & KVQ_ERRBIT_CAPACITY) return KVQ_ERR_CAPACITY;
+  if (w & KVQ_ERRBIT_EMPTY) return KVQ_ERR_EMPTY;
+  if (w & KVQ_ERRBIT_TIMEOUT) return KVQ_ERR_TIMEOUT;
+  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE | KVQ_ERRBIT_BADPOS | KVQ_ERRBIT_BADINDEX |
+           KVQ_ERRBIT_BADSCORE))
+    return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -343,7 +380,7 @@ bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128 || d == 256;
 
 kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
   if (!args) return KVQ_ERR_INVALID_ARG;
-  const kvq_rotate_args& A = *args;
+  kvq_rotate_args A = *args;
   if (A.total < 0 || A.head_dim < 32 || A.head_dim % 32 || (!A.q && !A.k && A.total > 0)) return KVQ_ERR_INVALID_ARG;
   if (!head_dim_ok(A.head_dim)) return KVQ_ERR_UNSUPPORTED;
   if (A.rotary_dim < 1 || A.rotary_dim > A.head_dim || (A.interleaved != 0 && A.interleaved != 1))
@@ -361,12 +398,13 @@ kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
                               A.k_out_stride_token, A.k_out_stride_head)) != KVQ_OK)
     return st;
   if (!aligned(A.rope, 16) || !aligned(A.positions, 4) || !aligned(A.err_word, 4)) return KVQ_ERR_MISALIGNED;
+  if (!A.err_word && (st = device_err_word(&A.err_word)) != KVQ_OK) return st;
   return from_cuda(kvq::launch_rotate(A, static_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream) {
   if (!args) return KVQ_ERR_INVALID_ARG;
-  const kvq_prompt_args& A = *args;
+  kvq_prompt_args A = *args;
   if (A.total < 0 || A.max_len < 0 || A.batch < 1 || !A.cu_seqlens || A.num_kv_heads < 1 || A.num_q_heads < 1 ||
       A.num_q_heads % A.num_kv_heads || A.head_dim < 32 || A.head_dim % 32 || (A.flags & ~(uint32_t)KVQ_OUT_F32))
     return KVQ_ERR_INVALID_ARG;
@@ -384,6 +422,8 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream) {
   if (!aligned(A.q, 16) || !aligned(A.k, 16) || !aligned(A.v, 16) || !aligned(A.out, 16) ||
       !aligned(A.cu_seqlens, 4) || !aligned(A.err_word, 4))
     return KVQ_ERR_MISALIGNED;
+  const kvq_status st = A.err_word ? KVQ_OK : device_err_word(&A.err_word);
+  if (st != KVQ_OK) return st;
   return from_cuda(kvq::launch_prompt_attention(A, static_cast<cudaStream_t>(stream)));
 }
 
@@ -403,8 +443,8 @@ size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int
 
 kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream) {
   if (!args) return KVQ_ERR_INVALID_ARG;
-  const kvq_beam_args& A = *args;
-  const kvq_status st = check_beams(A.batch, A.beams, A.vocab, A.n);
+  kvq_beam_args A = *args;
+  kvq_status st = check_beams(A.batch, A.beams, A.vocab, A.n);
   if (st != KVQ_OK) return st;
   if (!A.logits || !A.scores || !A.parent || !A.token || !A.score || !A.workspace ||
       (A.flags & ~(uint32_t)KVQ_LOGITS_F32) || A.stride_row < A.vocab)
@@ -414,6 +454,7 @@ kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream) {
       !aligned(A.token, 4) || !aligned(A.score, 4) || !aligned(A.err_word, 4))
     return KVQ_ERR_MISALIGNED;
   if (A.ws_bytes < kvq::beam_workspace_bytes(A.batch, A.beams, A.vocab, A.n)) return KVQ_ERR_INVALID_ARG;
+  if (!A.err_word && (st = device_err_word(&A.err_word)) != KVQ_OK) return st;
   return from_cuda(kvq::launch_beam_select(A, static_cast<cudaStream_t>(stream)));
 }
 
@@ -464,13 +505,22 @@ kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* 
   if (e != cudaSuccess) return KVQ_ERR_CUDA;
   if (word_out) *word_out = w;
   if (w & KVQ_ERRBIT_TIMEOUT) kvq::noalloc_forget_layout();
-  if (w & KVQ_ERRBIT_CAPACITY) return KVQ_ERR_CAPACITY;
-  if (w & KVQ_ERRBIT_EMPTY) return KVQ_ERR_EMPTY;
-  if (w & KVQ_ERRBIT_TIMEOUT) return KVQ_ERR_TIMEOUT;
-  if (w & (KVQ_ERRBIT_BADLEN | KVQ_ERRBIT_BADPAGE | KVQ_ERRBIT_BADPOS | KVQ_ERRBIT_BADINDEX |
-           KVQ_ERRBIT_BADSCORE))
-    return KVQ_ERR_INVALID_ARG;
-  return KVQ_OK;
+  return status_of(w);
+}
+
+kvq_status kvq_read_device_error(uint32_t* word_out, void* stream) {
+  static std::mutex one;  // reads through one place
+  std::lock_guard<std::mutex> lock(one);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t w = 0;
+  // (exchanged: calls on other streams may be setting bits)
+  take_errors_kernel<<<1, 1, 0, st>>>();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&w, g_err_taken, sizeof(w), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  if (word_out) *word_out = w;
+  return status_of(w);
 }
 
 const char* kvq_status_string(kvq_status status) {

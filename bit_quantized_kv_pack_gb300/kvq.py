@@ -50,7 +50,7 @@ EXPORTS = ("kvq_cache_bytes", "kvq_decode_workspace_bytes", "kvq_quantize_pack",
            "kvq_decode_attention_noalloc", "kvq_append_chunk", "kvq_chunk_workspace_bytes",
            "kvq_chunk_attention", "kvq_cross_attention", "kvq_read_tokens", "kvq_rotate", "kvq_prompt_attention",
            "kvq_beam_workspace_bytes", "kvq_beam_select", "kvq_reorder",
-           "kvq_read_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
+           "kvq_read_error", "kvq_read_device_error", "kvq_status_string", "kvq_version", "kvq_testing_wait_fault",
            "kvq_testing_check_arithmetic", "kvq_testing_mma_rounding", "kvq_testing_prompt_units")
 
 
@@ -178,6 +178,8 @@ def load(path: str | None = None):
             lib.kvq_testing_prompt_units.restype = ctypes.c_int
             lib.kvq_read_error.argtypes = [VP, ctypes.POINTER(ctypes.c_uint32), P]
             lib.kvq_read_error.restype = ctypes.c_int
+            lib.kvq_read_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), P]
+            lib.kvq_read_device_error.restype = ctypes.c_int
             lib.kvq_status_string.argtypes = [ctypes.c_int]
             lib.kvq_status_string.restype = ctypes.c_char_p
             lib.kvq_version.argtypes = []
@@ -780,7 +782,7 @@ def kvq_rotate(q: torch.Tensor | None, k: torch.Tensor | None, rope: torch.Tenso
     [rows][rotary_dim / 2][2], see rope_table).  ``pair_axis``: the axis of each pair
     (axes_of_pairs; None: axis 0 for all).  The outputs are new tensors, or q_out and
     k_out, which may be q and k themselves.  ``err``: a cache's err, for positions outside
-    the table."""
+    the table (None: the device's own word, kvq_read_device_error)."""
     x = q if q is not None else k
     if x is None or x.dim() != 3:
         raise ValueError("q or k must be [total][heads][d]")
@@ -815,7 +817,8 @@ def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_s
     """Causal attention over whole prompts in full precision: q fp16 [total][Hq][d], k and v
     [total][Hkv][d] (views with d contiguous: columns of a fused projection's output, say),
     prompt b being rows cu_seqlens[b] .. cu_seqlens[b+1] (int32 [B + 1]).  out [total][Hq][d],
-    fp16, or fp32 as for kvq_decode_attention.  ``err``: a cache's err."""
+    fp16, or fp32 as for kvq_decode_attention.  ``err``: a cache's err (None: the device's own
+    word, kvq_read_device_error); KVQ_ERRBIT_TIMEOUT in it says that rows of out are wrong."""
     shape, kv = q.shape, k.shape
     if len(shape) != 3 or len(kv) != 3 or kv != v.shape or kv[0] != shape[0] or kv[2] != shape[2]:
         raise ValueError("q must be [total][Hq][d], k and v [total][Hkv][d]")
@@ -860,7 +863,8 @@ def kvq_beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int, finished
     beams and tokens for each batch entry, best first (a beam's in the order of its logits).  ``finished``
     (uint8 or bool [B][W]): complete beams, which go on with ``end_token`` at their score.
     Returns (parent, token, score), each [B][n] (``out``: such a triple): parent is the row
-    b W + w, an index for kvq_reorder."""
+    b W + w, an index for kvq_reorder.  ``err``: a cache's err (None: the device's own word,
+    kvq_read_device_error)."""
     dtype, shape, index = logits.dtype, logits.shape, logits.get_device()
     if (len(shape) != 3 or dtype not in (torch.float16, torch.float32) or index < 0
             or (logits.stride(2) != 1 and shape[2] > 1)):
@@ -918,6 +922,15 @@ def kvq_read_error(cache: KVCache, stream=None) -> tuple[int, int]:
     word = ctypes.c_uint32(0)
     st = load().kvq_read_error(ctypes.byref(cache.view), ctypes.byref(word),
                                _stream(stream, cache.device))
+    return st, word.value
+
+
+def kvq_read_device_error(device="cuda", stream=None) -> tuple[int, int]:
+    """(status, raw error word) of the calls on a device that were given no ``err``, of any
+    stream; synchronizes the stream and clears the word."""
+    word = ctypes.c_uint32(0)
+    with torch.cuda.device(torch.device(device)):
+        st = load().kvq_read_device_error(ctypes.byref(word), _stream(stream, torch.device(device)))
     return st, word.value
 
 

@@ -105,7 +105,7 @@
  * ---------------------------------------------------------------------------
  * Conventions
  *   Ownership: the caller owns all memory and the stream.  The library allocates
- *     nothing and never synchronizes, except kvq_read_error.
+ *     nothing and never synchronizes, except kvq_read_error and kvq_read_device_error.
  *   Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *   Errors: argument errors return synchronously and launch nothing.  A failed
  *     launch returns KVQ_ERR_CUDA.  Data-dependent errors (capacity overflow, an
@@ -497,8 +497,8 @@ kvq_status kvq_read_tokens(const kvq_cache_desc* desc, const kvq_cache_view* vie
  *            the cache; all three read and write the columns of a fused projection's
  *            output in place), kvq_reorder (one cached prompt to all its beams)
  *   token    kvq_rotate, kvq_decode_step, kvq_beam_select, kvq_reorder
- * Where a call takes an err_word (a cache's, or any zeroed device word) and it is NULL,
- * errors that depend on data are not reported; the results are the same. */
+ * Where a call takes an err_word (a cache's, or any zeroed device word) and it is NULL, its
+ * bits go to a word that the library keeps for the current device: kvq_read_device_error. */
 
 /* Arguments of kvq_rotate; zero-initialise the struct. */
 typedef struct {
@@ -526,7 +526,7 @@ typedef struct {
   const int32_t* positions; /* int32 device [axes][total] */
   const uint8_t* pair_axis; /* HOST [rotary_dim / 2]: the axis of each pair (NULL: axis 0);
                                read during the call */
-  uint32_t* err_word;      /* device, or NULL */
+  uint32_t* err_word;      /* device, or NULL: the device's own word */
 } kvq_rotate_args;
 
 /* Rotate queries and keys to positions on several axes (time, height and width of the
@@ -559,7 +559,7 @@ typedef struct {
   int32_t max_len;
   void* out;               /* device [total][Hq][d], fp16 (fp32 with KVQ_OUT_F32); overlaps no input */
   uint32_t flags;          /* 0 or KVQ_OUT_F32 */
-  uint32_t* err_word;      /* device, or NULL */
+  uint32_t* err_word;      /* device, or NULL: the device's own word */
 } kvq_prompt_args;
 
 /* Causal attention over whole prompts in full precision (before the cache is packed):
@@ -577,6 +577,8 @@ typedef struct {
  * output infinite, or NaN beside one of the other sign or NaN (with fp16 output also where the
  * value's weight rounds to zero, below 2^-32 of the largest).  Entries of cu_seqlens that break the rule set
  * KVQ_ERRBIT_BADLEN (where they let prompts overlap, some may stay unwritten).
+ * The waits inside are bounded, by a second of wall time each (a GPU that is held up for that long
+ * counts too): KVQ_ERRBIT_TIMEOUT says that one ran out, and rows of the output are then wrong.
  * Asynchronous; lengths are read on the device. */
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream);
 
@@ -600,7 +602,7 @@ typedef struct {
   void* workspace;         /* device, 16-byte aligned, ws_bytes >= kvq_beam_workspace_bytes;
                               whatever it holds, each call writes what it reads; one call at a time */
   size_t ws_bytes;
-  uint32_t* err_word;      /* device, or NULL */
+  uint32_t* err_word;      /* device, or NULL: the device's own word */
 } kvq_beam_args;
 
 #define KVQ_LOGITS_F32 1u
@@ -652,6 +654,10 @@ kvq_status kvq_reorder(const kvq_cache_desc* dst_desc, const kvq_cache_view* dst
 /* Synchronize `stream`, copy *err_word to *word_out (may be NULL), clear it, and
  * return KVQ_OK if it was 0, else the status of its lowest set bit. */
 kvq_status kvq_read_error(const kvq_cache_view* view, uint32_t* word_out, void* stream);
+
+/* The same for the bits of calls on the current device, of any stream, that were given no
+ * err_word: what they set before `stream` gets here (and, of other streams, perhaps later). */
+kvq_status kvq_read_device_error(uint32_t* word_out, void* stream);
 
 /* Static text for a status code. */
 const char* kvq_status_string(kvq_status status);
