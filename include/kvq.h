@@ -568,7 +568,7 @@ typedef struct {
  * Weights are rounded to fp16 once (operands of the tensor cores; weights below 2^-21 of a
  * row's largest by at most 2^-32 of that), with KVQ_OUT_F32 they are two fp16 parts (22 bits);
  * scores and sums are fp32, the output is rounded once.  The tensor cores cut their sums off
- * (2^-23 a step of 16 tokens, towards zero): fp32 output is within 2e-5 of the sums of
+ * (2^-23 a step of 16 tokens, towards zero): fp32 output is within 2.3e-5 of the sums of
  * values of one sign and about 1e-6 of others, whatever the length.  Results do not depend
  * on timing; the order of a row's sums goes by how many blocks of rows there can be (total,
  * batch and heads), so that a prompt may differ in its last bits from the same one in
@@ -621,8 +621,10 @@ size_t kvq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int
  * score of -inf, so n entries always come back.
  * A beam with a NaN or +inf among its logits, or as its score, proposes nothing and sets
  * KVQ_ERRBIT_BADSCORE (a complete beam's logits are not looked at).
- * The sums of exponentials are fp32 (within 2^-20 of the whole), their logarithms and the
- * scores that are compared have 53 bits; scores are rounded to fp32 once, and one
+ * The sums of exponentials are fp32 (within 2^-20 of the whole) and so are their logarithms:
+ * a beam's normaliser, the same for all that it proposes, is within 2^-19, and proposals of two
+ * beams that are nearer to each other than twice that may come in either order.  Scores are
+ * compared as pairs of fp32 numbers, cut to 53 bits; they are rounded to fp32 once, and one
  * below fp32's range is -inf.  Beams of equal logits and scores have equal scores to the
  * last bit; results do not depend on timing.  Asynchronous. */
 kvq_status kvq_beam_select(const kvq_beam_args* args, void* stream);

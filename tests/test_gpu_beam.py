@@ -247,3 +247,31 @@ def test_scores_whose_differences_are_below_their_last_bit(V, dtype):
         assert to_np(token)[b].tolist() == [3] + order.tolist()
         assert to_np(parent)[b].tolist() == [b * W] + [b * W + 1] * (n - 1)
         assert to_np(score)[b].tolist() == [-1.0] + [float(low)] * (n - 1)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_near_ties_of_beams(dtype):
+    """Beams of the same logits in other places: the scores differ by what the sums' order makes.
+    Each normaliser is within 2^-19, so what is left out is no better than what is chosen by more
+    than 2^-18; a beam's own proposals come in the order of its logits."""
+    rng = np.random.default_rng(21)
+    B, W, V, n = 3, 8, 50021, 32
+    row = (rng.standard_normal(V) * 3).astype(dtype)
+    x = np.stack([[rng.permutation(row) for _ in range(W)] for _ in range(B)])
+    scores = (-20 + 1e-6 * rng.standard_normal((B, W))).astype(np.float32)
+    parent, token, score = (to_np(t) for t in kvq.kvq_beam_select(torch.from_numpy(x).to(DEV),
+                                                                  torch.from_numpy(scores).to(DEV), n))
+    x64 = x.astype(np.float64)
+    true = scores.astype(np.float64)[..., None] + x64 - np.log(np.exp(x64).sum(-1, keepdims=True))
+    for b in range(B):
+        w = parent[b] - b * W
+        mine = true[b, w, token[b]]
+        assert len(set(zip(w, token[b]))) == n
+        assert (mine[:-1] - mine[1:] >= -2.0 ** -18).all()
+        left = true[b].copy()
+        left[w, token[b]] = -np.inf
+        assert left.max() <= mine[-1] + 2.0 ** -18
+        assert (np.abs(score[b] - mine) <= 2.0 ** -19 + 2.0 ** -24 * np.abs(mine)).all()
+        for i in range(W):
+            of = token[b][w == i]
+            assert of.tolist() == np.argsort(-x64[b, i], kind="stable")[:len(of)].tolist()

@@ -352,3 +352,20 @@ def test_units_are_found_in_any_order(heads, tokens):
         got = kvq.kvq_testing_prompt_units(ints(cu), int(lens.max()), int(cu[-1]), heads, tokens, ints(list(order)))
         want = [line[u] if u < most else (-1, 0, 0, 0) for u in order]
         assert np.array_equal(to_np(got), np.array(want))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@EMPTY
+def test_the_stated_bound_for_values_of_one_sign(d, empty):
+    """2.3e-5 of the sum, whatever the length: a segment's sums are cut off by 2^-23 of what they
+    are then, half of it on average, in 256 steps (2048 tokens of 16, two parts of the weights):
+    2^-16; segments add up rounded to nearest, 2^-24 each; exponentials 2^-19; scores are cut off
+    likewise, in d / 16 steps, by 2^-23 of sums below 1: 2^-19; the rest 2^-20."""
+    n = 9001
+    q, k, v = inputs(d + 1, n, 1, 1, d, scale=0.1)
+    v = v.abs() + 0.25
+    out = kvq.kvq_prompt_attention(q, k, v, ends([n], empty), n, flags=kvq.KVQ_OUT_F32)
+    for lo in range(0, n, 3000):
+        rows = torch.arange(lo, min(n, lo + 3000), device=DEV)
+        want, _ = plain(q, k, v, rows, f32=True)
+        assert float(((out[rows].double() - want).abs() / want).max()) < 2.3e-5
