@@ -398,7 +398,7 @@ kvq_status kvq_rotate(const kvq_rotate_args* args, void* stream) {
                               A.k_out_stride_token, A.k_out_stride_head)) != KVQ_OK)
     return st;
   if (!aligned(A.rope, 16) || !aligned(A.positions, 4) || !aligned(A.err_word, 4)) return KVQ_ERR_MISALIGNED;
-  if (!A.err_word && (st = device_err_word(&A.err_word)) != KVQ_OK) return st;
+  if (!A.err_word && A.total > 0 && (st = device_err_word(&A.err_word)) != KVQ_OK) return st;
   return from_cuda(kvq::launch_rotate(A, static_cast<cudaStream_t>(stream)));
 }
 
@@ -422,7 +422,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* stream) {
   if (!aligned(A.q, 16) || !aligned(A.k, 16) || !aligned(A.v, 16) || !aligned(A.out, 16) ||
       !aligned(A.cu_seqlens, 4) || !aligned(A.err_word, 4))
     return KVQ_ERR_MISALIGNED;
-  const kvq_status st = A.err_word ? KVQ_OK : device_err_word(&A.err_word);
+  const kvq_status st = A.err_word || A.total == 0 ? KVQ_OK : device_err_word(&A.err_word);
   if (st != KVQ_OK) return st;
   return from_cuda(kvq::launch_prompt_attention(A, static_cast<cudaStream_t>(stream)));
 }

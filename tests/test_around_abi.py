@@ -193,3 +193,8 @@ def test_prompt_units_refuses(lib):
     good = [0x100000, 2, 10, 5, 4, 64, 0x200000, 3, 0x300000]
     for i, bad in ((0, 0), (1, 0), (2, -1), (3, -1), (4, 0), (5, 0), (6, 0), (7, 0), (8, 0), (8, 0x300008)):
         assert lib.kvq_testing_prompt_units(*[bad if i == j else x for j, x in enumerate(good)]) == INVALID
+
+
+def test_calls_without_rows_need_no_device(lib):
+    assert _rotate(lib, total=0, positions=0) == kvq.KVQ_OK
+    assert _prompt(lib, total=0, q=0, k=0, v=0, out=0) == kvq.KVQ_OK
