@@ -21,9 +21,9 @@
 //
 // Bound: the first pass by what a block does one after the other (loads, bound, sum, what
 // passes; three blocks an SM), the second by its chain of merges and barriers.  16 x 8 rows of
-// 128256 fp32 logits take 21 us (their bytes alone 10 at the copy rate; pieces of 8 vectors,
-// four blocks an SM, 21.5); 4 rows of 32000 take 6.4, 20 x 16 of 1002 with 32 proposals 18.5
-// (30 with four bounds of each warp, whether it has tokens or not).
+// 128256 fp32 logits take 19 us (their bytes alone 10 at the copy rate; pieces of 8 vectors,
+// four blocks an SM, 2 % more); 4 rows of 32000 take 5.9, 20 x 16 of 1002 with 32 proposals 11.5
+// (four bounds of each warp, whether it has tokens or not, took 1.6 times as long).
 #include "kvq_around.cuh"
 #include "kvq_ptx.cuh"
 

@@ -32,8 +32,10 @@
 //
 // Bound: at head_dim 128 the tensor cores take 2048 cycles for a tile of both lanes, and a
 // lane's own chain about 2600: softmax 1120 (loads from TMEM to the first exponential 280,
-// exponentials and weights 750), the MMA warp's waits, two batches of MMAs.  The MMA warp
-// itself is busy for about 1050 cycles a batch, which is what bounds head_dim 64.
+// exponentials and weights 750), the MMA warp's waits, two batches of MMAs.  At head_dim 64
+// the MMAs of both lanes take 1024 and the chain 2120, of which the MMA warp issues for 420:
+// two chains are too few to fill the tensor cores (27 % with fp32 output) or the exponentials
+// (17 %).
 // 16384 tokens of 32 heads on 8: 1360 us (1.62 PFLOP/s, 1270 between others of its kind);
 // 16 prompts of 115 to 2048 tokens: 176 us.
 //

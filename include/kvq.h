@@ -596,7 +596,8 @@ typedef struct {
   int32_t n;               /* selected per batch entry: 1..32, at most W V */
   int32_t end_token;       /* what a complete beam goes on with, 0..V-1 (read only with finished) */
   uint32_t flags;          /* 0 or KVQ_LOGITS_F32 */
-  int32_t* parent;         /* device [batch][n]: row of the beam (an index for kvq_reorder) */
+  int32_t* parent;         /* device [batch][n]: row of the beam (an index for kvq_reorder); the */
+                           /*   outputs overlap no input and not each other */
   int32_t* token;          /* device [batch][n] */
   float* score;            /* device [batch][n] */
   void* workspace;         /* device, 16-byte aligned, ws_bytes >= kvq_beam_workspace_bytes;
