@@ -516,6 +516,7 @@ __device__ __forceinline__ void check_role(const PromptAttnArgs& a, const Waits&
           if (__any_sync(0xffffffffu, wt.word(W_ABORT) != 0)) return;
           for (int i = lane; i < 3 * D; i += 32) sts(smem + C::OFF_NOTES + 4 * i, 0x7fffffffu);
           __syncwarp();
+          __threadfence_block();  // (an epilogue of this unit that needs no note may look already)
           wt.set_word(W_NOTED, u.no);
           clean = true;
         }
